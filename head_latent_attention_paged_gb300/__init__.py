@@ -1,7 +1,8 @@
 """Python binding of libmla_gb300.so (paged MLA latent-cache decode, sm_103a).
 
 Argument marshalling only: every step of the decode runs in the library's
-CUDA kernels.  Functions mirror the C ABI in include/mla_decode.h and take
+CUDA kernels.  Functions mirror the C ABI in include/mla_decode.h and
+include/mla_layer.h and take
 device addresses as ints (or any object with ``data_ptr()``, e.g. a torch
 tensor) and CUDA streams as ints (``torch.cuda.current_stream().cuda_stream``)
 or None for the default stream.  There is no fallback: if the library cannot
@@ -35,10 +36,28 @@ MLA_STATUS_TIMEOUT = 0x4
 
 MLA_TILE_TOKENS = 64
 
+MLA_DTYPE_BF16 = 0
+MLA_DTYPE_F16 = 1
+MLA_DTYPE_F32 = 2
+
+MLA_NORM_OUT_SAME = 0
+MLA_NORM_OUT_E4M3_E8M0 = 1
+MLA_NORM_OUT_E4M3_ROW = 2
+MLA_NORM_MAX_COLS = 32768
+
+MLA_ROPE_INTERLEAVED = 0
+MLA_ROPE_HALVES = 1
+MLA_ROPE_SCALING_NONE = 0
+MLA_ROPE_SCALING_LINEAR = 1
+MLA_ROPE_SCALING_PARTS = 2
+MLA_ROPE_SCALING_YARN = 3
+MLA_ROPE_MAX_DIM = 256
+
 EXPORTED = (
     "mla_decode_plan", "mla_q_absorb", "mla_decode_run", "mla_combine", "mla_uv_proj",
     "mla_get_status", "mla_clear_status", "mla_strerror", "mla_version",
     "mla_decode_run_static", "mla_cache_append", "mla_selftest_bounded_wait", "mla_decode_step",
+    "mla_rms_norm", "mla_rope_make_plan", "mla_rope", "mla_cache_append_tokens", "mla_cache_gather",
 )
 
 
@@ -63,6 +82,41 @@ class MlaPlan(ctypes.Structure):
         ("planned_tiles", ctypes.c_int64), ("ws_q_hat", ctypes.c_int64),
         ("split_tokens", ctypes.c_int32), ("sm_count", ctypes.c_int32),
         ("prefix_pass", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3),
+    ]
+
+
+class MlaNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("out_format", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+        ("residual_out_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+        ("scale_stride", ctypes.c_int64),
+    ]
+
+
+class MlaRopeConfig(ctypes.Structure):
+    _fields_ = [
+        ("layout", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("original_positions", ctypes.c_int32), ("theta", ctypes.c_double),
+        ("factor", ctypes.c_double), ("fast_rotations", ctypes.c_double),
+        ("slow_rotations", ctypes.c_double), ("amplitude", ctypes.c_double),
+    ]
+
+
+class MlaRopePlan(ctypes.Structure):
+    _fields_ = [
+        ("config", MlaRopeConfig), ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("turns", ctypes.c_uint64 * (MLA_ROPE_MAX_DIM // 2)),
+    ]
+
+
+class MlaRopeProblem(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rope_offset", ctypes.c_int32), ("dtype", ctypes.c_int32), ("transposed", ctypes.c_int32),
+        ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
     ]
 
 
@@ -95,6 +149,12 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mla_decode_run_static.argtypes = [P(MlaPlan), vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.mla_uv_proj.argtypes = [vp, vp, vp, i32, i32, vp]
     lib.mla_cache_append.argtypes = [P(MlaProblem), vp, vp, vp, ctypes.c_float, vp, vp, vp]
+    lib.mla_rms_norm.argtypes = [P(MlaNormProblem), vp, vp, vp, vp, vp, vp, vp]
+    lib.mla_rope_make_plan.argtypes = [P(MlaRopeConfig), P(MlaRopePlan)]
+    lib.mla_rope.argtypes = [P(MlaRopeProblem), P(MlaRopePlan), vp, vp, vp, vp]
+    lib.mla_cache_append_tokens.argtypes = [P(MlaProblem), i32, vp, i64, vp, vp, vp, vp,
+                                            ctypes.c_float, P(MlaRopePlan), vp, vp, vp]
+    lib.mla_cache_gather.argtypes = [P(MlaProblem), i32, vp, vp, vp, vp, vp, i64, vp, vp]
     lib.mla_selftest_bounded_wait.argtypes = [vp, i64, vp, vp]
     lib.mla_get_status.argtypes = [P(MlaPlan), vp, P(ctypes.c_uint32), vp]
     lib.mla_clear_status.argtypes = [P(MlaPlan), vp, vp]
@@ -241,6 +301,86 @@ def mla_selftest_bounded_wait(status, limit_ns: int, waited_ns=None, stream=None
 def mla_uv_proj(o_lat, w_uv, out, rows: int, num_heads: int, stream=None) -> None:
     _check("mla_uv_proj", load().mla_uv_proj(_ptr(o_lat), _ptr(w_uv), _ptr(out), int(rows),
                                              int(num_heads), _stream(stream)))
+
+
+def make_norm_problem(rows, cols, dtype=MLA_DTYPE_BF16, out_format=MLA_NORM_OUT_SAME, eps=1e-6,
+                      x_stride=None, residual_stride=None, residual_out_stride=None,
+                      out_stride=None, scale_stride=None) -> MlaNormProblem:
+    """Strides are in elements (scale_stride in bytes) and default to packed rows."""
+    s = [cols if v is None else v for v in (x_stride, residual_stride, residual_out_stride,
+                                            out_stride)]
+    return MlaNormProblem(rows, cols, dtype, out_format, eps, 0, *s,
+                          (cols + 31) // 32 if scale_stride is None else scale_stride)
+
+
+def mla_rms_norm(problem: MlaNormProblem, x, weight, out, residual=None, residual_out=None,
+                 scales=None, stream=None) -> None:
+    """out = h / sqrt(mean(h^2) + eps) * weight for each row, h = x + residual
+    (residual_out receives h); weight None is ones.  An 8-bit out_format writes
+    e4m3 codes to out and the scales to scales."""
+    _check("mla_rms_norm", load().mla_rms_norm(
+        ctypes.byref(problem), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out),
+        _ptr(out), _ptr(scales), _stream(stream)))
+
+
+def mla_rope_make_plan(config: MlaRopeConfig) -> MlaRopePlan:
+    plan = MlaRopePlan()
+    _check("mla_rope_make_plan", load().mla_rope_make_plan(ctypes.byref(config), ctypes.byref(plan)))
+    return plan
+
+
+def mla_rope_plan(layout=MLA_ROPE_INTERLEAVED, rope_dim=64, theta=1.0e6,
+                  scaling=MLA_ROPE_SCALING_NONE, factor=1.0, original_positions=0,
+                  fast_rotations=32.0, slow_rotations=1.0, amplitude=0.0) -> MlaRopePlan:
+    """The plan of a rotation: layout, theta and long-context scaling."""
+    return mla_rope_make_plan(MlaRopeConfig(layout, rope_dim, scaling, original_positions, theta,
+                                            factor, fast_rotations, slow_rotations, amplitude))
+
+
+def make_rope_problem(tokens, num_heads, head_dim, rope_offset=0, dtype=MLA_DTYPE_BF16,
+                      transposed=0, x_token_stride=None, x_head_stride=None,
+                      out_token_stride=None, out_head_stride=None) -> MlaRopeProblem:
+    """Strides are in elements; x defaults to packed [tokens][num_heads][head_dim]
+    and out to x's strides."""
+    xh = head_dim if x_head_stride is None else x_head_stride
+    xt = num_heads * xh if x_token_stride is None else x_token_stride
+    return MlaRopeProblem(tokens, num_heads, head_dim, rope_offset, dtype, transposed, xt, xh,
+                          xt if out_token_stride is None else out_token_stride,
+                          xh if out_head_stride is None else out_head_stride)
+
+
+def mla_rope(problem: MlaRopeProblem, plan: MlaRopePlan, x, positions, out=None,
+             stream=None) -> None:
+    """Rotate part of every head of token t to positions[t] (in place without
+    an out); a negative position leaves the token's out as it was."""
+    x = _ptr(x)
+    _check("mla_rope", load().mla_rope(ctypes.byref(problem), ctypes.byref(plan), x,
+                                       _ptr(positions), x if out is None else _ptr(out),
+                                       _stream(stream)))
+
+
+def mla_cache_append_tokens(problem: MlaProblem, tokens: int, rows, positions, block_table,
+                            kv_cache, requests=None, row_stride: int = 576, norm_weight=None,
+                            norm_eps: float = 1e-6, rope: Optional[MlaRopePlan] = None,
+                            status=None, stream=None) -> None:
+    """Write row t of rows (bf16, row_stride elements apart) at position
+    positions[t] of request requests[t] (None: tokens / batch consecutive rows
+    per request), its latent normed with norm_weight and its key rotated by
+    rope where given."""
+    _check("mla_cache_append_tokens", load().mla_cache_append_tokens(
+        ctypes.byref(problem), tokens, _ptr(rows), row_stride, _ptr(positions), _ptr(requests),
+        _ptr(block_table), _ptr(norm_weight), norm_eps,
+        None if rope is None else ctypes.byref(rope), _ptr(kv_cache), _ptr(status),
+        _stream(stream)))
+
+
+def mla_cache_gather(problem: MlaProblem, tokens: int, kv_cache, positions, block_table, out,
+                     requests=None, out_stride: int = 576, status=None, stream=None) -> None:
+    """The cached row at position positions[t] of request requests[t] as bf16
+    row t of out (out_stride elements apart)."""
+    _check("mla_cache_gather", load().mla_cache_gather(
+        ctypes.byref(problem), tokens, _ptr(kv_cache), _ptr(positions), _ptr(requests),
+        _ptr(block_table), _ptr(out), out_stride, _ptr(status), _stream(stream)))
 
 
 def mla_get_status(plan: MlaPlan, workspace, stream=None) -> int:

@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libmla_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["mla_api.cu", "mla_decode.cu", "mla_aux.cu", "mla_static.cu", "mla_append.cu"]
+SOURCES = ["mla_api.cu", "mla_decode.cu", "mla_aux.cu", "mla_static.cu", "mla_append.cu",
+           "mla_layer_api.cu", "mla_norm.cu", "mla_rope.cu", "mla_tokens.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr", "-Xptxas", "-v"]
@@ -42,7 +43,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(HERE, "..", "include", "mla_decode.h"))
+    include = os.path.join(HERE, "..", "include")
+    headers += [os.path.join(include, f) for f in os.listdir(include) if f.endswith(".h")]
     jobs = []
     objs = []
     for src in SOURCES:

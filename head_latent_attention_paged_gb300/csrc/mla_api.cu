@@ -128,6 +128,25 @@ cudaError_t set_smem_attr_once(const void* func, int slot, int bytes) {
   return err;
 }
 
+// The cache shape and options every entry point shares (the append needs
+// no more than this).
+int check_cache_shape(const mla_problem* pr) {
+  if (pr == nullptr) return MLA_ERR_INVALID_ARGUMENT;
+  if (pr->batch < 0 || pr->num_pages < 1 || pr->max_pages_per_seq < 1)
+    return MLA_ERR_INVALID_ARGUMENT;
+  if (pr->kv_lora_rank != kDc || pr->rope_dim != kDr || pr->nope_dim != kDnope ||
+      pr->v_head_dim != kDv)
+    return MLA_ERR_UNSUPPORTED;
+  if (pr->page_size != 16 && pr->page_size != 32 && pr->page_size != 64 && pr->page_size != 128)
+    return MLA_ERR_UNSUPPORTED;
+  if (pr->kv_dtype != MLA_KV_BF16 && pr->kv_dtype != MLA_KV_FP8_E4M3_E8M0 &&
+      pr->kv_dtype != MLA_KV_FP4_E2M1_E8M0)
+    return MLA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(pr->num_pages) * pr->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(pr->max_pages_per_seq) * pr->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
 }  // namespace mla
 
 namespace {
@@ -149,25 +168,6 @@ int decode_mode(const mla_problem& pr) {
 int32_t num_row_sets(const mla_problem& pr) {
   const int32_t g = group_of(pr);
   return pr.batch * ((pr.q_len + g - 1) / g);
-}
-
-// The cache shape and options every entry point shares (the append needs
-// no more than this).
-int validate_cache_shape(const mla_problem* pr) {
-  if (pr == nullptr) return MLA_ERR_INVALID_ARGUMENT;
-  if (pr->batch < 0 || pr->num_pages < 1 || pr->max_pages_per_seq < 1)
-    return MLA_ERR_INVALID_ARGUMENT;
-  if (pr->kv_lora_rank != kDc || pr->rope_dim != kDr || pr->nope_dim != kDnope ||
-      pr->v_head_dim != kDv)
-    return MLA_ERR_UNSUPPORTED;
-  if (pr->page_size != 16 && pr->page_size != 32 && pr->page_size != 64 && pr->page_size != 128)
-    return MLA_ERR_UNSUPPORTED;
-  if (pr->kv_dtype != MLA_KV_BF16 && pr->kv_dtype != MLA_KV_FP8_E4M3_E8M0 &&
-      pr->kv_dtype != MLA_KV_FP4_E2M1_E8M0)
-    return MLA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(pr->num_pages) * pr->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(pr->max_pages_per_seq) * pr->page_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-  return MLA_OK;
 }
 
 int validate_problem(const mla_problem* pr) {
@@ -538,7 +538,7 @@ int mla_uv_proj(const float* o_lat, const void* w_uv, void* out, int32_t rows, i
 int mla_cache_append(const mla_problem* problem, const void* new_rows, const int32_t* positions,
                      const int32_t* block_table, float rope_theta, void* kv_cache,
                      uint32_t* status, mla_stream_t stream) {
-  const int rc = validate_cache_shape(problem);
+  const int rc = check_cache_shape(problem);
   if (rc != MLA_OK) return rc;
   if (!new_rows || !positions || !block_table || !kv_cache) return MLA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(rope_theta) || rope_theta < 0.f || (rope_theta > 0.f && rope_theta <= 1.f))

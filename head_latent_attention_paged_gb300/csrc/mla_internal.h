@@ -137,6 +137,7 @@ cudaError_t set_smem_attr_once(const void* func, int slot, int bytes);
 void* current_context();
 
 // Host steps shared by the entry points (MLA_* return codes).
+int check_cache_shape(const mla_problem* problem);
 int plan_check(const mla_plan* plan);
 // Everything mla_decode_run checks before it queues any work.
 int check_run_args(const mla_plan* plan, const void* q, const void* w_uk, const void* kv_cache,
