@@ -228,6 +228,7 @@ int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan, const v
       !span_fits(H, pr.x_head_stride, size) || !span_fits(T, pr.out_token_stride, size) ||
       !span_fits(H, pr.out_head_stride, size))
     return MLA_ERR_INVALID_ARGUMENT;
+  if (H * D > INT32_MAX / 64) return MLA_ERR_UNSUPPORTED;
   if (T == 0) return MLA_OK;
   const int64_t out_heads = (H - 1) * pr.out_head_stride, out_tokens = (T - 1) * pr.out_token_stride;
   const int64_t x_heads = (H - 1) * pr.x_head_stride, x_tokens = (T - 1) * pr.x_token_stride;

@@ -173,7 +173,7 @@ MLA_API int mla_rope_make_plan(const mla_rope_config* config, mla_rope_plan* pla
 
 typedef struct {
   int32_t tokens;              /* >= 0 */
-  int32_t num_heads;           /* >= 1 */
+  int32_t num_heads;           /* >= 1; num_heads * head_dim <= 2^25 - 1 */
   int32_t head_dim;            /* elements of a head, >= rope_offset + rope_dim */
   int32_t rope_offset;         /* first rotated element of a head */
   int32_t dtype;               /* MLA_DTYPE_* */
@@ -198,8 +198,8 @@ typedef struct {
  * b cos t), A the amplitude, in 32 bits, rounded once.
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT (a size or stride, a plan not made
  * by mla_rope_make_plan, an out that overlaps x otherwise), MLA_ERR_UNSUPPORTED
- * (a dtype), MLA_ERR_MISALIGNED (less than the elements' alignment) or
- * MLA_ERR_CUDA.
+ * (a dtype, too many elements of a token), MLA_ERR_MISALIGNED (less than the
+ * elements' alignment) or MLA_ERR_CUDA.
  */
 MLA_API int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan, const void* x,
              const int32_t* positions, void* out, mla_stream_t stream);
