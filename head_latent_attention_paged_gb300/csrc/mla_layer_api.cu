@@ -95,7 +95,7 @@ int fill_tokens(const mla_problem* pr, int32_t tokens, const int32_t* positions,
   t->tokens = tokens;
   t->per_request = requests ? 1 : tokens / pr->batch;
   t->batch = pr->batch;
-  t->page_size = pr->page_size;
+  t->page_shift = pr->page_size == 16 ? 4 : pr->page_size == 32 ? 5 : pr->page_size == 64 ? 6 : 7;
   t->num_pages = pr->num_pages;
   t->max_pages = pr->max_pages_per_seq;
   t->kv_dtype = pr->kv_dtype;

@@ -46,7 +46,7 @@ struct TokenParams {            // the append's and the gather's common part
   const int32_t* block_table;
   uint32_t* status;             // or null
   int32_t tokens, per_request;
-  int32_t batch, page_size, num_pages, max_pages;
+  int32_t batch, page_shift, num_pages, max_pages;   // pages of 2^page_shift tokens
   int32_t kv_dtype;
 };
 

@@ -48,6 +48,21 @@ __device__ __forceinline__ float pow2_neg(int e) {
   return e == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
+// The scale bytes e + 127 of the two quantisers, e = ceil(log2(amax / 448)) or
+// ceil(log2(amax / 6)) clamped to -127 from below (0 for a zero amax): adding
+// the mantissa's distance from 1.75 (1.5) to the next power of two carries
+// into the exponent exactly where the ceiling does.  Bytes stay below 254, so
+// the reciprocal 2^-e is a normal number.
+__device__ __forceinline__ uint32_t e4m3_scale_byte(float amax) {
+  return max((__float_as_uint(amax) + 0x1FFFFFu) >> 23, 8u) - 8u;
+}
+__device__ __forceinline__ uint32_t e2m1_scale_byte(float amax) {
+  return max((__float_as_uint(amax) + 0x3FFFFFu) >> 23, 2u) - 2u;
+}
+__device__ __forceinline__ float scale_byte_reciprocal(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+
 // Round-to-nearest-even conversion to e4m3 with saturation at +-448.
 __device__ __forceinline__ uint32_t f32_to_e4m3(float v) {
   uint16_t two;

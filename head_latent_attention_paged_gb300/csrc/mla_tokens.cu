@@ -14,49 +14,65 @@ namespace mla {
 namespace {
 
 constexpr int kTokenWarps = 4;
-constexpr int kAppendBlocks = 152 * 8;   // resident blocks: each warp then takes further tokens
+constexpr int kChunkMax = 8;   // tokens a warp takes one after another
 
-// The slot of token t in the pool, -1 where the token is to be left alone
-// (negative position) and -2 where it has none (reported by lane 0).
-__device__ __forceinline__ int64_t token_slot(const TokenParams& p, int64_t t, int32_t pos, bool report) {
+// The slot of token t in the pool: -1 where the token is to be left alone
+// (negative position), -2 where it has none (which is reported).
+__device__ __forceinline__ int32_t token_slot(const TokenParams& p, int32_t t, int32_t pos) {
   if (pos < 0) return -1;
-  const int32_t r = p.requests ? p.requests[t] : static_cast<int32_t>(t / p.per_request);
+  const int32_t r = p.requests ? p.requests[t] : t / p.per_request;
   uint32_t bad = 0;
   int32_t page = 0;
-  if (r < 0 || r >= p.batch || pos >= static_cast<int64_t>(p.max_pages) * p.page_size) {
+  const int32_t index = pos >> p.page_shift;
+  if (r < 0 || r >= p.batch || index >= p.max_pages) {
     bad = MLA_STATUS_BAD_INDEX;
   } else {
-    page = p.block_table[static_cast<int64_t>(r) * p.max_pages + pos / p.page_size];
+    page = p.block_table[static_cast<int64_t>(r) * p.max_pages + index];
     if (page < 0 || page >= p.num_pages) bad = MLA_STATUS_BAD_PAGE;
   }
   if (bad) {
-    if (report && p.status) atomicOr(p.status, bad);
+    if (p.status) atomicOr(p.status, bad);
     return -2;
   }
-  return static_cast<int64_t>(page) * p.page_size + pos % p.page_size;
+  return (page << p.page_shift) + (pos & ((1 << p.page_shift) - 1));   // below 2^31: checked by the host
+}
+
+// A warp's tokens: `chunk` consecutive ones, their slots found side by side,
+// lane l holding token first + l's.
+struct WarpTokens {
+  int32_t first, count, pos, slot;
+};
+__device__ __forceinline__ WarpTokens warp_tokens(const TokenParams& p, int32_t chunk, int lane) {
+  WarpTokens w;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kTokenWarps + (threadIdx.x >> 5)) * chunk;
+  w.first = static_cast<int32_t>(min(first, static_cast<int64_t>(p.tokens)));
+  w.count = min(chunk, p.tokens - w.first);
+  w.pos = lane < w.count ? p.positions[w.first + lane] : -1;
+  w.slot = token_slot(p, w.first + lane, w.pos);
+  return w;
 }
 
 // Two bf16 of a word, as f32.
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // e4m3 codes of two values, the first in the low byte; e2m1 codes of two, the
 // first in the low nibble.  Nearest even, saturating, as f32_to_e4m3 and
 // f32_to_e2m1.
-__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack_e4m3(float2 v) {
   uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(v.y), "f"(v.x));
   return two;
 }
-__device__ __forceinline__ uint32_t pack_e2m1(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack_e2m1(float2 v) {
   uint32_t two;
   asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n cvt.u32.u8 %0, c;\n}"
       : "=r"(two)
-      : "f"(hi), "f"(lo));
+      : "f"(v.y), "f"(v.x));
   return two;
 }
 
@@ -82,128 +98,125 @@ __device__ __forceinline__ float lanes_max(float v, int lanes) {
   return v;
 }
 
-template <bool kFp8>
-__device__ __forceinline__ int group_exponent(float amax) {
-  if (!(amax > 0.f)) return -127;
-  return max(-127, min(127, kFp8 ? ceil_log2_over_448(amax) : ceil_log2_over_6(amax)));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float abs_max(const float2 (&v)[4]) {
+  float m = max3(fabsf(v[0].x), fabsf(v[0].y), fabsf(v[1].x));
+  m = max3(m, fabsf(v[1].y), fabsf(v[2].x));
+  m = max3(m, fabsf(v[2].y), fabsf(v[3].x));
+  return fmaxf(m, fabsf(v[3].y));
 }
 
 constexpr int kStageBytes = 640;   // a 594-byte row behind a shift of at most 14
 
 // One warp per token at a time.  Bound by memory (a 1,152-byte row read, a
 // 1,152-, 594- or 324-byte row written) where the instructions for a row's
-// norm, rotation and codes can be kept near 250: every value stays in its
-// lane, one shuffle reduction gives the norm, the cosine and sine are one pair
-// per lane, and the next row is on its way while one is computed.
+// norm, rotation and codes are few enough: every value stays in its lane, one
+// shuffle reduction gives the norm, the cosine and sine are one pair per lane,
+// arithmetic goes in pairs, slots are found one token per lane, and the next
+// row is on its way while one is computed.
 template <int kKv>
-__global__ void __launch_bounds__(32 * kTokenWarps) mla_append_tokens_kernel(const __grid_constant__ AppendTokensParams p) {
+__global__ void __launch_bounds__(32 * kTokenWarps)
+    mla_append_tokens_kernel(const __grid_constant__ AppendTokensParams p, const int32_t chunk) {
   __shared__ __align__(16) uint8_t stage_s[kKv == MLA_KV_FP8_E4M3_E8M0 ? kTokenWarps : 1][kStageBytes];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTokenWarps;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kTokenWarps + warp;
-  if (t >= p.t.tokens) return;
+  const WarpTokens tok = warp_tokens(p.t, chunk, lane);
+  if (tok.count <= 0) return;
+  const uint16_t* src = p.rows + tok.first * p.row_stride;
   RowWords next;
-  int32_t next_pos = p.t.positions[t];
-  load_row(&next, p.rows + t * p.row_stride, lane);
+  load_row(&next, src, lane);
   const uint64_t turns = p.rotate ? p.table.turns[lane] : 0;
-  uint4 wa = {}, wb = {};
+  float2 w[8];
   if (p.weight) {
-    wa = reinterpret_cast<const uint4*>(p.weight)[lane];
-    wb = reinterpret_cast<const uint4*>(p.weight)[32 + lane];
+    const uint4 a = reinterpret_cast<const uint4*>(p.weight)[lane], b = reinterpret_cast<const uint4*>(p.weight)[32 + lane];
+    const uint32_t words[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = make_float2(bf16_lo(words[i]), bf16_hi(words[i]));
   }
-  for (; t < p.t.tokens; t += stride) {
+  for (int j = 0; j < tok.count; ++j) {
     const RowWords row = next;
-    const int32_t pos = next_pos;
-    if (t + stride < p.t.tokens) {
-      next_pos = p.t.positions[t + stride];
-      load_row(&next, p.rows + (t + stride) * p.row_stride, lane);
-    }
-    const int64_t slot = token_slot(p.t, t, pos, lane == 0);
-    if (slot < 0) continue;
+    src += p.row_stride;
+    if (j + 1 < tok.count) load_row(&next, src, lane);
+    const int32_t pos = __shfl_sync(0xffffffffu, tok.pos, j), at = __shfl_sync(0xffffffffu, tok.slot, j);
+    if (at < 0) continue;
+    const int64_t slot = at;
     const uint32_t words[8] = {row.a.x, row.a.y, row.a.z, row.a.w, row.b.x, row.b.y, row.b.z, row.b.w};
-    float y[16];
+    float2 y[2][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[2 * i] = bf16_lo(words[i]);
-      y[2 * i + 1] = bf16_hi(words[i]);
-    }
+    for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = make_float2(bf16_lo(words[i]), bf16_hi(words[i]));
     if (p.weight) {
-      float sum = 0.f;
+      float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum = fmaf(y[i], y[i], sum);
+      for (int i = 0; i < 8; ++i) sum2 = __ffma2_rn(y[i >> 2][i & 3], y[i >> 2][i & 3], sum2);
+      float sum = sum2.x + sum2.y;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       const float rstd = rsqrtf(sum * (1.f / kDc) + p.eps);
-      const uint32_t w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[2 * i] = y[2 * i] * rstd * bf16_lo(w[i]);
-        y[2 * i + 1] = y[2 * i + 1] * rstd * bf16_hi(w[i]);
-      }
+      for (int i = 0; i < 8; ++i)
+        y[i >> 2][i & 3] = __fmul2_rn(__fmul2_rn(y[i >> 2][i & 3], make_float2(rstd, rstd)), w[i]);
     }
-    float k0 = bf16_lo(row.key), k1 = bf16_hi(row.key);
+    float2 k = make_float2(bf16_lo(row.key), bf16_hi(row.key));
     if (p.rotate) {
       float c, s;
       turn_cos_sin(turns, pos, &c, &s);
       c *= p.table.amplitude;
       s *= p.table.amplitude;
       if (p.table.halves) {   // value l of both halves to lane l, and back
-        const float a0 = __shfl_sync(0xffffffffu, k0, lane >> 1), a1 = __shfl_sync(0xffffffffu, k1, lane >> 1);
-        const float b0 = __shfl_sync(0xffffffffu, k0, 16 + (lane >> 1)), b1 = __shfl_sync(0xffffffffu, k1, 16 + (lane >> 1));
+        const float a0 = __shfl_sync(0xffffffffu, k.x, lane >> 1), a1 = __shfl_sync(0xffffffffu, k.y, lane >> 1);
+        const float b0 = __shfl_sync(0xffffffffu, k.x, 16 + (lane >> 1)), b1 = __shfl_sync(0xffffffffu, k.y, 16 + (lane >> 1));
         const float a = lane & 1 ? a1 : a0, b = lane & 1 ? b1 : b0;
         const float ya = a * c - b * s, yb = a * s + b * c;
         const int from = (2 * lane) & 31;
         const float ra0 = __shfl_sync(0xffffffffu, ya, from), ra1 = __shfl_sync(0xffffffffu, ya, from + 1);
         const float rb0 = __shfl_sync(0xffffffffu, yb, from), rb1 = __shfl_sync(0xffffffffu, yb, from + 1);
-        k0 = lane < 16 ? ra0 : rb0;
-        k1 = lane < 16 ? ra1 : rb1;
+        k = lane < 16 ? make_float2(ra0, ra1) : make_float2(rb0, rb1);
       } else {
-        const float a = k0, b = k1;
-        k0 = a * c - b * s;
-        k1 = a * s + b * c;
+        k = make_float2(k.x * c - k.y * s, k.x * s + k.y * c);
       }
     }
     if (kKv == MLA_KV_BF16) {
       uint8_t* dst = p.kv + slot * (kDqk * 2);
       uint4 oa = row.a, ob = row.b;   // as they came without a norm
       if (p.weight) {
-        oa = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        ob = make_uint4(pack_bf16(y[8], y[9]), pack_bf16(y[10], y[11]), pack_bf16(y[12], y[13]), pack_bf16(y[14], y[15]));
+        oa = make_uint4(pack_bf16(y[0][0]), pack_bf16(y[0][1]), pack_bf16(y[0][2]), pack_bf16(y[0][3]));
+        ob = make_uint4(pack_bf16(y[1][0]), pack_bf16(y[1][1]), pack_bf16(y[1][2]), pack_bf16(y[1][3]));
       }
       reinterpret_cast<uint4*>(dst)[lane] = oa;
       reinterpret_cast<uint4*>(dst)[32 + lane] = ob;
-      reinterpret_cast<uint32_t*>(dst + kDc * 2)[lane] = p.rotate ? pack_bf16(k0, k1) : row.key;
+      reinterpret_cast<uint32_t*>(dst + kDc * 2)[lane] = p.rotate ? pack_bf16(k) : row.key;
       continue;
     }
     constexpr bool kFp8 = kKv == MLA_KV_FP8_E4M3_E8M0;
-    float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m0 = fmaxf(m0, fabsf(y[i]));
-      m1 = fmaxf(m1, fabsf(y[8 + i]));
-    }
     // a group is 4 lanes of 8 values and 16 lanes of 2 (FP8), 2 and 8 (FP4)
-    m0 = lanes_max(m0, kFp8 ? 4 : 2);
-    m1 = lanes_max(m1, kFp8 ? 4 : 2);
-    const float mk = lanes_max(fmaxf(fabsf(k0), fabsf(k1)), kFp8 ? 16 : 8);
-    const int e0 = group_exponent<kFp8>(m0), e1 = group_exponent<kFp8>(m1), ek = group_exponent<kFp8>(mk);
-    const float s0 = pow2_neg(e0), s1 = pow2_neg(e1), sk = pow2_neg(ek);
+    const float m[2] = {lanes_max(abs_max(y[0]), kFp8 ? 4 : 2), lanes_max(abs_max(y[1]), kFp8 ? 4 : 2)};
+    const float mk = lanes_max(fmaxf(fabsf(k.x), fabsf(k.y)), kFp8 ? 16 : 8);
+    const uint32_t e[2] = {kFp8 ? e4m3_scale_byte(m[0]) : e2m1_scale_byte(m[0]),
+                           kFp8 ? e4m3_scale_byte(m[1]) : e2m1_scale_byte(m[1])};
+    const uint32_t ek = kFp8 ? e4m3_scale_byte(mk) : e2m1_scale_byte(mk);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float inv = scale_byte_reciprocal(e[h]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[h][i] = __fmul2_rn(y[h][i], make_float2(inv, inv));
+    }
+    const float ik = scale_byte_reciprocal(ek);
+    const float2 yk = __fmul2_rn(k, make_float2(ik, ik));
     // A group of zeros has codes 0 whatever their signs; a NaN stays one.
     if (kFp8) {
-      uint32_t code[8];
+      uint32_t code[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        code[i] = pack_e4m3(y[2 * i] * s0, y[2 * i + 1] * s0);
-        code[4 + i] = pack_e4m3(y[8 + 2 * i] * s1, y[9 + 2 * i] * s1);
-      }
-      uint32_t kcode = pack_e4m3(k0 * sk, k1 * sk);
+      for (int i = 0; i < 8; ++i) code[i >> 2][i & 3] = pack_e4m3(y[i >> 2][i & 3]);
+      uint32_t kcode = pack_e4m3(yk);
       // with amax 0 every code is a signed zero (0x00, 0x80) or NaN (0x7F, 0xFF)
-      auto unsign = [](uint32_t c) { return (c & 0x7F7Fu); };
-      if (m0 == 0.f)
-        for (int i = 0; i < 4; ++i) code[i] = unsign(code[i]);
-      if (m1 == 0.f)
-        for (int i = 4; i < 8; ++i) code[i] = unsign(code[i]);
-      if (mk == 0.f) kcode = unsign(kcode);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (m[h] == 0.f)
+          for (int i = 0; i < 4; ++i) code[h][i] &= 0x7F7Fu;
+      if (mk == 0.f) kcode &= 0x7F7Fu;
       // The row starts on any even address: it is laid out in shared memory at
       // the same place within 16 bytes and leaves in 16-byte stores, its ends
       // in pairs of bytes.
@@ -214,55 +227,57 @@ __global__ void __launch_bounds__(32 * kTokenWarps) mla_append_tokens_kernel(con
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        st2[4 * lane + i] = static_cast<uint16_t>(code[i]);
-        st2[128 + 4 * lane + i] = static_cast<uint16_t>(code[4 + i]);
+        st2[4 * lane + i] = static_cast<uint16_t>(code[0][i]);
+        st2[128 + 4 * lane + i] = static_cast<uint16_t>(code[1][i]);
       }
       st2[256 + lane] = static_cast<uint16_t>(kcode);
       if ((lane & 3) == 0) {
-        st[shift + kDqk + (lane >> 2)] = static_cast<uint8_t>(e0 + 127);
-        st[shift + kDqk + 8 + (lane >> 2)] = static_cast<uint8_t>(e1 + 127);
+        st[shift + kDqk + (lane >> 2)] = static_cast<uint8_t>(e[0]);
+        st[shift + kDqk + 8 + (lane >> 2)] = static_cast<uint8_t>(e[1]);
       }
-      if ((lane & 15) == 0) st[shift + kDqk + 16 + (lane >> 4)] = static_cast<uint8_t>(ek + 127);
+      if ((lane & 15) == 0) st[shift + kDqk + 16 + (lane >> 4)] = static_cast<uint8_t>(ek);
       __syncwarp();
-      const int first = shift ? 1 : 0, end = (shift + kFp8RowBytes) >> 4;   // whole pieces
-      uint8_t* base = dst - shift;
-      for (int j = first + lane; j < end; j += 32)
-        reinterpret_cast<uint4*>(base)[j] = reinterpret_cast<const uint4*>(st)[j];
+      // pieces first .. end - 1 are whole: 36 or 37 of them
+      const int first = shift ? 1 : 0, end = (shift + kFp8RowBytes) >> 4;
+      uint4* base = reinterpret_cast<uint4*>(dst - shift);
+      const uint4* from = reinterpret_cast<const uint4*>(st);
+      if (lane >= first) base[lane] = from[lane];
+      if (32 + lane < end) base[32 + lane] = from[32 + lane];
       const int head = (16 * first - shift) >> 1;                            // pairs before them
       const int tail = (shift + kFp8RowBytes - 16 * end) >> 1;               // and behind
-      const int at = lane < 8 ? (lane < head ? lane : -1)
-                              : (lane - 8 < tail ? 8 * end - (shift >> 1) + lane - 8 : -1);
-      if (lane < 16 && at >= 0) reinterpret_cast<uint16_t*>(dst)[at] = st2[at];
+      const int pair = lane < 8 ? lane : 8 * end - (shift >> 1) + lane - 8;
+      if (lane < 8 ? lane < head : lane - 8 < tail) reinterpret_cast<uint16_t*>(dst)[pair] = st2[pair];
     } else {
-      uint32_t c0 = 0, c1 = 0;
+      uint32_t c[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c0 |= pack_e2m1(y[2 * i] * s0, y[2 * i + 1] * s0) << (8 * i);
-        c1 |= pack_e2m1(y[8 + 2 * i] * s1, y[9 + 2 * i] * s1) << (8 * i);
-      }
-      uint32_t ck = pack_e2m1(k0 * sk, k1 * sk);
-      bool n0 = false, n1 = false;
+      for (int i = 0; i < 8; ++i) c[i >> 2] |= pack_e2m1(y[i >> 2][i & 3]) << (8 * (i & 3));
+      uint32_t ck = pack_e2m1(yk);
+      bool nan[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        n0 |= y[i] != y[i];
-        n1 |= y[8 + i] != y[8 + i];
+      for (int h = 0; h < 2; ++h) {
+        // a sum of magnitudes is NaN where a value is (they are at most 6, so
+        // it is finite otherwise)
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z += fabsf(y[h][i].x) + fabsf(y[h][i].y);
+        nan[h] = z != z;
       }
       // groups with a NaN get the NaN scale
-      const uint32_t nan0 = __ballot_sync(0xffffffffu, n0) >> (lane & ~1) & 3u;
-      const uint32_t nan1 = __ballot_sync(0xffffffffu, n1) >> (lane & ~1) & 3u;
-      const uint32_t nank = __ballot_sync(0xffffffffu, k0 != k0 || k1 != k1) >> (lane & ~7) & 0xFFu;
-      if (m0 == 0.f) c0 = 0;
-      if (m1 == 0.f) c1 = 0;
+      const uint32_t nan0 = __ballot_sync(0xffffffffu, nan[0]) >> (lane & ~1) & 3u;
+      const uint32_t nan1 = __ballot_sync(0xffffffffu, nan[1]) >> (lane & ~1) & 3u;
+      const uint32_t nank = __ballot_sync(0xffffffffu, k.x != k.x || k.y != k.y) >> (lane & ~7) & 0xFFu;
+      if (m[0] == 0.f) c[0] = 0;
+      if (m[1] == 0.f) c[1] = 0;
       if (mk == 0.f) ck = 0;
       uint8_t* dst = p.kv + slot * kFp4RowBytes;   // rows start on 4 bytes
-      reinterpret_cast<uint32_t*>(dst)[lane] = c0;
-      reinterpret_cast<uint32_t*>(dst)[32 + lane] = c1;
+      reinterpret_cast<uint32_t*>(dst)[lane] = c[0];
+      reinterpret_cast<uint32_t*>(dst)[32 + lane] = c[1];
       dst[256 + lane] = static_cast<uint8_t>(ck);
       if ((lane & 1) == 0) {
-        dst[kFp4CodeBytes + (lane >> 1)] = static_cast<uint8_t>(nan0 ? 255 : e0 + 127);
-        dst[kFp4CodeBytes + 16 + (lane >> 1)] = static_cast<uint8_t>(nan1 ? 255 : e1 + 127);
+        dst[kFp4CodeBytes + (lane >> 1)] = static_cast<uint8_t>(nan0 ? 255 : e[0]);
+        dst[kFp4CodeBytes + 16 + (lane >> 1)] = static_cast<uint8_t>(nan1 ? 255 : e[1]);
       }
-      if ((lane & 7) == 0) dst[kFp4CodeBytes + 32 + (lane >> 3)] = static_cast<uint8_t>(nank ? 255 : ek + 127);
+      if ((lane & 7) == 0) dst[kFp4CodeBytes + 32 + (lane >> 3)] = static_cast<uint8_t>(nank ? 255 : ek);
     }
   }
 }
@@ -277,7 +292,7 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
 // rounded once.
 __device__ __forceinline__ uint32_t scaled_bf16(uint32_t f16x2, float scale) {
   const __half2 h = *reinterpret_cast<const __half2*>(&f16x2);
-  return pack_bf16(__low2float(h) * scale, __high2float(h) * scale);
+  return pack_bf16(__fmul2_rn(__half22float2(h), make_float2(scale, scale)));
 }
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t codes, float scale) {
   uint32_t two;
@@ -290,85 +305,139 @@ __device__ __forceinline__ uint32_t e2m1x2_to_bf16(uint32_t codes, float scale) 
   return scaled_bf16(two, scale);
 }
 
-// One warp per token.  Bound by memory: a cached row read, 1,152 bytes
-// written.  Lanes hold the row as in the append (RowWords).
+// A cached row's bytes as its warp loads them: lanes as in RowWords.
 template <int kKv>
-__global__ void __launch_bounds__(32 * kTokenWarps) mla_gather_kernel(const GatherParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTokenWarps + (threadIdx.x >> 5);
-  if (t >= p.t.tokens) return;
-  const int64_t slot = token_slot(p.t, t, p.t.positions[t], lane == 0);
-  if (slot == -1) return;
-  RowWords r = {};
-  if (slot >= 0) {
-    if (kKv == MLA_KV_BF16) {
-      load_row(&r, reinterpret_cast<const uint16_t*>(p.kv) + slot * kDqk, lane);
-    } else if (kKv == MLA_KV_FP8_E4M3_E8M0) {
-      // rows start on even addresses: aligned words, shifted by two bytes
-      // where the row starts between them
-      const uint8_t* src = p.kv + slot * kFp8RowBytes;
-      const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 2);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(src - odd) + 2 * lane;
-      uint32_t a0 = w[0], a1 = w[1], b0 = w[64], b1 = w[65];
-      if (odd) {
-        const uint32_t a2 = w[2], b2 = w[66];
-        a0 = __funnelshift_r(a0, a1, 16);
-        a1 = __funnelshift_r(a1, a2, 16);
-        b0 = __funnelshift_r(b0, b1, 16);
-        b1 = __funnelshift_r(b1, b2, 16);
-      }
-      const uint32_t k = reinterpret_cast<const uint16_t*>(src + kDc)[lane];
-      const float s0 = e8m0_to_f32(src[kDqk + (lane >> 2)]), s1 = e8m0_to_f32(src[kDqk + 8 + (lane >> 2)]);
-      const float sk = e8m0_to_f32(src[kDqk + 16 + (lane >> 4)]);
-      r.a = make_uint4(e4m3x2_to_bf16(a0, s0), e4m3x2_to_bf16(a0 >> 16, s0), e4m3x2_to_bf16(a1, s0),
-                       e4m3x2_to_bf16(a1 >> 16, s0));
-      r.b = make_uint4(e4m3x2_to_bf16(b0, s1), e4m3x2_to_bf16(b0 >> 16, s1), e4m3x2_to_bf16(b1, s1),
-                       e4m3x2_to_bf16(b1 >> 16, s1));
-      r.key = e4m3x2_to_bf16(k, sk);
-    } else {
-      const uint8_t* src = p.kv + slot * kFp4RowBytes;   // rows start on 4 bytes
-      const uint32_t a = reinterpret_cast<const uint32_t*>(src)[lane], b = reinterpret_cast<const uint32_t*>(src)[32 + lane];
-      const uint32_t k = src[256 + lane];
-      const float s0 = e8m0_to_f32(src[kFp4CodeBytes + (lane >> 1)]), s1 = e8m0_to_f32(src[kFp4CodeBytes + 16 + (lane >> 1)]);
-      const float sk = e8m0_to_f32(src[kFp4CodeBytes + 32 + (lane >> 3)]);
-      r.a = make_uint4(e2m1x2_to_bf16(a & 255u, s0), e2m1x2_to_bf16(a >> 8 & 255u, s0),
-                       e2m1x2_to_bf16(a >> 16 & 255u, s0), e2m1x2_to_bf16(a >> 24, s0));
-      r.b = make_uint4(e2m1x2_to_bf16(b & 255u, s1), e2m1x2_to_bf16(b >> 8 & 255u, s1),
-                       e2m1x2_to_bf16(b >> 16 & 255u, s1), e2m1x2_to_bf16(b >> 24, s1));
-      r.key = e2m1x2_to_bf16(k, sk);
+struct CachedRow {
+  RowWords bf16;                // MLA_KV_BF16
+  uint32_t a[3], b[3], key;     // codes: FP8 in words from the aligned one at
+  uint32_t sa, sb, sk;          // or before the lane's first; scale bytes
+};
+
+template <int kKv>
+__device__ __forceinline__ void load_cached(CachedRow<kKv>* r, const uint8_t* kv, int64_t slot, int lane) {
+  if (kKv == MLA_KV_BF16) {
+    load_row(&r->bf16, reinterpret_cast<const uint16_t*>(kv) + slot * kDqk, lane);
+  } else if (kKv == MLA_KV_FP8_E4M3_E8M0) {
+    const uint8_t* src = kv + slot * kFp8RowBytes;
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 2);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(src - odd) + 2 * lane;
+    r->a[0] = w[0];
+    r->a[1] = w[1];
+    r->b[0] = w[64];
+    r->b[1] = w[65];
+    if (odd) {
+      r->a[2] = w[2];
+      r->b[2] = w[66];
     }
+    r->key = reinterpret_cast<const uint16_t*>(src + kDc)[lane];
+    r->sa = src[kDqk + (lane >> 2)];
+    r->sb = src[kDqk + 8 + (lane >> 2)];
+    r->sk = src[kDqk + 16 + (lane >> 4)];
+  } else {
+    const uint8_t* src = kv + slot * kFp4RowBytes;   // rows start on 4 bytes
+    r->a[0] = reinterpret_cast<const uint32_t*>(src)[lane];
+    r->b[0] = reinterpret_cast<const uint32_t*>(src)[32 + lane];
+    r->key = src[256 + lane];
+    r->sa = src[kFp4CodeBytes + (lane >> 1)];
+    r->sb = src[kFp4CodeBytes + 16 + (lane >> 1)];
+    r->sk = src[kFp4CodeBytes + 32 + (lane >> 3)];
   }
-  uint16_t* out = p.out + t * p.out_stride;
-  reinterpret_cast<uint4*>(out)[lane] = r.a;
-  reinterpret_cast<uint4*>(out)[32 + lane] = r.b;
-  reinterpret_cast<uint32_t*>(out + kDc)[lane] = r.key;
 }
 
-int blocks_of(int32_t tokens) { return tokens / kTokenWarps + (tokens % kTokenWarps != 0); }
+template <int kKv>
+__device__ __forceinline__ RowWords cached_to_bf16(const CachedRow<kKv>& c, int64_t slot) {
+  if (kKv == MLA_KV_BF16) return c.bf16;
+  RowWords r;
+  const float sa = e8m0_to_f32(c.sa), sb = e8m0_to_f32(c.sb), sk = e8m0_to_f32(c.sk);
+  if (kKv == MLA_KV_FP8_E4M3_E8M0) {
+    // a row of an odd slot starts two bytes into its first word (the pool
+    // starts on 16 bytes, a row has 594)
+    uint32_t a0 = c.a[0], a1 = c.a[1], b0 = c.b[0], b1 = c.b[1];
+    if (slot & 1) {
+      a0 = __funnelshift_r(a0, a1, 16);
+      a1 = __funnelshift_r(a1, c.a[2], 16);
+      b0 = __funnelshift_r(b0, b1, 16);
+      b1 = __funnelshift_r(b1, c.b[2], 16);
+    }
+    r.a = make_uint4(e4m3x2_to_bf16(a0, sa), e4m3x2_to_bf16(a0 >> 16, sa), e4m3x2_to_bf16(a1, sa),
+                     e4m3x2_to_bf16(a1 >> 16, sa));
+    r.b = make_uint4(e4m3x2_to_bf16(b0, sb), e4m3x2_to_bf16(b0 >> 16, sb), e4m3x2_to_bf16(b1, sb),
+                     e4m3x2_to_bf16(b1 >> 16, sb));
+    r.key = e4m3x2_to_bf16(c.key, sk);
+  } else {
+    const uint32_t a = c.a[0], b = c.b[0];
+    r.a = make_uint4(e2m1x2_to_bf16(a & 255u, sa), e2m1x2_to_bf16(a >> 8 & 255u, sa),
+                     e2m1x2_to_bf16(a >> 16 & 255u, sa), e2m1x2_to_bf16(a >> 24, sa));
+    r.b = make_uint4(e2m1x2_to_bf16(b & 255u, sb), e2m1x2_to_bf16(b >> 8 & 255u, sb),
+                     e2m1x2_to_bf16(b >> 16 & 255u, sb), e2m1x2_to_bf16(b >> 24, sb));
+    r.key = e2m1x2_to_bf16(c.key, sk);
+  }
+  return r;
+}
+
+// One warp per token at a time.  Bound by memory: a cached row read, 1,152
+// bytes written.  Slots are found one token per lane, so that the chain
+// position -> page -> row is walked once for a warp's tokens, and two rows are
+// on their way at a time.
+template <int kKv>
+__global__ void __launch_bounds__(32 * kTokenWarps)
+    mla_gather_kernel(const __grid_constant__ GatherParams p, const int32_t chunk) {
+  const int lane = threadIdx.x & 31;
+  const WarpTokens tok = warp_tokens(p.t, chunk, lane);
+  for (int j = 0; j < tok.count; j += 2) {
+    CachedRow<kKv> c[2];
+    int32_t slot[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      slot[i] = j + i < tok.count ? __shfl_sync(0xffffffffu, tok.slot, j + i) : -1;
+      if (slot[i] >= 0) load_cached(&c[i], p.kv, slot[i], lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (slot[i] == -1) continue;
+      RowWords r = {};
+      if (slot[i] >= 0) r = cached_to_bf16(c[i], slot[i]);
+      uint16_t* out = p.out + (tok.first + j + i) * p.out_stride;
+      reinterpret_cast<uint4*>(out)[lane] = r.a;
+      reinterpret_cast<uint4*>(out)[32 + lane] = r.b;
+      reinterpret_cast<uint32_t*>(out + kDc)[lane] = r.key;
+    }
+  }
+}
+
+// Tokens of a warp: one while there are multiprocessors to fill (latency),
+// then up to kChunkMax as the warps get to more than fit at once.
+int chunk_of(int32_t tokens) {
+  const int c = tokens / (152 * 32);
+  return c < 1 ? 1 : c > kChunkMax ? kChunkMax : c;
+}
+int blocks_of(int32_t tokens, int chunk) {
+  return static_cast<int>((static_cast<int64_t>(tokens) + kTokenWarps * chunk - 1) / (kTokenWarps * chunk));
+}
 
 }  // namespace
 
 cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream) {
   if (p.t.tokens == 0) return cudaSuccess;
-  const int blocks = min(blocks_of(p.t.tokens), kAppendBlocks);
+  const int chunk = chunk_of(p.t.tokens), blocks = blocks_of(p.t.tokens, chunk);
   if (p.t.kv_dtype == MLA_KV_BF16)
-    mla_append_tokens_kernel<MLA_KV_BF16><<<blocks, 32 * kTokenWarps, 0, stream>>>(p);
+    mla_append_tokens_kernel<MLA_KV_BF16><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
   else if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
-    mla_append_tokens_kernel<MLA_KV_FP8_E4M3_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p);
+    mla_append_tokens_kernel<MLA_KV_FP8_E4M3_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
   else
-    mla_append_tokens_kernel<MLA_KV_FP4_E2M1_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p);
+    mla_append_tokens_kernel<MLA_KV_FP4_E2M1_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
   return cudaGetLastError();
 }
 
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
   if (p.t.tokens == 0) return cudaSuccess;
-  const int blocks = blocks_of(p.t.tokens);
+  const int chunk = chunk_of(p.t.tokens), blocks = blocks_of(p.t.tokens, chunk);
   if (p.t.kv_dtype == MLA_KV_BF16)
-    mla_gather_kernel<MLA_KV_BF16><<<blocks, 32 * kTokenWarps, 0, stream>>>(p);
+    mla_gather_kernel<MLA_KV_BF16><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
   else if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
-    mla_gather_kernel<MLA_KV_FP8_E4M3_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p);
+    mla_gather_kernel<MLA_KV_FP8_E4M3_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
   else
-    mla_gather_kernel<MLA_KV_FP4_E2M1_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p);
+    mla_gather_kernel<MLA_KV_FP4_E2M1_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
   return cudaGetLastError();
 }
 
