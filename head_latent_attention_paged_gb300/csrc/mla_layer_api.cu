@@ -228,7 +228,9 @@ int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan, const v
       !span_fits(H, pr.x_head_stride, size) || !span_fits(T, pr.out_token_stride, size) ||
       !span_fits(H, pr.out_head_stride, size))
     return MLA_ERR_INVALID_ARGUMENT;
-  if (H * D > INT32_MAX / 64) return MLA_ERR_UNSUPPORTED;
+  if (H * D > INT32_MAX / 64 || pr.x_token_stride > INT32_MAX || pr.x_head_stride > INT32_MAX ||
+      pr.out_token_stride > INT32_MAX || pr.out_head_stride > INT32_MAX)
+    return MLA_ERR_UNSUPPORTED;
   if (T == 0) return MLA_OK;
   const int64_t out_heads = (H - 1) * pr.out_head_stride, out_tokens = (T - 1) * pr.out_token_stride;
   const int64_t x_heads = (H - 1) * pr.x_head_stride, x_tokens = (T - 1) * pr.x_token_stride;
@@ -247,10 +249,10 @@ int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan, const v
   p.x = x;
   p.out = out;
   p.positions = positions;
-  p.x_token_stride = pr.x_token_stride;
-  p.x_head_stride = pr.x_head_stride;
-  p.out_token_stride = pr.out_token_stride;
-  p.out_head_stride = pr.out_head_stride;
+  p.x_token_stride = static_cast<int32_t>(pr.x_token_stride);
+  p.x_head_stride = static_cast<int32_t>(pr.x_head_stride);
+  p.out_token_stride = static_cast<int32_t>(pr.out_token_stride);
+  p.out_head_stride = static_cast<int32_t>(pr.out_head_stride);
   p.tokens = pr.tokens;
   p.heads = pr.num_heads;
   p.head_dim = pr.head_dim;

@@ -33,7 +33,7 @@ struct RopeParams {
   const void* x;
   void* out;
   const int32_t* positions;
-  int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
+  int32_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
   int32_t tokens, heads, head_dim, offset, dim;
   int32_t dtype, transposed;
   RopeTable<MLA_ROPE_MAX_DIM / 2> table;

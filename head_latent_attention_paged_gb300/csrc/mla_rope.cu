@@ -1,12 +1,12 @@
 // Rotary positions on part of each head.
 //
 // Bound by memory: the rotated part of every head is read and written once.
-// A block takes a few tokens; one thread per (token, pair) computes the cosine
-// and sine into shared memory, from where all heads of the token use them, so
-// the functions cost one evaluation per token and pair.  The heads are then
-// units of 16 bytes (one piece, or in the half layout a piece of each half;
-// single pairs where the addresses do not allow that), a thread's first units
-// being loaded before the cosines are computed.
+// A head's rotated part is cut into units of 16 bytes (in the half layout 16
+// bytes of each half; single pairs where the addresses do not allow that).  A
+// thread owns one unit's place within the head for some heads of one token: it
+// sets their loads going, computes the unit's few cosines and sines meanwhile
+// and uses them for all its heads, so nothing goes through shared memory and
+// no thread waits for another.
 #include <cuda_runtime.h>
 
 #include "mla_layer_internal.h"
@@ -18,8 +18,7 @@ namespace mla {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnits = 4;       // units a thread has in flight
-constexpr int kRopeMaxTokens = 16;  // tokens of a block
+constexpr int kRopeHeads = 4;       // heads a thread has in flight
 
 // n / d for n < 2^31, as a multiplication (round-up method).
 struct Divider {
@@ -37,119 +36,105 @@ struct Divider {
 
 struct RopeLaunch {
   RopeParams p;
-  int32_t block_tokens;             // tokens of a block
   int32_t turn_units;               // of a head: rotated units, then copied ones
-  Divider units, heads;             // units of a head, heads
+  int32_t block_tokens;             // tokens of a block, one after another's groups
+  Divider units, groups;            // units of a head, threads sharing a token's heads
 };
 
-template <int kBytes>
-struct Piece;
-template <>
-struct Piece<16> { using type = uint4; };
-template <>
-struct Piece<4> { using type = uint32_t; };
-template <>
-struct Piece<2> { using type = uint16_t; };
-
+// One access of kVec elements: 16 bytes, or a single element.
 template <typename T, int kVec>
-union Elems {
-  typename Piece<sizeof(T) * kVec>::type raw;
-  T v[kVec];
-  __device__ Elems() {}
+struct Access {
+  uint4 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+  __device__ __forceinline__ void get(float* v) const { unpack16<T>(raw, v); }
+  __device__ __forceinline__ void put(const float* v) { raw = pack16<T>(v); }
+};
+template <typename T>
+struct Access<T, 1> {
+  T raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = raw; }
+  __device__ __forceinline__ void get(float* v) const { v[0] = to_f32(raw); }
+  __device__ __forceinline__ void put(const float* v) { raw = from_f32<T>(v[0]); }
 };
 
 template <typename T, int kVec, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_constant__ RopeLaunch a) {
-  extern __shared__ float2 cs[];    // [block_tokens][pairs], then the tokens' positions
   const RopeParams& p = a.p;
-  using E = Elems<T, kVec>;
-  using Raw = decltype(E::raw);
+  using E = Access<T, kVec>;
   // a rotated unit: kPieces pieces, kPairs pairs
   constexpr bool kTwo = kVec == 1 || kHalves;
   constexpr int kPieces = kTwo ? 2 : 1, kPairs = kTwo ? kVec : kVec / 2;
-  const int pairs = p.dim >> 1;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.block_tokens;
-  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.block_tokens), p.tokens - t0));
-  int32_t* pos_s = reinterpret_cast<int32_t*>(cs + a.block_tokens * pairs);
-  const uint32_t items = static_cast<uint32_t>(tokens) * a.units.d * a.heads.d;
-  const T* x = static_cast<const T*>(p.x);
-  T* out = static_cast<T*>(p.out);
-  E e[kRopeUnits][kPieces];
-  // where unit k lies: token of the block, head, first element (-1: none) and
-  // for a rotated unit its first pair
-  struct Place {
-    int32_t token, element, pair;
-    int64_t head;
-  };
-  auto place = [&](uint32_t k) {
-    Place q;
-    const uint32_t th = a.units.div(k), u = k - th * a.units.d, tok = a.heads.div(th);
-    q.token = static_cast<int32_t>(tok);
-    q.head = th - tok * a.heads.d;
-    q.pair = -1;
-    if (static_cast<int32_t>(u) < a.turn_units) {
-      q.pair = u * kPairs;
-      q.element = p.offset + (kVec == 1 && !kHalves ? 2 * u : u * kVec);
+  const uint32_t per_token = a.units.d * a.groups.d;
+  for (uint32_t k = blockIdx.y * kRopeThreads + threadIdx.x; k < a.block_tokens * per_token;
+       k += gridDim.y * kRopeThreads) {
+    const uint32_t row = a.units.div(k), u = k - row * a.units.d;
+    const uint32_t tok = a.groups.div(row), group = row - tok * a.groups.d;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.block_tokens + tok;
+    if (t >= p.tokens) return;
+    const int32_t pos = p.positions[t];
+    if (pos < 0) continue;
+    const bool turn = static_cast<int32_t>(u) < a.turn_units;
+    int32_t element;
+    if (turn) {
+      element = p.offset + (kVec == 1 && !kHalves ? 2 * u : u * kVec);
     } else {
       const int32_t c = (u - a.turn_units) * kVec;
-      q.element = c < p.offset ? c : c + p.dim;
+      element = c < p.offset ? c : c + p.dim;
     }
-    return q;
-  };
-  const int second = kHalves ? pairs : 1;   // elements to a unit's second piece
-  auto load = [&](uint32_t k0) {
+    const int second = kHalves ? p.dim >> 1 : 1;   // elements to a unit's second piece
+    const int64_t x_step = static_cast<int64_t>(a.groups.d) * p.x_head_stride;
+    const int64_t out_step = static_cast<int64_t>(a.groups.d) * p.out_head_stride;
+    const T* src = static_cast<const T*>(p.x) + t * p.x_token_stride +
+                   static_cast<int64_t>(group) * p.x_head_stride + element;
+    T* dst = static_cast<T*>(p.out) + t * p.out_token_stride +
+             static_cast<int64_t>(group) * p.out_head_stride + element;
+    float c[kPairs], s[kPairs];
+    bool ready = false;
+    for (int32_t h = group; h < p.heads; h += kRopeHeads * a.groups.d) {
+      E e[kRopeHeads][kPieces];
 #pragma unroll
-    for (int i = 0; i < kRopeUnits; ++i) {
-      const uint32_t k = k0 + i * kRopeThreads;
-      if (k >= items) continue;
-      const Place q = place(k);
-      const T* src = x + (t0 + q.token) * p.x_token_stride + q.head * p.x_head_stride + q.element;
-      e[i][0].raw = *reinterpret_cast<const Raw*>(src);
-      if (kTwo && q.pair >= 0) e[i][kPieces - 1].raw = *reinterpret_cast<const Raw*>(src + second);
-    }
-  };
-  load(threadIdx.x);
-  for (int i = threadIdx.x; i < tokens * pairs; i += kRopeThreads) {
-    const int tok = i / pairs;
-    const int32_t pos = p.positions[t0 + tok];
-    float c, s;
-    turn_cos_sin(p.table.turns[i - tok * pairs], pos, &c, &s);
-    cs[i] = make_float2(c * p.table.amplitude, (p.transposed ? -s : s) * p.table.amplitude);
-    if (i == tok * pairs) pos_s[tok] = pos;
-  }
-  __syncthreads();
-  for (uint32_t k0 = threadIdx.x; k0 < items; k0 += kRopeUnits * kRopeThreads) {
-#pragma unroll
-    for (int i = 0; i < kRopeUnits; ++i) {
-      const uint32_t k = k0 + i * kRopeThreads;
-      if (k >= items) continue;
-      const Place q = place(k);
-      if (pos_s[q.token] < 0) continue;
-      T* dst = out + (t0 + q.token) * p.out_token_stride + q.head * p.out_head_stride + q.element;
-      if (q.pair >= 0) {
-        const float2* f = cs + q.token * pairs + q.pair;
-        E y[kPieces];
+      for (int i = 0; i < kRopeHeads; ++i) {
+        if (h + i * static_cast<int32_t>(a.groups.d) >= p.heads) continue;
+        e[i][0].load(src + i * x_step);
+        if (kTwo && turn) e[i][kPieces - 1].load(src + i * x_step + second);
+      }
+      if (turn && !ready) {
+        ready = true;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          const float2 g = f[j];
-          const float va = to_f32(kTwo ? e[i][0].v[j % kVec] : e[i][0].v[2 * j % kVec]);
-          const float vb = to_f32(kTwo ? e[i][kPieces - 1].v[j % kVec] : e[i][0].v[(2 * j + 1) % kVec]);
-          const T ya = from_f32<T>(va * g.x - vb * g.y), yb = from_f32<T>(va * g.y + vb * g.x);
+          turn_cos_sin(p.table.turns[u * kPairs + j], pos, &c[j], &s[j]);
+          c[j] *= p.table.amplitude;
+          s[j] *= p.transposed ? -p.table.amplitude : p.table.amplitude;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRopeHeads; ++i) {
+        if (h + i * static_cast<int32_t>(a.groups.d) >= p.heads) continue;
+        if (turn) {
+          float v[kPieces * kVec];
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) e[i][j].get(v + j * kVec);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            float& va = v[kTwo ? j : 2 * j];
+            float& vb = v[kTwo ? kVec + j : 2 * j + 1];
+            const float ya = va * c[j] - vb * s[j], yb = va * s[j] + vb * c[j];
+            va = ya;
+            vb = yb;
+          }
+          e[i][0].put(v);
           if (kTwo) {
-            y[0].v[j % kVec] = ya;
-            y[kPieces - 1].v[j % kVec] = yb;
-          } else {
-            y[0].v[2 * j % kVec] = ya;
-            y[0].v[(2 * j + 1) % kVec] = yb;
+            e[i][kPieces - 1].put(v + (kPieces - 1) * kVec);
+            e[i][kPieces - 1].store(dst + i * out_step + second);
           }
         }
-        *reinterpret_cast<Raw*>(dst) = y[0].raw;
-        if (kTwo) *reinterpret_cast<Raw*>(dst + second) = y[kPieces - 1].raw;
-      } else {
-        *reinterpret_cast<Raw*>(dst) = e[i][0].raw;
+        e[i][0].store(dst + i * out_step);
       }
+      src += kRopeHeads * x_step;
+      dst += kRopeHeads * out_step;
     }
-    if (k0 + kRopeUnits * kRopeThreads < items) load(k0 + kRopeUnits * kRopeThreads);
   }
 }
 
@@ -158,21 +143,22 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   const bool halves = p.table.halves != 0;
   const int per_turn = kVec == 1 ? 2 : halves ? 2 * kVec : kVec;   // elements of a rotated unit
   const int turn_units = p.dim / per_turn;
-  const int copied = p.x == p.out ? 0 : (p.head_dim - p.dim) / kVec;
-  const int64_t per_token = static_cast<int64_t>(p.heads) * (turn_units + copied);
-  // tokens of a block: enough units to keep its threads busy, as long as
-  // that leaves two blocks for each multiprocessor
-  int64_t tokens = (2 * kRopeUnits * kRopeThreads + per_token - 1) / per_token;
-  if (tokens > p.tokens / (2 * 152)) tokens = p.tokens / (2 * 152);
-  if (tokens > kRopeMaxTokens) tokens = kRopeMaxTokens;
-  if (tokens < 1) tokens = 1;
-  RopeLaunch a{p, static_cast<int32_t>(tokens), turn_units, Divider(turn_units + copied), Divider(p.heads)};
-  const int blocks = static_cast<int>((p.tokens + tokens - 1) / tokens);
-  const int smem = static_cast<int>(tokens) * (p.dim / 2 * 8 + 4);
+  const int units = turn_units + (p.x == p.out ? 0 : (p.head_dim - p.dim) / kVec);
+  // threads that share a token's heads: as many as there are heads while
+  // that leaves the multiprocessors short of threads, then one for each
+  // kRopeHeads
+  const int64_t one = static_cast<int64_t>(p.tokens) * units;
+  const int few = (p.heads + kRopeHeads - 1) / kRopeHeads;
+  const int groups = one * few < 152 * 1024 ? p.heads : few;
+  const int64_t per_token = static_cast<int64_t>(units) * groups;
+  int64_t tokens = per_token < kRopeThreads ? kRopeThreads / per_token : 1;
+  const int split = per_token > kRopeThreads ? static_cast<int>((per_token + kRopeThreads - 1) / kRopeThreads) : 1;
+  RopeLaunch a{p, turn_units, static_cast<int32_t>(tokens), Divider(units), Divider(groups)};
+  const dim3 blocks(static_cast<unsigned>((p.tokens + tokens - 1) / tokens), split < 65535 ? split : 65535);
   if (halves)
-    mla_rope_kernel<T, kVec, true><<<blocks, kRopeThreads, smem, stream>>>(a);
+    mla_rope_kernel<T, kVec, true><<<blocks, kRopeThreads, 0, stream>>>(a);
   else
-    mla_rope_kernel<T, kVec, false><<<blocks, kRopeThreads, smem, stream>>>(a);
+    mla_rope_kernel<T, kVec, false><<<blocks, kRopeThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

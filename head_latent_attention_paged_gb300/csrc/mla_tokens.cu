@@ -107,7 +107,7 @@ __device__ __forceinline__ float abs_max(const float2 (&v)[4]) {
   float m = max3(fabsf(v[0].x), fabsf(v[0].y), fabsf(v[1].x));
   m = max3(m, fabsf(v[1].y), fabsf(v[2].x));
   m = max3(m, fabsf(v[2].y), fabsf(v[3].x));
-  return fmaxf(m, fabsf(v[3].y));
+  return max3(m, fabsf(v[3].y), 0.f);   // 0 where all are NaN
 }
 
 constexpr int kStageBytes = 640;   // a 594-byte row behind a shift of at most 14
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps)
     constexpr bool kFp8 = kKv == MLA_KV_FP8_E4M3_E8M0;
     // a group is 4 lanes of 8 values and 16 lanes of 2 (FP8), 2 and 8 (FP4)
     const float m[2] = {lanes_max(abs_max(y[0]), kFp8 ? 4 : 2), lanes_max(abs_max(y[1]), kFp8 ? 4 : 2)};
-    const float mk = lanes_max(fmaxf(fabsf(k.x), fabsf(k.y)), kFp8 ? 16 : 8);
+    const float mk = lanes_max(max3(fabsf(k.x), fabsf(k.y), 0.f), kFp8 ? 16 : 8);
     const uint32_t e[2] = {kFp8 ? e4m3_scale_byte(m[0]) : e2m1_scale_byte(m[0]),
                            kFp8 ? e4m3_scale_byte(m[1]) : e2m1_scale_byte(m[1])};
     const uint32_t ek = kFp8 ? e4m3_scale_byte(mk) : e2m1_scale_byte(mk);

@@ -179,7 +179,7 @@ typedef struct {
   int32_t dtype;               /* MLA_DTYPE_* */
   int32_t transposed;          /* 1: turn by minus the angle (the transposed map: the
                                   gradient; with amplitude 1 also the inverse) */
-  int64_t x_token_stride;      /* elements; heads of one token and tokens must not overlap */
+  int64_t x_token_stride;      /* elements, 0 .. 2^31 - 1; out's heads must not overlap */
   int64_t x_head_stride;
   int64_t out_token_stride;
   int64_t out_head_stride;
@@ -198,7 +198,7 @@ typedef struct {
  * b cos t), A the amplitude, in 32 bits, rounded once.
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT (a size or stride, a plan not made
  * by mla_rope_make_plan, an out that overlaps x otherwise), MLA_ERR_UNSUPPORTED
- * (a dtype, too many elements of a token), MLA_ERR_MISALIGNED (less than the
+ * (a dtype, a stride or a token's elements past the limits), MLA_ERR_MISALIGNED (less than the
  * elements' alignment) or MLA_ERR_CUDA.
  */
 MLA_API int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan, const void* x,
