@@ -6,6 +6,35 @@
 
 namespace mla {
 
+// The layer operators are launched as programmatic dependents of whatever
+// precedes them on their stream: the launch itself, and the set-up before
+// after_predecessor(), overlap the predecessor's tail.  A kernel touches no
+// memory but its parameters before that call, after which everything the
+// predecessor wrote is visible; it then lets its own successor start, which
+// waits in the same way until this kernel has completed.  (Small calls one
+// after another: 4.1 -> 1.4 us each.)
+#ifdef __CUDACC__
+__device__ __forceinline__ void after_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 blocks, int threads, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = blocks;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 struct NormParams {
   const void* x;
   const void* residual;         // or null

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
     const int k = i * width + t;
     if (k < pieces) reinterpret_cast<uint4*>(base)[k] = pack16<T>(v);
   };
+  after_predecessor();
   uint4 xe[R], re[R], we[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
       }
     }
   };
+  after_predecessor();
   uint32_t xw[R], rw[R];
   load(p.x, p.x_stride, xw);
   if (p.residual) load(p.residual, p.residual_stride, rw);
@@ -350,24 +352,24 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
 }
 
 template <typename T, int kOut, bool kWords, int R, int G>
-void launch_one(const NormParams& p, int threads, cudaStream_t stream) {
+cudaError_t launch_one(const NormParams& p, int threads, cudaStream_t stream) {
   constexpr int kRows = G == 0 ? 1 : kRowThreads / (G == 0 ? 1 : G);
   const int blocks = p.rows / kRows + (p.rows % kRows != 0);
-  auto launch = [&](auto kernel, int t) { kernel<<<blocks, t, 0, stream>>>(p); };
+  auto launch = [&](auto kernel, int t) { return launch_dependent(kernel, blocks, t, stream, p); };
   if constexpr (kWords && G != 0)
-    launch(mla_norm_words_kernel<T, kOut, R, G, kRowThreads>, kRowThreads);
+    return launch(mla_norm_words_kernel<T, kOut, R, G, kRowThreads>, kRowThreads);
   else if constexpr (G != 0)
-    launch(mla_norm_kernel<T, kOut, R, G, kRowThreads>, kRowThreads);
+    return launch(mla_norm_kernel<T, kOut, R, G, kRowThreads>, kRowThreads);
   else if constexpr (kWords)
-    threads <= 256 ? launch(mla_norm_words_kernel<T, kOut, R, 0, 256>, threads)
-                   : launch(mla_norm_words_kernel<T, kOut, R, 0, 1024>, threads);
+    return threads <= 256 ? launch(mla_norm_words_kernel<T, kOut, R, 0, 256>, threads)
+                          : launch(mla_norm_words_kernel<T, kOut, R, 0, 1024>, threads);
   else
-    threads <= 256 ? launch(mla_norm_kernel<T, kOut, R, 0, 256>, threads)
-                   : launch(mla_norm_kernel<T, kOut, R, 0, 1024>, threads);
+    return threads <= 256 ? launch(mla_norm_kernel<T, kOut, R, 0, 256>, threads)
+                          : launch(mla_norm_kernel<T, kOut, R, 0, 1024>, threads);
 }
 
 template <typename T, int kOut>
-void launch_formed(const NormParams& p, cudaStream_t stream) {
+cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(T);
   constexpr int kOutBytes = kOut == MLA_NORM_OUT_SAME ? 16 : V;
   auto fits = [&](const void* base, int64_t stride, int bytes, int size) {
@@ -399,26 +401,19 @@ void launch_formed(const NormParams& p, cudaStream_t stream) {
 }
 
 template <typename T>
-void launch_typed(const NormParams& p, cudaStream_t stream) {
-  if (p.out_format == MLA_NORM_OUT_SAME)
-    launch_formed<T, MLA_NORM_OUT_SAME>(p, stream);
-  else if (p.out_format == MLA_NORM_OUT_E4M3_E8M0)
-    launch_formed<T, MLA_NORM_OUT_E4M3_E8M0>(p, stream);
-  else
-    launch_formed<T, MLA_NORM_OUT_E4M3_ROW>(p, stream);
+cudaError_t launch_typed(const NormParams& p, cudaStream_t stream) {
+  if (p.out_format == MLA_NORM_OUT_SAME) return launch_formed<T, MLA_NORM_OUT_SAME>(p, stream);
+  if (p.out_format == MLA_NORM_OUT_E4M3_E8M0) return launch_formed<T, MLA_NORM_OUT_E4M3_E8M0>(p, stream);
+  return launch_formed<T, MLA_NORM_OUT_E4M3_ROW>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
-  if (p.dtype == MLA_DTYPE_BF16)
-    launch_typed<__nv_bfloat16>(p, stream);
-  else if (p.dtype == MLA_DTYPE_F16)
-    launch_typed<__half>(p, stream);
-  else
-    launch_typed<float>(p, stream);
-  return cudaGetLastError();
+  if (p.dtype == MLA_DTYPE_BF16) return launch_typed<__nv_bfloat16>(p, stream);
+  if (p.dtype == MLA_DTYPE_F16) return launch_typed<__half>(p, stream);
+  return launch_typed<float>(p, stream);
 }
 
 }  // namespace mla

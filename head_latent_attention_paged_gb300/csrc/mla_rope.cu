@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
   constexpr bool kTwo = kVec == 1 || kHalves;
   constexpr int kPieces = kTwo ? 2 : 1, kPairs = kTwo ? kVec : kVec / 2;
   const uint32_t per_token = a.units.d * a.groups.d;
+  after_predecessor();
   for (uint32_t k = blockIdx.y * kRopeThreads + threadIdx.x; k < a.block_tokens * per_token;
        k += gridDim.y * kRopeThreads) {
     const uint32_t row = a.units.div(k), u = k - row * a.units.d;
@@ -155,11 +156,8 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   const int split = per_token > kRopeThreads ? static_cast<int>((per_token + kRopeThreads - 1) / kRopeThreads) : 1;
   RopeLaunch a{p, turn_units, static_cast<int32_t>(tokens), Divider(units), Divider(groups)};
   const dim3 blocks(static_cast<unsigned>((p.tokens + tokens - 1) / tokens), split < 65535 ? split : 65535);
-  if (halves)
-    mla_rope_kernel<T, kVec, true><<<blocks, kRopeThreads, 0, stream>>>(a);
-  else
-    mla_rope_kernel<T, kVec, false><<<blocks, kRopeThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return halves ? launch_dependent(mla_rope_kernel<T, kVec, true>, blocks, kRopeThreads, stream, a)
+                : launch_dependent(mla_rope_kernel<T, kVec, false>, blocks, kRopeThreads, stream, a);
 }
 
 template <typename T>

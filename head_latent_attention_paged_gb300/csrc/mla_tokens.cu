@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps)
     mla_append_tokens_kernel(const __grid_constant__ AppendTokensParams p, const int32_t chunk) {
   __shared__ __align__(16) uint8_t stage_s[kKv == MLA_KV_FP8_E4M3_E8M0 ? kTokenWarps : 1][kStageBytes];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  after_predecessor();
   const WarpTokens tok = warp_tokens(p.t, chunk, lane);
   if (tok.count <= 0) return;
   const uint16_t* src = p.rows + tok.first * p.row_stride;
@@ -383,6 +384,7 @@ template <int kKv>
 __global__ void __launch_bounds__(32 * kTokenWarps)
     mla_gather_kernel(const __grid_constant__ GatherParams p, const int32_t chunk) {
   const int lane = threadIdx.x & 31;
+  after_predecessor();
   const WarpTokens tok = warp_tokens(p.t, chunk, lane);
   for (int j = 0; j < tok.count; j += 2) {
     CachedRow<kKv> c[2];
@@ -420,25 +422,23 @@ int blocks_of(int32_t tokens, int chunk) {
 cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream) {
   if (p.t.tokens == 0) return cudaSuccess;
   const int chunk = chunk_of(p.t.tokens), blocks = blocks_of(p.t.tokens, chunk);
+  const int threads = 32 * kTokenWarps;
   if (p.t.kv_dtype == MLA_KV_BF16)
-    mla_append_tokens_kernel<MLA_KV_BF16><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
-  else if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
-    mla_append_tokens_kernel<MLA_KV_FP8_E4M3_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
-  else
-    mla_append_tokens_kernel<MLA_KV_FP4_E2M1_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
-  return cudaGetLastError();
+    return launch_dependent(mla_append_tokens_kernel<MLA_KV_BF16>, blocks, threads, stream, p, chunk);
+  if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
+    return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP8_E4M3_E8M0>, blocks, threads, stream, p, chunk);
+  return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP4_E2M1_E8M0>, blocks, threads, stream, p, chunk);
 }
 
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
   if (p.t.tokens == 0) return cudaSuccess;
   const int chunk = chunk_of(p.t.tokens), blocks = blocks_of(p.t.tokens, chunk);
+  const int threads = 32 * kTokenWarps;
   if (p.t.kv_dtype == MLA_KV_BF16)
-    mla_gather_kernel<MLA_KV_BF16><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
-  else if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
-    mla_gather_kernel<MLA_KV_FP8_E4M3_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
-  else
-    mla_gather_kernel<MLA_KV_FP4_E2M1_E8M0><<<blocks, 32 * kTokenWarps, 0, stream>>>(p, chunk);
-  return cudaGetLastError();
+    return launch_dependent(mla_gather_kernel<MLA_KV_BF16>, blocks, threads, stream, p, chunk);
+  if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
+    return launch_dependent(mla_gather_kernel<MLA_KV_FP8_E4M3_E8M0>, blocks, threads, stream, p, chunk);
+  return launch_dependent(mla_gather_kernel<MLA_KV_FP4_E2M1_E8M0>, blocks, threads, stream, p, chunk);
 }
 
 }  // namespace mla
