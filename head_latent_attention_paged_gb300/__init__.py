@@ -313,14 +313,28 @@ def make_norm_problem(rows, cols, dtype=MLA_DTYPE_BF16, out_format=MLA_NORM_OUT_
                           (cols + 31) // 32 if scale_stride is None else scale_stride)
 
 
+# The layer calls below take a few microseconds on the device for a decode
+# step's sizes, less than a call per argument costs here: tensors and torch
+# streams are read in place, and anything else (addresses, stream handles, the
+# library not yet loaded) goes through _ptr and _stream.  A call falls back
+# before it is made: the attribute that is missing is one of its arguments'.
 def mla_rms_norm(problem: MlaNormProblem, x, weight, out, residual=None, residual_out=None,
                  scales=None, stream=None) -> None:
     """out = h / sqrt(mean(h^2) + eps) * weight for each row, h = x + residual
     (residual_out receives h); weight None is ones.  An 8-bit out_format writes
     e4m3 codes to out and the scales to scales."""
-    _check("mla_rms_norm", load().mla_rms_norm(
-        ctypes.byref(problem), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out),
-        _ptr(out), _ptr(scales), _stream(stream)))
+    try:
+        rc = _lib.mla_rms_norm(
+            problem, x.data_ptr(), None if residual is None else residual.data_ptr(),
+            None if weight is None else weight.data_ptr(),
+            None if residual_out is None else residual_out.data_ptr(), out.data_ptr(),
+            None if scales is None else scales.data_ptr(),
+            None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = load().mla_rms_norm(problem, _ptr(x), _ptr(residual), _ptr(weight),
+                                 _ptr(residual_out), _ptr(out), _ptr(scales), _stream(stream))
+    if rc:
+        raise MlaError("mla_rms_norm", rc)
 
 
 def mla_rope_make_plan(config: MlaRopeConfig) -> MlaRopePlan:
@@ -353,10 +367,17 @@ def mla_rope(problem: MlaRopeProblem, plan: MlaRopePlan, x, positions, out=None,
              stream=None) -> None:
     """Rotate part of every head of token t to positions[t] (in place without
     an out); a negative position leaves the token's out as it was."""
-    x = _ptr(x)
-    _check("mla_rope", load().mla_rope(ctypes.byref(problem), ctypes.byref(plan), x,
-                                       _ptr(positions), x if out is None else _ptr(out),
-                                       _stream(stream)))
+    try:
+        x = x.data_ptr()
+        rc = _lib.mla_rope(problem, plan, x, positions.data_ptr(),
+                           x if out is None else out.data_ptr(),
+                           None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        x = _ptr(x)
+        rc = load().mla_rope(problem, plan, x, _ptr(positions), x if out is None else _ptr(out),
+                             _stream(stream))
+    if rc:
+        raise MlaError("mla_rope", rc)
 
 
 def mla_cache_append_tokens(problem: MlaProblem, tokens: int, rows, positions, block_table,
@@ -367,20 +388,38 @@ def mla_cache_append_tokens(problem: MlaProblem, tokens: int, rows, positions, b
     positions[t] of request requests[t] (None: tokens / batch consecutive rows
     per request), its latent normed with norm_weight and its key rotated by
     rope where given."""
-    _check("mla_cache_append_tokens", load().mla_cache_append_tokens(
-        ctypes.byref(problem), tokens, _ptr(rows), row_stride, _ptr(positions), _ptr(requests),
-        _ptr(block_table), _ptr(norm_weight), norm_eps,
-        None if rope is None else ctypes.byref(rope), _ptr(kv_cache), _ptr(status),
-        _stream(stream)))
+    try:
+        rc = _lib.mla_cache_append_tokens(
+            problem, tokens, rows.data_ptr(), row_stride, positions.data_ptr(),
+            None if requests is None else requests.data_ptr(), block_table.data_ptr(),
+            None if norm_weight is None else norm_weight.data_ptr(), norm_eps, rope,
+            kv_cache.data_ptr(), None if status is None else status.data_ptr(),
+            None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = load().mla_cache_append_tokens(
+            problem, tokens, _ptr(rows), row_stride, _ptr(positions), _ptr(requests),
+            _ptr(block_table), _ptr(norm_weight), norm_eps, rope, _ptr(kv_cache), _ptr(status),
+            _stream(stream))
+    if rc:
+        raise MlaError("mla_cache_append_tokens", rc)
 
 
 def mla_cache_gather(problem: MlaProblem, tokens: int, kv_cache, positions, block_table, out,
                      requests=None, out_stride: int = 576, status=None, stream=None) -> None:
     """The cached row at position positions[t] of request requests[t] as bf16
     row t of out (out_stride elements apart)."""
-    _check("mla_cache_gather", load().mla_cache_gather(
-        ctypes.byref(problem), tokens, _ptr(kv_cache), _ptr(positions), _ptr(requests),
-        _ptr(block_table), _ptr(out), out_stride, _ptr(status), _stream(stream)))
+    try:
+        rc = _lib.mla_cache_gather(
+            problem, tokens, kv_cache.data_ptr(), positions.data_ptr(),
+            None if requests is None else requests.data_ptr(), block_table.data_ptr(),
+            out.data_ptr(), out_stride, None if status is None else status.data_ptr(),
+            None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = load().mla_cache_gather(
+            problem, tokens, _ptr(kv_cache), _ptr(positions), _ptr(requests), _ptr(block_table),
+            _ptr(out), out_stride, _ptr(status), _stream(stream))
+    if rc:
+        raise MlaError("mla_cache_gather", rc)
 
 
 def mla_get_status(plan: MlaPlan, workspace, stream=None) -> int:

@@ -20,11 +20,12 @@ __device__ __forceinline__ void after_predecessor() {
 }
 
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 blocks, int threads, cudaStream_t stream,
-                             const Args&... args) {
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 blocks, int threads, int smem,
+                             cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = blocks;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

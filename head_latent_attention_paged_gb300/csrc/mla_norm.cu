@@ -36,6 +36,14 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return two;
 }
 
+// Largest of a warp's values, NaN left out; 0 where there is none.
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, 0.f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
 template <int G, bool kMax>
 __device__ __forceinline__ float lanes_reduce(float v) {
 #pragma unroll
@@ -185,8 +193,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
 // aligned ones around it (they hold at least one element of the row each, so
 // the reads stay on the tensor's own words) and leaves in the aligned word
 // that begins with the lane below's second element; the ends of a warp's words
-// go as single elements.  All but the row's last words take the short paths
-// without a comparison per element.
+// go as single elements.  Rows too wide to be staged, or too few.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormParams p) {
   __shared__ float slots[2][32];
@@ -196,27 +203,25 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
   const int64_t row = G == 0 ? static_cast<int64_t>(blockIdx.x)
                              : static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + warp;
   const int k0 = (G == 0 ? warp * R * 32 : 0) + lane;
-  // elements from the warp's first word, and from the lane's, to the row's end
-  const int warp_left = (G == 0 || row < p.rows ? p.cols : 0) - (k0 - lane) * E, left = warp_left - lane * E;
-  auto whole = [&](int i) { return warp_left >= 32 * E * (i + 1); };     // every lane's word i
-  auto any = [&](int i) { return warp_left > 32 * E * i; };              // some lane's
+  // elements from the lane's first word to the row's end
+  const int left = (G == 0 || row < p.rows ? p.cols : 0) - k0 * E;
   auto has = [&](int i, int elems) { return left >= 32 * E * i + elems; };
   auto load = [&](const void* base, int64_t stride, uint32_t (&w)[R]) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * stride + k0 * E);
     const uint32_t* words = reinterpret_cast<const uint32_t*>(at & ~static_cast<uintptr_t>(3));
     const bool odd = E == 2 && (at & 2);
 #pragma unroll
-    for (int i = 0; i < R; ++i) w[i] = whole(i) || has(i, 1) ? words[32 * i] : 0u;
+    for (int i = 0; i < R; ++i) w[i] = has(i, 1) ? words[32 * i] : 0u;
     if (odd) {
       uint32_t hi[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) hi[i] = whole(i) || has(i, 2) ? words[32 * i + 1] : 0u;
+      for (int i = 0; i < R; ++i) hi[i] = has(i, 2) ? words[32 * i + 1] : 0u;
 #pragma unroll
       for (int i = 0; i < R; ++i) w[i] = __funnelshift_r(w[i], hi[i], 16);
     } else if (E == 2) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (!whole(i) && !has(i, 2)) w[i] &= 0xFFFFu;
+        if (!has(i, 2)) w[i] &= 0xFFFFu;
     }
   };
   auto store = [&](void* base, int64_t stride, const uint32_t (&w)[R]) {
@@ -226,7 +231,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     if (E == 1 || !(reinterpret_cast<uintptr_t>(dst) & 2)) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (whole(i) || has(i, E))
+        if (has(i, E))
           words[32 * i] = w[i];
         else if (has(i, 1))
           elem[32 * E * i] = static_cast<Half>(w[i]);
@@ -234,11 +239,10 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (!any(i)) continue;
         const uint32_t below = __shfl_up_sync(0xffffffffu, w[i], 1);
-        if (lane > 0 ? has(i, 1) : false) words[32 * i] = __funnelshift_r(below, w[i], 16);
-        if (lane == 0) elem[32 * E * i] = static_cast<Half>(w[i]);
-        if (whole(i) ? lane == 31 : has(i, 2) && (lane == 31 || !has(i, 3)))
+        if (lane > 0 && has(i, 1)) words[32 * i] = __funnelshift_r(below, w[i], 16);
+        if (lane == 0 && has(i, 1)) elem[32 * E * i] = static_cast<Half>(w[i]);
+        if (has(i, 2) && (lane == 31 || !has(i, 3)))
           elem[32 * E * i + 1] = static_cast<Half>(w[i] >> 16);
       }
     }
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
 #pragma unroll
       for (int j = 0; j < E; ++j) v[j] *= b[j];
     }
-    if (kOut != MLA_NORM_OUT_SAME && !whole(i)) {   // 0 where there is none: not 0 * inf
+    if (kOut != MLA_NORM_OUT_SAME) {   // 0 where there is none: not 0 * inf
 #pragma unroll
       for (int j = 0; j < E; ++j)
         if (!has(i, j + 1)) v[j] = 0.f;
@@ -306,7 +310,6 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const float* v = h + i * E;
-    if (!any(i)) continue;
     bool some = true;
     if (kOut == MLA_NORM_OUT_E4M3_E8M0) {
       // a group of 32 is 32 / E neighbouring lanes' words
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
   } else if (!(reinterpret_cast<uintptr_t>(out) & 1)) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (whole(i) || has(i, 2))
+      if (has(i, 2))
         reinterpret_cast<uint16_t*>(out)[32 * i] = static_cast<uint16_t>(xw[i]);
       else if (has(i, 1))
         out[64 * i] = static_cast<uint8_t>(xw[i]);
@@ -340,14 +343,170 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
   } else {   // as in store, by bytes
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      if (!any(i)) continue;
-      const uint32_t below = __shfl_up_sync(0xffffffffu, xw[i], 1);
-      if (lane > 0 ? has(i, 1) : false)
+        const uint32_t below = __shfl_up_sync(0xffffffffu, xw[i], 1);
+      if (lane > 0 && has(i, 1))
         reinterpret_cast<uint16_t*>(out - 1)[32 * i] = static_cast<uint16_t>((below >> 8) | (xw[i] << 8));
-      if (lane == 0) out[64 * i] = static_cast<uint8_t>(xw[i]);
-      if (whole(i) ? lane == 31 : has(i, 2) && (lane == 31 || !has(i, 3)))
+      if (lane == 0 && has(i, 1)) out[64 * i] = static_cast<uint8_t>(xw[i]);
+      if (has(i, 2) && (lane == 31 || !has(i, 3)))
         out[64 * i + 1] = static_cast<uint8_t>(xw[i] >> 8);
     }
+  }
+}
+
+// Many rows that the 16-byte pieces do not fit: a row passes through shared
+// memory, where it lies as it does around its 16-byte boundaries, so that
+// global memory sees 16-byte accesses (but for the row's ends) while the
+// threads take single elements, element t + i * blockDim for thread t.  A
+// block stays for several rows: the weights stay in registers, and the next
+// row is copied in asynchronously while one is computed.
+constexpr int kStagedBlocks = 152 * 6;
+
+__host__ __device__ inline int staged_buffer(int cols, int size) { return (cols * size + 15) / 16 * 16 + 16; }
+
+// A row's place: its elements start `shift` bytes into 16-byte line 0; lines
+// first .. end - 1 belong to it whole.
+struct Lines {
+  uint8_t* line;                 // global, 16-byte aligned
+  int shift, bytes, first, end;
+  __device__ Lines(const void* row, int n) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+    shift = static_cast<int>(at & 15);
+    line = reinterpret_cast<uint8_t*>(at - shift);
+    bytes = n;
+    first = shift ? 1 : 0;
+    end = (shift + n) >> 4;
+  }
+  // Byte offset of the element of the row's ends that thread t < 32 moves
+  // (lanes 0-15 those in front of the whole lines, 16-31 those behind), or -1.
+  __device__ __forceinline__ int edge(int t, int size) const {
+    const int lines_from = 16 * first, lines_to = 16 * (end > first ? end : first);
+    const int at = t < 16 ? shift + t * size : lines_to + (t - 16) * size;
+    const int stop = t < 16 ? min(lines_from, shift + bytes) : shift + bytes;
+    return t < 32 && at < stop ? at : -1;
+  }
+};
+
+__device__ __forceinline__ void copy_async_16(uint8_t* shared, const uint8_t* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
+               "l"(global)
+               : "memory");
+}
+
+template <typename T, int kOut, int R>
+__global__ void __launch_bounds__(256) mla_norm_staged_kernel(const NormParams p) {
+  extern __shared__ __align__(16) uint8_t buffers[];
+  __shared__ float slots[2][32];
+  constexpr int kSize = sizeof(T), kOutSize = kOut == MLA_NORM_OUT_SAME ? kSize : 1;
+  using Bits = typename std::conditional<kSize == 2, uint16_t, uint32_t>::type;
+  const int t = threadIdx.x, width = blockDim.x, buffer = staged_buffer(p.cols, kSize);
+  uint8_t* const sum_s = buffers + (p.residual ? 4 : 2) * buffer;   // residual_out's lines, then out's
+  uint8_t* const out_s = sum_s + (p.residual_out ? buffer : 0);
+  auto stage = [&](int s, int which) { return buffers + (p.residual ? 2 * s + which : s) * buffer; };
+  auto x_row = [&](int64_t row) { return Lines(static_cast<const T*>(p.x) + row * p.x_stride, p.cols * kSize); };
+  auto r_row = [&](int64_t row) {
+    return Lines(static_cast<const T*>(p.residual) + row * p.residual_stride, p.cols * kSize);
+  };
+  // The lines of a row into a buffer; its ends' elements into a register.
+  auto fetch = [&](const Lines& l, uint8_t* to) {
+    for (int i = l.first + t; i < l.end; i += width) copy_async_16(to + 16 * i, l.line + 16 * i);
+    const int at = l.edge(t, kSize);
+    return at >= 0 ? *reinterpret_cast<const Bits*>(l.line + at) : static_cast<Bits>(0);
+  };
+  auto put_edge = [&](const Lines& l, uint8_t* to, Bits v) {
+    const int at = l.edge(t, kSize);
+    if (at >= 0) *reinterpret_cast<Bits*>(to + at) = v;
+  };
+  auto flush = [&](const Lines& l, const uint8_t* from, auto size) {
+    constexpr int n = decltype(size)::value;
+    using B = typename std::conditional<n == 1, uint8_t, typename std::conditional<n == 2, uint16_t, uint32_t>::type>::type;
+    for (int i = l.first + t; i < l.end; i += width)
+      *reinterpret_cast<uint4*>(l.line + 16 * i) = *reinterpret_cast<const uint4*>(from + 16 * i);
+    const int at = l.edge(t, n);
+    if (at >= 0) *reinterpret_cast<B*>(l.line + at) = *reinterpret_cast<const B*>(from + at);
+  };
+  after_predecessor();
+  float w[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int c = t + i * width;
+    w[i] = p.weight && c < p.cols ? to_f32(static_cast<const T*>(p.weight)[c]) : 1.f;
+  }
+  Bits x_edge = 0, r_edge = 0;
+  auto prefetch = [&](int64_t row, int s) {
+    if (row < p.rows) {
+      x_edge = fetch(x_row(row), stage(s, 0));
+      if (p.residual) r_edge = fetch(r_row(row), stage(s, 1));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  prefetch(blockIdx.x, 0);
+  int s = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, s ^= 1) {
+    const Lines xl = x_row(row), rl = r_row(row);
+    put_edge(xl, stage(s, 0), x_edge);
+    if (p.residual) put_edge(rl, stage(s, 1), r_edge);
+    // the other buffers were read before the last row's sums met
+    prefetch(row + gridDim.x, s ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const Bits* xs = reinterpret_cast<const Bits*>(stage(s, 0) + xl.shift) + t;
+    const Bits* rs = reinterpret_cast<const Bits*>(stage(s, 1) + rl.shift) + t;
+    const Lines ol(static_cast<T*>(p.residual_out) + row * p.residual_out_stride, p.cols * kSize);
+    T* sums = reinterpret_cast<T*>(sum_s + ol.shift) + t;
+    float h[R];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      h[i] = 0.f;
+      if (t + i * width < p.cols) {
+        const Bits xb = xs[i * width];
+        h[i] = to_f32(*reinterpret_cast<const T*>(&xb));
+        if (p.residual) {
+          const Bits rb = rs[i * width];
+          h[i] += to_f32(*reinterpret_cast<const T*>(&rb));
+        }
+        if (p.residual_out) sums[i * width] = from_f32<T>(h[i]);
+      }
+      sum = fmaf(h[i], h[i], sum);
+    }
+    const float rstd = rsqrtf(row_reduce<0, false>(sum, slots[0]) / static_cast<float>(p.cols) + p.eps);
+    if (p.residual_out) flush(ol, sum_s, std::integral_constant<int, kSize>());
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      h[i] = t + i * width < p.cols ? h[i] * rstd * w[i] : 0.f;   // 0 where there is none: not 0 * inf
+      if (kOut == MLA_NORM_OUT_E4M3_ROW) amax = max_nan(amax, fabsf(h[i]));
+    }
+    const Lines yl(static_cast<uint8_t*>(p.out) + row * p.out_stride * kOutSize, p.cols * kOutSize);
+    uint8_t* ys = out_s + yl.shift;
+    float inv = 1.f;
+    if (kOut == MLA_NORM_OUT_E4M3_ROW) {
+      const float scale = max_nan(row_reduce<0, true>(amax, slots[1]) / 448.f, kMinRowScale);
+      inv = 1.f / scale;
+      if (t == 0) static_cast<float*>(p.scales)[row] = scale;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = t + i * width;
+      if (kOut == MLA_NORM_OUT_SAME) {
+        if (c < p.cols) reinterpret_cast<T*>(ys)[c] = from_f32<T>(h[i]);
+        continue;
+      }
+      bool some = true;
+      if (kOut == MLA_NORM_OUT_E4M3_E8M0) {   // a group is a warp's elements
+        const float a = lanes_max(fabsf(h[i]));
+        some = a > 0.f;
+        const uint32_t byte = e4m3_scale_byte(a);
+        inv = scale_byte_reciprocal(byte);
+        if (c < p.cols && (t & 31) == 0)
+          static_cast<uint8_t*>(p.scales)[row * p.scale_stride + (c >> 5)] = static_cast<uint8_t>(byte);
+      }
+      uint32_t code = e4m3x2(h[i] * inv, 0.f);
+      if (!some) code &= 0x7Fu;   // zeros without their signs (or NaN)
+      if (c < p.cols) ys[c] = static_cast<uint8_t>(code);
+    }
+    __syncthreads();
+    flush(yl, out_s, std::integral_constant<int, kOutSize>());
   }
 }
 
@@ -355,7 +514,7 @@ template <typename T, int kOut, bool kWords, int R, int G>
 cudaError_t launch_one(const NormParams& p, int threads, cudaStream_t stream) {
   constexpr int kRows = G == 0 ? 1 : kRowThreads / (G == 0 ? 1 : G);
   const int blocks = p.rows / kRows + (p.rows % kRows != 0);
-  auto launch = [&](auto kernel, int t) { return launch_dependent(kernel, blocks, t, stream, p); };
+  auto launch = [&](auto kernel, int t) { return launch_dependent(kernel, blocks, t, 0, stream, p); };
   if constexpr (kWords && G != 0)
     return launch(mla_norm_words_kernel<T, kOut, R, G, kRowThreads>, kRowThreads);
   else if constexpr (G != 0)
@@ -366,6 +525,19 @@ cudaError_t launch_one(const NormParams& p, int threads, cudaStream_t stream) {
   else
     return threads <= 256 ? launch(mla_norm_kernel<T, kOut, R, 0, 256>, threads)
                           : launch(mla_norm_kernel<T, kOut, R, 0, 1024>, threads);
+}
+
+template <typename T, int kOut, int R>
+cudaError_t launch_staged(const NormParams& p, int threads, cudaStream_t stream) {
+  const int buffer = staged_buffer(p.cols, sizeof(T));
+  const int smem = buffer * ((p.residual ? 4 : 2) + (p.residual_out ? 1 : 0)) +
+                   staged_buffer(p.cols, kOut == MLA_NORM_OUT_SAME ? sizeof(T) : 1);
+  auto kernel = mla_norm_staged_kernel<T, kOut, R>;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_dependent(kernel, p.rows < kStagedBlocks ? p.rows : kStagedBlocks, threads, smem, stream, p);
 }
 
 template <typename T, int kOut>
@@ -391,6 +563,13 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
     if (n <= 1024 && !many) return launch_one<T, kOut, false, 1, 0>(p, threads(n, 1), stream);
     if (n <= 4096) return launch_one<T, kOut, false, 4, 0>(p, threads(n, 4), stream);
     return launch_one<T, kOut, false, kMost, 0>(p, threads(n, kMost), stream);
+  }
+  if (many && p.cols > 256 && p.cols * sizeof(T) <= 16384) {
+    const int t = p.cols <= 4096 ? 128 : 256;
+    if (p.cols <= 8 * t) return launch_staged<T, kOut, 8>(p, t, stream);
+    if (p.cols <= 16 * t) return launch_staged<T, kOut, 16>(p, t, stream);
+    if (p.cols <= 24 * t) return launch_staged<T, kOut, 24>(p, t, stream);
+    return launch_staged<T, kOut, 32>(p, t, stream);
   }
   constexpr int kMost = sizeof(T) == 4 ? 32 : 16;   // words of a thread
   const int n = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;

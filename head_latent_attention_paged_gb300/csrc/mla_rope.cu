@@ -156,8 +156,8 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   const int split = per_token > kRopeThreads ? static_cast<int>((per_token + kRopeThreads - 1) / kRopeThreads) : 1;
   RopeLaunch a{p, turn_units, static_cast<int32_t>(tokens), Divider(units), Divider(groups)};
   const dim3 blocks(static_cast<unsigned>((p.tokens + tokens - 1) / tokens), split < 65535 ? split : 65535);
-  return halves ? launch_dependent(mla_rope_kernel<T, kVec, true>, blocks, kRopeThreads, stream, a)
-                : launch_dependent(mla_rope_kernel<T, kVec, false>, blocks, kRopeThreads, stream, a);
+  return halves ? launch_dependent(mla_rope_kernel<T, kVec, true>, blocks, kRopeThreads, 0, stream, a)
+                : launch_dependent(mla_rope_kernel<T, kVec, false>, blocks, kRopeThreads, 0, stream, a);
 }
 
 template <typename T>

@@ -424,10 +424,10 @@ cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t strea
   const int chunk = chunk_of(p.t.tokens), blocks = blocks_of(p.t.tokens, chunk);
   const int threads = 32 * kTokenWarps;
   if (p.t.kv_dtype == MLA_KV_BF16)
-    return launch_dependent(mla_append_tokens_kernel<MLA_KV_BF16>, blocks, threads, stream, p, chunk);
+    return launch_dependent(mla_append_tokens_kernel<MLA_KV_BF16>, blocks, threads, 0, stream, p, chunk);
   if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
-    return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP8_E4M3_E8M0>, blocks, threads, stream, p, chunk);
-  return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP4_E2M1_E8M0>, blocks, threads, stream, p, chunk);
+    return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP8_E4M3_E8M0>, blocks, threads, 0, stream, p, chunk);
+  return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP4_E2M1_E8M0>, blocks, threads, 0, stream, p, chunk);
 }
 
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
@@ -435,10 +435,10 @@ cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
   const int chunk = chunk_of(p.t.tokens), blocks = blocks_of(p.t.tokens, chunk);
   const int threads = 32 * kTokenWarps;
   if (p.t.kv_dtype == MLA_KV_BF16)
-    return launch_dependent(mla_gather_kernel<MLA_KV_BF16>, blocks, threads, stream, p, chunk);
+    return launch_dependent(mla_gather_kernel<MLA_KV_BF16>, blocks, threads, 0, stream, p, chunk);
   if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
-    return launch_dependent(mla_gather_kernel<MLA_KV_FP8_E4M3_E8M0>, blocks, threads, stream, p, chunk);
-  return launch_dependent(mla_gather_kernel<MLA_KV_FP4_E2M1_E8M0>, blocks, threads, stream, p, chunk);
+    return launch_dependent(mla_gather_kernel<MLA_KV_FP8_E4M3_E8M0>, blocks, threads, 0, stream, p, chunk);
+  return launch_dependent(mla_gather_kernel<MLA_KV_FP4_E2M1_E8M0>, blocks, threads, 0, stream, p, chunk);
 }
 
 }  // namespace mla
