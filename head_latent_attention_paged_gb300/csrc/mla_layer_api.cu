@@ -166,6 +166,7 @@ int mla_rms_norm(const mla_norm_problem* problem, const void* x, const void* res
   p.dtype = pr.dtype;
   p.out_format = pr.out_format;
   p.eps = pr.eps;
+  p.inv_cols = 1.f / static_cast<float>(pr.cols);
   return launch_norm(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -46,7 +46,7 @@ struct NormParams {
   int64_t x_stride, residual_stride, residual_out_stride, out_stride, scale_stride;
   int32_t rows, cols;
   int32_t dtype, out_format;
-  float eps;
+  float eps, inv_cols;          // inv_cols: 1 / cols
 };
 cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
 

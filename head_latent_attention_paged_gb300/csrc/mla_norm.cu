@@ -36,14 +36,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return two;
 }
 
-// Largest of a warp's values, NaN left out; 0 where there is none.
-__device__ __forceinline__ float lanes_max(float v) {
-  v = fmaxf(v, 0.f);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
 template <int G, bool kMax>
 __device__ __forceinline__ float lanes_reduce(float v) {
 #pragma unroll
@@ -124,7 +116,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
     for (int i = 0; i < R; ++i) store(ro, i, h + i * V);
   }
   if (!kWeightFirst) load_weight();
-  const float rstd = rsqrtf(row_reduce<G, false>(sum, slots[0]) / static_cast<float>(p.cols) + p.eps);
+  const float rstd = rsqrtf(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -152,7 +144,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
   uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride;
   float inv = 1.f;
   if (kOut == MLA_NORM_OUT_E4M3_ROW) {
-    const float scale = max_nan(row_reduce<G, true>(amax, slots[1]) / 448.f, kMinRowScale);
+    const float scale = max_nan(row_reduce<G, true>(amax, slots[1]) * (1.f / 448.f), kMinRowScale);
     inv = 1.f / scale;
     if (pieces && t == 0) static_cast<float*>(p.scales)[row] = scale;
   }
@@ -272,7 +264,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     store(p.residual_out, p.residual_out_stride, xw);
   }
   if (p.weight) load(p.weight, 0, rw);
-  const float rstd = rsqrtf(row_reduce<G, false>(sum, slots[0]) / static_cast<float>(p.cols) + p.eps);
+  const float rstd = rsqrtf(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -303,7 +295,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
   }
   float inv = 1.f;
   if (kOut == MLA_NORM_OUT_E4M3_ROW) {
-    const float scale = max_nan(row_reduce<G, true>(amax, slots[1]) / 448.f, kMinRowScale);
+    const float scale = max_nan(row_reduce<G, true>(amax, slots[1]) * (1.f / 448.f), kMinRowScale);
     inv = 1.f / scale;
     if (has(0, 1) && k0 == 0) static_cast<float*>(p.scales)[row] = scale;
   }
@@ -356,10 +348,13 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
 // Many rows that the 16-byte pieces do not fit: a row passes through shared
 // memory, where it lies as it does around its 16-byte boundaries, so that
 // global memory sees 16-byte accesses (but for the row's ends) while the
-// threads take single elements, element t + i * blockDim for thread t.  A
-// block stays for several rows: the weights stay in registers, and the next
+// threads take words of E elements, word t + i * kWidth for thread t.  A block
+// stays for several rows: the weights stay in registers, and the next
 // row is copied in asynchronously while one is computed.
-constexpr int kStagedBlocks = 152 * 6;
+// Blocks of a multiprocessor, all resident at once, as far as registers go.
+__host__ __device__ constexpr int staged_resident(int width, int words) {
+  return width > 128 ? 2 : words > 12 ? 5 : 6;
+}
 
 __host__ __device__ inline int staged_buffer(int cols, int size) { return (cols * size + 15) / 16 * 16 + 16; }
 
@@ -367,22 +362,20 @@ __host__ __device__ inline int staged_buffer(int cols, int size) { return (cols 
 // first .. end - 1 belong to it whole.
 struct Lines {
   uint8_t* line;                 // global, 16-byte aligned
-  int shift, bytes, first, end;
-  __device__ Lines(const void* row, int n) {
+  int shift, first, end;
+  __device__ __forceinline__ Lines(const void* row, int bytes) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(row);
     shift = static_cast<int>(at & 15);
     line = reinterpret_cast<uint8_t*>(at - shift);
-    bytes = n;
-    first = shift ? 1 : 0;
-    end = (shift + n) >> 4;
+    first = (shift + 15) >> 4;
+    end = (shift + bytes) >> 4;
   }
-  // Byte offset of the element of the row's ends that thread t < 32 moves
-  // (lanes 0-15 those in front of the whole lines, 16-31 those behind), or -1.
-  __device__ __forceinline__ int edge(int t, int size) const {
-    const int lines_from = 16 * first, lines_to = 16 * (end > first ? end : first);
-    const int at = t < 16 ? shift + t * size : lines_to + (t - 16) * size;
-    const int stop = t < 16 ? min(lines_from, shift + bytes) : shift + bytes;
-    return t < 32 && at < stop ? at : -1;
+  // Byte offset of the element of the row's ends that lane l moves (0-15 those
+  // in front of the whole lines, 16-31 those behind), or -1.  Rows have at
+  // least one whole line.
+  __device__ __forceinline__ int edge(int l, int size, int bytes) const {
+    const int at = l < 16 ? shift + l * size : 16 * end + (l - 16) * size;
+    return at < (l < 16 ? 16 * first : shift + bytes) ? at : -1;
   }
 };
 
@@ -392,118 +385,201 @@ __device__ __forceinline__ void copy_async_16(uint8_t* shared, const uint8_t* gl
                : "memory");
 }
 
-template <typename T, int kOut, int R>
-__global__ void __launch_bounds__(256) mla_norm_staged_kernel(const NormParams p) {
+// R words of each thread between registers and a row in shared memory that
+// starts on any element; words that the row does not have are skipped (n: the
+// elements from the thread's first word to the row's end).
+template <typename T, int kWidth, int R>
+__device__ __forceinline__ void read_words(uint32_t (&w)[R], const uint8_t* row, int n) {
+  constexpr int E = Word<T>::kElems;
+  if (E == 1 || !(reinterpret_cast<uintptr_t>(row) & 2)) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < R; ++i) w[i] = n > E * kWidth * i ? p[kWidth * i] : 0u;
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + E * threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      w[i] = n > E * kWidth * i ? p[E * kWidth * i] | static_cast<uint32_t>(p[E * kWidth * i + 1]) << 16 : 0u;
+  }
+}
+template <typename T, int kWidth, int R>
+__device__ __forceinline__ void write_words(const uint32_t (&w)[R], uint8_t* row, int n) {
+  constexpr int E = Word<T>::kElems;
+  if (E == 1 || !(reinterpret_cast<uintptr_t>(row) & 2)) {
+    uint32_t* p = reinterpret_cast<uint32_t*>(row) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (n > E * kWidth * i) p[kWidth * i] = w[i];
+  } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(row) + E * threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (n > E * kWidth * i) {
+        p[E * kWidth * i] = static_cast<uint16_t>(w[i]);
+        p[E * kWidth * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+      }
+  }
+}
+
+// Every buffer has a spare element behind the row's place, zero in the input
+// buffers, so that the last word of a row of 16-bit elements may be half.
+template <typename T, int kOut, int kWidth, int R>
+__global__ void __launch_bounds__(kWidth, staged_resident(kWidth, R)) mla_norm_staged_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t buffers[];
   __shared__ float slots[2][32];
-  constexpr int kSize = sizeof(T), kOutSize = kOut == MLA_NORM_OUT_SAME ? kSize : 1;
+  constexpr int E = Word<T>::kElems, kSize = sizeof(T), kOutSize = kOut == MLA_NORM_OUT_SAME ? kSize : 1;
   using Bits = typename std::conditional<kSize == 2, uint16_t, uint32_t>::type;
-  const int t = threadIdx.x, width = blockDim.x, buffer = staged_buffer(p.cols, kSize);
+  const int t = threadIdx.x, bytes = p.cols * kSize, buffer = staged_buffer(p.cols, kSize);
+  const int n = p.cols - E * t;   // elements from the thread's first word to the row's end
   uint8_t* const sum_s = buffers + (p.residual ? 4 : 2) * buffer;   // residual_out's lines, then out's
   uint8_t* const out_s = sum_s + (p.residual_out ? buffer : 0);
   auto stage = [&](int s, int which) { return buffers + (p.residual ? 2 * s + which : s) * buffer; };
-  auto x_row = [&](int64_t row) { return Lines(static_cast<const T*>(p.x) + row * p.x_stride, p.cols * kSize); };
-  auto r_row = [&](int64_t row) {
-    return Lines(static_cast<const T*>(p.residual) + row * p.residual_stride, p.cols * kSize);
-  };
   // The lines of a row into a buffer; its ends' elements into a register.
   auto fetch = [&](const Lines& l, uint8_t* to) {
-    for (int i = l.first + t; i < l.end; i += width) copy_async_16(to + 16 * i, l.line + 16 * i);
-    const int at = l.edge(t, kSize);
-    return at >= 0 ? *reinterpret_cast<const Bits*>(l.line + at) : static_cast<Bits>(0);
+    const uint8_t* from = l.line + 16 * t;
+    to += 16 * t;
+#pragma unroll
+    for (int i = 0; i <= R / 4; ++i)   // 4 R kWidth bytes at most
+      if (t + kWidth * i >= l.first && t + kWidth * i < l.end) copy_async_16(to + 16 * kWidth * i, from + 16 * kWidth * i);
+    Bits v = 0;
+    if (t < 32) {
+      const int at = l.edge(t, kSize, bytes);
+      if (at >= 0) v = *reinterpret_cast<const Bits*>(l.line + at);
+    }
+    return v;
   };
   auto put_edge = [&](const Lines& l, uint8_t* to, Bits v) {
-    const int at = l.edge(t, kSize);
+    if (t >= 32) return;
+    const int at = l.edge(t, kSize, bytes);
     if (at >= 0) *reinterpret_cast<Bits*>(to + at) = v;
+    if (t == 0) *reinterpret_cast<Bits*>(to + l.shift + bytes) = 0;
   };
   auto flush = [&](const Lines& l, const uint8_t* from, auto size) {
-    constexpr int n = decltype(size)::value;
-    using B = typename std::conditional<n == 1, uint8_t, typename std::conditional<n == 2, uint16_t, uint32_t>::type>::type;
-    for (int i = l.first + t; i < l.end; i += width)
-      *reinterpret_cast<uint4*>(l.line + 16 * i) = *reinterpret_cast<const uint4*>(from + 16 * i);
-    const int at = l.edge(t, n);
-    if (at >= 0) *reinterpret_cast<B*>(l.line + at) = *reinterpret_cast<const B*>(from + at);
+    constexpr int z = decltype(size)::value;
+    using B = typename std::conditional<z == 1, uint8_t, typename std::conditional<z == 2, uint16_t, uint32_t>::type>::type;
+    uint8_t* to = l.line + 16 * t;
+#pragma unroll
+    for (int i = 0; i <= R * z / (4 * kSize); ++i)
+      if (t + kWidth * i >= l.first && t + kWidth * i < l.end)
+        *reinterpret_cast<uint4*>(to + 16 * kWidth * i) = *reinterpret_cast<const uint4*>(from + 16 * (t + kWidth * i));
+    if (t < 32) {
+      const int at = l.edge(t, z, p.cols * z);
+      if (at >= 0) *reinterpret_cast<B*>(l.line + at) = *reinterpret_cast<const B*>(from + at);
+    }
   };
   after_predecessor();
-  float w[R];
+  float w[R * E];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int c = t + i * width;
+  for (int i = 0; i < R * E; ++i) {
+    const int c = (t + i / E * kWidth) * E + i % E;
     w[i] = p.weight && c < p.cols ? to_f32(static_cast<const T*>(p.weight)[c]) : 1.f;
   }
-  Bits x_edge = 0, r_edge = 0;
-  auto prefetch = [&](int64_t row, int s) {
-    if (row < p.rows) {
-      x_edge = fetch(x_row(row), stage(s, 0));
-      if (p.residual) r_edge = fetch(r_row(row), stage(s, 1));
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  prefetch(blockIdx.x, 0);
+  // the rows' addresses, a step of gridDim rows from one to the next
+  const int64_t row0 = blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + row0 * p.x_stride;
+  const T* r = static_cast<const T*>(p.residual) + row0 * p.residual_stride;
+  T* ro = static_cast<T*>(p.residual_out) + row0 * p.residual_out_stride;
+  uint8_t* y = static_cast<uint8_t*>(p.out) + row0 * p.out_stride * kOutSize;
+  const int64_t x_step = gridDim.x * p.x_stride, r_step = gridDim.x * p.residual_stride;
+  const int64_t ro_step = gridDim.x * p.residual_out_stride, y_step = gridDim.x * p.out_stride * kOutSize;
+  Lines xl(x, bytes), rl(r, bytes);
+  Bits x_edge = fetch(xl, stage(0, 0)), r_edge = p.residual ? fetch(rl, stage(0, 1)) : static_cast<Bits>(0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
   int s = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, s ^= 1) {
-    const Lines xl = x_row(row), rl = r_row(row);
+  for (int64_t row = row0; row < p.rows; row += gridDim.x, s ^= 1, ro += ro_step, y += y_step) {
+    const int x_shift = xl.shift, r_shift = rl.shift;
     put_edge(xl, stage(s, 0), x_edge);
     if (p.residual) put_edge(rl, stage(s, 1), r_edge);
-    // the other buffers were read before the last row's sums met
-    prefetch(row + gridDim.x, s ^ 1);
+    // the next row, into buffers that were read before the last row's sums met
+    if (row + gridDim.x < p.rows) {
+      x += x_step;
+      xl = Lines(x, bytes);
+      x_edge = fetch(xl, stage(s ^ 1, 0));
+      if (p.residual) {
+        r += r_step;
+        rl = Lines(r, bytes);
+        r_edge = fetch(rl, stage(s ^ 1, 1));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
-    const Bits* xs = reinterpret_cast<const Bits*>(stage(s, 0) + xl.shift) + t;
-    const Bits* rs = reinterpret_cast<const Bits*>(stage(s, 1) + rl.shift) + t;
-    const Lines ol(static_cast<T*>(p.residual_out) + row * p.residual_out_stride, p.cols * kSize);
-    T* sums = reinterpret_cast<T*>(sum_s + ol.shift) + t;
-    float h[R];
+    uint32_t words[R];
+    float h[R * E];
+    read_words<T, kWidth>(words, stage(s, 0) + x_shift, n);
+#pragma unroll
+    for (int i = 0; i < R; ++i) Word<T>::get(words[i], h + i * E);
+    if (p.residual) {
+      read_words<T, kWidth>(words, stage(s, 1) + r_shift, n);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float b[E];
+        Word<T>::get(words[i], b);
+#pragma unroll
+        for (int j = 0; j < E; ++j) h[i * E + j] += b[j];
+      }
+    }
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      h[i] = 0.f;
-      if (t + i * width < p.cols) {
-        const Bits xb = xs[i * width];
-        h[i] = to_f32(*reinterpret_cast<const T*>(&xb));
-        if (p.residual) {
-          const Bits rb = rs[i * width];
-          h[i] += to_f32(*reinterpret_cast<const T*>(&rb));
-        }
-        if (p.residual_out) sums[i * width] = from_f32<T>(h[i]);
-      }
-      sum = fmaf(h[i], h[i], sum);
+    for (int i = 0; i < R * E; ++i) sum = fmaf(h[i], h[i], sum);
+    const Lines ol(ro, bytes);
+    if (p.residual_out) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) words[i] = Word<T>::put(h + i * E);
+      write_words<T, kWidth>(words, sum_s + ol.shift, n);
     }
-    const float rstd = rsqrtf(row_reduce<0, false>(sum, slots[0]) / static_cast<float>(p.cols) + p.eps);
+    const float rstd = rsqrtf(row_reduce<0, false>(sum, slots[0]) * p.inv_cols + p.eps);
     if (p.residual_out) flush(ol, sum_s, std::integral_constant<int, kSize>());
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      h[i] = t + i * width < p.cols ? h[i] * rstd * w[i] : 0.f;   // 0 where there is none: not 0 * inf
+    for (int i = 0; i < R * E; ++i) {
+      h[i] = h[i] * rstd * w[i];   // elements that are not there: 0, or like all others where rstd is not finite
       if (kOut == MLA_NORM_OUT_E4M3_ROW) amax = max_nan(amax, fabsf(h[i]));
     }
-    const Lines yl(static_cast<uint8_t*>(p.out) + row * p.out_stride * kOutSize, p.cols * kOutSize);
+    const Lines yl(y, p.cols * kOutSize);
     uint8_t* ys = out_s + yl.shift;
-    float inv = 1.f;
-    if (kOut == MLA_NORM_OUT_E4M3_ROW) {
-      const float scale = max_nan(row_reduce<0, true>(amax, slots[1]) / 448.f, kMinRowScale);
-      inv = 1.f / scale;
-      if (t == 0) static_cast<float*>(p.scales)[row] = scale;
-    }
+    if (kOut == MLA_NORM_OUT_SAME) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int c = t + i * width;
-      if (kOut == MLA_NORM_OUT_SAME) {
-        if (c < p.cols) reinterpret_cast<T*>(ys)[c] = from_f32<T>(h[i]);
-        continue;
+      for (int i = 0; i < R; ++i) words[i] = Word<T>::put(h + i * E);
+      write_words<T, kWidth>(words, ys, n);
+    } else {
+      float inv = 1.f;
+      if (kOut == MLA_NORM_OUT_E4M3_ROW) {
+        const float scale = max_nan(row_reduce<0, true>(amax, slots[1]) * (1.f / 448.f), kMinRowScale);
+        inv = 1.f / scale;
+        if (t == 0) static_cast<float*>(p.scales)[row] = scale;
       }
-      bool some = true;
-      if (kOut == MLA_NORM_OUT_E4M3_E8M0) {   // a group is a warp's elements
-        const float a = lanes_max(fabsf(h[i]));
-        some = a > 0.f;
-        const uint32_t byte = e4m3_scale_byte(a);
-        inv = scale_byte_reciprocal(byte);
-        if (c < p.cols && (t & 31) == 0)
-          static_cast<uint8_t*>(p.scales)[row * p.scale_stride + (c >> 5)] = static_cast<uint8_t>(byte);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float* v = h + i * E;
+        bool some = true;
+        if (kOut == MLA_NORM_OUT_E4M3_E8M0) {   // a group is 32 / E neighbouring lanes' words
+          float a = 0.f;
+#pragma unroll
+          for (int j = 0; j < E; ++j) a = fmaxf(a, fabsf(v[j]));
+#pragma unroll
+          for (int o = 16 / E; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          some = a > 0.f;
+          const uint32_t byte = e4m3_scale_byte(a);
+          inv = scale_byte_reciprocal(byte);
+          if (n > E * kWidth * i && t % (32 / E) == 0)
+            static_cast<uint8_t*>(p.scales)[row * p.scale_stride + (t + kWidth * i) * E / 32] = static_cast<uint8_t>(byte);
+        }
+        words[i] = e4m3x2(v[0] * inv, v[E - 1] * inv);
+        if (!some) words[i] &= 0x7F7Fu;   // zeros without their signs (or NaN)
       }
-      uint32_t code = e4m3x2(h[i] * inv, 0.f);
-      if (!some) code &= 0x7Fu;   // zeros without their signs (or NaN)
-      if (c < p.cols) ys[c] = static_cast<uint8_t>(code);
+      if (E == 2 && !(reinterpret_cast<uintptr_t>(ys) & 1)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (n > E * kWidth * i) reinterpret_cast<uint16_t*>(ys)[t + kWidth * i] = static_cast<uint16_t>(words[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (n > E * kWidth * i) {
+            ys[E * (t + kWidth * i)] = static_cast<uint8_t>(words[i]);
+            if (E == 2) ys[E * (t + kWidth * i) + 1] = static_cast<uint8_t>(words[i] >> 8);
+          }
+      }
     }
     __syncthreads();
     flush(yl, out_s, std::integral_constant<int, kOutSize>());
@@ -527,17 +603,19 @@ cudaError_t launch_one(const NormParams& p, int threads, cudaStream_t stream) {
                           : launch(mla_norm_kernel<T, kOut, R, 0, 1024>, threads);
 }
 
-template <typename T, int kOut, int R>
-cudaError_t launch_staged(const NormParams& p, int threads, cudaStream_t stream) {
+template <typename T, int kOut, int kWidth, int R>
+cudaError_t launch_staged(const NormParams& p, cudaStream_t stream) {
   const int buffer = staged_buffer(p.cols, sizeof(T));
   const int smem = buffer * ((p.residual ? 4 : 2) + (p.residual_out ? 1 : 0)) +
                    staged_buffer(p.cols, kOut == MLA_NORM_OUT_SAME ? sizeof(T) : 1);
-  auto kernel = mla_norm_staged_kernel<T, kOut, R>;
+  auto kernel = mla_norm_staged_kernel<T, kOut, kWidth, R>;
   if (smem > 48 * 1024) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
   }
-  return launch_dependent(kernel, p.rows < kStagedBlocks ? p.rows : kStagedBlocks, threads, smem, stream, p);
+  const int fit = 232448 / (smem + 2048);   // and as far as shared memory goes
+  const int blocks = 152 * (fit < staged_resident(kWidth, R) ? fit : staged_resident(kWidth, R));
+  return launch_dependent(kernel, p.rows < blocks ? p.rows : blocks, kWidth, smem, stream, p);
 }
 
 template <typename T, int kOut>
@@ -564,19 +642,18 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
     if (n <= 4096) return launch_one<T, kOut, false, 4, 0>(p, threads(n, 4), stream);
     return launch_one<T, kOut, false, kMost, 0>(p, threads(n, kMost), stream);
   }
-  if (many && p.cols > 256 && p.cols * sizeof(T) <= 16384) {
-    const int t = p.cols <= 4096 ? 128 : 256;
-    if (p.cols <= 8 * t) return launch_staged<T, kOut, 8>(p, t, stream);
-    if (p.cols <= 16 * t) return launch_staged<T, kOut, 16>(p, t, stream);
-    if (p.cols <= 24 * t) return launch_staged<T, kOut, 24>(p, t, stream);
-    return launch_staged<T, kOut, 32>(p, t, stream);
+  const int words = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;
+  if (many && words > 128 && words <= 4096) {
+    if (words <= 512) return launch_staged<T, kOut, 128, 4>(p, stream);
+    if (words <= 1024) return launch_staged<T, kOut, 128, 8>(p, stream);
+    if (words <= 1536) return launch_staged<T, kOut, 128, 12>(p, stream);
+    if (words <= 2048) return launch_staged<T, kOut, 128, 16>(p, stream);
+    return launch_staged<T, kOut, 256, 16>(p, stream);
   }
   constexpr int kMost = sizeof(T) == 4 ? 32 : 16;   // words of a thread
-  const int n = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;
-  if (n <= 128) return launch_one<T, kOut, true, 4, 32>(p, 0, stream);
-  if (n <= 4096 && !many) return launch_one<T, kOut, true, 4, 0>(p, threads(n, 4), stream);
-  if (n <= 16384) return launch_one<T, kOut, true, 16, 0>(p, threads(n, 16), stream);
-  return launch_one<T, kOut, true, kMost, 0>(p, threads(n, kMost), stream);
+  if (words <= 128) return launch_one<T, kOut, true, 4, 32>(p, 0, stream);
+  if (words <= 4096) return launch_one<T, kOut, true, 4, 0>(p, threads(words, 4), stream);
+  return launch_one<T, kOut, true, kMost, 0>(p, threads(words, kMost), stream);
 }
 
 template <typename T>
