@@ -17,8 +17,10 @@ namespace mla {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 4;       // heads a thread has in flight
+constexpr int kRopeThreads = 128;
+constexpr int kRopeHeads = 5;       // heads a thread has in flight
+constexpr int kRopeMostHeads = 10;  // and takes altogether
+constexpr int64_t kRopeFill = 152 * 2048;
 
 // n / d for n < 2^31, as a multiplication (round-up method).
 struct Divider {
@@ -145,12 +147,15 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   const int per_turn = kVec == 1 ? 2 : halves ? 2 * kVec : kVec;   // elements of a rotated unit
   const int turn_units = p.dim / per_turn;
   const int units = turn_units + (p.x == p.out ? 0 : (p.head_dim - p.dim) / kVec);
-  // threads that share a token's heads: as many as there are heads while
-  // that leaves the multiprocessors short of threads, then one for each
-  // kRopeHeads
+  // threads that share a token's heads: the fewer, the more heads use a
+  // thread's cosines, as long as there are threads to fill the
+  // multiprocessors
   const int64_t one = static_cast<int64_t>(p.tokens) * units;
-  const int few = (p.heads + kRopeHeads - 1) / kRopeHeads;
-  const int groups = one * few < 152 * 1024 ? p.heads : few;
+  int groups = p.heads;
+  for (int per_thread = 2; per_thread <= kRopeMostHeads; ++per_thread) {
+    const int g = (p.heads + per_thread - 1) / per_thread;
+    if (one * g >= kRopeFill) groups = g;
+  }
   const int64_t per_token = static_cast<int64_t>(units) * groups;
   int64_t tokens = per_token < kRopeThreads ? kRopeThreads / per_token : 1;
   const int split = per_token > kRopeThreads ? static_cast<int>((per_token + kRopeThreads - 1) / kRopeThreads) : 1;
