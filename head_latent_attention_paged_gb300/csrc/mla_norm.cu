@@ -15,6 +15,7 @@
 #include "mla_layer_internal.h"
 #include "mla_quant.cuh"
 #include "mla_types.cuh"
+#include "sm103_ptx.cuh"
 
 namespace mla {
 
@@ -379,12 +380,6 @@ struct Lines {
   }
 };
 
-__device__ __forceinline__ void copy_async_16(uint8_t* shared, const uint8_t* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))),
-               "l"(global)
-               : "memory");
-}
-
 // R words of each thread between registers and a row in shared memory that
 // starts on any element; words that the row does not have are skipped (n: the
 // elements from the thread's first word to the row's end).
@@ -440,7 +435,7 @@ __global__ void __launch_bounds__(kWidth, staged_resident(kWidth, R)) mla_norm_s
     to += 16 * t;
 #pragma unroll
     for (int i = 0; i <= R / 4; ++i)   // 4 R kWidth bytes at most
-      if (t + kWidth * i >= l.first && t + kWidth * i < l.end) copy_async_16(to + 16 * kWidth * i, from + 16 * kWidth * i);
+      if (t + kWidth * i >= l.first && t + kWidth * i < l.end) cp_async_16(to + 16 * kWidth * i, from + 16 * kWidth * i, 16);
     Bits v = 0;
     if (t < 32) {
       const int at = l.edge(t, kSize, bytes);
@@ -484,7 +479,7 @@ __global__ void __launch_bounds__(kWidth, staged_resident(kWidth, R)) mla_norm_s
   const int64_t ro_step = gridDim.x * p.residual_out_stride, y_step = gridDim.x * p.out_stride * kOutSize;
   Lines xl(x, bytes), rl(r, bytes);
   Bits x_edge = fetch(xl, stage(0, 0)), r_edge = p.residual ? fetch(rl, stage(0, 1)) : static_cast<Bits>(0);
-  asm volatile("cp.async.commit_group;" ::: "memory");
+  cp_async_commit();
   int s = 0;
   for (int64_t row = row0; row < p.rows; row += gridDim.x, s ^= 1, ro += ro_step, y += y_step) {
     const int x_shift = xl.shift, r_shift = rl.shift;
@@ -501,8 +496,8 @@ __global__ void __launch_bounds__(kWidth, staged_resident(kWidth, R)) mla_norm_s
         r_edge = fetch(rl, stage(s ^ 1, 1));
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    cp_async_commit();
+    cp_async_wait<1>();
     __syncthreads();
     uint32_t words[R];
     float h[R * E];

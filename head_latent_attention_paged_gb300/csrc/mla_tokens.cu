@@ -5,8 +5,11 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "mla_layer_internal.h"
 #include "mla_quant.cuh"
+#include "sm103_ptx.cuh"
 #include "mla_turn.cuh"
 
 namespace mla {
@@ -16,9 +19,9 @@ namespace {
 constexpr int kTokenWarps = 4;
 // Tokens a warp takes one after another, at most: the append's warps keep the
 // norm's weights and the rotation's table, the gather's only their slots (100,011
-// rows into FP8: 4 43.2, 8 39.5, 16 38.1, 32 41.2 us; 204,800 rows out of FP8: 2
+// rows into FP8: 8 37.4, 16 37.8 us, into bf16 37.6, 39.3; 204,800 rows out of FP8: 2
 // 66.9, 4 61.4, 8 62.8, 16 66.4 us).
-constexpr int kAppendChunk = 16, kGatherChunk = 4;
+constexpr int kAppendChunk = 8, kGatherChunk = 4;
 
 // The slot of token t in the pool: -1 where the token is to be left alone
 // (negative position), -2 where it has none (which is reported).
@@ -79,6 +82,16 @@ __device__ __forceinline__ uint32_t pack_e2m1(float2 v) {
       : "f"(v.y), "f"(v.x));
   return two;
 }
+__device__ __forceinline__ uint32_t pack_e2m1(const float2 (&v)[4]) {   // eight, in order from the low nibble
+  uint32_t w;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(w)
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+  return w;
+}
 
 // The warp's row: lane l holds latent values 8 l .. 8 l + 7 and 256 + 8 l ..,
 // and key values 2 l and 2 l + 1.
@@ -94,11 +107,11 @@ __device__ __forceinline__ void load_row(RowWords* r, const uint16_t* src, int l
   r->key = reinterpret_cast<const uint32_t*>(src + kDc)[lane];
 }
 
-// Maximum over aligned sets of `lanes` lanes.
-__device__ __forceinline__ float lanes_max(float v, int lanes) {
+// Maximum over aligned sets of kLanes lanes.
+template <int kLanes>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (o < lanes) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -116,43 +129,85 @@ __device__ __forceinline__ float abs_max(const float2 (&v)[4]) {
 
 constexpr int kStageBytes = 640;   // a 594-byte row behind a shift of at most 14
 
-// One warp per token at a time.  Bound by memory (a 1,152-byte row read, a
-// 1,152-, 594- or 324-byte row written) where the instructions for a row's
-// norm, rotation and codes are few enough: every value stays in its lane, one
-// shuffle reduction gives the norm, the cosine and sine are one pair per lane,
-// arithmetic goes in pairs, slots are found one token per lane, and the next
-// row is on its way while one is computed.
-template <int kKv>
+// kBytes of a row, laid out in shared memory as they lie around the row's
+// 16-byte boundaries (`shift` bytes into the first line), to global memory:
+// whole 16-byte lines, and the row's ends in units of kUnit bytes, which
+// divides its address.  A warp writes a row.
+template <int kBytes, int kUnit>
+__device__ __forceinline__ void write_row(uint8_t* dst, const uint8_t* stage, int shift, int lane) {
+  using Unit = typename std::conditional<kUnit == 2, uint16_t, uint32_t>::type;
+  constexpr int kSide = 16 / kUnit;                       // lanes for each end
+  const int first = (shift + 15) >> 4, end = (shift + kBytes) >> 4;   // whole lines: kBytes / 16 or one less
+  uint4* lines = reinterpret_cast<uint4*>(dst - shift);
+  const uint4* from = reinterpret_cast<const uint4*>(stage);
+  if (lane >= first && lane < end) lines[lane] = from[lane];
+  if (kBytes > 32 * 16 && 32 + lane < end) lines[32 + lane] = from[32 + lane];
+  const int at = lane < kSide ? shift + kUnit * lane : 16 * end + kUnit * (lane - kSide);
+  if (lane < 2 * kSide && at < (lane < kSide ? 16 * first : shift + kBytes))
+    *reinterpret_cast<Unit*>(dst - shift + at) = *reinterpret_cast<const Unit*>(stage + at);
+}
+
+// One warp per token at a time.  A row costs 1,152 bytes read and 1,152, 594
+// or 324 written; what bounds the kernel beside those is the number of its
+// instructions (about 240 a row into FP8).  So every value stays in its lane,
+// one shuffle reduction gives the norm, the cosine and sine are one pair per
+// lane, arithmetic goes in pairs, slots are found one token per lane, the next
+// rows are on their way while one is computed (copied asynchronously into the
+// lane's own places in a ring in shared memory: loads into registers were
+// moved behind the arithmetic by the compiler, 37 -> 60 us for 100,011 rows),
+// and norm and rotation are compiled in or out.
+constexpr int kRing = 4;   // rows of a warp on their way or in use
+
+template <int kKv, bool kNorm, bool kRotate>
 __global__ void __launch_bounds__(32 * kTokenWarps, 7)
     mla_append_tokens_kernel(const __grid_constant__ AppendTokensParams p, const int32_t chunk) {
-  __shared__ __align__(16) uint8_t stage_s[kKv == MLA_KV_FP8_E4M3_E8M0 ? kTokenWarps : 1][kStageBytes];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ __align__(16) uint8_t ring_s[kTokenWarps][kRing][kDqk * 2];
+  __shared__ __align__(16) uint8_t stage_s[kKv == MLA_KV_BF16 ? 1 : kTokenWarps][kStageBytes];
+  const int lane = threadIdx.x & 31;
   after_predecessor();
   const WarpTokens tok = warp_tokens(p.t, chunk, lane);
   if (tok.count <= 0) return;
-  const uint16_t* src = p.rows + tok.first * p.row_stride;
-  RowWords next;
-  load_row(&next, src, lane);
-  const uint64_t turns = p.rotate ? p.table.turns[lane] : 0;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(p.rows + tok.first * p.row_stride) + 16 * lane;
+  uint8_t* const ring = ring_s[threadIdx.x >> 5][0] + 16 * lane;
+  auto fetch = [&](int j) {   // each lane the pieces that it will read
+    if (j < tok.count) {
+      uint8_t* to = ring + (j % kRing) * (kDqk * 2);
+      cp_async_16(to, src, 16);
+      cp_async_16(to + 512, src + 512, 16);
+      cp_async_4(to + 2 * kDc - 12 * lane, src + 2 * kDc - 12 * lane);
+      src += 2 * p.row_stride;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int j = 0; j < kRing - 1; ++j) fetch(j);
+  const uint64_t turns = kRotate ? p.table.turns[lane] : 0;
+  const float amplitude = p.table.amplitude;
+  const bool halves = p.table.halves != 0;
   float2 w[8];
-  if (p.weight) {
+  if (kNorm) {
     const uint4 a = reinterpret_cast<const uint4*>(p.weight)[lane], b = reinterpret_cast<const uint4*>(p.weight)[32 + lane];
     const uint32_t words[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = make_float2(bf16_lo(words[i]), bf16_hi(words[i]));
   }
+  uint8_t* const stage = stage_s[kKv == MLA_KV_BF16 ? 0 : threadIdx.x >> 5];
   for (int j = 0; j < tok.count; ++j) {
-    const RowWords row = next;
-    src += p.row_stride;
-    if (j + 1 < tok.count) load_row(&next, src, lane);
+    fetch(j + kRing - 1);
     const int32_t pos = __shfl_sync(0xffffffffu, tok.pos, j), at = __shfl_sync(0xffffffffu, tok.slot, j);
+    cp_async_wait<kRing - 1>();
     if (at < 0) continue;
     const int64_t slot = at;
+    const uint8_t* in = ring + (j % kRing) * (kDqk * 2);
+    RowWords row;
+    row.a = *reinterpret_cast<const uint4*>(in);
+    row.b = *reinterpret_cast<const uint4*>(in + 512);
+    row.key = *reinterpret_cast<const uint32_t*>(in + 2 * kDc - 12 * lane);
     const uint32_t words[8] = {row.a.x, row.a.y, row.a.z, row.a.w, row.b.x, row.b.y, row.b.z, row.b.w};
     float2 y[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = make_float2(bf16_lo(words[i]), bf16_hi(words[i]));
-    if (p.weight) {
+    if (kNorm) {
       float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum2 = __ffma2_rn(y[i >> 2][i & 3], y[i >> 2][i & 3], sum2);
@@ -165,12 +220,12 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
         y[i >> 2][i & 3] = __fmul2_rn(__fmul2_rn(y[i >> 2][i & 3], make_float2(rstd, rstd)), w[i]);
     }
     float2 k = make_float2(bf16_lo(row.key), bf16_hi(row.key));
-    if (p.rotate) {
+    if (kRotate) {
       float c, s;
       turn_cos_sin(turns, pos, &c, &s);
-      c *= p.table.amplitude;
-      s *= p.table.amplitude;
-      if (p.table.halves) {   // value l of both halves to lane l, and back
+      c *= amplitude;
+      s *= amplitude;
+      if (halves) {   // value l of both halves to lane l, and back
         const float a0 = __shfl_sync(0xffffffffu, k.x, lane >> 1), a1 = __shfl_sync(0xffffffffu, k.y, lane >> 1);
         const float b0 = __shfl_sync(0xffffffffu, k.x, 16 + (lane >> 1)), b1 = __shfl_sync(0xffffffffu, k.y, 16 + (lane >> 1));
         const float a = lane & 1 ? a1 : a0, b = lane & 1 ? b1 : b0;
@@ -186,22 +241,22 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
     if (kKv == MLA_KV_BF16) {
       uint8_t* dst = p.kv + slot * (kDqk * 2);
       uint4 oa = row.a, ob = row.b;   // as they came without a norm
-      if (p.weight) {
+      if (kNorm) {
         oa = make_uint4(pack_bf16(y[0][0]), pack_bf16(y[0][1]), pack_bf16(y[0][2]), pack_bf16(y[0][3]));
         ob = make_uint4(pack_bf16(y[1][0]), pack_bf16(y[1][1]), pack_bf16(y[1][2]), pack_bf16(y[1][3]));
       }
       reinterpret_cast<uint4*>(dst)[lane] = oa;
       reinterpret_cast<uint4*>(dst)[32 + lane] = ob;
-      reinterpret_cast<uint32_t*>(dst + kDc * 2)[lane] = p.rotate ? pack_bf16(k) : row.key;
+      reinterpret_cast<uint32_t*>(dst + kDc * 2)[lane] = kRotate ? pack_bf16(k) : row.key;
       continue;
     }
     constexpr bool kFp8 = kKv == MLA_KV_FP8_E4M3_E8M0;
-    // a group is 4 lanes of 8 values and 16 lanes of 2 (FP8), 2 and 8 (FP4)
-    const float m[2] = {lanes_max(abs_max(y[0]), kFp8 ? 4 : 2), lanes_max(abs_max(y[1]), kFp8 ? 4 : 2)};
-    const float mk = lanes_max(max3(fabsf(k.x), fabsf(k.y), 0.f), kFp8 ? 16 : 8);
-    const uint32_t e[2] = {kFp8 ? e4m3_scale_byte(m[0]) : e2m1_scale_byte(m[0]),
-                           kFp8 ? e4m3_scale_byte(m[1]) : e2m1_scale_byte(m[1])};
-    const uint32_t ek = kFp8 ? e4m3_scale_byte(mk) : e2m1_scale_byte(mk);
+    constexpr int kGroup = kFp8 ? 4 : 2;   // lanes of a group of the latent; of the key four times as many
+    const float m[2] = {lanes_max<kGroup>(abs_max(y[0])), lanes_max<kGroup>(abs_max(y[1]))};
+    const float mk = lanes_max<4 * kGroup>(max3(fabsf(k.x), fabsf(k.y), 0.f));
+    uint32_t e[2] = {kFp8 ? e4m3_scale_byte(m[0]) : e2m1_scale_byte(m[0]),
+                     kFp8 ? e4m3_scale_byte(m[1]) : e2m1_scale_byte(m[1])};
+    uint32_t ek = kFp8 ? e4m3_scale_byte(mk) : e2m1_scale_byte(mk);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float inv = scale_byte_reciprocal(e[h]);
@@ -210,80 +265,59 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
     }
     const float ik = scale_byte_reciprocal(ek);
     const float2 yk = __fmul2_rn(k, make_float2(ik, ik));
+    constexpr int kRow = kFp8 ? kFp8RowBytes : kFp4RowBytes, kCodes = kFp8 ? kDqk : kFp4CodeBytes;
+    uint8_t* dst = p.kv + slot * kRow;
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15);   // even; a multiple of 4 in FP4
+    uint8_t* st = stage + shift;
     // A group of zeros has codes 0 whatever their signs; a NaN stays one.
+    const bool zeros = fminf(fminf(m[0], m[1]), mk) == 0.f;
     if (kFp8) {
-      uint32_t code[2][4];
+      uint32_t code[9];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) code[i >> 2][i & 3] = pack_e4m3(y[i >> 2][i & 3]);
-      uint32_t kcode = pack_e4m3(yk);
-      // with amax 0 every code is a signed zero (0x00, 0x80) or NaN (0x7F, 0xFF)
+      for (int i = 0; i < 8; ++i) code[i] = pack_e4m3(y[i >> 2][i & 3]);
+      code[8] = pack_e4m3(yk);
+      if (zeros) {   // codes there are signed zeros (0x00, 0x80) or NaN (0x7F, 0xFF)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (m[h] == 0.f)
-          for (int i = 0; i < 4; ++i) code[h][i] &= 0x7F7Fu;
-      if (mk == 0.f) kcode &= 0x7F7Fu;
-      // The row starts on any even address: it is laid out in shared memory at
-      // the same place within 16 bytes and leaves in 16-byte stores, its ends
-      // in pairs of bytes.
-      uint8_t* dst = p.kv + slot * kFp8RowBytes;
-      const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15);
-      uint8_t* st = stage_s[warp];
-      uint16_t* st2 = reinterpret_cast<uint16_t*>(st + shift);
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        st2[4 * lane + i] = static_cast<uint16_t>(code[0][i]);
-        st2[128 + 4 * lane + i] = static_cast<uint16_t>(code[1][i]);
+        for (int i = 0; i < 9; ++i)
+          if ((i < 8 ? m[i >> 2 & 1] : mk) == 0.f) code[i] &= 0x7F7Fu;
       }
-      st2[256 + lane] = static_cast<uint16_t>(kcode);
-      if ((lane & 3) == 0) {
-        st[shift + kDqk + (lane >> 2)] = static_cast<uint8_t>(e[0]);
-        st[shift + kDqk + 8 + (lane >> 2)] = static_cast<uint8_t>(e[1]);
-      }
-      if ((lane & 15) == 0) st[shift + kDqk + 16 + (lane >> 4)] = static_cast<uint8_t>(ek);
       __syncwarp();
-      // pieces first .. end - 1 are whole: 36 or 37 of them
-      const int first = shift ? 1 : 0, end = (shift + kFp8RowBytes) >> 4;
-      uint4* base = reinterpret_cast<uint4*>(dst - shift);
-      const uint4* from = reinterpret_cast<const uint4*>(st);
-      if (lane >= first) base[lane] = from[lane];
-      if (32 + lane < end) base[32 + lane] = from[32 + lane];
-      const int head = (16 * first - shift) >> 1;                            // pairs before them
-      const int tail = (shift + kFp8RowBytes - 16 * end) >> 1;               // and behind
-      const int pair = lane < 8 ? lane : 8 * end - (shift >> 1) + lane - 8;
-      if (lane < 8 ? lane < head : lane - 8 < tail) reinterpret_cast<uint16_t*>(dst)[pair] = st2[pair];
+      uint16_t* st2 = reinterpret_cast<uint16_t*>(st);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) st2[(i >> 2) * 128 + 4 * lane + (i & 3)] = static_cast<uint16_t>(code[i]);
+      st2[256 + lane] = static_cast<uint16_t>(code[8]);
     } else {
-      uint32_t c[2] = {0, 0};
+      uint32_t c[2] = {pack_e2m1(y[0]), pack_e2m1(y[1])}, ck = pack_e2m1(yk);
+      // a sum of magnitudes is NaN where a value is (they are at most 6, or infinite)
+      float nan = fabsf(k.x) + fabsf(k.y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i >> 2] |= pack_e2m1(y[i >> 2][i & 3]) << (8 * (i & 3));
-      uint32_t ck = pack_e2m1(yk);
-      bool nan[2];
+      for (int i = 0; i < 8; ++i) nan += fabsf(y[i >> 2][i & 3].x) + fabsf(y[i >> 2][i & 3].y);
+      if (__any_sync(0xffffffffu, nan != nan || zeros)) {   // rare: NaN groups get the NaN scale
+        bool n[2] = {false, false};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // a sum of magnitudes is NaN where a value is (they are at most 6, so
-        // it is finite otherwise)
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z += fabsf(y[h][i].x) + fabsf(y[h][i].y);
-        nan[h] = z != z;
+        for (int i = 0; i < 8; ++i) n[i >> 2] |= y[i >> 2][i & 3].x != y[i >> 2][i & 3].x || y[i >> 2][i & 3].y != y[i >> 2][i & 3].y;
+        const uint32_t nan0 = __ballot_sync(0xffffffffu, n[0]) >> (lane & ~1) & 3u;
+        const uint32_t nan1 = __ballot_sync(0xffffffffu, n[1]) >> (lane & ~1) & 3u;
+        const uint32_t nank = __ballot_sync(0xffffffffu, k.x != k.x || k.y != k.y) >> (lane & ~7) & 0xFFu;
+        if (m[0] == 0.f) c[0] = 0;
+        if (m[1] == 0.f) c[1] = 0;
+        if (mk == 0.f) ck = 0;
+        if (nan0) e[0] = 255;
+        if (nan1) e[1] = 255;
+        if (nank) ek = 255;
       }
-      // groups with a NaN get the NaN scale
-      const uint32_t nan0 = __ballot_sync(0xffffffffu, nan[0]) >> (lane & ~1) & 3u;
-      const uint32_t nan1 = __ballot_sync(0xffffffffu, nan[1]) >> (lane & ~1) & 3u;
-      const uint32_t nank = __ballot_sync(0xffffffffu, k.x != k.x || k.y != k.y) >> (lane & ~7) & 0xFFu;
-      if (m[0] == 0.f) c[0] = 0;
-      if (m[1] == 0.f) c[1] = 0;
-      if (mk == 0.f) ck = 0;
-      uint8_t* dst = p.kv + slot * kFp4RowBytes;   // rows start on 4 bytes
-      reinterpret_cast<uint32_t*>(dst)[lane] = c[0];
-      reinterpret_cast<uint32_t*>(dst)[32 + lane] = c[1];
-      dst[256 + lane] = static_cast<uint8_t>(ck);
-      if ((lane & 1) == 0) {
-        dst[kFp4CodeBytes + (lane >> 1)] = static_cast<uint8_t>(nan0 ? 255 : e[0]);
-        dst[kFp4CodeBytes + 16 + (lane >> 1)] = static_cast<uint8_t>(nan1 ? 255 : e[1]);
-      }
-      if ((lane & 7) == 0) dst[kFp4CodeBytes + 32 + (lane >> 3)] = static_cast<uint8_t>(nank ? 255 : ek);
+      __syncwarp();
+      reinterpret_cast<uint32_t*>(st)[lane] = c[0];
+      reinterpret_cast<uint32_t*>(st)[32 + lane] = c[1];
+      st[256 + lane] = static_cast<uint8_t>(ck);
     }
+    if (lane % kGroup == 0) {
+      st[kCodes + lane / kGroup] = static_cast<uint8_t>(e[0]);
+      st[kCodes + 32 / kGroup + lane / kGroup] = static_cast<uint8_t>(e[1]);
+    }
+    if (lane % (4 * kGroup) == 0) st[kCodes + 64 / kGroup + lane / (4 * kGroup)] = static_cast<uint8_t>(ek);
+    __syncwarp();
+    write_row<kRow, kFp8 ? 2 : 4>(dst, stage, shift, lane);
   }
 }
 
@@ -423,15 +457,24 @@ int blocks_of(int32_t tokens, int chunk) {
 
 }  // namespace
 
+namespace {
+
+template <int kKv>
+cudaError_t launch_append_into(const AppendTokensParams& p, cudaStream_t stream) {
+  const int chunk = chunk_of(p.t.tokens, kAppendChunk), blocks = blocks_of(p.t.tokens, chunk);
+  auto launch = [&](auto kernel) { return launch_dependent(kernel, blocks, 32 * kTokenWarps, 0, stream, p, chunk); };
+  if (p.weight)
+    return p.rotate ? launch(mla_append_tokens_kernel<kKv, true, true>) : launch(mla_append_tokens_kernel<kKv, true, false>);
+  return p.rotate ? launch(mla_append_tokens_kernel<kKv, false, true>) : launch(mla_append_tokens_kernel<kKv, false, false>);
+}
+
+}  // namespace
+
 cudaError_t launch_append_tokens(const AppendTokensParams& p, cudaStream_t stream) {
   if (p.t.tokens == 0) return cudaSuccess;
-  const int chunk = chunk_of(p.t.tokens, kAppendChunk), blocks = blocks_of(p.t.tokens, chunk);
-  const int threads = 32 * kTokenWarps;
-  if (p.t.kv_dtype == MLA_KV_BF16)
-    return launch_dependent(mla_append_tokens_kernel<MLA_KV_BF16>, blocks, threads, 0, stream, p, chunk);
-  if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0)
-    return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP8_E4M3_E8M0>, blocks, threads, 0, stream, p, chunk);
-  return launch_dependent(mla_append_tokens_kernel<MLA_KV_FP4_E2M1_E8M0>, blocks, threads, 0, stream, p, chunk);
+  if (p.t.kv_dtype == MLA_KV_BF16) return launch_append_into<MLA_KV_BF16>(p, stream);
+  if (p.t.kv_dtype == MLA_KV_FP8_E4M3_E8M0) return launch_append_into<MLA_KV_FP8_E4M3_E8M0>(p, stream);
+  return launch_append_into<MLA_KV_FP4_E2M1_E8M0>(p, stream);
 }
 
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
