@@ -17,10 +17,15 @@ namespace mla {
 
 namespace {
 
+// 32,768 tokens of 20 heads (64 of 256, bf16) and 4,099 of 8 (96 of 128, f32,
+// out of place): 4 heads in flight and up to 12 27.9 and 6.1 us, up to 8 28.3 and
+// 6.1, up to 20 29.0 and 6.1; 5 in flight and up to 10 27.5 and 6.4; 2 and 12 29.5
+// and 6.7; blocks of 256 28.2 and 6.6; cosines shared through shared memory 35
+// and 10.4.
 constexpr int kRopeThreads = 128;
-constexpr int kRopeHeads = 5;       // heads a thread has in flight
-constexpr int kRopeMostHeads = 10;  // and takes altogether
-constexpr int64_t kRopeFill = 152 * 2048;
+constexpr int kRopeHeads = 4;       // heads a thread has in flight
+constexpr int kRopeMostHeads = 12;  // and takes altogether
+constexpr int64_t kRopeFill = 152 * 1024;   // threads to have before they take more
 
 // n / d for n < 2^31, as a multiplication (round-up method).
 struct Divider {

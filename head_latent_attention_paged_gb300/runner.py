@@ -7,9 +7,10 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (MLA_KV_BF16, MLA_KV_FP4_E2M1_E8M0, MLA_KV_FP8_E4M3_E8M0, make_problem,
-               mla_clear_status, mla_combine, mla_decode_plan, mla_decode_run, mla_decode_step,
-               mla_get_status, mla_q_absorb, mla_uv_proj)
+from . import (MLA_KV_BF16, MLA_KV_FP4_E2M1_E8M0, MLA_KV_FP8_E4M3_E8M0, MlaRopePlan,
+               make_norm_problem, make_problem, make_rope_problem, mla_cache_append_tokens,
+               mla_cache_gather, mla_clear_status, mla_combine, mla_decode_plan, mla_decode_run,
+               mla_decode_step, mla_get_status, mla_q_absorb, mla_rms_norm, mla_rope, mla_uv_proj)
 
 
 def to_device_bf16(bits: np.ndarray, device) -> torch.Tensor:
@@ -138,6 +139,112 @@ class DecodeStep:
         """Kernels one step() launches: the decode, then the merge with W_UV,
         behind the prefix pre-pass when the plan has one."""
         return 2 + int(self.plan.prefix_pass)
+
+
+class AttentionLayer:
+    """One MLA layer's attention between hidden states and hidden states, over
+    a paged latent cache that it keeps:
+
+        x = norm(hidden + residual)                      mla_rms_norm
+        q_a || row = x W_qkv_a                           (library product)
+        cache <- norm(c_kv) || rotate(k_rope)            mla_cache_append_tokens
+        q = rotate(norm(q_a) W_q_b)                      mla_rms_norm, mla_rope
+        o = attention of q over the cache                mla_decode_step
+        out = o W_o                                      (library product)
+
+    decode() runs a whole step of `q_len` tokens for each of `batch` requests;
+    prompt() only caches the rows of a prompt's tokens (any mixture of
+    requests), context() reads cached rows back.  Weights are bf16 tensors on
+    the device: hidden_norm [hidden], w_qkv_a [hidden, q_rank + 576], q_norm
+    [q_rank], kv_norm [512], w_q_b [q_rank, H * 256], w_uk [H, 512, 192], w_uv
+    [H, 512, 256], w_o [H * 256, hidden].  Buffers are made once: every call
+    can be captured in a CUDA graph, and calls of one AttentionLayer are
+    ordered on one stream.
+    """
+
+    NOPE, ROPE, HEAD, ROW = 192, 64, 256, 576
+
+    def __init__(self, *, hidden_norm, w_qkv_a, q_norm, kv_norm, w_q_b, w_uk, w_uv, w_o, batch: int,
+                 q_len: int = 1, page_size: int = 64, num_pages: int, max_pages: int,
+                 rope: MlaRopePlan, kv_dtype: int = MLA_KV_BF16, eps: float = 1e-6,
+                 sm_scale: float = 1.0 / 16.0, sm_count: Optional[int] = None):
+        dev = w_qkv_a.device
+        self.device, self.eps, self.rope = dev, float(eps), rope
+        self.B, self.Q, self.H = batch, q_len, int(w_uk.shape[0])
+        self.rows = rows = batch * q_len
+        self.hidden, self.q_rank = int(w_qkv_a.shape[0]), int(w_q_b.shape[0])
+        self.hidden_norm, self.q_norm, self.kv_norm = hidden_norm, q_norm, kv_norm
+        self.w_qkv_a, self.w_q_b, self.w_uk, self.w_uv, self.w_o = w_qkv_a, w_q_b, w_uk, w_uv, w_o
+        if sm_count is None:
+            sm_count = torch.cuda.get_device_properties(dev).multi_processor_count
+        row_bytes = {MLA_KV_BF16: 2 * self.ROW, MLA_KV_FP8_E4M3_E8M0: 594, MLA_KV_FP4_E2M1_E8M0: 324}[kv_dtype]
+        self.cache = torch.zeros((num_pages, page_size * row_bytes), dtype=torch.uint8, device=dev)
+        self.problem = make_problem(batch, q_len, self.H, page_size, num_pages, max_pages,
+                                    kv_dtype=kv_dtype, sm_scale=sm_scale)
+        self.plan = mla_decode_plan(self.problem, None, sm_count)
+        self.workspace = torch.zeros(int(self.plan.workspace_bytes), dtype=torch.uint8, device=dev)
+        self.status_word = torch.zeros(1, dtype=torch.int32, device=dev)
+
+        def new(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        self.residual, self.x = new(rows, self.hidden), new(rows, self.hidden)
+        self.qkv_a, self.q_a = new(rows, self.q_rank + self.ROW), new(rows, self.q_rank)
+        self.q, self.out = new(rows, self.H, self.HEAD), new(rows, self.hidden)
+        self.o = new(rows, self.H, self.HEAD)
+        self.o_lat = new(rows, self.H, 512, dtype=torch.float32)
+        self.lse = new(rows, self.H, dtype=torch.float32)
+        self.hidden_problem = make_norm_problem(rows, self.hidden, eps=self.eps)
+        self.q_problem = make_norm_problem(rows, self.q_rank, eps=self.eps,
+                                           x_stride=self.q_rank + self.ROW)
+        self.rope_problem = make_rope_problem(rows, self.H, self.HEAD, rope_offset=self.NOPE)
+
+    def _append(self, qkv_a, positions, block_table, requests, stream):
+        width = self.q_rank + self.ROW
+        mla_cache_append_tokens(self.problem, int(qkv_a.shape[0]), qkv_a[:, self.q_rank:], positions,
+                                block_table, self.cache, requests=requests, row_stride=width,
+                                norm_weight=self.kv_norm, norm_eps=self.eps, rope=self.rope,
+                                status=self.status_word, stream=stream)
+
+    def decode(self, hidden, residual, positions, block_table, seq_lens):
+        """hidden, residual (or None): bf16 [B * Q, hidden]; positions int32
+        [B * Q] of the new tokens (-1: a padded row, whose request has length
+        0); seq_lens int32 [B] with the new tokens.  Returns (out, residual):
+        the attention's output and the residual stream to add it to."""
+        stream = torch.cuda.current_stream(self.device)
+        mla_rms_norm(self.hidden_problem, hidden, self.hidden_norm, self.x, residual=residual,
+                     residual_out=None if residual is None else self.residual, stream=stream)
+        torch.matmul(self.x, self.w_qkv_a, out=self.qkv_a)
+        self._append(self.qkv_a, positions, block_table, None, stream)
+        mla_rms_norm(self.q_problem, self.qkv_a, self.q_norm, self.q_a, stream=stream)
+        torch.matmul(self.q_a, self.w_q_b, out=self.q.view(self.rows, -1))
+        mla_rope(self.rope_problem, self.rope, self.q, positions, stream=stream)
+        mla_decode_step(self.plan, self.q, self.w_uk, self.cache, block_table, seq_lens, None,
+                        self.workspace, self.w_uv, self.o_lat, self.lse, self.o, stream)
+        torch.matmul(self.o.view(self.rows, -1), self.w_o, out=self.out)
+        return self.out, hidden if residual is None else self.residual
+
+    def prompt(self, hidden, positions, requests, block_table):
+        """Cache the rows of prompt tokens: hidden bf16 [T, hidden] (the layer's
+        input, residual added), token t at positions[t] of requests[t]."""
+        stream = torch.cuda.current_stream(self.device)
+        x = torch.empty_like(hidden)
+        mla_rms_norm(make_norm_problem(int(hidden.shape[0]), self.hidden, eps=self.eps), hidden,
+                     self.hidden_norm, x, stream=stream)
+        self._append(torch.matmul(x, self.w_qkv_a), positions, block_table, requests, stream)
+
+    def context(self, positions, requests, block_table):
+        """The cached rows at (requests[t], positions[t]) as bf16 [T, 576]."""
+        out = torch.zeros((int(positions.shape[0]), self.ROW), dtype=torch.bfloat16, device=self.device)
+        mla_cache_gather(self.problem, int(positions.shape[0]), self.cache, positions, block_table, out,
+                         requests=requests, status=self.status_word,
+                         stream=torch.cuda.current_stream(self.device))
+        return out
+
+    def status(self) -> int:
+        """Status bits of the appends, gathers and decodes so far (waits)."""
+        return int(self.status_word.item()) | mla_get_status(
+            self.plan, self.workspace, torch.cuda.current_stream(self.device))
 
 
 class HostPipeline:
