@@ -37,6 +37,26 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return two;
 }
 
+// 1 / sqrt(v) with one Newton step whose residual 1 - v r^2 is formed exactly
+// (the product and its rounding error), so that the result is off by little
+// more than its own rounding.
+__device__ __forceinline__ float rsqrt_exact(float v) {
+  const float r = rsqrtf(v);
+  const float p = v * r, p_low = fmaf(v, r, -p);
+  const float rest = fmaf(-p_low, r, fmaf(-p, r, 1.f));
+  const float better = fmaf(0.5f * r, rest, r);
+  return fabsf(rest) < 1.f ? better : r;   // zero, infinite and NaN v keep theirs
+}
+
+// h * rstd * w; where it decides a group's power of two, with the first
+// product's rounding error taken along, since a scale on the other side of its
+// border halves or doubles all its codes.
+template <int kOut>
+__device__ __forceinline__ float norm_product(float h, float rstd, float w) {
+  const float p = h * rstd;
+  return kOut == MLA_NORM_OUT_E4M3_E8M0 ? fmaf(p, w, fmaf(h, rstd, -p) * w) : p * w;
+}
+
 template <int G, bool kMax>
 __device__ __forceinline__ float lanes_reduce(float v) {
 #pragma unroll
@@ -117,18 +137,19 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
     for (int i = 0; i < R; ++i) store(ro, i, h + i * V);
   }
   if (!kWeightFirst) load_weight();
-  const float rstd = rsqrtf(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
+  const float rstd = rsqrt_exact(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float* v = h + i * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= rstd;
     if (p.weight) {
       float b[V];
       unpack16<T>(we[i], b);
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] *= b[j];
+      for (int j = 0; j < V; ++j) v[j] = norm_product<kOut>(v[j], rstd, b[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] *= rstd;
     }
     if (kOut == MLA_NORM_OUT_E4M3_ROW) {
       const bool in = i * width + t < pieces;   // else 0 * inf is possible
@@ -265,18 +286,19 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     store(p.residual_out, p.residual_out_stride, xw);
   }
   if (p.weight) load(p.weight, 0, rw);
-  const float rstd = rsqrtf(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
+  const float rstd = rsqrt_exact(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float* v = h + i * E;
-#pragma unroll
-    for (int j = 0; j < E; ++j) v[j] *= rstd;
     if (p.weight) {
       float b[E];
       Word<T>::get(rw[i], b);
 #pragma unroll
-      for (int j = 0; j < E; ++j) v[j] *= b[j];
+      for (int j = 0; j < E; ++j) v[j] = norm_product<kOut>(v[j], rstd, b[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] *= rstd;
     }
     if (kOut != MLA_NORM_OUT_SAME) {   // 0 where there is none: not 0 * inf
 #pragma unroll
@@ -523,12 +545,12 @@ __global__ void __launch_bounds__(kWidth, staged_resident(kWidth, R)) mla_norm_s
       for (int i = 0; i < R; ++i) words[i] = Word<T>::put(h + i * E);
       write_words<T, kWidth>(words, sum_s + ol.shift, n);
     }
-    const float rstd = rsqrtf(row_reduce<0, false>(sum, slots[0]) * p.inv_cols + p.eps);
+    const float rstd = rsqrt_exact(row_reduce<0, false>(sum, slots[0]) * p.inv_cols + p.eps);
     if (p.residual_out) flush(ol, sum_s, std::integral_constant<int, kSize>());
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < R * E; ++i) {
-      h[i] = h[i] * rstd * w[i];   // elements that are not there: 0, or like all others where rstd is not finite
+      h[i] = norm_product<kOut>(h[i], rstd, w[i]);   // elements that are not there: 0, or like all others where rstd is not finite
       if (kOut == MLA_NORM_OUT_E4M3_ROW) amax = max_nan(amax, fabsf(h[i]));
     }
     const Lines yl(y, p.cols * kOutSize);
