@@ -6,8 +6,8 @@
 // weight are read once and each output written once; that traffic is the
 // bound.  Rows that consist of whole 16-byte pieces on 16-byte boundaries are
 // owned by G threads, each with R pieces, piece i of thread t being number i *
-// G + t of the row, so a warp's accesses are contiguous.  Other rows go in
-// 32-bit words instead (mla_norm_words_kernel).
+// G + t of the row, so a warp's accesses are contiguous (mla_norm_kernel).
+// Other rows go in 32-bit words instead (mla_norm_words_kernel).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -15,7 +15,6 @@
 #include "mla_layer_internal.h"
 #include "mla_quant.cuh"
 #include "mla_types.cuh"
-#include "sm103_ptx.cuh"
 
 namespace mla {
 
@@ -80,6 +79,9 @@ __device__ __forceinline__ float row_reduce(float v, float* slots) {
   return lanes_reduce<32, kMax>(v);
 }
 
+// Rows of whole 16-byte pieces.  Bound by memory: 16384 x 4096 bf16 with a
+// residual to e4m3 with group scales 69.6 us, 6.75 TB/s, 0.99 of the measured
+// copy rate; 8192 x 4096 bf16 with a residual to bf16 40.2 us, 0.98.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams p) {
   __shared__ float slots[2][32];
@@ -207,7 +209,11 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
 // aligned ones around it (they hold at least one element of the row each, so
 // the reads stay on the tensor's own words) and leaves in the aligned word
 // that begins with the lane below's second element; the ends of a warp's words
-// go as single elements.  Rows too wide to be staged, or too few.
+// go as single elements.  A warp whose words the row has all of (kAll) goes
+// without a comparison for each.  Bound by its instructions (about 40 a word):
+// 5003 x 2881 f16 with a residual to e4m3 with row scales 26.5 us, 3.8 TB/s.
+// Measured for that case and left: 16-byte pieces shifted between lanes 41.7 us,
+// the row staged through shared memory around its 16-byte lines 28.1 us.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormParams p) {
   __shared__ float slots[2][32];
@@ -219,45 +225,87 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
   const int k0 = (G == 0 ? warp * R * 32 : 0) + lane;
   // elements from the lane's first word to the row's end
   const int left = (G == 0 || row < p.rows ? p.cols : 0) - k0 * E;
-  auto has = [&](int i, int elems) { return left >= 32 * E * i + elems; };
-  auto load = [&](const void* base, int64_t stride, uint32_t (&w)[R]) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * stride + k0 * E);
+  const bool all = left + lane * E >= 32 * E * R;   // of the warp: the same for its lanes
+  using All = std::true_type;
+  using Some = std::false_type;
+  // whether word i has so many elements
+  auto has = [&](auto kAll, int i, int elems) { return decltype(kAll)::value || left >= 32 * E * i + elems; };
+  // whether its last element is stored by its own lane: no lane behind it has one
+  auto last = [&](auto kAll, int i) {
+    return decltype(kAll)::value ? lane == 31 : has(kAll, i, 2) && (lane == 31 || !has(kAll, i, 3));
+  };
+  auto load_as = [&](auto kAll, uintptr_t at, uint32_t (&w)[R]) {
     const uint32_t* words = reinterpret_cast<const uint32_t*>(at & ~static_cast<uintptr_t>(3));
-    const bool odd = E == 2 && (at & 2);
 #pragma unroll
-    for (int i = 0; i < R; ++i) w[i] = has(i, 1) ? words[32 * i] : 0u;
-    if (odd) {
+    for (int i = 0; i < R; ++i) w[i] = has(kAll, i, 1) ? words[32 * i] : 0u;
+    if (E == 2 && (at & 2)) {
       uint32_t hi[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) hi[i] = has(i, 2) ? words[32 * i + 1] : 0u;
+      for (int i = 0; i < R; ++i) hi[i] = has(kAll, i, 2) ? words[32 * i + 1] : 0u;
 #pragma unroll
       for (int i = 0; i < R; ++i) w[i] = __funnelshift_r(w[i], hi[i], 16);
     } else if (E == 2) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (!has(i, 2)) w[i] &= 0xFFFFu;
+        if (!has(kAll, i, 2)) w[i] &= 0xFFFFu;
     }
   };
-  auto store = [&](void* base, int64_t stride, const uint32_t (&w)[R]) {
-    T* dst = static_cast<T*>(base) + row * stride + k0 * E;
+  auto load = [&](const void* base, int64_t stride, uint32_t (&w)[R]) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * stride + k0 * E);
+    if (all)
+      load_as(All(), at, w);
+    else
+      load_as(Some(), at, w);
+  };
+  auto store_as = [&](auto kAll, T* dst, const uint32_t (&w)[R]) {
     uint32_t* words = reinterpret_cast<uint32_t*>(reinterpret_cast<uintptr_t>(dst) & ~static_cast<uintptr_t>(3));
     Half* elem = reinterpret_cast<Half*>(dst);
     if (E == 1 || !(reinterpret_cast<uintptr_t>(dst) & 2)) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        if (has(i, E))
+        if (has(kAll, i, E))
           words[32 * i] = w[i];
-        else if (has(i, 1))
+        else if (has(kAll, i, 1))
           elem[32 * E * i] = static_cast<Half>(w[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const uint32_t below = __shfl_up_sync(0xffffffffu, w[i], 1);
-        if (lane > 0 && has(i, 1)) words[32 * i] = __funnelshift_r(below, w[i], 16);
-        if (lane == 0 && has(i, 1)) elem[32 * E * i] = static_cast<Half>(w[i]);
-        if (has(i, 2) && (lane == 31 || !has(i, 3)))
-          elem[32 * E * i + 1] = static_cast<Half>(w[i] >> 16);
+        if (lane > 0 && has(kAll, i, 1)) words[32 * i] = __funnelshift_r(below, w[i], 16);
+        if (lane == 0 && has(kAll, i, 1)) elem[32 * E * i] = static_cast<Half>(w[i]);
+        if (last(kAll, i)) elem[32 * E * i + 1] = static_cast<Half>(w[i] >> 16);
+      }
+    }
+  };
+  auto store = [&](void* base, int64_t stride, const uint32_t (&w)[R]) {
+    T* dst = static_cast<T*>(base) + row * stride + k0 * E;
+    if (all)
+      store_as(All(), dst, w);
+    else
+      store_as(Some(), dst, w);
+  };
+  auto store_codes_as = [&](auto kAll, uint8_t* dst, const uint32_t (&c)[R]) {
+    if (E == 1) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (has(kAll, i, 1)) dst[32 * i] = static_cast<uint8_t>(c[i]);
+    } else if (!(reinterpret_cast<uintptr_t>(dst) & 1)) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (has(kAll, i, 2))
+          reinterpret_cast<uint16_t*>(dst)[32 * i] = static_cast<uint16_t>(c[i]);
+        else if (has(kAll, i, 1))
+          dst[64 * i] = static_cast<uint8_t>(c[i]);
+      }
+    } else {   // as in store_as, by bytes
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint32_t below = __shfl_up_sync(0xffffffffu, c[i], 1);
+        if (lane > 0 && has(kAll, i, 1))
+          reinterpret_cast<uint16_t*>(dst - 1)[32 * i] = static_cast<uint16_t>((below >> 8) | (c[i] << 8));
+        if (lane == 0 && has(kAll, i, 1)) dst[64 * i] = static_cast<uint8_t>(c[i]);
+        if (last(kAll, i)) dst[64 * i + 1] = static_cast<uint8_t>(c[i] >> 8);
       }
     }
   };
@@ -287,7 +335,6 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
   }
   if (p.weight) load(p.weight, 0, rw);
   const float rstd = rsqrt_exact(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
-  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float* v = h + i * E;
@@ -300,15 +347,6 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
 #pragma unroll
       for (int j = 0; j < E; ++j) v[j] *= rstd;
     }
-    if (kOut != MLA_NORM_OUT_SAME) {   // 0 where there is none: not 0 * inf
-#pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (!has(i, j + 1)) v[j] = 0.f;
-    }
-    if (kOut == MLA_NORM_OUT_E4M3_ROW) {
-#pragma unroll
-      for (int j = 0; j < E; ++j) amax = max_nan(amax, fabsf(v[j]));
-    }
   }
   if (kOut == MLA_NORM_OUT_SAME) {
 #pragma unroll
@@ -316,11 +354,19 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     store(p.out, p.out_stride, xw);
     return;
   }
+  if (!all) {   // 0 where there is none: not 0 * inf
+#pragma unroll
+    for (int i = 0; i < R * E; ++i)
+      if (!has(Some(), i / E, i % E + 1)) h[i] = 0.f;
+  }
   float inv = 1.f;
   if (kOut == MLA_NORM_OUT_E4M3_ROW) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < R * E; ++i) amax = max_nan(amax, fabsf(h[i]));
     const float scale = max_nan(row_reduce<G, true>(amax, slots[1]) * (1.f / 448.f), kMinRowScale);
     inv = 1.f / scale;
-    if (has(0, 1) && k0 == 0) static_cast<float*>(p.scales)[row] = scale;
+    if (left > 0 && k0 == 0) static_cast<float*>(p.scales)[row] = scale;
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -336,271 +382,17 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
       some = a > 0.f;
       const uint32_t byte = e4m3_scale_byte(a);
       inv = scale_byte_reciprocal(byte);
-      if (has(i, 1) && lane % (32 / E) == 0)
+      if (lane % (32 / E) == 0 && has(Some(), i, 1))
         static_cast<uint8_t*>(p.scales)[row * p.scale_stride + (k0 + 32 * i) * E / 32] = static_cast<uint8_t>(byte);
     }
     xw[i] = e4m3x2(v[0] * inv, v[E - 1] * inv);
     if (!some) xw[i] &= 0x7F7Fu;   // zeros without their signs (or NaN)
   }
   uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride + k0 * E;
-  if (E == 1) {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (has(i, 1)) out[32 * i] = static_cast<uint8_t>(xw[i]);
-  } else if (!(reinterpret_cast<uintptr_t>(out) & 1)) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (has(i, 2))
-        reinterpret_cast<uint16_t*>(out)[32 * i] = static_cast<uint16_t>(xw[i]);
-      else if (has(i, 1))
-        out[64 * i] = static_cast<uint8_t>(xw[i]);
-    }
-  } else {   // as in store, by bytes
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const uint32_t below = __shfl_up_sync(0xffffffffu, xw[i], 1);
-      if (lane > 0 && has(i, 1))
-        reinterpret_cast<uint16_t*>(out - 1)[32 * i] = static_cast<uint16_t>((below >> 8) | (xw[i] << 8));
-      if (lane == 0 && has(i, 1)) out[64 * i] = static_cast<uint8_t>(xw[i]);
-      if (has(i, 2) && (lane == 31 || !has(i, 3)))
-        out[64 * i + 1] = static_cast<uint8_t>(xw[i] >> 8);
-    }
-  }
-}
-
-// Many rows that the 16-byte pieces do not fit: a row passes through shared
-// memory, where it lies as it does around its 16-byte boundaries, so that
-// global memory sees 16-byte accesses (but for the row's ends) while the
-// threads take words of E elements, word t + i * kWidth for thread t.  A block
-// stays for several rows: the weights stay in registers, and the next
-// row is copied in asynchronously while one is computed.
-// Blocks of a multiprocessor, all resident at once, as far as registers go.
-__host__ __device__ constexpr int staged_resident(int width, int words) {
-  return width > 128 ? 2 : words > 12 ? 5 : 6;
-}
-
-__host__ __device__ inline int staged_buffer(int cols, int size) { return (cols * size + 15) / 16 * 16 + 16; }
-
-// A row's place: its elements start `shift` bytes into 16-byte line 0; lines
-// first .. end - 1 belong to it whole.
-struct Lines {
-  uint8_t* line;                 // global, 16-byte aligned
-  int shift, first, end;
-  __device__ __forceinline__ Lines(const void* row, int bytes) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
-    shift = static_cast<int>(at & 15);
-    line = reinterpret_cast<uint8_t*>(at - shift);
-    first = (shift + 15) >> 4;
-    end = (shift + bytes) >> 4;
-  }
-  // Byte offset of the element of the row's ends that lane l moves (0-15 those
-  // in front of the whole lines, 16-31 those behind), or -1.  Rows have at
-  // least one whole line.
-  __device__ __forceinline__ int edge(int l, int size, int bytes) const {
-    const int at = l < 16 ? shift + l * size : 16 * end + (l - 16) * size;
-    return at < (l < 16 ? 16 * first : shift + bytes) ? at : -1;
-  }
-};
-
-// R words of each thread between registers and a row in shared memory that
-// starts on any element; words that the row does not have are skipped (n: the
-// elements from the thread's first word to the row's end).
-template <typename T, int kWidth, int R>
-__device__ __forceinline__ void read_words(uint32_t (&w)[R], const uint8_t* row, int n) {
-  constexpr int E = Word<T>::kElems;
-  if (E == 1 || !(reinterpret_cast<uintptr_t>(row) & 2)) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < R; ++i) w[i] = n > E * kWidth * i ? p[kWidth * i] : 0u;
-  } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + E * threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      w[i] = n > E * kWidth * i ? p[E * kWidth * i] | static_cast<uint32_t>(p[E * kWidth * i + 1]) << 16 : 0u;
-  }
-}
-template <typename T, int kWidth, int R>
-__device__ __forceinline__ void write_words(const uint32_t (&w)[R], uint8_t* row, int n) {
-  constexpr int E = Word<T>::kElems;
-  if (E == 1 || !(reinterpret_cast<uintptr_t>(row) & 2)) {
-    uint32_t* p = reinterpret_cast<uint32_t*>(row) + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (n > E * kWidth * i) p[kWidth * i] = w[i];
-  } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(row) + E * threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (n > E * kWidth * i) {
-        p[E * kWidth * i] = static_cast<uint16_t>(w[i]);
-        p[E * kWidth * i + 1] = static_cast<uint16_t>(w[i] >> 16);
-      }
-  }
-}
-
-// Every buffer has a spare element behind the row's place, zero in the input
-// buffers, so that the last word of a row of 16-bit elements may be half.
-template <typename T, int kOut, int kWidth, int R>
-__global__ void __launch_bounds__(kWidth, staged_resident(kWidth, R)) mla_norm_staged_kernel(const NormParams p) {
-  extern __shared__ __align__(16) uint8_t buffers[];
-  __shared__ float slots[2][32];
-  constexpr int E = Word<T>::kElems, kSize = sizeof(T), kOutSize = kOut == MLA_NORM_OUT_SAME ? kSize : 1;
-  using Bits = typename std::conditional<kSize == 2, uint16_t, uint32_t>::type;
-  const int t = threadIdx.x, bytes = p.cols * kSize, buffer = staged_buffer(p.cols, kSize);
-  const int n = p.cols - E * t;   // elements from the thread's first word to the row's end
-  uint8_t* const sum_s = buffers + (p.residual ? 4 : 2) * buffer;   // residual_out's lines, then out's
-  uint8_t* const out_s = sum_s + (p.residual_out ? buffer : 0);
-  auto stage = [&](int s, int which) { return buffers + (p.residual ? 2 * s + which : s) * buffer; };
-  // The lines of a row into a buffer; its ends' elements into a register.
-  auto fetch = [&](const Lines& l, uint8_t* to) {
-    const uint8_t* from = l.line + 16 * t;
-    to += 16 * t;
-#pragma unroll
-    for (int i = 0; i <= R / 4; ++i)   // 4 R kWidth bytes at most
-      if (t + kWidth * i >= l.first && t + kWidth * i < l.end) cp_async_16(to + 16 * kWidth * i, from + 16 * kWidth * i, 16);
-    Bits v = 0;
-    if (t < 32) {
-      const int at = l.edge(t, kSize, bytes);
-      if (at >= 0) v = *reinterpret_cast<const Bits*>(l.line + at);
-    }
-    return v;
-  };
-  auto put_edge = [&](const Lines& l, uint8_t* to, Bits v) {
-    if (t >= 32) return;
-    const int at = l.edge(t, kSize, bytes);
-    if (at >= 0) *reinterpret_cast<Bits*>(to + at) = v;
-    if (t == 0) *reinterpret_cast<Bits*>(to + l.shift + bytes) = 0;
-  };
-  auto flush = [&](const Lines& l, const uint8_t* from, auto size) {
-    constexpr int z = decltype(size)::value;
-    using B = typename std::conditional<z == 1, uint8_t, typename std::conditional<z == 2, uint16_t, uint32_t>::type>::type;
-    uint8_t* to = l.line + 16 * t;
-#pragma unroll
-    for (int i = 0; i <= R * z / (4 * kSize); ++i)
-      if (t + kWidth * i >= l.first && t + kWidth * i < l.end)
-        *reinterpret_cast<uint4*>(to + 16 * kWidth * i) = *reinterpret_cast<const uint4*>(from + 16 * (t + kWidth * i));
-    if (t < 32) {
-      const int at = l.edge(t, z, p.cols * z);
-      if (at >= 0) *reinterpret_cast<B*>(l.line + at) = *reinterpret_cast<const B*>(from + at);
-    }
-  };
-  after_predecessor();
-  float w[R * E];
-#pragma unroll
-  for (int i = 0; i < R * E; ++i) {
-    const int c = (t + i / E * kWidth) * E + i % E;
-    w[i] = p.weight && c < p.cols ? to_f32(static_cast<const T*>(p.weight)[c]) : 1.f;
-  }
-  // the rows' addresses, a step of gridDim rows from one to the next
-  const int64_t row0 = blockIdx.x;
-  const T* x = static_cast<const T*>(p.x) + row0 * p.x_stride;
-  const T* r = static_cast<const T*>(p.residual) + row0 * p.residual_stride;
-  T* ro = static_cast<T*>(p.residual_out) + row0 * p.residual_out_stride;
-  uint8_t* y = static_cast<uint8_t*>(p.out) + row0 * p.out_stride * kOutSize;
-  const int64_t x_step = gridDim.x * p.x_stride, r_step = gridDim.x * p.residual_stride;
-  const int64_t ro_step = gridDim.x * p.residual_out_stride, y_step = gridDim.x * p.out_stride * kOutSize;
-  Lines xl(x, bytes), rl(r, bytes);
-  Bits x_edge = fetch(xl, stage(0, 0)), r_edge = p.residual ? fetch(rl, stage(0, 1)) : static_cast<Bits>(0);
-  cp_async_commit();
-  int s = 0;
-  for (int64_t row = row0; row < p.rows; row += gridDim.x, s ^= 1, ro += ro_step, y += y_step) {
-    const int x_shift = xl.shift, r_shift = rl.shift;
-    put_edge(xl, stage(s, 0), x_edge);
-    if (p.residual) put_edge(rl, stage(s, 1), r_edge);
-    // the next row, into buffers that were read before the last row's sums met
-    if (row + gridDim.x < p.rows) {
-      x += x_step;
-      xl = Lines(x, bytes);
-      x_edge = fetch(xl, stage(s ^ 1, 0));
-      if (p.residual) {
-        r += r_step;
-        rl = Lines(r, bytes);
-        r_edge = fetch(rl, stage(s ^ 1, 1));
-      }
-    }
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();
-    uint32_t words[R];
-    float h[R * E];
-    read_words<T, kWidth>(words, stage(s, 0) + x_shift, n);
-#pragma unroll
-    for (int i = 0; i < R; ++i) Word<T>::get(words[i], h + i * E);
-    if (p.residual) {
-      read_words<T, kWidth>(words, stage(s, 1) + r_shift, n);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float b[E];
-        Word<T>::get(words[i], b);
-#pragma unroll
-        for (int j = 0; j < E; ++j) h[i * E + j] += b[j];
-      }
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < R * E; ++i) sum = fmaf(h[i], h[i], sum);
-    const Lines ol(ro, bytes);
-    if (p.residual_out) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) words[i] = Word<T>::put(h + i * E);
-      write_words<T, kWidth>(words, sum_s + ol.shift, n);
-    }
-    const float rstd = rsqrt_exact(row_reduce<0, false>(sum, slots[0]) * p.inv_cols + p.eps);
-    if (p.residual_out) flush(ol, sum_s, std::integral_constant<int, kSize>());
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < R * E; ++i) {
-      h[i] = norm_product<kOut>(h[i], rstd, w[i]);   // elements that are not there: 0, or like all others where rstd is not finite
-      if (kOut == MLA_NORM_OUT_E4M3_ROW) amax = max_nan(amax, fabsf(h[i]));
-    }
-    const Lines yl(y, p.cols * kOutSize);
-    uint8_t* ys = out_s + yl.shift;
-    if (kOut == MLA_NORM_OUT_SAME) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) words[i] = Word<T>::put(h + i * E);
-      write_words<T, kWidth>(words, ys, n);
-    } else {
-      float inv = 1.f;
-      if (kOut == MLA_NORM_OUT_E4M3_ROW) {
-        const float scale = max_nan(row_reduce<0, true>(amax, slots[1]) * (1.f / 448.f), kMinRowScale);
-        inv = 1.f / scale;
-        if (t == 0) static_cast<float*>(p.scales)[row] = scale;
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float* v = h + i * E;
-        bool some = true;
-        if (kOut == MLA_NORM_OUT_E4M3_E8M0) {   // a group is 32 / E neighbouring lanes' words
-          float a = 0.f;
-#pragma unroll
-          for (int j = 0; j < E; ++j) a = fmaxf(a, fabsf(v[j]));
-#pragma unroll
-          for (int o = 16 / E; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-          some = a > 0.f;
-          const uint32_t byte = e4m3_scale_byte(a);
-          inv = scale_byte_reciprocal(byte);
-          if (n > E * kWidth * i && t % (32 / E) == 0)
-            static_cast<uint8_t*>(p.scales)[row * p.scale_stride + (t + kWidth * i) * E / 32] = static_cast<uint8_t>(byte);
-        }
-        words[i] = e4m3x2(v[0] * inv, v[E - 1] * inv);
-        if (!some) words[i] &= 0x7F7Fu;   // zeros without their signs (or NaN)
-      }
-      if (E == 2 && !(reinterpret_cast<uintptr_t>(ys) & 1)) {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (n > E * kWidth * i) reinterpret_cast<uint16_t*>(ys)[t + kWidth * i] = static_cast<uint16_t>(words[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (n > E * kWidth * i) {
-            ys[E * (t + kWidth * i)] = static_cast<uint8_t>(words[i]);
-            if (E == 2) ys[E * (t + kWidth * i) + 1] = static_cast<uint8_t>(words[i] >> 8);
-          }
-      }
-    }
-    __syncthreads();
-    flush(yl, out_s, std::integral_constant<int, kOutSize>());
-  }
+  if (all)
+    store_codes_as(All(), out, xw);
+  else
+    store_codes_as(Some(), out, xw);
 }
 
 template <typename T, int kOut, bool kWords, int R, int G>
@@ -608,31 +400,15 @@ cudaError_t launch_one(const NormParams& p, int threads, cudaStream_t stream) {
   constexpr int kRows = G == 0 ? 1 : kRowThreads / (G == 0 ? 1 : G);
   const int blocks = p.rows / kRows + (p.rows % kRows != 0);
   auto launch = [&](auto kernel, int t) { return launch_dependent(kernel, blocks, t, 0, stream, p); };
-  if constexpr (kWords && G != 0)
-    return launch(mla_norm_words_kernel<T, kOut, R, G, kRowThreads>, kRowThreads);
-  else if constexpr (G != 0)
-    return launch(mla_norm_kernel<T, kOut, R, G, kRowThreads>, kRowThreads);
-  else if constexpr (kWords)
-    return threads <= 256 ? launch(mla_norm_words_kernel<T, kOut, R, 0, 256>, threads)
-                          : launch(mla_norm_words_kernel<T, kOut, R, 0, 1024>, threads);
-  else
-    return threads <= 256 ? launch(mla_norm_kernel<T, kOut, R, 0, 256>, threads)
-                          : launch(mla_norm_kernel<T, kOut, R, 0, 1024>, threads);
-}
-
-template <typename T, int kOut, int kWidth, int R>
-cudaError_t launch_staged(const NormParams& p, cudaStream_t stream) {
-  const int buffer = staged_buffer(p.cols, sizeof(T));
-  const int smem = buffer * ((p.residual ? 4 : 2) + (p.residual_out ? 1 : 0)) +
-                   staged_buffer(p.cols, kOut == MLA_NORM_OUT_SAME ? sizeof(T) : 1);
-  auto kernel = mla_norm_staged_kernel<T, kOut, kWidth, R>;
-  if (smem > 48 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
-  }
-  const int fit = 232448 / (smem + 2048);   // and as far as shared memory goes
-  const int blocks = 152 * (fit < staged_resident(kWidth, R) ? fit : staged_resident(kWidth, R));
-  return launch_dependent(kernel, p.rows < blocks ? p.rows : blocks, kWidth, smem, stream, p);
+  auto kernel = [](auto most) {   // most: the registers are shared out for that many threads
+    if constexpr (kWords)
+      return mla_norm_words_kernel<T, kOut, R, G, decltype(most)::value>;
+    else
+      return mla_norm_kernel<T, kOut, R, G, decltype(most)::value>;
+  };
+  if constexpr (G != 0) return launch(kernel(std::integral_constant<int, kRowThreads>()), kRowThreads);
+  if (threads <= 256) return launch(kernel(std::integral_constant<int, 256>()), threads);
+  return launch(kernel(std::integral_constant<int, 1024>()), threads);
 }
 
 template <typename T, int kOut>
@@ -647,7 +423,14 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
                      fits(p.residual, p.residual_stride, 16, sizeof(T)) && fits(p.weight, 0, 16, sizeof(T)) &&
                      fits(p.residual_out, p.residual_out_stride, 16, sizeof(T)) &&
                      fits(p.out, p.out_stride, kOutBytes, kOut == MLA_NORM_OUT_SAME ? sizeof(T) : 1);
-  const bool many = p.rows >= 512;   // enough rows to fill the multiprocessors with few threads each
+  // Few rows: many threads for each, so that one row takes little time; many:
+  // fewer threads with more pieces, since each joins the row's sums.  bf16 with
+  // a residual, rows x cols, us with one piece a thread and with four: 64 x 4096
+  // 1.9 and 2.3, 256 x 4096 2.3 and 2.6, 512 x 4096 3.1 and 3.2, 2048 x 8192 23.4
+  // and 21.7, 4096 x 4096 21.7 and 21.4.  Up to 128 pieces many rows have a warp
+  // each: 512 x 512 1.8 (a block each: 2.2), 16384 x 512 11.9 (17.6), 16384 x 1024
+  // 21.1 (21.5); up to 8 pieces 8 lanes: 16384 x 64 2.3 (a warp: 5.0).
+  const bool many = p.rows >= 512;
   auto threads = [](int units, int R) { return ((units + R - 1) / R + 31) / 32 * 32; };
   if (whole) {
     constexpr int kMost = sizeof(T) == 4 ? 8 : 4;   // pieces of a thread in a block of 1,024: the widest row
@@ -659,18 +442,17 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
     if (n <= 4096) return launch_one<T, kOut, false, 4, 0>(p, threads(n, 4), stream);
     return launch_one<T, kOut, false, kMost, 0>(p, threads(n, kMost), stream);
   }
-  const int words = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;
-  if (many && words > 128 && words <= 4096) {
-    if (words <= 512) return launch_staged<T, kOut, 128, 4>(p, stream);
-    if (words <= 1024) return launch_staged<T, kOut, 128, 8>(p, stream);
-    if (words <= 1536) return launch_staged<T, kOut, 128, 12>(p, stream);
-    if (words <= 2048) return launch_staged<T, kOut, 128, 16>(p, stream);
-    return launch_staged<T, kOut, 256, 16>(p, stream);
-  }
-  constexpr int kMost = sizeof(T) == 4 ? 32 : 16;   // words of a thread
-  if (words <= 128) return launch_one<T, kOut, true, 4, 32>(p, 0, stream);
-  if (words <= 4096) return launch_one<T, kOut, true, 4, 0>(p, threads(words, 4), stream);
-  return launch_one<T, kOut, true, kMost, 0>(p, threads(words, kMost), stream);
+  // Words of a thread, by the same rule: 5003 x 2881 f16 to e4m3 with row scales
+  // 4 27.9, 6 26.0, 8 26.5, 12 25.2 us, but 16384 x 777 bf16 26.5, 27.7, 25.2, 32.2;
+  // 4000 x 8191 f32 to e4m3 8 106, 16 84 us (1,024 threads have 64 registers each);
+  // 128 x 2881 bf16 4 2.7, 16 3.3 us.
+  constexpr int kMost = sizeof(T) == 4 ? 32 : 16;
+  const int n = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;
+  if (n <= 128) return launch_one<T, kOut, true, 4, 32>(p, 0, stream);
+  if (n <= 2048 && !many) return launch_one<T, kOut, true, 4, 0>(p, threads(n, 4), stream);
+  if (n <= 4096) return launch_one<T, kOut, true, 8, 0>(p, threads(n, 8), stream);
+  if (n <= 16384) return launch_one<T, kOut, true, 16, 0>(p, threads(n, 16), stream);
+  return launch_one<T, kOut, true, kMost, 0>(p, threads(n, kMost), stream);
 }
 
 template <typename T>

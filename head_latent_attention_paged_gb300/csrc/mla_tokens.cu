@@ -156,7 +156,7 @@ __device__ __forceinline__ void write_row(uint8_t* dst, const uint8_t* stage, in
 // lane's own places in a ring in shared memory: loads into registers were
 // moved behind the arithmetic by the compiler, 37 -> 60 us for 100,011 rows),
 // and norm and rotation are compiled in or out.
-constexpr int kRing = 4;   // rows of a warp on their way or in use
+constexpr int kRing = 3;   // rows of a warp on their way or in use
 
 template <int kKv, bool kNorm, bool kRotate>
 __global__ void __launch_bounds__(32 * kTokenWarps, 7)

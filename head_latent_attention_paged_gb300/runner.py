@@ -199,6 +199,14 @@ class AttentionLayer:
                                            x_stride=self.q_rank + self.ROW)
         self.rope_problem = make_rope_problem(rows, self.H, self.HEAD, rope_offset=self.NOPE)
 
+    def _check(self, hidden, rows, **int32):
+        """Kernels take addresses: what their shapes say has to be so."""
+        if tuple(hidden.shape) != (rows, self.hidden) or hidden.dtype != torch.bfloat16 or not hidden.is_contiguous():
+            raise ValueError(f"hidden states must be packed bf16 [{rows}, {self.hidden}]")
+        for name, (t, n) in int32.items():
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name} must be {n} packed int32 values")
+
     def _append(self, qkv_a, positions, block_table, requests, stream):
         width = self.q_rank + self.ROW
         mla_cache_append_tokens(self.problem, int(qkv_a.shape[0]), qkv_a[:, self.q_rank:], positions,
@@ -211,6 +219,9 @@ class AttentionLayer:
         [B * Q] of the new tokens (-1: a padded row, whose request has length
         0); seq_lens int32 [B] with the new tokens.  Returns (out, residual):
         the attention's output and the residual stream to add it to."""
+        for h in (hidden, residual) if residual is not None else (hidden,):
+            self._check(h, self.rows, positions=(positions, self.rows), seq_lens=(seq_lens, self.B),
+                        block_table=(block_table, self.B * self.problem.max_pages_per_seq))
         stream = torch.cuda.current_stream(self.device)
         mla_rms_norm(self.hidden_problem, hidden, self.hidden_norm, self.x, residual=residual,
                      residual_out=None if residual is None else self.residual, stream=stream)
@@ -227,6 +238,9 @@ class AttentionLayer:
     def prompt(self, hidden, positions, requests, block_table):
         """Cache the rows of prompt tokens: hidden bf16 [T, hidden] (the layer's
         input, residual added), token t at positions[t] of requests[t]."""
+        n = int(positions.numel())
+        self._check(hidden, n, positions=(positions, n), requests=(requests, n),
+                    block_table=(block_table, self.B * self.problem.max_pages_per_seq))
         stream = torch.cuda.current_stream(self.device)
         x = torch.empty_like(hidden)
         mla_rms_norm(make_norm_problem(int(hidden.shape[0]), self.hidden, eps=self.eps), hidden,

@@ -181,5 +181,11 @@ def test_decode_step_in_a_graph_and_a_padded_batch(m):
         assert np.abs(_f64(layer.lse)[r] - lse[r]).max() <= 5e-4
     assert bool((out[2] == 0).all()) and bool((layer.lse[2] == -float("inf")).all())
     assert layer.status() == 0
+    with pytest.raises(ValueError):                      # shapes and types that the kernels cannot see
+        layer.decode(hidden.float(), None, pos, bt, lens)
+    with pytest.raises(ValueError):
+        layer.decode(hidden, None, pos.long(), bt, lens)
+    with pytest.raises(ValueError):
+        layer.prompt(hidden, pos, pos[:3], bt)
     page = int(bt[2, 0])
     assert torch.equal(layer.cache[page], cache[page])

@@ -77,6 +77,19 @@ class _Norm:
         return L.rms_norm(_f64(self.x), None if self.residual is None else _f64(self.residual),
                           None if self.weight is None else _f64(self.weight), np.float32(self.eps))
 
+    def check_rows(self, keep, label=""):
+        """Check some of the rows, and the guards of all."""
+        names = ("x", "residual", "ro", "out", "scales")
+        whole = {k: getattr(self, k) for k in names}
+        for k, v in whole.items():
+            setattr(self, k, None if v is None else v[keep])
+        bases, self.out_base, self.ro_base = (self.out_base, self.ro_base), None, None
+        self.check(label=label)
+        for k, v in whole.items():
+            setattr(self, k, v)
+        self.out_base, self.ro_base = bases
+        self.check_guards(label)
+
     def check(self, ref=None, label=""):
         h, y, t = ref or self.reference()
         if self.ro is not None:
@@ -124,6 +137,19 @@ def test_norm_widths(m, kind, out):
 
 
 @pytest.mark.parametrize("out", ["same", "mx", "row"])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_norm_widths_of_many_rows(m, kind, out):
+    """The variants that many rows take, at each one's widths."""
+    rng = np.random.default_rng(13)
+    for cols in (40, 100, 130, 257, 512, 768, 1000, 1030, 2048, 2881, 4096, 4100, 8191, 8192, 10001, 16384, 20001,
+                 32767, 32768):
+        rows = 515
+        n = _Norm(m, rng, rows, cols, kind, out, residual=True)
+        n.run()
+        n.check_rows(torch.tensor([0, 1, 2, 3, 4, 5, 6, 7, 254, 511, 512, 513, 514]), f"{kind} {out} {cols}")
+
+
+@pytest.mark.parametrize("out", ["same", "mx", "row"])
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,cols,pad,shift,residual,weight", [
     (3, 768, 576, 0, False, True), (130, 512, 8, 0, True, False), (3, 512, 4, 0, True, True),
@@ -140,10 +166,10 @@ def test_norm_strides(m, kind, out, rows, cols, pad, shift, residual, weight):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
-@pytest.mark.parametrize("cols", [96, 777, 4096])
+@pytest.mark.parametrize("rows,cols", [(37, 96), (37, 777), (600, 777), (37, 4096), (3, 2881), (520, 2881)])
 @pytest.mark.parametrize("which", ["out=x", "ro=residual", "ro=x", "out=x ro=residual", "out=residual"])
-def test_norm_in_place(m, kind, cols, which):
-    n = _Norm(m, np.random.default_rng(6), 37, cols, kind, "same", True)
+def test_norm_in_place(m, kind, rows, cols, which):
+    n = _Norm(m, np.random.default_rng(6), rows, cols, kind, "same", True)
     ref = n.reference()
     if "out=x" in which:
         n.out_base, n.out = n.x, n.x
@@ -298,6 +324,43 @@ def test_rope_far_positions(m):
     for layout in ("pairs", "halves"):
         _rope_case(m, np.random.default_rng(4), len(pos), 4, 64, 0, 64, layout, "f32", "none", True, False,
                    positions=pos)
+
+
+def test_rope_of_a_broadcast_input(m):
+    """One key turned for every head of an output: a head stride of 0 on the
+    input, whose elements are read again for each head."""
+    rng = np.random.default_rng(9)
+    x, pos = _rand(rng, (30, 80), "bf16"), rng.integers(0, 5000, 30).astype(np.int32)
+    out = torch.zeros(30, 7, 80, dtype=torch.bfloat16, device="cuda")
+    pr = m.make_rope_problem(30, 7, 80, rope_offset=16, x_token_stride=80, x_head_stride=0, out_token_stride=560,
+                             out_head_stride=80)
+    m.mla_rope(pr, m.mla_rope_plan(), x, torch.from_numpy(pos).cuda(), out)
+    freq, _ = L.rope_frequencies(64)
+    y, t = L.rope(_f64(x)[:, 16:], pos, freq)
+    for h in range(7):
+        assert torch.equal(out[:, h, :16], x[:, :16])
+        L.assert_rounded(_f64(out)[:, h, 16:], y, t, "bf16")
+
+
+def test_rope_past_32_bits_of_offset(m):
+    """Heads of more than 2^32 bytes, in place: the last tokens are turned
+    where they are, the others as their positions say (-1: not at all)."""
+    tokens, heads, head_dim = (1 << 17) + 3, 64, 256
+    x = torch.zeros(tokens, heads, head_dim, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(10)
+    x[-5:] = _rand(rng, (5, heads, head_dim), "bf16")
+    x[7] = 1.0
+    before = _f64(x[-5:])
+    pos = torch.full((tokens,), -1, dtype=torch.int32, device="cuda")
+    pos[-5:] = torch.tensor([0, 5, 77, -1, 100000], dtype=torch.int32)
+    m.mla_rope(m.make_rope_problem(tokens, heads, head_dim, rope_offset=192), m.mla_rope_plan(), x, pos)
+    freq, _ = L.rope_frequencies(64)
+    y, t = L.rope(before[..., 192:], [0, 5, 77, 0, 100000], freq)
+    y[3], t[3] = before[3, :, 192:], 0.0
+    got = _f64(x[-5:])
+    L.assert_rounded(got[..., 192:], y, t, "bf16")
+    assert np.array_equal(got[..., :192], before[..., :192])
+    assert bool((x[7] == 1.0).all()) and bool((x[8:-5] == 0).all())
 
 
 def test_rope_gradient(m):
@@ -541,6 +604,33 @@ def test_rows_past_32_bits_of_offset(m, kv):
 
 
 # ---------------------------------------------------------------- streams and graphs
+def test_addresses_in_place_of_tensors(m):
+    """The calls take device addresses and stream handles as well."""
+    rng = np.random.default_rng(31)
+    stream = torch.cuda.Stream()
+    n = _Norm(m, rng, 9, 96, "bf16", "row", True)
+    pool = _Pool(m, rng, "fp4", 32, 3, 2)
+    rows, q = _rand(rng, (6, 576), "bf16"), _rand(rng, (6, 2, 64), "bf16")
+    pos = torch.tensor([0, 33, 5, 6, 63, 1], dtype=torch.int32, device="cuda")
+    out, q0 = torch.zeros_like(rows), _f64(q)
+    torch.cuda.synchronize()
+    st = stream.cuda_stream
+    m.mla_rms_norm(n.problem, n.x.data_ptr(), n.weight.data_ptr(), n.out.data_ptr(), residual=n.residual.data_ptr(),
+                   residual_out=n.ro.data_ptr(), scales=n.scales.data_ptr(), stream=st)
+    m.mla_rope(m.make_rope_problem(6, 2, 64), m.mla_rope_plan(), q.data_ptr(), pos.data_ptr(), stream=st)
+    m.mla_cache_append_tokens(pool.problem, 6, rows.data_ptr(), pos.data_ptr(), pool.bt.data_ptr(), pool.dev.data_ptr(),
+                              status=pool.status.data_ptr(), stream=st)
+    m.mla_cache_gather(pool.problem, 6, pool.dev.data_ptr(), pos.data_ptr(), pool.bt.data_ptr(), out.data_ptr(), stream=st)
+    torch.cuda.synchronize()
+    n.check()
+    freq, _ = L.rope_frequencies(64)
+    y, t = L.rope(q0, pos.cpu().numpy(), freq)
+    L.assert_rounded(_f64(q), y, t, "bf16")
+    slots = pool.slots(pos.cpu().numpy(), np.repeat(np.arange(3), 2))
+    L.assert_cache_rows(pool.rows(slots), _f64(rows), np.zeros((6, 576)), "fp4")
+    assert np.array_equal(_f64(out), L.gather_rows(pool.dev.cpu().numpy(), slots, "fp4"))
+
+
 def test_calls_on_streams_and_in_a_graph(m):
     """The four operators on a side stream, two sets of buffers at a time on
     two streams, and captured and replayed on new inputs: the same bits."""
