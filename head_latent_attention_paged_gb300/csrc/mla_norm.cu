@@ -429,13 +429,15 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
   // 1.9 and 2.3, 256 x 4096 2.3 and 2.6, 512 x 4096 3.1 and 3.2, 2048 x 8192 23.4
   // and 21.7, 4096 x 4096 21.7 and 21.4.  Up to 128 pieces many rows have a warp
   // each: 512 x 512 1.8 (a block each: 2.2), 16384 x 512 11.9 (17.6), 16384 x 1024
-  // 21.1 (21.5); up to 8 pieces 8 lanes: 16384 x 64 2.3 (a warp: 5.0).
+  // 21.1 (21.5), up to 32 pieces half a warp: 16384 x 128 3.3 (a warp: 5.0), and up
+  // to 8 pieces 8 lanes: 16384 x 64 2.3 (5.0).
   const bool many = p.rows >= 512;
   auto threads = [](int units, int R) { return ((units + R - 1) / R + 31) / 32 * 32; };
   if (whole) {
     constexpr int kMost = sizeof(T) == 4 ? 8 : 4;   // pieces of a thread in a block of 1,024: the widest row
     const int n = p.cols / V;
     if (n <= 8) return launch_one<T, kOut, false, 1, 8>(p, 0, stream);
+    if (n <= 32 && many) return launch_one<T, kOut, false, 2, 16>(p, 0, stream);
     if (n <= 32) return launch_one<T, kOut, false, 1, 32>(p, 0, stream);
     if (n <= 128 && many) return launch_one<T, kOut, false, 4, 32>(p, 0, stream);
     if (n <= 1024 && !many) return launch_one<T, kOut, false, 1, 0>(p, threads(n, 1), stream);
@@ -445,10 +447,12 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
   // Words of a thread, by the same rule: 5003 x 2881 f16 to e4m3 with row scales
   // 4 27.9, 6 26.0, 8 26.5, 12 25.2 us, but 16384 x 777 bf16 26.5, 27.7, 25.2, 32.2;
   // 4000 x 8191 f32 to e4m3 8 106, 16 84 us (1,024 threads have 64 registers each);
-  // 128 x 2881 bf16 4 2.7, 16 3.3 us.
+  // 128 x 2881 bf16 4 2.7, 16 3.3 us.  Up to 256 words many rows have a warp each:
+  // 14607 x 481 bf16 7.6 us (a block each: 15.6).
   constexpr int kMost = sizeof(T) == 4 ? 32 : 16;
   const int n = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;
   if (n <= 128) return launch_one<T, kOut, true, 4, 32>(p, 0, stream);
+  if (n <= 256 && many) return launch_one<T, kOut, true, 8, 32>(p, 0, stream);
   if (n <= 2048 && !many) return launch_one<T, kOut, true, 4, 0>(p, threads(n, 4), stream);
   if (n <= 4096) return launch_one<T, kOut, true, 8, 0>(p, threads(n, 8), stream);
   if (n <= 16384) return launch_one<T, kOut, true, 16, 0>(p, threads(n, 16), stream);

@@ -18,14 +18,17 @@ namespace mla {
 namespace {
 
 // 32,768 tokens of 20 heads (64 of 256, bf16) and 4,099 of 8 (96 of 128, f32,
-// out of place): 4 heads in flight and up to 12 27.9 and 6.1 us, up to 8 28.3 and
-// 6.1, up to 20 29.0 and 6.1; 5 in flight and up to 10 27.5 and 6.4; 2 and 12 29.5
-// and 6.7; blocks of 256 28.2 and 6.6; cosines shared through shared memory 35
-// and 10.4.
+// halves, out of place): 4 heads in flight and up to 12 28.0 and 6.1 us, up to 8
+// 28.3 and 6.1, up to 20 29.0 and 6.1; 2 and 12 29.5 and 6.7; blocks of 256 28.3
+// and 6.3; cosines shared through shared memory 35 and 10.4.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeHeads = 4;       // heads a thread has in flight
 constexpr int kRopeMostHeads = 12;  // and takes altogether
-constexpr int64_t kRopeFill = 152 * 1024;   // threads to have before they take more
+// Threads to have before they take more heads each: 639 tokens of 45 heads (128
+// of 256) with 512, 768 and 1,024 for each multiprocessor 3.1, 3.6 and 4.1 us, 333
+// of 29 (192, f32, halves) 3.5, 3.1 and 4.6.  A thread with eight cosines (bf16
+// halves) counts as four: 2,688 of 11 (64 of 256) 2.6 us, as one 4.0.
+constexpr int64_t kRopeFill = 152 * 768;
 
 // n / d for n < 2^31, as a multiplication (round-up method).
 struct Divider {
@@ -74,6 +77,12 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
   constexpr bool kTwo = kVec == 1 || kHalves;
   constexpr int kPieces = kTwo ? 2 : 1, kPairs = kTwo ? kVec : kVec / 2;
   const uint32_t per_token = a.units.d * a.groups.d;
+  // The table to shared memory: a warp's lanes read many of its entries, one
+  // after another where they are parameters (45 heads of 128 turned, 639 tokens:
+  // 6.0 -> 4.1 us).  It is there before the predecessor's end.
+  __shared__ uint64_t turns[MLA_ROPE_MAX_DIM / 2];
+  for (int i = threadIdx.x; i < p.dim >> 1; i += kRopeThreads) turns[i] = p.table.turns[i];
+  __syncthreads();
   after_predecessor();
   for (uint32_t k = blockIdx.y * kRopeThreads + threadIdx.x; k < a.block_tokens * per_token;
        k += gridDim.y * kRopeThreads) {
@@ -112,7 +121,7 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
         ready = true;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          turn_cos_sin(p.table.turns[u * kPairs + j], pos, &c[j], &s[j]);
+          turn_cos_sin(turns[u * kPairs + j], pos, &c[j], &s[j]);
           c[j] *= p.table.amplitude;
           s[j] *= p.transposed ? -p.table.amplitude : p.table.amplitude;
         }
@@ -156,10 +165,11 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   // thread's cosines, as long as there are threads to fill the
   // multiprocessors
   const int64_t one = static_cast<int64_t>(p.tokens) * units;
+  const int pairs = kVec == 1 ? 1 : halves ? kVec : kVec / 2;   // of a unit: cosines of a thread
   int groups = p.heads;
   for (int per_thread = 2; per_thread <= kRopeMostHeads; ++per_thread) {
     const int g = (p.heads + per_thread - 1) / per_thread;
-    if (one * g >= kRopeFill) groups = g;
+    if (one * g * (pairs > 4 ? 4 : 1) >= kRopeFill) groups = g;
   }
   const int64_t per_token = static_cast<int64_t>(units) * groups;
   int64_t tokens = per_token < kRopeThreads ? kRopeThreads / per_token : 1;

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
   __shared__ __align__(16) uint8_t ring_s[kTokenWarps][kRing][kDqk * 2];
   __shared__ __align__(16) uint8_t stage_s[kKv == MLA_KV_BF16 ? 1 : kTokenWarps][kStageBytes];
   const int lane = threadIdx.x & 31;
+  const uint64_t turns = kRotate ? p.table.turns[lane] : 0;
   after_predecessor();
   const WarpTokens tok = warp_tokens(p.t, chunk, lane);
   if (tok.count <= 0) return;
@@ -181,7 +182,6 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
   };
 #pragma unroll
   for (int j = 0; j < kRing - 1; ++j) fetch(j);
-  const uint64_t turns = kRotate ? p.table.turns[lane] : 0;
   const float amplitude = p.table.amplitude;
   const bool halves = p.table.halves != 0;
   float2 w[8];
