@@ -5,10 +5,10 @@
 // bytes of each half; single pairs where the addresses do not allow that).  A
 // thread owns one unit's place within the head for some heads of one token: it
 // sets their loads going, computes the unit's few cosines and sines meanwhile
-// and uses them for all its heads, so only the table goes through shared
-// memory and no thread waits for another.  32,768 tokens of 20 heads, 64 of 256 turned in
-// place, 28.0 us: 6.0 TB/s in pieces of 128 bytes every 512 (27.1 us where the
-// turned parts lie side by side).
+// and uses them for all its heads, so only the table goes through shared memory
+// and no thread waits for another's values.  32,768 tokens of 20 heads, 64 of
+// 256 turned in place, 28.0 us: 6.0 TB/s in pieces of 128 bytes every 512 (27.1
+// us where the turned parts lie side by side).
 #include <cuda_runtime.h>
 
 #include "mla_layer_internal.h"
