@@ -201,6 +201,7 @@ int mla_rope_make_plan(const mla_rope_config* config, mla_rope_plan* plan_out) {
       w = 1.0 - std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
     }
     const double g = c.scaling == MLA_ROPE_SCALING_NONE ? f : w * f + (1.0 - w) * (f / c.factor);
+    if (!std::isfinite(g)) return MLA_ERR_INVALID_ARGUMENT;
     // the fraction of a turn per position in 2^-64ths: whole turns do not count
     const double turns = g / two_pi;
     const double scaled = std::ldexp(turns - std::floor(turns), 64);

@@ -123,6 +123,7 @@ def test_rope_amplitude_and_fast_frequencies(m):
     (dict(theta=1.0), INVALID), (dict(theta=float("inf")), INVALID), (dict(theta=float("nan")), INVALID),
     (dict(amplitude=-1.0), INVALID), (dict(amplitude=float("nan")), INVALID), (dict(amplitude=1e300), INVALID),
     (dict(scaling=1, factor=0.0), INVALID), (dict(scaling=1, factor=float("nan")), INVALID),
+    (dict(scaling=1, factor=5e-324), INVALID),                           # no finite frequency
     (dict(scaling=2, factor=2.0), INVALID),                              # no original length
     (dict(scaling=3, factor=2.0, original_positions=64, fast_rotations=1.0), INVALID),
     (dict(scaling=2, factor=2.0, original_positions=64, slow_rotations=0.0), INVALID),
