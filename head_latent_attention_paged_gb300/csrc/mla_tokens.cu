@@ -149,10 +149,10 @@ __device__ __forceinline__ void write_row(uint8_t* dst, const uint8_t* stage, in
 
 // One warp per token at a time.  A row costs 1,152 bytes read and 1,152, 594
 // or 324 written; into the quantised caches the number of instructions bounds
-// the kernel (290 a row with norm and rotation, 210 without, issued in 68 % of
+// the kernel (280 a row with norm and rotation, 200 without, issued in 68 % of
 // the cycles), into bf16 ones memory: 100,011 rows of 2,688 bytes' stride with
-// both 37.3 us into FP8 (4.7 TB/s), 34.7 into FP4, 38.0 into bf16 (6.1 TB/s);
-// without 30.9, 27.5 and 37.1.  So every value stays in its lane,
+// both 36.3 us into FP8 (4.8 TB/s), 34.7 into FP4, 38.0 into bf16 (6.1 TB/s);
+// without 30.5, 27.4 and 37.1.  So every value stays in its lane,
 // one shuffle reduction gives the norm, the cosine and sine are one pair per
 // lane, arithmetic goes in pairs, slots are found one token per lane, the next
 // rows are on their way while one is computed (copied asynchronously into the
@@ -260,51 +260,39 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
     uint32_t e[2] = {kFp8 ? e4m3_scale_byte(m[0]) : e2m1_scale_byte(m[0]),
                      kFp8 ? e4m3_scale_byte(m[1]) : e2m1_scale_byte(m[1])};
     uint32_t ek = kFp8 ? e4m3_scale_byte(mk) : e2m1_scale_byte(mk);
+    // y / 2^e; a group of zeros gets codes 0 whatever their signs, which adding
+    // +0 does there, and adding -0 changes nothing elsewhere.  A NaN stays one.
+    auto scaled = [](float2 v, uint32_t byte, float amax) {
+      const float inv = scale_byte_reciprocal(byte), sign = amax == 0.f ? 0.f : -0.f;
+      return __ffma2_rn(v, make_float2(inv, inv), make_float2(sign, sign));
+    };
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float inv = scale_byte_reciprocal(e[h]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[h][i] = __fmul2_rn(y[h][i], make_float2(inv, inv));
-    }
-    const float ik = scale_byte_reciprocal(ek);
-    const float2 yk = __fmul2_rn(k, make_float2(ik, ik));
+    for (int i = 0; i < 8; ++i) y[i >> 2][i & 3] = scaled(y[i >> 2][i & 3], e[i >> 2], m[i >> 2]);
+    const float2 yk = scaled(k, ek, mk);
     constexpr int kRow = kFp8 ? kFp8RowBytes : kFp4RowBytes, kCodes = kFp8 ? kDqk : kFp4CodeBytes;
     uint8_t* dst = p.kv + slot * kRow;
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(dst) & 15);   // even; a multiple of 4 in FP4
     uint8_t* st = stage + shift;
-    // A group of zeros has codes 0 whatever their signs; a NaN stays one.
-    const bool zeros = fminf(fminf(m[0], m[1]), mk) == 0.f;
     if (kFp8) {
-      uint32_t code[9];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) code[i] = pack_e4m3(y[i >> 2][i & 3]);
-      code[8] = pack_e4m3(yk);
-      if (zeros) {   // codes there are signed zeros (0x00, 0x80) or NaN (0x7F, 0xFF)
-#pragma unroll
-        for (int i = 0; i < 9; ++i)
-          if ((i < 8 ? m[i >> 2 & 1] : mk) == 0.f) code[i] &= 0x7F7Fu;
-      }
       __syncwarp();
       uint16_t* st2 = reinterpret_cast<uint16_t*>(st);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) st2[(i >> 2) * 128 + 4 * lane + (i & 3)] = static_cast<uint16_t>(code[i]);
-      st2[256 + lane] = static_cast<uint16_t>(code[8]);
+      for (int i = 0; i < 8; ++i)
+        st2[(i >> 2) * 128 + 4 * lane + (i & 3)] = static_cast<uint16_t>(pack_e4m3(y[i >> 2][i & 3]));
+      st2[256 + lane] = static_cast<uint16_t>(pack_e4m3(yk));
     } else {
-      uint32_t c[2] = {pack_e2m1(y[0]), pack_e2m1(y[1])}, ck = pack_e2m1(yk);
+      const uint32_t c[2] = {pack_e2m1(y[0]), pack_e2m1(y[1])}, ck = pack_e2m1(yk);
       // a sum of magnitudes is NaN where a value is (they are at most 6, or infinite)
       float nan = fabsf(k.x) + fabsf(k.y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) nan += fabsf(y[i >> 2][i & 3].x) + fabsf(y[i >> 2][i & 3].y);
-      if (__any_sync(0xffffffffu, nan != nan || zeros)) {   // rare: NaN groups get the NaN scale
+      if (__any_sync(0xffffffffu, nan != nan)) {   // rare: NaN groups get the NaN scale
         bool n[2] = {false, false};
 #pragma unroll
         for (int i = 0; i < 8; ++i) n[i >> 2] |= y[i >> 2][i & 3].x != y[i >> 2][i & 3].x || y[i >> 2][i & 3].y != y[i >> 2][i & 3].y;
         const uint32_t nan0 = __ballot_sync(0xffffffffu, n[0]) >> (lane & ~1) & 3u;
         const uint32_t nan1 = __ballot_sync(0xffffffffu, n[1]) >> (lane & ~1) & 3u;
         const uint32_t nank = __ballot_sync(0xffffffffu, k.x != k.x || k.y != k.y) >> (lane & ~7) & 0xFFu;
-        if (m[0] == 0.f) c[0] = 0;
-        if (m[1] == 0.f) c[1] = 0;
-        if (mk == 0.f) ck = 0;
         if (nan0) e[0] = 255;
         if (nan1) e[1] = 255;
         if (nank) ek = 255;
