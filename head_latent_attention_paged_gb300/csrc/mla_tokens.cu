@@ -48,16 +48,16 @@ __device__ __forceinline__ int32_t token_slot(const TokenParams& p, int32_t t, i
 // lane l holding token first + l's.
 struct WarpTokens {
   int32_t first, count, pos, slot;
+  __device__ __forceinline__ WarpTokens(const TokenParams& p, int32_t chunk) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kTokenWarps + (threadIdx.x >> 5)) * chunk;
+    first = static_cast<int32_t>(min(at, static_cast<int64_t>(p.tokens)));
+    count = min(chunk, p.tokens - first);
+  }
+  __device__ __forceinline__ void find(const TokenParams& p, int lane) {
+    pos = lane < count ? p.positions[first + lane] : -1;
+    slot = token_slot(p, first + lane, pos);
+  }
 };
-__device__ __forceinline__ WarpTokens warp_tokens(const TokenParams& p, int32_t chunk, int lane) {
-  WarpTokens w;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kTokenWarps + (threadIdx.x >> 5)) * chunk;
-  w.first = static_cast<int32_t>(min(first, static_cast<int64_t>(p.tokens)));
-  w.count = min(chunk, p.tokens - w.first);
-  w.pos = lane < w.count ? p.positions[w.first + lane] : -1;
-  w.slot = token_slot(p, w.first + lane, w.pos);
-  return w;
-}
 
 // Two bf16 of a word, as f32.
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
   __shared__ __align__(16) uint8_t stage_s[kKv == MLA_KV_BF16 ? 1 : kTokenWarps][kStageBytes];
   const int lane = threadIdx.x & 31;
   after_predecessor();
-  const WarpTokens tok = warp_tokens(p.t, chunk, lane);
+  WarpTokens tok(p.t, chunk);
   if (tok.count <= 0) return;
   const uint8_t* src = reinterpret_cast<const uint8_t*>(p.rows + tok.first * p.row_stride) + 16 * lane;
   uint8_t* const ring = ring_s[threadIdx.x >> 5][0] + 16 * lane;
@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
   };
 #pragma unroll
   for (int j = 0; j < kRing - 1; ++j) fetch(j);
+  tok.find(p.t, lane);   // a chain of three loads, beside the rows
   const uint64_t turns = kRotate ? p.table.turns[lane] : 0;
   const float amplitude = p.table.amplitude;
   const bool halves = p.table.halves != 0;
@@ -416,7 +417,8 @@ __global__ void __launch_bounds__(32 * kTokenWarps)
     mla_gather_kernel(const __grid_constant__ GatherParams p, const int32_t chunk) {
   const int lane = threadIdx.x & 31;
   after_predecessor();
-  const WarpTokens tok = warp_tokens(p.t, chunk, lane);
+  WarpTokens tok(p.t, chunk);
+  tok.find(p.t, lane);
   for (int j = 0; j < tok.count; j += 2) {
     CachedRow<kKv> c[2];
     int32_t slot[2];
