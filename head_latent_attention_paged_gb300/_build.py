@@ -19,7 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libmla_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["mla_api.cu", "mla_decode.cu", "mla_aux.cu", "mla_static.cu", "mla_append.cu",
-           "mla_layer_api.cu", "mla_norm.cu", "mla_rope.cu", "mla_tokens.cu"]
+           "mla_layer_api.cu", "mla_norm_bf16.cu", "mla_norm_f16.cu", "mla_norm_f32.cu",
+           "mla_rope.cu", "mla_tokens.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -1,5 +1,7 @@
 // Host side of include/mla_layer.h: argument checks, the rotary table and the
 // launches.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -167,7 +169,11 @@ int mla_rms_norm(const mla_norm_problem* problem, const void* x, const void* res
   p.out_format = pr.out_format;
   p.eps = pr.eps;
   p.inv_cols = 1.f / static_cast<float>(pr.cols);
-  return launch_norm(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = pr.dtype == MLA_DTYPE_BF16  ? launch_norm_of<__nv_bfloat16>(p, st)
+                          : pr.dtype == MLA_DTYPE_F16 ? launch_norm_of<__half>(p, st)
+                                                      : launch_norm_of<float>(p, st);
+  return err == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_rope_make_plan(const mla_rope_config* config, mla_rope_plan* plan_out) {

@@ -48,7 +48,9 @@ struct NormParams {
   int32_t dtype, out_format;
   float eps, inv_cols;          // inv_cols: 1 / cols
 };
-cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
+// For the element types of MLA_DTYPE_*, each in a source of its own.
+template <typename T>
+cudaError_t launch_norm_of(const NormParams& p, cudaStream_t stream);
 
 // A rotation as the kernels take it, by value: pair i turns by turns[i] *
 // pos (wrapping) 2^-64ths of a turn.

@@ -1,4 +1,5 @@
-// RMS norm of rows, with the residual's addition and 8-bit outputs:
+// RMS norm of rows, with the residual's addition and 8-bit outputs (compiled once
+// for each element type, mla_norm_*.cu):
 // h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight.
 //
 // One pass over memory: a row stays in its threads' registers (in 32 bits)
@@ -8,6 +9,8 @@
 // owned by G threads, each with R pieces, piece i of thread t being number i *
 // G + t of the row, so a warp's accesses are contiguous (mla_norm_kernel).
 // Other rows go in 32-bit words instead (mla_norm_words_kernel).
+#pragma once
+
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
 // that begins with the lane below's second element; the ends of a warp's words
 // go as single elements.  A warp whose words the row has all of (kAll) goes
 // without a comparison for each.  Bound by its instructions (about 40 a word):
-// 5003 x 2881 f16 with a residual to e4m3 with row scales 26.5 us, 3.8 TB/s.
+// 5003 x 2881 f16 with a residual to e4m3 with row scales 25.1 us, 4.0 TB/s.
 // Measured for that case and left: 16-byte pieces shifted between lanes 41.7 us,
 // the row staged through shared memory around its 16-byte lines 28.1 us.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
@@ -444,35 +447,33 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
     if (n <= 4096) return launch_one<T, kOut, false, 4, 0>(p, threads(n, 4), stream);
     return launch_one<T, kOut, false, kMost, 0>(p, threads(n, kMost), stream);
   }
-  // Words of a thread, by the same rule: 5003 x 2881 f16 to e4m3 with row scales
-  // 4 27.9, 6 26.0, 8 26.5, 12 25.2 us, but 16384 x 777 bf16 26.5, 27.7, 25.2, 32.2;
-  // 4000 x 8191 f32 to e4m3 8 106, 16 84 us (1,024 threads have 64 registers each);
-  // 128 x 2881 bf16 4 2.7, 16 3.3 us.  Up to 256 words many rows have a warp each:
-  // 14607 x 481 bf16 7.6 us (a block each: 15.6).
+  // Words of a thread, by the same rule: few rows 4 (128 x 2881 bf16 2.7 us, 16
+  // words 3.3).  Many rows 12 where that leaves no more places empty than 8, else 8:
+  // 5003 x 2881 f16 to e4m3 with row scales 4 27.9, 8 26.5, 12 25.1, 16 30.3 us, 3359
+  // x 7466 f16 8 27.6, 12 22.7, but 16384 x 777 bf16 8 25.2, 12 32.2.  Up to 256 and 384
+  // words many rows have a warp each: 14607 x 481 bf16 7.6 us (a block each: 15.6), 18503
+  // x 708 f16 to e4m3 27.4 (32.3).  Wide rows 16, since 1,024 threads have 64 registers
+  // each: 4000 x 8191 f32 to e4m3 84 us (8 words: 106).
   constexpr int kMost = sizeof(T) == 4 ? 32 : 16;
   const int n = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;
   if (n <= 128) return launch_one<T, kOut, true, 4, 32>(p, 0, stream);
   if (n <= 256 && many) return launch_one<T, kOut, true, 8, 32>(p, 0, stream);
   if (n <= 2048 && !many) return launch_one<T, kOut, true, 4, 0>(p, threads(n, 4), stream);
+  if (n <= 384 && many) return launch_one<T, kOut, true, 12, 32>(p, 0, stream);
+  if (n <= 6144 && (n + 383) / 384 * 384 <= (n + 255) / 256 * 256)
+    return launch_one<T, kOut, true, 12, 0>(p, threads(n, 12), stream);
   if (n <= 4096) return launch_one<T, kOut, true, 8, 0>(p, threads(n, 8), stream);
   if (n <= 16384) return launch_one<T, kOut, true, 16, 0>(p, threads(n, 16), stream);
   return launch_one<T, kOut, true, kMost, 0>(p, threads(n, kMost), stream);
 }
 
+}  // namespace
+
 template <typename T>
-cudaError_t launch_typed(const NormParams& p, cudaStream_t stream) {
+cudaError_t launch_norm_of(const NormParams& p, cudaStream_t stream) {
   if (p.out_format == MLA_NORM_OUT_SAME) return launch_formed<T, MLA_NORM_OUT_SAME>(p, stream);
   if (p.out_format == MLA_NORM_OUT_E4M3_E8M0) return launch_formed<T, MLA_NORM_OUT_E4M3_E8M0>(p, stream);
   return launch_formed<T, MLA_NORM_OUT_E4M3_ROW>(p, stream);
-}
-
-}  // namespace
-
-cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
-  if (p.rows == 0) return cudaSuccess;
-  if (p.dtype == MLA_DTYPE_BF16) return launch_typed<__nv_bfloat16>(p, stream);
-  if (p.dtype == MLA_DTYPE_F16) return launch_typed<__half>(p, stream);
-  return launch_typed<float>(p, stream);
 }
 
 }  // namespace mla

@@ -7,7 +7,7 @@
 // sets their loads going, computes the unit's few cosines and sines meanwhile
 // and uses them for all its heads, so only the table goes through shared memory
 // and no thread waits for another's values.  32,768 tokens of 20 heads, 64 of
-// 256 turned in place, 28.0 us: 6.0 TB/s in pieces of 128 bytes every 512 (27.1
+// 256 turned in place, 27.6 us: 6.1 TB/s in pieces of 128 bytes every 512 (27.1
 // us where the turned parts lie side by side).
 #include <cuda_runtime.h>
 
