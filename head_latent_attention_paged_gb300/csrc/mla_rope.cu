@@ -48,9 +48,10 @@ struct Divider {
 
 struct RopeLaunch {
   RopeParams p;
-  int32_t turn_units;               // of a head: rotated units, then copied ones
-  int32_t block_tokens;             // tokens of a block, one after another's groups
-  Divider units, groups;            // units of a head, threads sharing a token's heads
+  int32_t block_tokens;             // tokens of a block
+  uint32_t turn_all, all;            // its threads' places: rotated units of all its tokens' heads, then
+                                    // copied ones, so that few warps have both
+  Divider turns, copies, groups;    // of a head: rotated and copied units; threads sharing a token's heads
 };
 
 // One access of kVec elements: 16 bytes, or a single element.
@@ -71,14 +72,13 @@ struct Access<T, 1> {
   __device__ __forceinline__ void put(const float* v) { raw = from_f32<T>(v[0]); }
 };
 
-template <typename T, int kVec, bool kHalves>
+template <typename T, int kVec, bool kHalves, int kHeads>
 __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_constant__ RopeLaunch a) {
   const RopeParams& p = a.p;
   using E = Access<T, kVec>;
   // a rotated unit: kPieces pieces, kPairs pairs
   constexpr bool kTwo = kVec == 1 || kHalves;
   constexpr int kPieces = kTwo ? 2 : 1, kPairs = kTwo ? kVec : kVec / 2;
-  const uint32_t per_token = a.units.d * a.groups.d;
   // The table to shared memory: a warp's lanes read many of its entries, one
   // after another where they are parameters (45 heads of 128 turned, 639 tokens:
   // 6.0 -> 4.1 us).  It is there before the predecessor's end.
@@ -86,23 +86,23 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
   for (int i = threadIdx.x; i < p.dim >> 1; i += kRopeThreads) turns[i] = p.table.turns[i];
   __syncthreads();
   after_predecessor();
-  for (uint32_t k = blockIdx.y * kRopeThreads + threadIdx.x; k < a.block_tokens * per_token;
-       k += gridDim.y * kRopeThreads) {
-    const uint32_t row = a.units.div(k), u = k - row * a.units.d;
+  for (uint32_t k = blockIdx.y * kRopeThreads + threadIdx.x; k < a.all; k += gridDim.y * kRopeThreads) {
+    const bool turn = k < a.turn_all;
+    const Divider& units = turn ? a.turns : a.copies;
+    const uint32_t at = turn ? k : k - a.turn_all, row = units.div(at), u = at - row * units.d;
     const uint32_t tok = a.groups.div(row), group = row - tok * a.groups.d;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * a.block_tokens + tok;
-    if (t >= p.tokens) return;
+    if (t >= p.tokens) continue;
     // on its way beside the first heads where registers allow: units of one
     // piece (a decode step 1.85 -> 1.67 us; units of two 22.5 -> 23.8 for 8192 x 32
     // heads of 128)
     const int32_t pos = p.positions[t];
     if (kTwo && pos < 0) continue;
-    const bool turn = static_cast<int32_t>(u) < a.turn_units;
     int32_t element;
     if (turn) {
       element = p.offset + (kVec == 1 && !kHalves ? 2 * u : u * kVec);
     } else {
-      const int32_t c = (u - a.turn_units) * kVec;
+      const int32_t c = u * kVec;
       element = c < p.offset ? c : c + p.dim;
     }
     const int second = kHalves ? p.dim >> 1 : 1;   // elements to a unit's second piece
@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
              static_cast<int64_t>(group) * p.out_head_stride + element;
     float c[kPairs], s[kPairs];
     bool ready = false;
-    for (int32_t h = group; h < p.heads; h += kRopeHeads * a.groups.d) {
-      E e[kRopeHeads][kPieces];
+    for (int32_t h = group; h < p.heads; h += kHeads * a.groups.d) {
+      E e[kHeads][kPieces];
 #pragma unroll
-      for (int i = 0; i < kRopeHeads; ++i) {
+      for (int i = 0; i < kHeads; ++i) {
         if (h + i * static_cast<int32_t>(a.groups.d) >= p.heads) continue;
         e[i][0].load(src + i * x_step);
         if (kTwo && turn) e[i][kPieces - 1].load(src + i * x_step + second);
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
         }
       }
 #pragma unroll
-      for (int i = 0; i < kRopeHeads; ++i) {
+      for (int i = 0; i < kHeads; ++i) {
         if (h + i * static_cast<int32_t>(a.groups.d) >= p.heads) continue;
         if (turn) {
           float v[kPieces * kVec];
@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_kernel(const __grid_con
         }
         e[i][0].store(dst + i * out_step);
       }
-      src += kRopeHeads * x_step;
-      dst += kRopeHeads * out_step;
+      src += kHeads * x_step;
+      dst += kHeads * out_step;
     }
   }
 }
@@ -166,7 +166,7 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   const bool halves = p.table.halves != 0;
   const int per_turn = kVec == 1 ? 2 : halves ? 2 * kVec : kVec;   // elements of a rotated unit
   const int turn_units = p.dim / per_turn;
-  const int units = turn_units + (p.x == p.out ? 0 : (p.head_dim - p.dim) / kVec);
+  const int copies = p.x == p.out ? 0 : (p.head_dim - p.dim) / kVec, units = turn_units + copies;
   // threads that share a token's heads: the fewer, the more heads use a
   // thread's cosines, as long as there are threads to fill the
   // multiprocessors
@@ -180,10 +180,14 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   const int64_t per_token = static_cast<int64_t>(units) * groups;
   int64_t tokens = per_token < kRopeThreads ? kRopeThreads / per_token : 1;
   const int split = per_token > kRopeThreads ? static_cast<int>((per_token + kRopeThreads - 1) / kRopeThreads) : 1;
-  RopeLaunch a{p, turn_units, static_cast<int32_t>(tokens), Divider(units), Divider(groups)};
+  const int rows = static_cast<int>(tokens) * groups;
+  RopeLaunch a{p, static_cast<int32_t>(tokens), static_cast<uint32_t>(rows) * turn_units, static_cast<uint32_t>(rows) * units,
+               Divider(turn_units), Divider(copies > 0 ? copies : 1), Divider(groups)};
   const dim3 blocks(static_cast<unsigned>((p.tokens + tokens - 1) / tokens), split < 65535 ? split : 65535);
-  return halves ? launch_dependent(mla_rope_kernel<T, kVec, true>, blocks, kRopeThreads, 0, stream, a)
-                : launch_dependent(mla_rope_kernel<T, kVec, false>, blocks, kRopeThreads, 0, stream, a);
+  auto launch = [&](auto kernel) { return launch_dependent(kernel, blocks, kRopeThreads, 0, stream, a); };
+  if (groups == p.heads)   // a head for each thread: no registers for more
+    return halves ? launch(mla_rope_kernel<T, kVec, true, 1>) : launch(mla_rope_kernel<T, kVec, false, 1>);
+  return halves ? launch(mla_rope_kernel<T, kVec, true, kRopeHeads>) : launch(mla_rope_kernel<T, kVec, false, kRopeHeads>);
 }
 
 template <typename T>
