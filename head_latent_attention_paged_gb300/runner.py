@@ -218,11 +218,15 @@ class AttentionLayer:
         """hidden, residual (or None): bf16 [B * Q, hidden]; positions int32
         [B * Q] of the new tokens (-1: a padded row, whose request has length
         0); seq_lens int32 [B] with the new tokens.  Returns (out, residual):
-        the attention's output and the residual stream to add it to."""
+        the attention's output and the residual stream to add it to (hidden
+        itself without a residual).  Both may be the layer's own buffers, which
+        the next decode() overwrites; either may be an input to that call."""
         for h in (hidden, residual) if residual is not None else (hidden,):
             self._check(h, self.rows, positions=(positions, self.rows), seq_lens=(seq_lens, self.B),
                         block_table=(block_table, self.B * self.problem.max_pages_per_seq))
         stream = torch.cuda.current_stream(self.device)
+        if residual is None and hidden.data_ptr() == self.out.data_ptr():
+            hidden = self.residual.copy_(hidden)   # it is returned, and `out` is written below
         mla_rms_norm(self.hidden_problem, hidden, self.hidden_norm, self.x, residual=residual,
                      residual_out=None if residual is None else self.residual, stream=stream)
         torch.matmul(self.x, self.w_qkv_a, out=self.qkv_a)
