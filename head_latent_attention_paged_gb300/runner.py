@@ -199,13 +199,19 @@ class AttentionLayer:
                                            x_stride=self.q_rank + self.ROW)
         self.rope_problem = make_rope_problem(rows, self.H, self.HEAD, rope_offset=self.NOPE)
 
-    def _check(self, hidden, rows, **int32):
-        """Kernels take addresses: what their shapes say has to be so."""
-        if tuple(hidden.shape) != (rows, self.hidden) or hidden.dtype != torch.bfloat16 or not hidden.is_contiguous():
-            raise ValueError(f"hidden states must be packed bf16 [{rows}, {self.hidden}]")
+    def _check_int32(self, **int32):
+        """Kernels take addresses: what their arguments' shapes say has to be so."""
         for name, (t, n) in int32.items():
-            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
-                raise ValueError(f"{name} must be {n} packed int32 values")
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{name} must be {n} packed int32 values on {self.device}")
+
+    def _check_hidden(self, hidden, rows):
+        if (tuple(hidden.shape) != (rows, self.hidden) or hidden.dtype != torch.bfloat16
+                or not hidden.is_contiguous() or hidden.device != self.device):
+            raise ValueError(f"hidden states must be packed bf16 [{rows}, {self.hidden}] on {self.device}")
+
+    def _check_table(self, block_table):
+        self._check_int32(block_table=(block_table, self.B * self.problem.max_pages_per_seq))
 
     def _append(self, qkv_a, positions, block_table, requests, stream):
         width = self.q_rank + self.ROW
@@ -222,8 +228,9 @@ class AttentionLayer:
         itself without a residual).  Both may be the layer's own buffers, which
         the next decode() overwrites; either may be an input to that call."""
         for h in (hidden, residual) if residual is not None else (hidden,):
-            self._check(h, self.rows, positions=(positions, self.rows), seq_lens=(seq_lens, self.B),
-                        block_table=(block_table, self.B * self.problem.max_pages_per_seq))
+            self._check_hidden(h, self.rows)
+        self._check_int32(positions=(positions, self.rows), seq_lens=(seq_lens, self.B))
+        self._check_table(block_table)
         stream = torch.cuda.current_stream(self.device)
         if residual is None and hidden.data_ptr() == self.out.data_ptr():
             hidden = self.residual.copy_(hidden)   # it is returned, and `out` is written below
@@ -243,8 +250,9 @@ class AttentionLayer:
         """Cache the rows of prompt tokens: hidden bf16 [T, hidden] (the layer's
         input, residual added), token t at positions[t] of requests[t]."""
         n = int(positions.numel())
-        self._check(hidden, n, positions=(positions, n), requests=(requests, n),
-                    block_table=(block_table, self.B * self.problem.max_pages_per_seq))
+        self._check_hidden(hidden, n)
+        self._check_int32(positions=(positions, n), requests=(requests, n))
+        self._check_table(block_table)
         stream = torch.cuda.current_stream(self.device)
         x = torch.empty_like(hidden)
         mla_rms_norm(make_norm_problem(int(hidden.shape[0]), self.hidden, eps=self.eps), hidden,
@@ -253,8 +261,11 @@ class AttentionLayer:
 
     def context(self, positions, requests, block_table):
         """The cached rows at (requests[t], positions[t]) as bf16 [T, 576]."""
-        out = torch.zeros((int(positions.shape[0]), self.ROW), dtype=torch.bfloat16, device=self.device)
-        mla_cache_gather(self.problem, int(positions.shape[0]), self.cache, positions, block_table, out,
+        n = int(positions.numel())
+        self._check_int32(positions=(positions, n), requests=(requests, n))
+        self._check_table(block_table)
+        out = torch.zeros((n, self.ROW), dtype=torch.bfloat16, device=self.device)
+        mla_cache_gather(self.problem, n, self.cache, positions, block_table, out,
                          requests=requests, status=self.status_word,
                          stream=torch.cuda.current_stream(self.device))
         return out
