@@ -173,6 +173,20 @@ class AttentionLayer:
         self.B, self.Q, self.H = batch, q_len, int(w_uk.shape[0])
         self.rows = rows = batch * q_len
         self.hidden, self.q_rank = int(w_qkv_a.shape[0]), int(w_q_b.shape[0])
+        if self.q_rank % 8 != 0:   # a cache row starts behind q_rank elements, on 16 bytes
+            raise ValueError(f"w_q_b has a rank of {self.q_rank}, which is no multiple of 8")
+        if rope.config.rope_dim != self.ROPE:
+            raise ValueError(f"the rotation must turn {self.ROPE} elements, not {rope.config.rope_dim}")
+        heads = self.H * self.HEAD
+        for name, w, shape, packed in (   # packed: read by kernels, by its address
+                ("w_uk", w_uk, (self.H, 512, self.NOPE), True), ("w_q_b", w_q_b, (self.q_rank, heads), False),
+                ("w_qkv_a", w_qkv_a, (self.hidden, self.q_rank + self.ROW), False),
+                ("hidden_norm", hidden_norm, (self.hidden,), True), ("q_norm", q_norm, (self.q_rank,), True),
+                ("kv_norm", kv_norm, (512,), True), ("w_uv", w_uv, (self.H, 512, 256), True),
+                ("w_o", w_o, (heads, self.hidden), False)):
+            if (tuple(w.shape) != shape or w.dtype != torch.bfloat16 or w.device != dev
+                    or (packed and not w.is_contiguous())):
+                raise ValueError(f"{name} must be a {'packed ' if packed else ''}bf16 tensor {list(shape)} on {dev}")
         self.hidden_norm, self.q_norm, self.kv_norm = hidden_norm, q_norm, kv_norm
         self.w_qkv_a, self.w_q_b, self.w_uk, self.w_uv, self.w_o = w_qkv_a, w_q_b, w_uk, w_uv, w_o
         if sm_count is None:

@@ -78,3 +78,35 @@ def test_decode_refuses(layer, name, bad, with_residual):
     if with_residual and name == "hidden states":
         with pytest.raises(ValueError, match=name):
             layer.decode(**dict(a, hidden=hidden, residual=bad))
+
+
+@pytest.mark.parametrize("name", list(_weights()))
+@pytest.mark.parametrize("how", ["type", "short", "device", "dims"])
+def test_weights_are_refused(name, how):
+    good = _weights()[name]
+    bad = {"type": good.float(), "short": good[:-1], "device": good.to("meta"), "dims": good[None]}[how]
+    # sizes come from three of the weights: one that is short is told from the others by none
+    with pytest.raises(ValueError, match="must be a|multiple of 8" if how in ("short", "device") else name):
+        _make(**{name: bad})
+
+
+@pytest.mark.parametrize("name", ["hidden_norm", "q_norm", "kv_norm", "w_uk", "w_uv"])
+def test_unpacked_weights_are_refused(name):
+    """Those that kernels read by their address; the library products take strides."""
+    good = _weights()[name]
+    with pytest.raises(ValueError, match=name):
+        _make(**{name: torch.zeros(*good.shape[:-1], 2 * good.shape[-1], dtype=good.dtype)[..., ::2]})
+    for name in ("w_qkv_a", "w_q_b", "w_o"):
+        _make(**{name: torch.zeros_like(_weights()[name].T).T})
+
+
+def test_ranks_and_rotations_are_refused():
+    import head_latent_attention_paged_gb300 as m
+
+    def w(*shape):
+        return torch.zeros(shape, dtype=torch.bfloat16)
+
+    with pytest.raises(ValueError, match="multiple of 8"):      # cache rows start behind the query latent
+        _make(q_norm=w(60), w_qkv_a=w(HIDDEN, 60 + 576), w_q_b=w(60, HEADS * 256))
+    with pytest.raises(ValueError, match="64"):
+        _make(rope=m.mla_rope_plan(rope_dim=32))
