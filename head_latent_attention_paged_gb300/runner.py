@@ -159,7 +159,8 @@ class AttentionLayer:
     [q_rank], kv_norm [512], w_q_b [q_rank, H * 256], w_uk [H, 512, 192], w_uv
     [H, 512, 256], w_o [H * 256, hidden].  Buffers are made once: every call
     can be captured in a CUDA graph, and calls of one AttentionLayer are
-    ordered on one stream.
+    ordered on one stream, the current one of the layer's device (which need
+    not be the current device).
     """
 
     NOPE, ROPE, HEAD, ROW = 192, 64, 256, 576
@@ -245,19 +246,20 @@ class AttentionLayer:
             self._check_hidden(h, self.rows)
         self._check_int32(positions=(positions, self.rows), seq_lens=(seq_lens, self.B))
         self._check_table(block_table)
-        stream = torch.cuda.current_stream(self.device)
-        if residual is None and hidden.data_ptr() == self.out.data_ptr():
-            hidden = self.residual.copy_(hidden)   # it is returned, and `out` is written below
-        mla_rms_norm(self.hidden_problem, hidden, self.hidden_norm, self.x, residual=residual,
-                     residual_out=None if residual is None else self.residual, stream=stream)
-        torch.matmul(self.x, self.w_qkv_a, out=self.qkv_a)
-        self._append(self.qkv_a, positions, block_table, None, stream)
-        mla_rms_norm(self.q_problem, self.qkv_a, self.q_norm, self.q_a, stream=stream)
-        torch.matmul(self.q_a, self.w_q_b, out=self.q.view(self.rows, -1))
-        mla_rope(self.rope_problem, self.rope, self.q, positions, stream=stream)
-        mla_decode_step(self.plan, self.q, self.w_uk, self.cache, block_table, seq_lens, None,
-                        self.workspace, self.w_uv, self.o_lat, self.lse, self.o, stream)
-        torch.matmul(self.o.view(self.rows, -1), self.w_o, out=self.out)
+        with torch.cuda.device(self.device):
+            stream = torch.cuda.current_stream(self.device)
+            if residual is None and hidden.data_ptr() == self.out.data_ptr():
+                hidden = self.residual.copy_(hidden)   # it is returned, and `out` is written below
+            mla_rms_norm(self.hidden_problem, hidden, self.hidden_norm, self.x, residual=residual,
+                         residual_out=None if residual is None else self.residual, stream=stream)
+            torch.matmul(self.x, self.w_qkv_a, out=self.qkv_a)
+            self._append(self.qkv_a, positions, block_table, None, stream)
+            mla_rms_norm(self.q_problem, self.qkv_a, self.q_norm, self.q_a, stream=stream)
+            torch.matmul(self.q_a, self.w_q_b, out=self.q.view(self.rows, -1))
+            mla_rope(self.rope_problem, self.rope, self.q, positions, stream=stream)
+            mla_decode_step(self.plan, self.q, self.w_uk, self.cache, block_table, seq_lens, None,
+                            self.workspace, self.w_uv, self.o_lat, self.lse, self.o, stream)
+            torch.matmul(self.o.view(self.rows, -1), self.w_o, out=self.out)
         return self.out, hidden if residual is None else self.residual
 
     def prompt(self, hidden, positions, requests, block_table):
@@ -267,27 +269,30 @@ class AttentionLayer:
         self._check_hidden(hidden, n)
         self._check_int32(positions=(positions, n), requests=(requests, n))
         self._check_table(block_table)
-        stream = torch.cuda.current_stream(self.device)
-        x = torch.empty_like(hidden)
-        mla_rms_norm(make_norm_problem(int(hidden.shape[0]), self.hidden, eps=self.eps), hidden,
-                     self.hidden_norm, x, stream=stream)
-        self._append(torch.matmul(x, self.w_qkv_a), positions, block_table, requests, stream)
+        with torch.cuda.device(self.device):
+            stream = torch.cuda.current_stream(self.device)
+            x = torch.empty_like(hidden)
+            mla_rms_norm(make_norm_problem(n, self.hidden, eps=self.eps), hidden, self.hidden_norm, x,
+                         stream=stream)
+            self._append(torch.matmul(x, self.w_qkv_a), positions, block_table, requests, stream)
 
     def context(self, positions, requests, block_table):
         """The cached rows at (requests[t], positions[t]) as bf16 [T, 576]."""
         n = int(positions.numel())
         self._check_int32(positions=(positions, n), requests=(requests, n))
         self._check_table(block_table)
-        out = torch.zeros((n, self.ROW), dtype=torch.bfloat16, device=self.device)
-        mla_cache_gather(self.problem, n, self.cache, positions, block_table, out,
-                         requests=requests, status=self.status_word,
-                         stream=torch.cuda.current_stream(self.device))
+        with torch.cuda.device(self.device):
+            out = torch.zeros((n, self.ROW), dtype=torch.bfloat16, device=self.device)
+            mla_cache_gather(self.problem, n, self.cache, positions, block_table, out,
+                             requests=requests, status=self.status_word,
+                             stream=torch.cuda.current_stream(self.device))
         return out
 
     def status(self) -> int:
         """Status bits of the appends, gathers and decodes so far (waits)."""
-        return int(self.status_word.item()) | mla_get_status(
-            self.plan, self.workspace, torch.cuda.current_stream(self.device))
+        with torch.cuda.device(self.device):
+            return int(self.status_word.item()) | mla_get_status(
+                self.plan, self.workspace, torch.cuda.current_stream(self.device))
 
 
 class HostPipeline:

@@ -110,3 +110,35 @@ def test_ranks_and_rotations_are_refused():
         _make(q_norm=w(60), w_qkv_a=w(HIDDEN, 60 + 576), w_q_b=w(60, HEADS * 256))
     with pytest.raises(ValueError, match="64"):
         _make(rope=m.mla_rope_plan(rope_dim=32))
+
+
+def test_calls_are_made_on_the_layers_device(monkeypatch):
+    """The library works on the current device: with another one current, a
+    layer's calls make its own current around every launch.  (Recorded calls in
+    place of the library's; no second GPU is needed.)"""
+    from head_latent_attention_paged_gb300 import runner
+    layer = _make()
+    current, seen = [None], []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    calls = ("mla_rms_norm", "mla_rope", "mla_cache_append_tokens", "mla_cache_gather", "mla_decode_step", "mla_get_status")
+    for name in calls:
+        monkeypatch.setattr(runner, name, lambda *a, name=name, **k: seen.append((name, current[-1])) or 0)
+    hidden, table = torch.zeros(BATCH, HIDDEN, dtype=torch.bfloat16), _int(BATCH, MAX_PAGES)
+    layer.decode(hidden, None, _int(BATCH), table, _int(BATCH))
+    layer.prompt(hidden, _int(BATCH), _int(BATCH), table)
+    layer.context(_int(BATCH), _int(BATCH), table)
+    assert layer.status() == 0
+    assert {name for name, _ in seen} == set(calls)
+    assert all(device == layer.device for _, device in seen) and current == [None]
