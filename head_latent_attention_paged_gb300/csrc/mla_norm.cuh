@@ -82,12 +82,41 @@ __device__ __forceinline__ float row_reduce(float v, float* slots) {
   return lanes_reduce<32, kMax>(v);
 }
 
+// 1 / sqrt(mean(h^2) + eps) of a row from its threads' sums of squares.  Where
+// the squares leave the range of 32 bits (a mean below 2^-100, whose small terms
+// were lost, or past the largest number) h is scaled by a power of two and they
+// are summed again: small rows by 2^100, which is exact, large ones by 2^-34, by
+// which no value loses bits whose product is not lost as well (a row's mean is
+// past 2^112, so a product of 2^-149 comes from 2^-93), and by 2^-38 more for
+// their squares alone.  Infinite values keep their infinite sum.  The squares
+// of f16 values do not get that far.  One step after another, by their
+// volatile order, since registers for more would be taken from every row.
+template <typename T, int G, int N>
+__device__ __forceinline__ float row_rstd(float (&h)[N], float sum, const NormParams& p, float (*slots)[32]) {
+  const float mean = row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps;
+  if (std::is_same<T, __half>::value) return rsqrt_exact(mean);
+  const bool small = mean < 0x1p-100f, large = mean == INFINITY;
+  // one decision for all threads that reduce together
+  if (G == 0 || G == 32 ? small || large : __any_sync(0xffffffffu, small || large)) {
+    const float f = small ? 0x1p100f : large ? 0x1p-34f : 1.f, g = large ? 0x1p-38f : 1.f;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      asm volatile("{\n .reg .f32 v;\n mul.f32 %0, %0, %2;\n mul.f32 v, %0, %3;\n fma.rn.f32 %1, v, v, %1;\n}"
+                   : "+f"(h[i]), "+f"(sum)
+                   : "f"(f), "f"(g));
+    return rsqrt_exact(row_reduce<G, false>(sum, slots[1]) * p.inv_cols + p.eps * f * g * f * g) * g;
+  }
+  return rsqrt_exact(mean);
+}
+
 // Rows of whole 16-byte pieces.  Bound by memory: 16384 x 4096 bf16 with a
 // residual to e4m3 with group scales 69.6 us, 6.75 TB/s, 0.99 of the measured
 // copy rate; 8192 x 4096 bf16 with a residual to bf16 40.2 us, 0.98.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams p) {
-  __shared__ float slots[2][32];
+__global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads)   // at most 64 registers
+    mla_norm_kernel(const NormParams p) {
+  __shared__ float slots[3][32];
   constexpr int V = 16 / sizeof(T);
   const int width = G == 0 ? blockDim.x : G;     // threads of a row
   const int t = G == 0 ? threadIdx.x : threadIdx.x % (G == 0 ? 1 : G);
@@ -142,7 +171,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
     for (int i = 0; i < R; ++i) store(ro, i, h + i * V);
   }
   if (!kWeightFirst) load_weight();
-  const float rstd = rsqrt_exact(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
+  const float rstd = row_rstd<T, G>(h, sum, p, slots);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -171,7 +200,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
   uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride;
   float inv = 1.f;
   if (kOut == MLA_NORM_OUT_E4M3_ROW) {
-    const float scale = max_nan(row_reduce<G, true>(amax, slots[1]) * (1.f / 448.f), kMinRowScale);
+    const float scale = max_nan(row_reduce<G, true>(amax, slots[2]) * (1.f / 448.f), kMinRowScale);
     inv = 1.f / scale;
     if (pieces && t == 0) static_cast<float*>(p.scales)[row] = scale;
   }
@@ -219,7 +248,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_kernel(const NormParams 
 // the row staged through shared memory around its 16-byte lines 28.1 us.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormParams p) {
-  __shared__ float slots[2][32];
+  __shared__ float slots[3][32];
   constexpr int E = Word<T>::kElems;
   using Half = typename std::conditional<E == 2, uint16_t, uint32_t>::type;   // an element's bits
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -337,7 +366,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     store(p.residual_out, p.residual_out_stride, xw);
   }
   if (p.weight) load(p.weight, 0, rw);
-  const float rstd = rsqrt_exact(row_reduce<G, false>(sum, slots[0]) * p.inv_cols + p.eps);
+  const float rstd = row_rstd<T, G>(h, sum, p, slots);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float* v = h + i * E;
@@ -367,7 +396,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < R * E; ++i) amax = max_nan(amax, fabsf(h[i]));
-    const float scale = max_nan(row_reduce<G, true>(amax, slots[1]) * (1.f / 448.f), kMinRowScale);
+    const float scale = max_nan(row_reduce<G, true>(amax, slots[2]) * (1.f / 448.f), kMinRowScale);
     inv = 1.f / scale;
     if (left > 0 && k0 == 0) static_cast<float*>(p.scales)[row] = scale;
   }

@@ -102,8 +102,9 @@ typedef struct {
  *                  MLA_NORM_OUT_E4M3_ROW: f32 [rows]; otherwise NULL
  * Pointers need the alignment of their elements; rows that start on 16-byte
  * boundaries are read and written in 16-byte pieces.  Elements behind a row's
- * cols are left as they were.  A row whose squares sum past the 32-bit range
- * (values beyond about 1e19) gives zeros (and NaN for an infinity).
+ * cols are left as they were.  Finite rows of any size are normed, their
+ * squares out of the 32-bit range too; a row with an infinity gives zeros (and
+ * NaN for it), a row of zeros without an eps NaN.
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT (a size, a missing or a surplus
  * pointer, an output that overlaps an input other than as said),
  * MLA_ERR_UNSUPPORTED (a dtype, an out_format, cols past the limit),

@@ -1,0 +1,52 @@
+"""The layer operators (include/mla_layer.h) on the GPU where their documented
+results are hardest to keep: the ends of the 32-bit range, exact quotients,
+infinities and signed zeros."""
+import numpy as np
+import pytest
+
+from oracle import fp8 as F8
+from oracle import layer as L
+from mla_testlib import ensure_built
+from test_gpu_layer import _Norm, _Pool, _dt, _f64, _rand
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def m():
+    ensure_built()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import head_latent_attention_paged_gb300 as mod
+    return mod
+
+
+# Widths of each kernel: a few lanes, a warp, a block for a row, on 16-byte
+# boundaries (shift 0) and off them.
+FORMS = [(3, 64, 0), (3, 64, 1), (600, 100, 0), (600, 130, 1), (3, 4096, 0), (520, 2048, 0), (520, 2881, 0),
+         (2, 32768, 0), (2, 32768, 1)]
+
+
+@pytest.mark.parametrize("out", ["same", "mx", "row"])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,shift", FORMS)
+def test_norm_over_the_range_of_32_bits(m, kind, out, rows, cols, shift):
+    """Finite rows whose squares leave the range of 32 bits at either end are
+    normed like any other, with no eps and with one; a row of zeros without an
+    eps is NaN (0 / 0).  Rows of both ends in one call, ordinary ones between."""
+    rng = np.random.default_rng(1)
+    for eps in (0.0, 1e-6, 2.0 ** -140):
+        n = _Norm(m, rng, rows, cols, kind, out, residual=True, shift=shift, eps=eps)
+        scale = torch.tensor([2.0 ** -115, 2.0 ** 110, 1.0, 2.0 ** -70, 2.0 ** 60, 2.0 ** 45, 2.0 ** -55],
+                             device="cuda").repeat(rows // 7 + 1)[:rows, None]
+        n.x.copy_((n.x.float() * scale).to(_dt(kind)))
+        n.residual.copy_((n.residual.float() * scale).to(_dt(kind)))
+        n.run()
+        keep = torch.arange(min(rows, 14))
+        n.check_rows(keep, f"{kind} {out} {rows}x{cols} eps {eps}")
+    n = _Norm(m, rng, rows, cols, kind, out, residual=False, shift=shift, eps=0.0)
+    n.x[1] = 0.0
+    n.run()
+    got = n.out if out == "same" else torch.from_numpy(F8.e4m3_to_f64(n.out.cpu().numpy()))
+    assert bool(got[1].isnan().all()) and not bool(got[0].isnan().any())
