@@ -216,10 +216,11 @@ MLA_API int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan,
  * FP8 latent written with inlined scales).  Row t belongs to position
  * positions[t] of request requests[t]: page block_table[r][pos / P], slot
  * pos % P.  On the way the latent is normed (norm_weight given: c * weight /
- * sqrt(mean(c^2) + norm_eps)) and the key rotated to its position (rope
- * given), in 32 bits, and the values rounded once, to bf16 or by the cache's
- * quantiser (the formulas of mla_cache_append; without norm and rope the same
- * bytes; a NaN becomes a NaN code in FP8 and a NaN scale, byte 255, in FP4).
+ * sqrt(mean(c^2) + norm_eps), rows of any size as in mla_rms_norm) and the key
+ * rotated to its position (rope given), in 32 bits, and the values rounded
+ * once, to bf16 or by the cache's quantiser (the formulas of mla_cache_append;
+ * without norm and rope the same bytes; a NaN becomes a NaN code in FP8 and a
+ * NaN scale, byte 255, in FP4).
  *   problem     : the cache's shape as for mla_cache_append (batch = requests)
  *   rows        : bf16, token t's [c_kv (512) || k_rope (64)] at rows + t *
  *                 row_stride (elements, >= 576, a multiple of 8): a slice of a

@@ -50,3 +50,20 @@ def test_norm_over_the_range_of_32_bits(m, kind, out, rows, cols, shift):
     n.run()
     got = n.out if out == "same" else torch.from_numpy(F8.e4m3_to_f64(n.out.cpu().numpy()))
     assert bool(got[1].isnan().all()) and not bool(got[0].isnan().any())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_append_over_the_range_of_32_bits(m, kv):
+    """The append's latent norm over the same range."""
+    rng = np.random.default_rng(2)
+    for eps in (0.0, 1e-6):
+        pool = _Pool(m, rng, kv, 64, 1, 1)
+        rows = _rand(rng, (28, 576), "bf16")
+        scale = torch.tensor([2.0 ** -115, 2.0 ** 110, 1.0, 2.0 ** -70, 2.0 ** 60, 2.0 ** 45, 2.0 ** -55],
+                             device="cuda").repeat(4)[:, None]
+        rows[:, :512] = (rows[:, :512].float() * scale).to(torch.bfloat16)
+        weight = _rand(rng, (512,), "bf16")
+        pos = torch.arange(28, dtype=torch.int32, device="cuda")
+        m.mla_cache_append_tokens(pool.problem, 28, rows, pos, pool.bt, pool.dev, norm_weight=weight, norm_eps=eps)
+        y, t = L.row_values(_f64(rows), np.arange(28), _f64(weight), np.float32(eps))
+        L.assert_cache_rows(pool.rows(pool.slots(np.arange(28), np.zeros(28, dtype=int))), y, t, kv, f"eps {eps}")
