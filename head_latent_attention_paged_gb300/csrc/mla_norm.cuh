@@ -59,6 +59,24 @@ __device__ __forceinline__ float norm_product(float h, float rstd, float w) {
   return kOut == MLA_NORM_OUT_E4M3_E8M0 ? fmaf(p, w, fmaf(h, rstd, -p) * w) : p * w;
 }
 
+// The scale of a row, amax / 448 to nearest (tried for every mantissa), at least
+// 2^-126, and NaN or infinite with amax.
+__device__ __forceinline__ float row_scale(float amax) {
+  const float q = amax * (1.f / 448.f);
+  const float s = fmaf(-fmaf(q, 448.f, -amax), 1.f / 448.f, q);
+  return max_nan(amax == INFINITY ? amax : s, kMinRowScale);
+}
+
+// y / scale to nearest, from -y and neg_inv, -1 / scale to nearest: the product
+// and its remainder's share.  (By the negatives a zero keeps its sign, and two
+// values go through packed arithmetic.)  scale is 0 in the place of an infinite
+// one, whose quotients are 0.
+__device__ __forceinline__ float2 quotients(float2 neg_y, float scale, float neg_inv) {
+  const float2 inv = make_float2(neg_inv, neg_inv);
+  const float2 q = __fmul2_rn(neg_y, inv);
+  return __ffma2_rn(__ffma2_rn(q, make_float2(scale, scale), neg_y), inv, q);
+}
+
 template <int G, bool kMax>
 __device__ __forceinline__ float lanes_reduce(float v) {
 #pragma unroll
@@ -171,7 +189,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads)   // at most 
     for (int i = 0; i < R; ++i) store(ro, i, h + i * V);
   }
   if (!kWeightFirst) load_weight();
-  const float rstd = row_rstd<T, G>(h, sum, p, slots);
+  constexpr float kSign = kOut == MLA_NORM_OUT_E4M3_ROW ? -1.f : 1.f;   // for quotients()
+  const float rstd = kSign * row_rstd<T, G>(h, sum, p, slots);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -198,12 +217,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads)   // at most 
     return;
   }
   uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride;
-  float inv = 1.f;
+  float inv = 1.f, scale = 1.f;
   if (kOut == MLA_NORM_OUT_E4M3_ROW) {
-    const float scale = max_nan(row_reduce<G, true>(amax, slots[2]) * (1.f / 448.f), kMinRowScale);
-    inv = 1.f / scale;
+    scale = row_scale(row_reduce<G, true>(amax, slots[2]));
+    inv = -1.f / scale;
     if (pieces && t == 0) static_cast<float*>(p.scales)[row] = scale;
+    if (scale == INFINITY) scale = 0.f;
   }
+  auto codes = [&](float a, float b) {
+    const float2 y = kOut == MLA_NORM_OUT_E4M3_ROW ? quotients(make_float2(a, b), scale, inv) : make_float2(a * inv, b * inv);
+    return e4m3x2(y.x, y.y);
+  };
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int k = i * width + t;
@@ -226,7 +250,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads)   // at most 
 #pragma unroll
     for (int j = 0; j < V / 4; ++j) {
       const float* y = v + 4 * j;
-      c[j] = e4m3x2(y[0] * inv, y[1] * inv) | e4m3x2(y[2] * inv, y[3] * inv) << 16;
+      c[j] = codes(y[0], y[1]) | codes(y[2], y[3]) << 16;
       if (!any) c[j] &= 0x7F7F7F7Fu;   // zeros without their signs (or NaN)
     }
     if (k < pieces && V == 8) reinterpret_cast<uint2*>(out)[k] = make_uint2(c[0], c[V / 4 - 1]);
@@ -366,7 +390,8 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     store(p.residual_out, p.residual_out_stride, xw);
   }
   if (p.weight) load(p.weight, 0, rw);
-  const float rstd = row_rstd<T, G>(h, sum, p, slots);
+  constexpr float kSign = kOut == MLA_NORM_OUT_E4M3_ROW ? -1.f : 1.f;   // for quotients()
+  const float rstd = kSign * row_rstd<T, G>(h, sum, p, slots);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float* v = h + i * E;
@@ -391,15 +416,20 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
     for (int i = 0; i < R * E; ++i)
       if (!has(Some(), i / E, i % E + 1)) h[i] = 0.f;
   }
-  float inv = 1.f;
+  float inv = 1.f, scale = 1.f;
   if (kOut == MLA_NORM_OUT_E4M3_ROW) {
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < R * E; ++i) amax = max_nan(amax, fabsf(h[i]));
-    const float scale = max_nan(row_reduce<G, true>(amax, slots[2]) * (1.f / 448.f), kMinRowScale);
-    inv = 1.f / scale;
+    scale = row_scale(row_reduce<G, true>(amax, slots[2]));
+    inv = -1.f / scale;
     if (left > 0 && k0 == 0) static_cast<float*>(p.scales)[row] = scale;
+    if (scale == INFINITY) scale = 0.f;
   }
+  auto codes = [&](float a, float b) {
+    const float2 y = kOut == MLA_NORM_OUT_E4M3_ROW ? quotients(make_float2(a, b), scale, inv) : make_float2(a * inv, b * inv);
+    return e4m3x2(y.x, y.y);
+  };
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const float* v = h + i * E;
@@ -417,7 +447,7 @@ __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormP
       if (lane % (32 / E) == 0 && has(Some(), i, 1))
         static_cast<uint8_t*>(p.scales)[row * p.scale_stride + (k0 + 32 * i) * E / 32] = static_cast<uint8_t>(byte);
     }
-    xw[i] = e4m3x2(v[0] * inv, v[E - 1] * inv);
+    xw[i] = codes(v[0], v[E - 1]);
     if (!some) xw[i] &= 0x7F7Fu;   // zeros without their signs (or NaN)
   }
   uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_stride + k0 * E;

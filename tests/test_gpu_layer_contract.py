@@ -67,3 +67,44 @@ def test_append_over_the_range_of_32_bits(m, kv):
         m.mla_cache_append_tokens(pool.problem, 28, rows, pos, pool.bt, pool.dev, norm_weight=weight, norm_eps=eps)
         y, t = L.row_values(_f64(rows), np.arange(28), _f64(weight), np.float32(eps))
         L.assert_cache_rows(pool.rows(pool.slots(np.arange(28), np.zeros(28, dtype=int))), y, t, kv, f"eps {eps}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols,shift", [(2, 64, 0), (2, 128, 1), (700, 256, 0), (2, 4096, 0), (2, 4096, 1),
+                                             (515, 2048, 0), (515, 512, 1)])
+def test_norm_row_scales_are_quotients(m, kind, rows, cols, shift):
+    """scale = amax / 448 and code = e4m3(y / scale), both quotients rounded
+    once to 32 bits: rows of +-1 without an eps have y = +-weight exactly, the
+    weights lie on and beside the codes' midpoints."""
+    rng = np.random.default_rng(cols + shift)
+    codes = np.arange(0, 126)
+    mid = (F8.e4m3_to_f64(codes) + F8.e4m3_to_f64(codes + 1)) / 2
+    for _ in range(8):
+        n = _Norm(m, rng, rows, cols, kind, "row", residual=False, shift=shift, eps=0.0)
+        top = np.exp2(rng.uniform(-3, 6)) if kind == "f16" else np.exp2(rng.uniform(-60, 90))
+        w = torch.from_numpy(top * rng.uniform(-1, 1, cols)).to(_dt(kind))
+        w[0] = top
+        scale = np.float32(float(w.abs().max().to(torch.float32))) / np.float32(448)
+        beside = (mid[rng.integers(0, len(mid), cols // 2)] * float(scale)).astype(np.float32)
+        beside = beside.view(np.int32) + rng.integers(-2, 3, cols // 2).astype(np.int32)
+        w[cols // 2:] = torch.from_numpy(beside.view(np.float32)).to(_dt(kind)).clamp(max=float(w[0]))
+        n.weight = w.cuda()
+        n.x.copy_(torch.from_numpy(rng.choice([-1.0, 1.0], (rows, cols))))
+        n.run()
+        y = (n.x.double() * n.weight.double()).cpu().numpy().astype(np.float32)
+        assert np.array_equal(n.scales.cpu().numpy(), np.broadcast_to(scale, rows))
+        want = F8._round_to_e4m3((y / scale).astype(np.float64))
+        assert np.array_equal(F8.e4m3_to_f64(n.out.cpu().numpy()), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,shift", [(5, 64, 0), (5, 96, 1), (600, 1024, 0), (600, 1030, 1)])
+def test_norm_of_an_infinite_value_with_row_scales(m, kind, rows, cols, shift):
+    """An infinite weight makes its values and their rows' scales infinite: the
+    others' codes are their quotients by it, 0, and its own NaN."""
+    n = _Norm(m, np.random.default_rng(6), rows, cols, kind, "row", residual=False, shift=shift)
+    n.weight[5] = float("inf")
+    n.run()
+    code = F8.e4m3_to_f64(n.out.cpu().numpy())
+    assert bool(n.scales.isposinf().all()) and np.isnan(code[:, 5]).all()
+    assert (np.delete(code, 5, axis=1) == 0).all()
