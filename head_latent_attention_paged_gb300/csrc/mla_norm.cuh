@@ -56,7 +56,9 @@ __device__ __forceinline__ float rsqrt_exact(float v) {
 template <int kOut>
 __device__ __forceinline__ float norm_product(float h, float rstd, float w) {
   const float p = h * rstd;
-  return kOut == MLA_NORM_OUT_E4M3_E8M0 ? fmaf(p, w, fmaf(h, rstd, -p) * w) : p * w;
+  // p + 0: the error of a product that is -0 has to be -0 as well, or their sum
+  // is +0
+  return kOut == MLA_NORM_OUT_E4M3_E8M0 ? fmaf(p, w, fmaf(h, rstd, -(p + 0.f)) * w) : p * w;
 }
 
 // The scale of a row, amax / 448 to nearest (tried for every mantissa), at least

@@ -108,3 +108,25 @@ def test_norm_of_an_infinite_value_with_row_scales(m, kind, rows, cols, shift):
     code = F8.e4m3_to_f64(n.out.cpu().numpy())
     assert bool(n.scales.isposinf().all()) and np.isnan(code[:, 5]).all()
     assert (np.delete(code, 5, axis=1) == 0).all()
+
+
+@pytest.mark.parametrize("out", ["same", "mx", "row"])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,shift", [(5, 64, 0), (5, 96, 1), (600, 1024, 0), (600, 1030, 1)])
+def test_norm_signs_of_zeros(m, kind, out, rows, cols, shift):
+    """A zero keeps its sign through the product with the weight, except where
+    a whole group (with group scales) is zero: its codes are 0."""
+    rng = np.random.default_rng(4)
+    n = _Norm(m, rng, rows, cols, kind, out, residual=False, shift=shift)
+    n.x[:, 3:9] = -0.0
+    n.x[:, 12:17] = 0.0
+    n.x[:, 32:64] = -0.0
+    n.weight[::2] = n.weight[::2].abs()
+    n.weight[1::2] = -n.weight[1::2].abs()
+    n.run()
+    n_neg = torch.signbit(n.x) ^ torch.signbit(n.weight)
+    got = torch.signbit(n.out) if out == "same" else n.out >= 0x80
+    cols_of = list(range(3, 9)) + list(range(12, 17)) + ([] if out == "mx" else list(range(32, 64)))
+    assert torch.equal(got[:, cols_of], n_neg[:, cols_of])
+    if out == "mx":
+        assert int(n.out[:, 32:64].max()) == 0 and int(n.scales[:, 1].max()) == 0
