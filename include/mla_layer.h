@@ -92,7 +92,9 @@ typedef struct {
  *
  *   x            : [rows][x_stride]
  *   residual     : NULL, or [rows][residual_stride]
- *   weight       : NULL (ones), or [cols]
+ *   weight       : NULL (ones), or [cols].  Under an infinite one
+ *                  MLA_NORM_OUT_E4M3_E8M0 gives a NaN code or +-448; the other
+ *                  groups do not see it
  *   residual_out : NULL, or [rows][residual_out_stride]; needs residual.  May
  *                  be residual or x itself (same address and stride).
  *   out          : [rows][out_stride] of dtype or of bytes.  In dtype it may be

@@ -130,3 +130,19 @@ def test_norm_signs_of_zeros(m, kind, out, rows, cols, shift):
     assert torch.equal(got[:, cols_of], n_neg[:, cols_of])
     if out == "mx":
         assert int(n.out[:, 32:64].max()) == 0 and int(n.scales[:, 1].max()) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,shift", [(5, 64, 0), (5, 96, 1), (600, 1024, 0), (600, 1030, 1)])
+def test_norm_of_an_infinite_weight_with_group_scales(m, kind, rows, cols, shift):
+    """NaN or the largest code under the weight, in its own group alone."""
+    rng = np.random.default_rng(6)
+    n = _Norm(m, rng, rows, cols, kind, "mx", residual=False, shift=shift)
+    n.weight[5], n.weight[6] = float("inf"), float("-inf")
+    n.run()
+    code = F8.e4m3_to_f64(n.out.cpu().numpy())
+    assert (np.isnan(code[:, 5:7]) | (np.abs(code[:, 5:7]) == 448)).all()
+    assert not np.isnan(np.delete(code, [5, 6], axis=1)).any()
+    _, y, t = n.reference()
+    L.assert_quantised(code[:, 32:], n.scales[:, 1:].cpu().numpy().astype(np.int64) - 127, y[:, 32:], t[:, 32:], 32,
+                       "e4m3")
