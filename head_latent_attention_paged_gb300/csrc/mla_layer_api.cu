@@ -250,9 +250,12 @@ int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan, const v
   if (!aligned(x, size) || !aligned(out, size) || !aligned(positions, 4)) return MLA_ERR_MISALIGNED;
   const bool in_place = x == out && (T == 1 || pr.x_token_stride == pr.out_token_stride) &&
                         (H == 1 || pr.x_head_stride == pr.out_head_stride);
-  const Rows rx{x, 0, (x_heads + x_tokens + D) * size, 1}, ro{out, 0, (out_heads + out_tokens + D) * size, 1};
+  // tokens as rows, each over all its heads, and heads as rows, each over all
+  // its tokens: x and out are apart where either of the two are
+  const Rows xt{x, pr.x_token_stride * size, (x_heads + D) * size, T}, ot{out, pr.out_token_stride * size, (out_heads + D) * size, T};
+  const Rows xh{x, pr.x_head_stride * size, (x_tokens + D) * size, H}, oh{out, pr.out_head_stride * size, (out_tokens + D) * size, H};
   const Rows rp{positions, 0, T * 4, 1};
-  if ((!in_place && overlap(rx, ro)) || overlap(ro, rp)) return MLA_ERR_INVALID_ARGUMENT;
+  if ((!in_place && overlap(xt, ot) && overlap(xh, oh)) || overlap(ot, rp)) return MLA_ERR_INVALID_ARGUMENT;
   RopeParams p;
   p.x = x;
   p.out = out;

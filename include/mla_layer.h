@@ -108,9 +108,10 @@ typedef struct {
  * squares out of the 32-bit range too; a row with an infinity gives zeros (and
  * NaN for it), a row of zeros without an eps NaN.
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT (a size, a missing or a surplus
- * pointer, an output that overlaps an input other than as said),
- * MLA_ERR_UNSUPPORTED (a dtype, an out_format, cols past the limit),
- * MLA_ERR_MISALIGNED or MLA_ERR_CUDA.
+ * pointer, an output that overlaps an input other than as said: rows of one
+ * stride in bytes by their elements, as column ranges of one buffer, others by
+ * their whole span), MLA_ERR_UNSUPPORTED (a dtype, an out_format, cols past the
+ * limit), MLA_ERR_MISALIGNED or MLA_ERR_CUDA.
  */
 MLA_API int mla_rms_norm(const mla_norm_problem* problem, const void* x, const void* residual,
                  const void* weight, void* residual_out, void* out, void* scales,
@@ -200,8 +201,10 @@ typedef struct {
  * With pair (a, b) at angle t: a' = A (a cos t - b sin t), b' = A (a sin t +
  * b cos t), A the amplitude, in 32 bits, rounded once.
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT (a size or stride, a plan not made
- * by mla_rope_make_plan, an out that overlaps x otherwise), MLA_ERR_UNSUPPORTED
- * (a dtype, a stride or a token's elements past the limits), MLA_ERR_MISALIGNED (less than the
+ * by mla_rope_make_plan, an out that overlaps x otherwise: where their tokens'
+ * or their heads' strides are equal the elements count, as in column ranges of
+ * one buffer, else the whole span), MLA_ERR_UNSUPPORTED (a dtype, a stride or a
+ * token's elements past the limits), MLA_ERR_MISALIGNED (less than the
  * elements' alignment) or MLA_ERR_CUDA.
  */
 MLA_API int mla_rope(const mla_rope_problem* problem, const mla_rope_plan* plan, const void* x,

@@ -146,3 +146,32 @@ def test_norm_of_an_infinite_weight_with_group_scales(m, kind, rows, cols, shift
     _, y, t = n.reference()
     L.assert_quantised(code[:, 32:], n.scales[:, 1:].cpu().numpy().astype(np.int64) - 127, y[:, 32:], t[:, 32:], 32,
                        "e4m3")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("order", ["token", "head"])
+def test_rope_between_columns_of_one_buffer(m, kind, order):
+    """Heads turned out of one column range of a wide buffer into another,
+    token by token or head by head: they share no element."""
+    rng = np.random.default_rng(7)
+    tokens, heads, D = 37, 5, 64
+    outer, inner = (tokens, heads) if order == "token" else (heads, tokens)
+    buf = _rand(rng, (outer, 2 * inner * D + 64), kind)
+    x = buf[:, :inner * D].unflatten(1, (inner, D))
+    out = buf[:, inner * D:2 * inner * D].unflatten(1, (inner, D))
+    if order == "head":
+        x, out = x.transpose(0, 1), out.transpose(0, 1)
+    before = buf.clone()
+    x64 = _f64(x)
+    pos = rng.integers(0, 4096, tokens).astype(np.int32)
+    pr = m.make_rope_problem(tokens, heads, D, 0, 0 if kind == "bf16" else 2, 0, x.stride(0), x.stride(1),
+                             out.stride(0), out.stride(1))
+    m.mla_rope(pr, m.mla_rope_plan(), x, torch.from_numpy(pos).cuda(), out)
+    freq, _ = L.rope_frequencies(64)
+    y, t = L.rope(x64, pos, freq)
+    L.assert_rounded(_f64(out), y, t, kind)
+    assert torch.equal(buf[:, :inner * D], before[:, :inner * D])
+    assert torch.equal(buf[:, 2 * inner * D:], before[:, 2 * inner * D:])
+    with pytest.raises(m.MlaError) as e:     # half a head earlier: some of x's elements
+        m.mla_rope(pr, m.mla_rope_plan(), x, torch.from_numpy(pos).cuda(), buf.flatten()[inner * D - D // 2:])
+    assert e.value.code == m.MLA_ERR_INVALID_ARGUMENT
