@@ -1,6 +1,6 @@
 """The layer operators (include/mla_layer.h) on the GPU where their documented
 results are hardest to keep: the ends of the 32-bit range, exact quotients,
-infinities and signed zeros."""
+infinities and signed zeros, calls so large that a warp takes many tokens."""
 import numpy as np
 import pytest
 
@@ -175,3 +175,61 @@ def test_rope_between_columns_of_one_buffer(m, kind, order):
     with pytest.raises(m.MlaError) as e:     # half a head earlier: some of x's elements
         m.mla_rope(pr, m.mla_rope_plan(), x, torch.from_numpy(pos).cuda(), buf.flatten()[inner * D - D // 2:])
     assert e.value.code == m.MLA_ERR_INVALID_ARGUMENT
+
+
+# ---------------------------------------------------------------- many tokens
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("tokens,requests,full", [(9731, 5, True), (20011, 7, False), (40009, 3, True), (30000, 6, True)])
+def test_many_tokens_of_a_warp(m, kv, tokens, requests, full):
+    """Prompt-sized calls, where a warp takes several tokens one after another:
+    tokens of no position and of no slot lie between the others, and a last
+    warp has fewer.  Every row written is compared with the oracle, every
+    other one with what it held; the gather returns the cache's values.  30,000
+    tokens go without a list of requests, in equal shares."""
+    rng = np.random.default_rng(tokens)
+    page, share = 64, tokens // requests
+    in_order = tokens % requests == 0
+    max_pages = -(-(share if in_order else tokens // (requests - 1)) // page) + 1
+    pool = _Pool(m, rng, kv, page, requests, max_pages)
+    cap = max_pages * page
+    if in_order:
+        req = np.repeat(np.arange(requests), share).astype(np.int32)
+        pos = np.concatenate([rng.permutation(cap)[:share] for _ in range(requests)]).astype(np.int32)
+    else:
+        pick = rng.choice(requests * cap, tokens, replace=False)
+        req, pos = (pick // cap).astype(np.int32), (pick % cap).astype(np.int32)
+    pool.table[1, 1], pool.table[requests - 1, 0] = pool.num_pages + 3, -7
+    pool.bt = torch.from_numpy(pool.table).cuda()
+    kind = rng.integers(0, 12, tokens)
+    pos[kind == 0] = -1
+    pos[kind == 1] = cap + rng.integers(0, 9, int((kind == 1).sum()))
+    if not in_order:
+        req[kind == 2] = requests
+        req[kind == 3] = -1
+    pos[:9] = -1                                          # a warp's tokens, all of them
+    stride = 584
+    wide = _rand(rng, (tokens, stride), "bf16")
+    rows = wide[:, 8:]
+    weight = _rand(rng, (512,), "bf16") if full else None
+    plan = m.mla_rope_plan(layout=m.MLA_ROPE_HALVES if requests == 3 else m.MLA_ROPE_INTERLEAVED) if full else None
+    freq = L.rope_frequencies(64)[0] if full else None
+    positions, of = torch.from_numpy(pos).cuda(), None if in_order else torch.from_numpy(req).cuda()
+    m.mla_cache_append_tokens(pool.problem, tokens, rows, positions, pool.bt, pool.dev, requests=of, row_stride=stride,
+                              norm_weight=weight, rope=plan, status=pool.status)
+    slots = pool.slots(pos, req)
+    live = slots >= 0
+    bits = m.MLA_STATUS_BAD_INDEX | m.MLA_STATUS_BAD_PAGE
+    assert int(pool.status) == bits
+    y, t = L.row_values(_f64(rows)[live], pos[live], None if weight is None else _f64(weight), np.float32(1e-6), freq, 1.0,
+                        "halves" if requests == 3 else "pairs")
+    L.assert_cache_rows(pool.rows(slots[live]), y, t, kv)
+    pool.check_untouched(slots[live])
+    pool.status.zero_()
+    out = torch.full((tokens, 640), 7.0, dtype=torch.bfloat16, device="cuda")
+    m.mla_cache_gather(pool.problem, tokens, pool.dev, positions, pool.bt, out, requests=of, out_stride=640,
+                       status=pool.status)
+    assert int(pool.status) == bits
+    want = np.full((tokens, 640), 7.0)
+    want[slots == -2, :576] = 0.0
+    want[live, :576] = L.gather_rows(pool.dev.cpu().numpy(), slots[live], kv)
+    assert np.array_equal(_f64(out), want)
