@@ -161,8 +161,10 @@ typedef struct {
 
 /* Filled by mla_rope_make_plan; treat as opaque.  turns[i] is pair i's turn
  * per position in units of 2^-64 of a full turn: turns[i] * pos, wrapping,
- * is the angle's exact fraction of a turn, so far positions lose nothing
- * (the error is below pos * 2^-52 turns). */
+ * is the angle's exact fraction of a turn, so far positions lose nothing.
+ * (The frequencies are in 53 bits: an angle is off by less than pos * 2^-52
+ * turns, and where a scaling's factor is below 1, which raises frequencies, by
+ * less than pos * 2^-52 / factor.) */
 typedef struct {
   mla_rope_config config;
   float amplitude;
