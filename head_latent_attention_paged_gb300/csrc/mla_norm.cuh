@@ -32,13 +32,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// e4m3 codes of two values, the first in the low byte: nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(hi), "f"(lo));
-  return two;
-}
-
 // 1 / sqrt(v) with one Newton step whose residual 1 - v r^2 is formed exactly
 // (the product and its rounding error), so that the result is off by little
 // more than its own rounding.

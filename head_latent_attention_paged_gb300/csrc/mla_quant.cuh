@@ -63,11 +63,33 @@ __device__ __forceinline__ float scale_byte_reciprocal(uint32_t byte) {
   return __uint_as_float((254u - byte) << 23);
 }
 
-// Round-to-nearest-even conversion to e4m3 with saturation at +-448.
-__device__ __forceinline__ uint32_t f32_to_e4m3(float v) {
+// e4m3 codes of two values, the first in the low byte: nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(two) : "f"(v));
-  return two & 0xFFu;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(hi), "f"(lo));
+  return two;
+}
+
+__device__ __forceinline__ uint32_t f32_to_e4m3(float v) { return e4m3x2(v, v) & 0xFFu; }
+
+// e2m1 codes of two values, the first in the low nibble, and of eight: as
+// f32_to_e2m1.
+__device__ __forceinline__ uint32_t pack_e2m1(float2 v) {
+  uint32_t two;
+  asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n cvt.u32.u8 %0, c;\n}"
+      : "=r"(two)
+      : "f"(v.y), "f"(v.x));
+  return two;
+}
+__device__ __forceinline__ uint32_t pack_e2m1(const float2 (&v)[4]) {   // eight, in order from the low nibble
+  uint32_t w;
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(w)
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+  return w;
 }
 
 }  // namespace mla

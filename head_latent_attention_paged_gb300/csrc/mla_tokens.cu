@@ -67,32 +67,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// e4m3 codes of two values, the first in the low byte; e2m1 codes of two, the
-// first in the low nibble.  Nearest even, saturating, as f32_to_e4m3 and
-// f32_to_e2m1.
-__device__ __forceinline__ uint32_t pack_e4m3(float2 v) {
-  uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(v.y), "f"(v.x));
-  return two;
-}
-__device__ __forceinline__ uint32_t pack_e2m1(float2 v) {
-  uint32_t two;
-  asm("{\n .reg .b8 c;\n cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n cvt.u32.u8 %0, c;\n}"
-      : "=r"(two)
-      : "f"(v.y), "f"(v.x));
-  return two;
-}
-__device__ __forceinline__ uint32_t pack_e2m1(const float2 (&v)[4]) {   // eight, in order from the low nibble
-  uint32_t w;
-  asm("{\n .reg .b8 a, b, c, d;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
-      " mov.b32 %0, {a, b, c, d};\n}"
-      : "=r"(w)
-      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
-  return w;
-}
-
 // The warp's row: lane l holds latent values 8 l .. 8 l + 7 and 256 + 8 l ..,
 // and key values 2 l and 2 l + 1.
 struct RowWords {
@@ -306,8 +280,8 @@ __global__ void __launch_bounds__(32 * kTokenWarps, 7)
       uint16_t* st2 = reinterpret_cast<uint16_t*>(st);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        st2[(i >> 2) * 128 + 4 * lane + (i & 3)] = static_cast<uint16_t>(pack_e4m3(y[i >> 2][i & 3]));
-      st2[256 + lane] = static_cast<uint16_t>(pack_e4m3(yk));
+        st2[(i >> 2) * 128 + 4 * lane + (i & 3)] = static_cast<uint16_t>(e4m3x2(y[i >> 2][i & 3].x, y[i >> 2][i & 3].y));
+      st2[256 + lane] = static_cast<uint16_t>(e4m3x2(yk.x, yk.y));
     } else {
       const uint32_t c[2] = {pack_e2m1(y[0]), pack_e2m1(y[1])}, ck = pack_e2m1(yk);
       // a sum of magnitudes is NaN where a value is (they are at most 6, or infinite)
