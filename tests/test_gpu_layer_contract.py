@@ -177,6 +177,62 @@ def test_rope_between_columns_of_one_buffer(m, kind, order):
     assert e.value.code == m.MLA_ERR_INVALID_ARGUMENT
 
 
+# ---------------------------------------------------------------- streams
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_call_waits_for_another_streams_work(m, captured):
+    """Calls start while their predecessor on the stream still runs; a long one
+    on another stream, waited for by an event in between, is waited for all the
+    same, before its output is read and before its input is written: eager, and
+    as a captured graph's fork and join."""
+    rng = np.random.default_rng(14)
+    tokens, heads, dim = 40000, 32, 128
+    x = _rand(rng, (tokens, heads, dim), "bf16")
+    turned, small = torch.empty_like(x), _rand(rng, (64, 512), "bf16")
+    small_out, out = torch.empty_like(small), torch.empty(tokens, heads * dim, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    plan, rp = m.mla_rope_plan(rope_dim=dim), m.make_rope_problem(tokens, heads, dim)
+    np_small, np_big = m.make_norm_problem(64, 512), m.make_norm_problem(tokens, heads * dim)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        two.wait_stream(one)
+        m.mla_rope(rp, plan, x, pos, turned, stream=two)             # long, x to turned
+        m.mla_rms_norm(np_small, small, None, small_out, stream=one)
+        one.wait_stream(two)
+        m.mla_rms_norm(np_big, turned, None, out, stream=one)        # reads turned
+        m.mla_rms_norm(np_big, out, None, x, stream=one)             # writes x
+
+    def alone():
+        m.mla_rope(rp, plan, x, pos, turned)
+        m.mla_rms_norm(np_big, turned, None, out)
+        m.mla_rms_norm(np_big, out, None, x)
+
+    first = x.clone()
+    want = []
+    for _ in range(3):
+        alone()
+        want.append((out.clone(), x.clone()))
+    torch.cuda.synchronize()
+    graph = None
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=one):
+            step()
+        torch.cuda.synchronize()
+    for _ in range(4):
+        x.copy_(first)
+        turned.zero_()
+        torch.cuda.synchronize()
+        for w_out, w_x in want:
+            if captured:
+                graph.replay()
+                torch.cuda.synchronize()
+            else:
+                step()
+                torch.cuda.synchronize()
+            assert torch.equal(out, w_out) and torch.equal(x, w_x)
+
+
 # ---------------------------------------------------------------- many tokens
 @pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("tokens,requests,full", [(9731, 5, True), (20011, 7, False), (40009, 3, True), (30000, 6, True)])
