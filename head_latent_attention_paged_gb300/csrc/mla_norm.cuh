@@ -124,8 +124,9 @@ __device__ __forceinline__ float row_rstd(float (&h)[N], float sum, const NormPa
 }
 
 // Rows of whole 16-byte pieces.  Bound by memory: 16384 x 4096 bf16 with a
-// residual to e4m3 with group scales 69.6 us, 6.75 TB/s, 0.99 of the measured
-// copy rate; 8192 x 4096 bf16 with a residual to bf16 40.2 us, 0.98.
+// residual to e4m3 with group scales 69.6 us, 6.78 TB/s, 1.00 of the measured
+// copy rate; with row scales 69.0; 8192 x 4096 bf16 with a residual to bf16 40.1
+// us, 0.99.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads)   // at most 64 registers
     mla_norm_kernel(const NormParams p) {
@@ -261,10 +262,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads)   // at most 
 // the reads stay on the tensor's own words) and leaves in the aligned word
 // that begins with the lane below's second element; the ends of a warp's words
 // go as single elements.  A warp whose words the row has all of (kAll) goes
-// without a comparison for each.  Bound by its instructions (about 40 a word):
-// 5003 x 2881 f16 with a residual to e4m3 with row scales 25.1 us, 4.0 TB/s.
-// Measured for that case and left: 16-byte pieces shifted between lanes 41.7 us,
-// the row staged through shared memory around its 16-byte lines 28.1 us.
+// without a comparison for each.  5003 x 2881 f16 with a residual to e4m3 with
+// row scales: 25.4 us, 4.0 TB/s.  Neither memory nor the issue slots are full (a
+// warp runs 72 instructions for 32 words, issued in 60 % of the cycles): at 64
+// registers 28 warps fit a multiprocessor, and they wait for their loads, for one
+// another at the row's two sums and for shuffles.  Left after measuring them for
+// that case: 16-byte pieces shifted between lanes 41.7 us, the row staged through
+// shared memory around its 16-byte lines 28.1 us.
 template <typename T, int kOut, int R, int G, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) mla_norm_words_kernel(const NormParams p) {
   __shared__ float slots[3][32];
@@ -482,12 +486,12 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
                      fits(p.out, p.out_stride, kOutBytes, kOut == MLA_NORM_OUT_SAME ? sizeof(T) : 1);
   // Few rows: many threads for each, so that one row takes little time; many:
   // fewer threads with more pieces, since each joins the row's sums.  bf16 with
-  // a residual, rows x cols, us with one piece a thread and with four: 64 x 4096
-  // 1.9 and 2.3, 256 x 4096 2.3 and 2.6, 512 x 4096 3.1 and 3.2, 2048 x 8192 23.4
-  // and 21.7, 4096 x 4096 21.7 and 21.4.  Up to 128 pieces many rows have a warp
-  // each: 512 x 512 1.8 (a block each: 2.2), 16384 x 512 11.9 (17.6), 16384 x 1024
-  // 21.1 (21.5), up to 32 pieces half a warp: 16384 x 128 3.3 (a warp: 5.0), and up
-  // to 8 pieces 8 lanes: 16384 x 64 2.3 (5.0).
+  // a residual to bf16, rows x cols, us with one piece a thread and with four: 64 x
+  // 4096 1.9 and 2.1, 256 x 4096 2.3 and 2.5, 512 x 4096 3.0 and 3.1, 2048 x 8192
+  // 23.4 and 21.6, 4096 x 4096 21.7 and 21.4.  Up to 128 pieces many rows have a
+  // warp each: 512 x 512 1.8 (a block each: 2.1), 16384 x 512 12.0 (17.6), 16384 x
+  // 1024 21.2 (21.6), up to 32 pieces half a warp: 16384 x 128 3.3 (a warp: 5.0), and
+  // up to 8 pieces 8 lanes: 16384 x 64 2.4 (5.0).
   const bool many = p.rows >= 512;
   auto threads = [](int units, int R) { return ((units + R - 1) / R + 31) / 32 * 32; };
   if (whole) {
@@ -501,13 +505,15 @@ cudaError_t launch_formed(const NormParams& p, cudaStream_t stream) {
     if (n <= 4096) return launch_one<T, kOut, false, 4, 0>(p, threads(n, 4), stream);
     return launch_one<T, kOut, false, kMost, 0>(p, threads(n, kMost), stream);
   }
-  // Words of a thread, by the same rule: few rows 4 (128 x 2881 bf16 2.7 us, 16
-  // words 3.3).  Many rows 12 where that leaves no more places empty than 8, else 8:
-  // 5003 x 2881 f16 to e4m3 with row scales 4 27.9, 8 26.5, 12 25.1, 16 30.3 us, 3359
-  // x 7466 f16 8 27.6, 12 22.7, but 16384 x 777 bf16 8 25.2, 12 32.2.  Up to 256 and 384
-  // words many rows have a warp each: 14607 x 481 bf16 7.6 us (a block each: 15.6), 18503
-  // x 708 f16 to e4m3 27.4 (32.3).  Wide rows 16, since 1,024 threads have 64 registers
-  // each: 4000 x 8191 f32 to e4m3 84 us (8 words: 106).
+  // Words of a thread, by the same rule: few rows 4 (128 x 2881 bf16 with a
+  // residual 2.6 us, 8 words 3.2, 16 4.5).  Many rows 12 where that leaves no more
+  // places empty than 8, else 8: 5003 x 2881 f16 with a residual to e4m3 with row
+  // scales 4 28.6, 8 27.2, 12 25.5, 16 30.9 us, 3359 x 7466 f16 without one 8 27.9,
+  // 12 22.8, but 16384 x 777 bf16 with one 8 25.1, 12 32.2.  Up to 256 and 384 words
+  // many rows have a warp each: 14607 x 481 bf16 without a residual 7.6 us (a block
+  // each: 15.5), 18503 x 708 f16 with one to e4m3 with group scales 27.5 (27.7, with
+  // 8 words 32.6).  Wide rows 16, since 1,024 threads have 64 registers each: 4000 x
+  // 8191 f32 with a residual to e4m3 with group scales 82 us (8 words: 89).
   constexpr int kMost = sizeof(T) == 4 ? 32 : 16;
   const int n = (p.cols + Word<T>::kElems - 1) / Word<T>::kElems;
   if (n <= 128) return launch_one<T, kOut, true, 4, 32>(p, 0, stream);

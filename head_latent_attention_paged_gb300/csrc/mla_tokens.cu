@@ -19,8 +19,8 @@ namespace {
 constexpr int kTokenWarps = 4;
 // Tokens a warp takes one after another, at most: the append's warps keep the
 // norm's weights and the rotation's table, the gather's only their slots (100,011
-// rows into FP8: 8 37.4, 16 37.8 us, into bf16 37.6, 39.3; 204,800 rows out of FP8: 2
-// 66.9, 4 61.4, 8 62.8, 16 66.4 us).
+// rows normed and rotated into FP8: 4 37.9, 8 36.0, 16 37.4 us, into bf16 37.9, 37.2,
+// 39.3; 204,800 rows out of FP8: 2 66.9, 4 61.4, 8 62.8, 16 66.3 us).
 constexpr int kAppendChunk = 8, kGatherChunk = 4;
 
 // The slot of token t in the pool: -1 where the token is to be left alone
@@ -122,17 +122,18 @@ __device__ __forceinline__ void write_row(uint8_t* dst, const uint8_t* stage, in
 }
 
 // One warp per token at a time.  A row costs 1,152 bytes read and 1,152, 594
-// or 324 written; into the quantised caches the number of instructions bounds
-// the kernel (280 a row with norm and rotation, 200 without, issued in 68 % of
-// the cycles), into bf16 ones memory: 100,011 rows of 2,688 bytes' stride with
-// both 36.3 us into FP8 (4.8 TB/s), 34.7 into FP4, 38.0 into bf16 (6.1 TB/s);
-// without 30.5, 27.4 and 37.1.  So every value stays in its lane,
-// one shuffle reduction gives the norm, the cosine and sine are one pair per
-// lane, arithmetic goes in pairs, slots are found one token per lane, the next
-// rows are on their way while one is computed (copied asynchronously into the
-// lane's own places in a ring in shared memory: loads into registers were
-// moved behind the arithmetic by the compiler, 37 -> 60 us for 100,011 rows),
-// and norm and rotation are compiled in or out.
+// or 324 written; 100,011 rows of 2,688 bytes' stride with norm and rotation take
+// 36.0 us into FP8 (4.9 TB/s), 35.9 into FP4, 37.2 into bf16 (6.2 TB/s), and without
+// 29.2, 25.8 and 36.2.  Into bf16 memory bounds the kernel; into the quantised
+// caches it is the warp's own chain of shuffles, stage and write-out: 295 (FP8)
+// and 300 (FP4) instructions a row issue in 70 % of the cycles, with at most 28
+// warps on a multiprocessor, 203 and 211 without norm and rotation.  So every
+// value stays in its lane, one shuffle reduction gives the norm, the cosine and
+// sine are one pair per lane, arithmetic goes in pairs, slots are found one token
+// per lane, the next rows are on their way while one is computed (copied
+// asynchronously into the lane's own places in a ring in shared memory: loads into
+// registers were moved behind the arithmetic by the compiler, 37 -> 60 us when it
+// was tried), and norm and rotation are compiled in or out.
 constexpr int kRing = 3;   // rows of a warp on their way or in use
 
 template <int kKv, bool kNorm, bool kRotate>
@@ -411,8 +412,8 @@ __device__ __forceinline__ RowWords cached_to_bf16(const CachedRow<kKv>& c, int6
 // bytes written.  Slots are found one token per lane, so that the chain
 // position -> page -> row is walked once for a warp's tokens, and two rows are
 // on their way at a time.  204,800 rows out of FP8 61.4 us: the 236 MB written
-// alone take 61.3 us at the 3.85 TB/s of a plain fill; out of FP4 52.4, out of
-// bf16 72.1 us (6.57 TB/s, 0.97 of the copy rate).
+// alone take 61.3 us at the 3.85 TB/s of a plain fill; out of FP4 52.2, out of
+// bf16 71.4 us (6.64 TB/s, 0.98 of the copy rate).
 template <int kKv>
 __global__ void __launch_bounds__(32 * kTokenWarps)
     mla_gather_kernel(const __grid_constant__ GatherParams p, const int32_t chunk) {

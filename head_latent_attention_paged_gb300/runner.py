@@ -157,8 +157,9 @@ class AttentionLayer:
     requests), context() reads cached rows back.  Weights are bf16 tensors on
     the device: hidden_norm [hidden], w_qkv_a [hidden, q_rank + 576], q_norm
     [q_rank], kv_norm [512], w_q_b [q_rank, H * 256], w_uk [H, 512, 192], w_uv
-    [H, 512, 256], w_o [H * 256, hidden].  Buffers are made once: every call
-    can be captured in a CUDA graph, and calls of one AttentionLayer are
+    [H, 512, 256], w_o [H * 256, hidden].  decode()'s buffers are made once,
+    prompt() and context() take theirs from torch's allocator; these three can
+    be captured in a CUDA graph, and calls of one AttentionLayer are
     ordered on one stream, the current one of the layer's device (which need
     not be the current device).
     """
