@@ -235,7 +235,8 @@ def test_a_call_waits_for_another_streams_work(m, captured):
 
 # ---------------------------------------------------------------- many tokens
 @pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
-@pytest.mark.parametrize("tokens,requests,full", [(9731, 5, True), (20011, 7, False), (40009, 3, True), (30000, 6, True)])
+@pytest.mark.parametrize("tokens,requests,full", [(9731, 5, True), (20011, 7, False), (40009, 3, True), (45003, 4, False),
+                                                  (30000, 6, True)])
 def test_many_tokens_of_a_warp(m, kv, tokens, requests, full):
     """Prompt-sized calls, where a warp takes several tokens one after another:
     tokens of no position and of no slot lie between the others, and a last
