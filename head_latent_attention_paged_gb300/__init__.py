@@ -1,8 +1,8 @@
 """Python binding of libmla_gb300.so (paged MLA latent-cache decode, sm_103a).
 
 Argument marshalling only: every step of the decode runs in the library's
-CUDA kernels.  Functions mirror the C ABI in include/mla_decode.h and
-include/mla_layer.h and take
+CUDA kernels.  Functions mirror the C ABI in include/mla_decode.h,
+include/mla_layer.h and include/mla_chunk.h and take
 device addresses as ints (or any object with ``data_ptr()``, e.g. a torch
 tensor) and CUDA streams as ints (``torch.cuda.current_stream().cuda_stream``)
 or None for the default stream.  There is no fallback: if the library cannot
@@ -53,11 +53,15 @@ MLA_ROPE_SCALING_PARTS = 2
 MLA_ROPE_SCALING_YARN = 3
 MLA_ROPE_MAX_DIM = 256
 
+MLA_CHUNK_MAX_HEADS = 128
+
 EXPORTED = (
     "mla_decode_plan", "mla_q_absorb", "mla_decode_run", "mla_combine", "mla_uv_proj",
     "mla_get_status", "mla_clear_status", "mla_strerror", "mla_version",
     "mla_decode_run_static", "mla_cache_append", "mla_selftest_bounded_wait", "mla_decode_step",
     "mla_rms_norm", "mla_rope_make_plan", "mla_rope", "mla_cache_append_tokens", "mla_cache_gather",
+    "mla_chunk_make_plan", "mla_chunk_attend", "mla_cache_weights", "mla_evict_make_plan",
+    "mla_cache_evict",
 )
 
 
@@ -120,6 +124,25 @@ class MlaRopeProblem(ctypes.Structure):
     ]
 
 
+class MlaChunkPlan(ctypes.Structure):
+    _fields_ = [
+        ("problem", MlaProblem), ("tokens", ctypes.c_int32), ("sm_count", ctypes.c_int32),
+        ("context_tokens", ctypes.c_int64), ("clusters", ctypes.c_int32), ("mark", ctypes.c_int32),
+        ("ws_partial_o", ctypes.c_int64), ("ws_partial_lse", ctypes.c_int64),
+        ("ws_segments", ctypes.c_int64), ("ws_starts", ctypes.c_int64), ("ws_rows", ctypes.c_int64),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
+class MlaEvictPlan(ctypes.Structure):
+    _fields_ = [
+        ("problem", MlaProblem), ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32),
+        ("recent", ctypes.c_int32), ("mark", ctypes.c_int32), ("most_moves", ctypes.c_int64),
+        ("ws_counts", ctypes.c_int64), ("ws_moves", ctypes.c_int64),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 class MlaError(RuntimeError):
     def __init__(self, fn: str, code: int):
         self.code = code
@@ -155,6 +178,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mla_cache_append_tokens.argtypes = [P(MlaProblem), i32, vp, i64, vp, vp, vp, vp,
                                             ctypes.c_float, P(MlaRopePlan), vp, vp, vp]
     lib.mla_cache_gather.argtypes = [P(MlaProblem), i32, vp, vp, vp, vp, vp, i64, vp, vp]
+    lib.mla_chunk_make_plan.argtypes = [P(MlaProblem), i32, i64, i32, P(MlaChunkPlan), P(sz)]
+    lib.mla_chunk_attend.argtypes = [P(MlaChunkPlan), vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp]
+    lib.mla_cache_weights.argtypes = [P(MlaChunkPlan), vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, i64, vp, vp]
+    lib.mla_evict_make_plan.argtypes = [P(MlaProblem), i32, i32, i32, P(MlaEvictPlan), P(sz)]
+    lib.mla_cache_evict.argtypes = [P(MlaEvictPlan), vp, vp, vp, vp, vp, i64, vp, sz, vp, vp, vp, vp, vp]
     lib.mla_selftest_bounded_wait.argtypes = [vp, i64, vp, vp]
     lib.mla_get_status.argtypes = [P(MlaPlan), vp, P(ctypes.c_uint32), vp]
     lib.mla_clear_status.argtypes = [P(MlaPlan), vp, vp]
@@ -420,6 +448,97 @@ def mla_cache_gather(problem: MlaProblem, tokens: int, kv_cache, positions, bloc
             _ptr(out), out_stride, _ptr(status), _stream(stream))
     if rc:
         raise MlaError("mla_cache_gather", rc)
+
+
+def mla_chunk_make_plan(problem: MlaProblem, tokens: int, context_tokens: int = 0,
+                        sm_count: int = 152) -> MlaChunkPlan:
+    """The plan of mla_chunk_attend and mla_cache_weights for `tokens` query
+    tokens; context_tokens: the most cached rows of one call (quantised caches)."""
+    plan, ws = MlaChunkPlan(), ctypes.c_size_t(0)
+    _check("mla_chunk_make_plan", load().mla_chunk_make_plan(
+        ctypes.byref(problem), int(tokens), int(context_tokens), int(sm_count), ctypes.byref(plan),
+        ctypes.byref(ws)))
+    return plan
+
+
+def mla_chunk_attend(plan: MlaChunkPlan, q_hat, query_starts, kv_cache, block_table, seq_lens,
+                     workspace, o_lat, lse, status=None, stream=None, workspace_bytes=None) -> None:
+    """Causal attention of the new tokens query_starts[b] .. query_starts[b + 1]
+    of each request over its cached rows (its own among them): o_lat bf16
+    [tokens][H][512], lse f32 [tokens][H]."""
+    size = _nbytes(workspace, workspace_bytes, plan)
+    try:
+        rc = _lib.mla_chunk_attend(
+            plan, q_hat.data_ptr(), query_starts.data_ptr(), kv_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), workspace.data_ptr(), size,
+            o_lat.data_ptr(), lse.data_ptr(), None if status is None else status.data_ptr(),
+            None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = load().mla_chunk_attend(
+            plan, _ptr(q_hat), _ptr(query_starts), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens),
+            _ptr(workspace), size, _ptr(o_lat), _ptr(lse), _ptr(status), _stream(stream))
+    if rc:
+        raise MlaError("mla_chunk_attend", rc)
+
+
+def mla_cache_weights(plan: MlaChunkPlan, q_hat, lse, query_starts, kv_cache, block_table, seq_lens,
+                      workspace, weights_out, weights_in=None, stride=None, status=None, stream=None,
+                      workspace_bytes=None) -> None:
+    """weights_out[b][t] = weights_in[b][t] (None: 0) + the weight that request
+    b's queries give to its cached row t, f32 [batch][stride] (stride None: of a
+    tensor, its last dimension)."""
+    size = _nbytes(workspace, workspace_bytes, plan)
+    stride = int(weights_out.shape[-1]) if stride is None else stride
+    try:
+        rc = _lib.mla_cache_weights(
+            plan, q_hat.data_ptr(), lse.data_ptr(), query_starts.data_ptr(), kv_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), workspace.data_ptr(), size,
+            None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(), stride,
+            None if status is None else status.data_ptr(),
+            None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = load().mla_cache_weights(
+            plan, _ptr(q_hat), _ptr(lse), _ptr(query_starts), _ptr(kv_cache), _ptr(block_table),
+            _ptr(seq_lens), _ptr(workspace), size, _ptr(weights_in), _ptr(weights_out), stride,
+            _ptr(status), _stream(stream))
+    if rc:
+        raise MlaError("mla_cache_weights", rc)
+
+
+def mla_evict_make_plan(problem: MlaProblem, budget: int, sinks: int = 0, recent: int = 0) -> MlaEvictPlan:
+    """The plan of mla_cache_evict: rows that a request keeps, and which positions
+    are kept before all others (the first `sinks`, the last `recent`)."""
+    plan, ws = MlaEvictPlan(), ctypes.c_size_t(0)
+    _check("mla_evict_make_plan", load().mla_evict_make_plan(
+        ctypes.byref(problem), int(budget), int(sinks), int(recent), ctypes.byref(plan), ctypes.byref(ws)))
+    return plan
+
+
+def mla_cache_evict(plan: MlaEvictPlan, kv_cache, block_table, seq_lens, weights, positions,
+                    workspace, seq_lens_out=None, weights_out=None, positions_out=None, stride=None,
+                    status=None, stream=None, workspace_bytes=None) -> None:
+    """Cut each request's cache to the plan's budget: kept rows behind it move
+    into the slots below that became free.  Outputs that are not given are their
+    inputs."""
+    size = _nbytes(workspace, workspace_bytes, plan)
+    stride = int(weights.shape[-1]) if stride is None else stride
+    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    weights_out = weights if weights_out is None else weights_out
+    positions_out = positions if positions_out is None else positions_out
+    try:
+        rc = _lib.mla_cache_evict(
+            plan, kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), weights.data_ptr(),
+            positions.data_ptr(), stride, workspace.data_ptr(), size, seq_lens_out.data_ptr(),
+            weights_out.data_ptr(), positions_out.data_ptr(),
+            None if status is None else status.data_ptr(),
+            None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = load().mla_cache_evict(
+            plan, _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens), _ptr(weights), _ptr(positions),
+            stride, _ptr(workspace), size, _ptr(seq_lens_out), _ptr(weights_out),
+            _ptr(positions_out), _ptr(status), _stream(stream))
+    if rc:
+        raise MlaError("mla_cache_evict", rc)
 
 
 def mla_get_status(plan: MlaPlan, workspace, stream=None) -> int:

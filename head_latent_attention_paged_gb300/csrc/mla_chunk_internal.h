@@ -1,0 +1,77 @@
+// Internal declarations of the operators in include/mla_chunk.h.
+#pragma once
+
+#include "../../include/mla_chunk.h"
+#include "mla_layer_internal.h"
+
+namespace mla {
+
+// What the attention and the weights read alike.
+struct ChunkParams {
+  const uint16_t* q;            // bf16 [tokens][heads][576]
+  const int32_t* starts;        // [batch + 1]
+  const uint8_t* kv;
+  const int32_t* block_table;   // [batch][max_pages]
+  const int32_t* lens;          // [batch]
+  uint32_t* status;             // or null
+  int32_t tokens, batch, heads;
+  int32_t page_shift, num_pages, max_pages, kv_dtype, causal;
+  float scale_log2;             // sm_scale * log2(e)
+};
+
+struct AttendParams {
+  ChunkParams c;
+  uint16_t* o;                  // bf16 [tokens][heads][512]
+  float* lse;                   // [tokens][heads]
+};
+cudaError_t launch_chunk_attend(const AttendParams& p, cudaStream_t stream);
+
+struct WeightsParams {
+  ChunkParams c;
+  const float* lse;
+  const float* in;              // [batch][stride], or null
+  float* out;                   // [batch][stride]
+  int64_t stride;
+};
+cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t stream);
+
+struct EvictParams {
+  uint8_t* kv;
+  const int32_t* block_table;
+  const int32_t* lens;
+  const float* weights;
+  const int32_t* positions;
+  int32_t* lens_out;
+  float* weights_out;
+  int32_t* positions_out;
+  int32_t* counts;              // [batch] rows to move
+  int32_t* moves;               // [batch][most_moves][2]: slot to, slot from
+  uint32_t* status;             // or null
+  int64_t stride, most_moves;
+  int32_t batch, budget, sinks, recent;
+  int32_t page_shift, num_pages, max_pages, row_bytes;
+};
+cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// A request's new tokens and cached rows; what lies outside its bounds is
+// taken as the nearest one (`bad` says so).
+struct ChunkRequest {
+  int32_t first, count, len;
+  bool bad;
+  __device__ __forceinline__ ChunkRequest(const ChunkParams& p, int32_t b) {
+    const int32_t s = p.starts[b], e = p.starts[b + 1], l = p.lens[b];
+    const int32_t most = p.max_pages << p.page_shift;
+    first = min(max(s, 0), p.tokens);
+    count = min(max(e, first), p.tokens) - first;
+    len = min(max(l, 0), most);
+    bad = s != first || e != first + count || l != len;
+  }
+  // rows that token j of the request sees
+  __device__ __forceinline__ int32_t seen(int32_t j, int32_t causal) const {
+    return causal ? min(max(len - count + j + 1, 0), len) : len;
+  }
+};
+#endif
+
+}  // namespace mla
