@@ -54,6 +54,7 @@ MLA_ROPE_SCALING_YARN = 3
 MLA_ROPE_MAX_DIM = 256
 
 MLA_CHUNK_MAX_HEADS = 128
+MLA_CHUNK_MAX_REQUESTS = 8192
 
 EXPORTED = (
     "mla_decode_plan", "mla_q_absorb", "mla_decode_run", "mla_combine", "mla_uv_proj",

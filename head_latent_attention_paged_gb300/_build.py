@@ -20,7 +20,8 @@ LIB_NAME = "libmla_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["mla_api.cu", "mla_decode.cu", "mla_aux.cu", "mla_static.cu", "mla_append.cu",
            "mla_layer_api.cu", "mla_norm_bf16.cu", "mla_norm_f16.cu", "mla_norm_f32.cu",
-           "mla_rope.cu", "mla_tokens.cu", "mla_chunk_api.cu", "mla_chunk.cu", "mla_evict.cu"]
+           "mla_rope.cu", "mla_tokens.cu", "mla_chunk_api.cu", "mla_chunk.cu", "mla_weights.cu", "mla_expand.cu",
+           "mla_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -36,17 +36,15 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// 2-D bf16 tensor map: `rows` rows of `cols` elements (row stride
-// `row_bytes`), box of box_cols x box_rows, 128-byte swizzle.  Encoded maps
-// are kept in a small table keyed by every argument, so a decode step that
-// reuses its cache and weights does no encoding on the host.
+// Encoded tensor maps are kept in a small table keyed by every argument, so a
+// step that reuses its cache and weights does no encoding on the host.
 struct MapKey {
   const void* base;
   uint64_t cols, rows, row_bytes;
-  uint32_t box_cols, box_rows;
+  uint32_t box_cols, box_rows, box_chunks;   // box_chunks: 0 in a 2-D map
   bool operator==(const MapKey& o) const {
     return base == o.base && cols == o.cols && rows == o.rows && row_bytes == o.row_bytes &&
-           box_cols == o.box_cols && box_rows == o.box_rows;
+           box_cols == o.box_cols && box_rows == o.box_rows && box_chunks == o.box_chunks;
   }
 };
 constexpr int kMapCacheSize = 32;
@@ -55,9 +53,9 @@ MapKey g_map_keys[kMapCacheSize];
 CUtensorMap g_maps[kMapCacheSize];
 int g_map_count = 0, g_map_next = 0;
 
-bool make_map_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
-                   uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows) {
-  const MapKey key{base, cols, rows, row_bytes, box_cols, box_rows};
+// The map of `key`: 2-D, `rows` rows of `cols` elements, or 3-D, the same rows as
+// chunks of 64 elements (x: an element of a chunk, y: a row, z: a chunk).
+bool make_map(CUtensorMap* map, const MapKey& key) {
   {
     std::lock_guard<std::mutex> lock(g_map_mutex);
     for (int i = 0; i < g_map_count; ++i)
@@ -68,11 +66,12 @@ bool make_map_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t r
   }
   auto enc = tensor_map_encoder();
   if (!enc) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+  const bool chunks = key.box_chunks != 0;
+  const cuuint64_t dims[3] = {chunks ? kChunkElems : key.cols, key.rows, key.cols / kChunkElems};
+  const cuuint64_t strides[2] = {key.row_bytes, kChunkElems * 2};
+  const cuuint32_t box[3] = {key.box_cols, key.box_rows, key.box_chunks};
+  const cuuint32_t es[3] = {1, 1, 1};
+  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, chunks ? 3 : 2, const_cast<void*>(key.base), dims, strides, box,
           es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
@@ -86,6 +85,16 @@ bool make_map_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t r
 }  // namespace
 
 namespace mla {
+
+bool make_map_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                   uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows) {
+  return make_map(map, MapKey{base, cols, rows, row_bytes, box_cols, box_rows, 0});
+}
+
+bool make_map_chunks_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                          uint64_t row_bytes, uint32_t box_rows, uint32_t box_chunks) {
+  return make_map(map, MapKey{base, cols, rows, row_bytes, kChunkElems, box_rows, box_chunks});
+}
 
 // The current CUDA context (a driver handle, queried through the runtime's
 // entry-point lookup so the library needs no link-time driver dependency).
@@ -108,7 +117,7 @@ void* current_context() {
 }
 
 cudaError_t set_smem_attr_once(const void* func, int slot, int bytes) {
-  constexpr int kDevices = 64, kSlots = 16;
+  constexpr int kDevices = 64, kSlots = 24;
   static std::mutex mu;
   static int done[kDevices][kSlots] = {};
   static void* ctx_of[kDevices][kSlots] = {};

@@ -1,143 +1,685 @@
-// Attention of a chunk of new tokens over the paged cache, and the weights
-// that queries give to cached rows: one warp per row.
+// Attention of a chunk of new tokens over the paged latent cache: pairs of CTAs
+// (tcgen05, cta_group::2) over the rows (token, head) of a request.
+//
+//     s = scale q . row        S [128 x 128] = Q [128 x 576] K^T
+//     p = exp2(s - ref)        O [128 x 512] += P [128 x 128] V
+//
+// over tiles of 128 cached rows, K the whole rows and V their first 512 values,
+// so the cached tile is the operand of both products.  The running reference
+// of the exponent moves only when a row's maximum outgrows it by 2^8.
+//
+// Why pairs: O takes 128 x 512 accumulators, all of one SM's tensor memory.
+// Two CTAs with 64 of the 128 rows each keep O (256 columns: with M = 128 over
+// a pair, lanes 64..127 hold the second half of a row's columns) beside two S
+// (64 columns each), and the operand that both need is read from both shared
+// memories: each CTA loads half of a tile's tokens for S and half of its latent
+// columns for O.
 #include <cuda_runtime.h>
 
 #include "mla_chunk_internal.h"
+#include "mla_pair.cuh"
 #include "mla_rows.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kRows = 128;              // rows of a row tile, 64 in each CTA
+constexpr int kHalf = 64;
+constexpr int kTok = 128;               // cached rows of a tile
+constexpr int kThreads = 256;           // 4 warps that load and issue, 4 of the softmax
+// Two rings, each a tile deep and filled by a warp of its own (a wait by parity
+// cannot tell a slot's use from the one two before, so every slot has one warp
+// that fills it): K in three 64-wide chunks of this CTA's 64 tokens, V in 32
+// tokens of its 256 columns.
+constexpr int kKChunks = 3, kKSlots = 3, kKSlotBytes = kKChunks * kChunkBytes;
+constexpr int kVTokens = 32, kVSlots = 4, kVSlotBytes = kVTokens * 512;
+constexpr int kQBytes = kChunks * kChunkBytes;
+constexpr int kPBytes = 2 * kChunkBytes;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s per wait
+constexpr int kColO = 0, kColS = 256;   // tensor memory columns
+// What a row tile costs besides its tiles, in tokens of one (its queries' load,
+// its output): the work is cut where the sum of tokens and this is even.
+constexpr int kRowTileCost = 256;
 
-struct RowValues {   // a lane's 18 of a row's 576 values
-  float v[18];
+struct Control {
+  uint64_t k_full[kKSlots], k_empty[kKSlots];   // full: in the leader, both CTAs' bytes
+  uint64_t v_full[kVSlots], v_empty[kVSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], s_free[2], p_full, pv_done;
+  float part[2][2][kHalf];                // [parity][half of the tile][row]: maxima
+  float sums[2][2][kHalf];                // [rounded, not][half][row]
+  int64_t warp_sum[kThreads / 32];
+  int32_t work[6];                        // first (request, row tile, tile) and end
+  uint32_t tmem;
+  int abort;
 };
 
-__device__ __forceinline__ RowValues values_of(const RowWords& r) {
-  RowValues x;
-  const uint32_t w[9] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w, r.key};
-#pragma unroll
-  for (int i = 0; i < 9; ++i) {
-    x.v[2 * i] = bf16_lo(w[i]);
-    x.v[2 * i + 1] = bf16_hi(w[i]);
+constexpr int kOffP = kQBytes, kOffK = kOffP + kPBytes, kOffV = kOffK + kKSlots * kKSlotBytes;
+constexpr int kOffControl = kOffV + kVSlots * kVSlotBytes;
+constexpr int kSmemBytes = kOffControl + sizeof(Control);
+static_assert(kSmemBytes <= kMaxSmemBytes, "shared memory");
+static_assert((MLA_CHUNK_MAX_REQUESTS + 1) * 8 <= kKSlots * kKSlotBytes, "the cost prefix borrows the ring");
+
+struct AttendKernelParams {
+  AttendParams a;
+  float* part_o;                // [2 * clusters][128][512]
+  float* part_lse;              // [2 * clusters][128]
+  int4* segments;               // [2 * clusters]: kind, first row, rows, 0
+  const int32_t* dense;         // [batch + 1] first expanded row, or null: rows in pages
+  int32_t capacity;             // expanded rows there are
+  int32_t box_rows;             // rows of a K box, min(page, 64)
+};
+
+// What a cluster's segment slots say to the merge.
+enum SegmentKind : int32_t { kNone = 0, kOpens = 1, kContinues = 2, kIdle = 3 };
+
+// A request as the work is cut: its rows, row tiles and what each of them sees.
+struct Rows {
+  ChunkRequest r;
+  int32_t limit;                // rows from here on are masked out (expanded rows there are)
+  int64_t rows;                 // (token, head)
+  int32_t row_tiles;
+  __device__ __forceinline__ Rows(const AttendKernelParams& p, int32_t b) : r(p.a.c, b) {
+    rows = static_cast<int64_t>(r.count) * p.a.c.heads;
+    row_tiles = static_cast<int32_t>((rows + kRows - 1) / kRows);
+    limit = r.len;
+    if (p.dense && r.count > 0) limit = min(r.len, max(p.capacity - p.dense[b], 0));
   }
-  return x;
-}
-
-__device__ __forceinline__ float dot(const RowValues& a, const RowValues& b) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 18; ++i) s = fmaf(a.v[i], b.v[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// The pool slot of row t of request b, or -1.
-__device__ __forceinline__ int32_t slot_of(const ChunkParams& p, int32_t b, int32_t t) {
-  const int32_t page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (t >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) {
-    if (p.status) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
-    return -1;
+  __device__ __forceinline__ int32_t tiles(const AttendKernelParams& p, int32_t i) const {
+    const int64_t last = min(static_cast<int64_t>(i + 1) * kRows, rows) - 1;
+    const int32_t n = min(r.seen(static_cast<int32_t>(last / p.a.c.heads), p.a.c.causal), limit);
+    return (n + kTok - 1) / kTok;
   }
-  return (page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+  // the cost of the first i row tiles: what they see, to within a tile each
+  __device__ __forceinline__ int64_t cost(const AttendKernelParams& p, int64_t i) const {
+    const int32_t first = p.a.c.causal ? max(r.len - r.count, 0) : r.len;
+    return i * (kRowTileCost + first) + (p.a.c.causal ? i * i * (kRows / 2) / p.a.c.heads : 0);
+  }
+};
+
+// Where cost x lies: request, row tile and tile.
+__device__ void find_cut(const AttendKernelParams& p, const int64_t* prefix, int64_t x, int32_t* cut) {
+  const int32_t batch = p.a.c.batch;
+  if (x >= prefix[batch]) {
+    cut[0] = batch;
+    cut[1] = cut[2] = 0;
+    return;
+  }
+  int32_t lo = 0, hi = batch - 1;         // the last request whose prefix is at most x
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) / 2;
+    if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  const Rows r(p, lo);
+  const int64_t y = x - prefix[lo];
+  int32_t i = 0, last = r.row_tiles - 1;
+  while (i < last) {
+    const int32_t mid = i + (last - i + 1) / 2;
+    if (r.cost(p, mid) <= y) i = mid; else last = mid - 1;
+  }
+  const int64_t from = r.cost(p, i), to = r.cost(p, i + 1);
+  cut[0] = lo;
+  cut[1] = i;
+  cut[2] = static_cast<int32_t>(r.tiles(p, i) * (y - from) / (to - from));
 }
 
-template <int kKv>
-__device__ __forceinline__ RowValues cached_row(const ChunkParams& p, int32_t slot, int lane) {
-  CachedRow<kKv> c;
-  load_cached(&c, p.kv, slot, lane);
-  return values_of(cached_to_bf16(c, slot));
-}
+// A stretch of one row tile's tiles.
+struct Segment {
+  int32_t b, first_tile, end_tile, tiles;   // tiles: of the whole row tile
+  int32_t row_tile;
+  int64_t row0;                 // of all rows (token, head)
+  int32_t rows;                 // valid ones of 128
+  ChunkRequest r;
+  int32_t limit;
+  bool first;                   // of this cluster
+};
 
-template <int kKv>
-__global__ void __launch_bounds__(32 * kWarps) mla_chunk_attend_kernel(const __grid_constant__ AttendParams p) {
-  const int lane = threadIdx.x & 31;
-  after_predecessor();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int32_t token = static_cast<int32_t>(row / p.c.heads);
-  if (token >= p.c.tokens) return;
-  for (int32_t b = 0; b < p.c.batch; ++b) {
-    const ChunkRequest r(p.c, b);
-    if (r.bad && p.c.status && lane == 0) atomicOr(p.c.status, MLA_STATUS_BAD_INDEX);
-    if (token < r.first || token >= r.first + r.count) continue;
-    RowWords qw;
-    load_row(&qw, p.c.q + row * kDqk, lane);
-    const RowValues q = values_of(qw);
-    float m = -INFINITY, l = 0.f, acc[16] = {};
-    const int32_t seen = r.seen(token - r.first, p.c.causal);
-    for (int32_t t = 0; t < seen; ++t) {
-      const int32_t slot = slot_of(p.c, b, t);
-      if (slot < 0) continue;
-      const RowValues k = cached_row<kKv>(p.c, slot, lane);
-      const float s = dot(q, k) * p.c.scale_log2;
-      const float top = fmaxf(m, s);
-      const float keep = m == -INFINITY ? 0.f : exp2f(m - top), e = exp2f(s - top);
-      m = top;
-      l = l * keep + e;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = fmaf(e, k.v[i], acc[i] * keep);
+// The segments between a cluster's cuts, in order; every role walks them itself.
+struct Walk {
+  int32_t b, i, k;
+  const int32_t* end;
+  bool first = true;
+  __device__ __forceinline__ explicit Walk(const int32_t* work) : b(work[0]), i(work[1]), k(work[2]), end(work + 3) {}
+  template <typename F>
+  __device__ __forceinline__ void each(const AttendKernelParams& p, F f) {
+    while (b < end[0] || (b == end[0] && (i < end[1] || (i == end[1] && k < end[2])))) {
+      const Rows r(p, b);
+      if (i >= r.row_tiles) {
+        ++b;
+        i = k = 0;
+        continue;
+      }
+      const bool last = b == end[0] && i == end[1];
+      const int32_t tiles = r.tiles(p, i);
+      const int64_t local = static_cast<int64_t>(i) * kRows;
+      Segment s{b, k, last ? end[2] : tiles, tiles, i, static_cast<int64_t>(r.r.first) * p.a.c.heads + local,
+                static_cast<int32_t>(min(static_cast<int64_t>(kRows), r.rows - local)), r.r, r.limit, first};
+      first = false;
+      if (!f(s) || last) return;
+      ++i;
+      k = 0;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(make_float2(acc[2 * i] * inv, acc[2 * i + 1] * inv));
-    uint4* o = reinterpret_cast<uint4*>(p.o + row * kDc);
-    o[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-    o[32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
+};
+
+// 2^x with the hardware approximation (2^-inf = 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <int kKv>
-__global__ void __launch_bounds__(32 * kWarps) mla_cache_weights_kernel(const __grid_constant__ WeightsParams p) {
-  const int lane = threadIdx.x & 31;
+// A warp's view of a tile's cached rows: lane l < 8 holds the pool row of the
+// tile's tokens 16 l .. 16 l + 15, or -1.
+struct TileRows {
+  int32_t base;
+  uint32_t bad;                 // pieces of 16 tokens in pages outside the pool
+  bool whole;                   // 128 rows, all there
+  __device__ __forceinline__ TileRows(const AttendKernelParams& p, const Segment& s, int32_t tile, int lane) {
+    const ChunkParams& c = p.a.c;
+    const int32_t tok = tile * kTok + 16 * (lane & 7);
+    base = -1;
+    bool out = false;
+    if (tok < s.limit) {
+      const int32_t page = c.block_table[static_cast<int64_t>(s.b) * c.max_pages + (tok >> c.page_shift)];
+      out = page < 0 || page >= c.num_pages;
+      if (!out) base = p.dense ? p.dense[s.b] + tok : (page << c.page_shift) + (tok & ((1 << c.page_shift) - 1));
+    }
+    bad = __ballot_sync(0xffffffffu, out) & 255u;
+    whole = __all_sync(0xffffffffu, base >= 0) && (tile + 1) * static_cast<int64_t>(kTok) <= s.limit;
+  }
+  // the pool rows of four tokens from t (of the tile, a multiple of 4), -1 for none
+  __device__ __forceinline__ void four(int32_t t, int32_t left, int32_t (&row)[4]) const {
+    const int32_t at = __shfl_sync(0xffffffffu, base, t >> 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q] = at >= 0 && t + q < left ? at + (t & 15) + q : -1;
+  }
+};
+
+struct Maps {
+  CUtensorMap q, k, v, gather;  // boxes of queries, K, V, and one row high
+};
+
+__device__ __forceinline__ void give_up(Control* c, uint32_t* status) {
+  c->abort = 1;
+  if (status) atomicOr(status, MLA_STATUS_TIMEOUT);
+}
+
+// Copies in flight when a role has given up land within microseconds.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mla_chunk_attend_kernel(const __grid_constant__ AttendKernelParams p, const __grid_constant__ Maps maps) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Control* ctl = reinterpret_cast<Control*>(smem + kOffControl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(&ctl->k_full[i], 1);
+      mbar_init(&ctl->k_empty[i], 1);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
+      mbar_init(&ctl->v_full[i], 1);
+      mbar_init(&ctl->v_empty[i], 1);
+    }
+    mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->s_free[i], 8);
+    }
+    mbar_init(&ctl->p_full, 8);
+    mbar_init(&ctl->pv_done, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.gather);
+  }
+  // the pair allocates together: not before both CTAs run
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 2) pair_tmem_alloc(&ctl->tmem, 512);
   after_predecessor();
-  const int32_t b = blockIdx.y;
-  const ChunkRequest r(p.c, b);
-  if (r.bad && p.c.status && threadIdx.x == 0) atomicOr(p.c.status, MLA_STATUS_BAD_INDEX);
-  const int64_t end = r.len < p.stride ? r.len : p.stride;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < end;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    float sum = 0.f;
-    const int32_t slot = r.count > 0 ? slot_of(p.c, b, static_cast<int32_t>(t)) : -1;
-    if (slot >= 0) {
-      const RowValues k = cached_row<kKv>(p.c, slot, lane);
-      for (int32_t j = 0; j < r.count; ++j) {
-        if (t >= r.seen(j, p.c.causal)) continue;
-        for (int32_t h = 0; h < p.c.heads; ++h) {
-          const int64_t row = static_cast<int64_t>(r.first + j) * p.c.heads + h;
-          RowWords qw;
-          load_row(&qw, p.c.q + row * kDqk, lane);
-          const float lse = p.lse[row];
-          const float s = dot(values_of(qw), k) * p.c.scale_log2;
-          sum += lse == -INFINITY ? 0.f : exp2f(s - lse * 1.4426950408889634f);
+
+  // the cost prefix over requests, and this cluster's cuts
+  {
+    int64_t* prefix = reinterpret_cast<int64_t*>(smem + kOffK);
+    const int32_t batch = p.a.c.batch, each = (batch + kThreads - 1) / kThreads;
+    const int32_t lo = min(static_cast<int32_t>(threadIdx.x) * each, batch), hi = min(lo + each, batch);
+    int64_t sum = 0;
+    bool bad = false;
+    for (int32_t b = lo; b < hi; ++b) {
+      const Rows r(p, b);
+      bad |= r.r.bad || r.limit < r.r.len;
+      sum += r.cost(p, r.row_tiles);
+    }
+    if (bad && blockIdx.x == 0 && p.a.c.status) atomicOr(p.a.c.status, MLA_STATUS_BAD_INDEX);
+    int64_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) ctl->warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t at = upto - sum;
+    for (int w = 0; w < warp; ++w) at += ctl->warp_sum[w];
+    for (int32_t b = lo; b < hi; ++b) {
+      prefix[b] = at;
+      const Rows r(p, b);
+      at += r.cost(p, r.row_tiles);
+    }
+    if (threadIdx.x == kThreads - 1) prefix[batch] = at;
+    __syncthreads();
+    if (threadIdx.x == 0 || threadIdx.x == 32) {
+      const int64_t total = prefix[batch];
+      const int c = cluster + (threadIdx.x == 32);
+      find_cut(p, prefix, total / clusters * c + min(static_cast<int64_t>(c), total % clusters),
+               ctl->work + (threadIdx.x == 32 ? 3 : 0));
+    }
+    fence_proxy_async_smem();   // before copies land on the prefix
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();           // both CTAs have their half of tensor memory
+  tc_fence_after();
+
+  const uint32_t tmem = ctl->tmem;
+  volatile int* abort = &ctl->abort;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (pair_wait(bar, parity, abort, kWaitLimitNs)) return true;
+    give_up(ctl, p.a.c.status);
+    return false;
+  };
+  Walk walk(ctl->work);
+  // Use `pos` of a ring of n slots: free to be filled, and (in the leader) what
+  // both CTAs will write to it announced.
+  const auto next_slot = [&](uint64_t* full, uint64_t* empty, uint32_t slot, uint32_t use, uint32_t bytes) {
+    bool ok = true;
+    if (lane == 0) {
+      if (use > 0) ok = wait(&empty[slot], (use - 1) & 1);
+      if (ok && rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
+    }
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  };
+
+  if (warp == 0) {
+    // queries and K: this CTA's 64 rows, and its 64 tokens of every tile
+    uint32_t pos = 0, nq = 0;
+    walk.each(p, [&](const Segment& s) {
+      const int n = s.end_tile - s.first_tile;
+      if (n <= 0) return true;
+      bool ok = true;
+      if (nq > 0 && lane == 0) ok = wait(&ctl->q_empty, (nq - 1) & 1);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+      ++nq;
+      const uint32_t q_bar = mapa_shared(smem_u32(&ctl->q_full), 0);
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(&ctl->q_full, 2 * kQBytes);
+        for (int c = 0; c < kChunks; c += kKChunks)
+          pair_tma_load_3d(smem + c * kChunkBytes, &maps.q, q_bar, 0, static_cast<int32_t>(s.row0) + kHalf * rank, c);
+      }
+      for (int i = 0; i < n; ++i) {
+        const int32_t tile = s.first_tile + i;
+        const TileRows rows(p, s, tile, lane);
+        if (rows.bad && rank == 0 && lane == 0 && p.a.c.status) atomicOr(p.a.c.status, MLA_STATUS_BAD_PAGE);
+        const int32_t left = s.limit - tile * kTok;
+        // boxes of box_rows tokens, all three chunks at once where a box holds all 64
+        const int pieces = kHalf / p.box_rows, boxes = pieces == 1 ? 1 : kKChunks * pieces;
+        const int piece = lane & (pieces - 1), chunk = lane / pieces;
+        const int32_t row = __shfl_sync(0xffffffffu, rows.base, 4 * rank + piece * (p.box_rows >> 4));
+        int32_t four[4];
+        rows.four(kHalf * rank + 4 * (lane & 15), left, four);
+        for (int j = 0; j < kKSlots; ++j, ++pos) {
+          const uint32_t slot = pos % kKSlots;
+          if (!next_slot(ctl->k_full, ctl->k_empty, slot, pos / kKSlots, kKSlotBytes)) return false;
+          uint8_t* dst = smem + kOffK + slot * kKSlotBytes;
+          const uint32_t bar = mapa_shared(smem_u32(&ctl->k_full[slot]), 0);
+          if (rows.whole) {
+            if (lane < boxes)
+              pair_tma_load_3d(dst + chunk * kChunkBytes + piece * p.box_rows * 128, &maps.k, bar, 0, row,
+                               kKChunks * j + chunk);
+          } else {
+            for (int c = lane >> 4; c < kKChunks; c += 2)
+              pair_tma_gather4(dst + c * kChunkBytes + (lane & 15) * 512, &maps.gather, bar,
+                               (kKChunks * j + c) * kChunkElems, four);
+          }
         }
       }
+      return true;
+    });
+  } else if (warp == 3) {
+    // V: this CTA's 256 latent columns of every token of the tile
+    uint32_t pos = 0;
+    const int v_rows = min(p.box_rows, 32);
+    walk.each(p, [&](const Segment& s) {
+      const int n = s.end_tile - s.first_tile;
+      if (n <= 0) return true;
+      for (int i = 0; i < n; ++i) {
+        const int32_t tile = s.first_tile + i;
+        const TileRows rows(p, s, tile, lane);
+        const int32_t left = s.limit - tile * kTok;
+        for (int g = 0; g < kVSlots; ++g, ++pos) {
+          const uint32_t slot = pos % kVSlots;
+          if (!next_slot(ctl->v_full, ctl->v_empty, slot, pos / kVSlots, kVSlotBytes)) return false;
+          uint8_t* dst = smem + kOffV + slot * kVSlotBytes;
+          const uint32_t bar = mapa_shared(smem_u32(&ctl->v_full[slot]), 0);
+          if (rows.whole) {
+            const int32_t row = __shfl_sync(0xffffffffu, rows.base, 2 * g + (lane & 1));
+            if (lane < 32 / v_rows)
+              pair_tma_load_3d(dst + lane * (kVSlotBytes / 2), &maps.v, bar, 0, row, 4 * rank);
+          } else {
+            const int atom = lane >> 3, group = lane & 7;
+            int32_t four[4];
+            rows.four(32 * g + 4 * group, left, four);
+            const int offset = v_rows == 32 ? atom * 4096 + group * 512
+                                            : (group >> 2) * (kVSlotBytes / 2) + atom * 2048 + (group & 3) * 512;
+            pair_tma_gather4(dst + offset, &maps.gather, bar, (4 * rank + atom) * kChunkElems, four);
+          }
+        }
+      }
+      return true;
+    });
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      // the pair's MMAs: S of tile i, then O += P V of tile i - 1
+      const uint32_t idesc_s = make_idesc_bf16(kRows, kTok, false, false);
+      const uint32_t idesc_o = make_idesc_bf16(kRows, 256, false, true);
+      const uint64_t q0 = make_smem_desc(smem_u32(smem), 16, 1024, kSmemLayoutSW128);
+      const uint64_t p0 = make_smem_desc(smem_u32(smem + kOffP), 16, 1024, kSmemLayoutSW128);
+      const uint64_t k0 = make_smem_desc(smem_u32(smem + kOffK), 16, 1024, kSmemLayoutSW128);
+      const int v_rows = min(p.box_rows, 32), v_atom = v_rows * 128;
+      const uint64_t v0 = make_smem_desc(smem_u32(smem + kOffV), v_atom, 1024, kSmemLayoutSW128);
+      const int v_step = v_rows == 32 ? 2048 : kVSlotBytes / 2;   // to the slot's second 16 tokens
+      uint32_t k_pos = 0, v_pos = 0, nq = 0, tile = 0;
+      walk.each(p, [&](const Segment& s) {
+        const int n = s.end_tile - s.first_tile;
+        if (n <= 0) return true;
+        if (!wait(&ctl->q_full, nq & 1)) return false;
+        ++nq;
+        for (int i = 0; i <= n; ++i) {
+          if (i < n) {
+            const uint32_t t = tile + i, col = tmem + kColS + 64 * (t & 1);
+            if (t >= 2 && !wait(&ctl->s_free[t & 1], ((t >> 1) - 1) & 1)) return false;
+            for (int j = 0; j < kKSlots; ++j, ++k_pos) {
+              const uint32_t slot = k_pos % kKSlots;
+              if (!wait(&ctl->k_full[slot], (k_pos / kKSlots) & 1)) return false;
+              tc_fence_after();
+              const uint64_t kb = k0 + ((slot * kKSlotBytes) >> 4), qa = q0 + ((j * kKSlotBytes) >> 4);
+#pragma unroll
+              for (int m = 0; m < 4 * kKChunks; ++m) {
+                const uint64_t o = ((m >> 2) * kChunkBytes + (m & 3) * 32) >> 4;
+                pair_mma_bf16(col, qa + o, kb + o, idesc_s, j > 0 || m > 0);
+              }
+              pair_commit(&ctl->k_empty[slot]);
+            }
+            pair_commit(&ctl->s_full[t & 1]);
+            if (i == n - 1) pair_commit(&ctl->q_empty);
+          }
+          if (i > 0) {
+            const uint32_t t = tile + i - 1;
+            if (!wait(&ctl->p_full, t & 1)) return false;
+            for (int g = 0; g < kVSlots; ++g, ++v_pos) {
+              const uint32_t slot = v_pos % kVSlots;
+              if (!wait(&ctl->v_full[slot], (v_pos / kVSlots) & 1)) return false;
+              tc_fence_after();
+              const uint64_t vb = v0 + ((slot * kVSlotBytes) >> 4);
+              const uint64_t pa = p0 + (((g >> 1) * kChunkBytes + (g & 1) * 64) >> 4);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {   // 16 tokens m & 1, columns 128 (m >> 1) .. of each CTA's 256
+                pair_mma_bf16(tmem + kColO + 128 * (m >> 1), pa + (((m & 1) * 32) >> 4),
+                              vb + (((m & 1) * v_step + (m >> 1) * 2 * v_atom) >> 4), idesc_o,
+                              i > 1 || g > 0 || (m & 1));
+              }
+              pair_commit(&ctl->v_empty[slot]);
+            }
+            pair_commit(&ctl->pv_done);
+          }
+        }
+        tile += n;
+        return true;
+      });
     }
-    if (lane == 0) p.out[b * p.stride + t] = (p.in ? p.in[b * p.stride + t] : 0.f) + sum;
+    __syncwarp();
+  } else if (warp >= 4) {
+    // softmax: lane l of tensor memory is row l % 64, tokens 64 (l / 64) ..
+    const int l = threadIdx.x & 127, row = l & 63, half = l >> 6, quad = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t p_bar = mapa_shared(smem_u32(&ctl->p_full), 0);
+    const uint32_t s_bar[2] = {mapa_shared(smem_u32(&ctl->s_free[0]), 0), mapa_shared(smem_u32(&ctl->s_free[1]), 0)};
+    uint8_t* const prow = smem + kOffP + half * kChunkBytes + row * 128;
+    const float scale = p.a.c.scale_log2;
+    uint32_t tile = 0;
+    int slots_used = 0;
+    bool failed = false;
+    walk.each(p, [&](const Segment& s) {
+      const int n = s.end_tile - s.first_tile;
+      const int32_t at = static_cast<int32_t>(kHalf * rank) + row;   // of the row tile
+      const bool valid = at < s.rows;
+      const int64_t grow = s.row0 + at;
+      const int32_t token = static_cast<int32_t>((static_cast<int64_t>(s.row_tile) * kRows + at) / p.a.c.heads);
+      const int32_t seen = valid ? min(s.r.seen(token, p.a.c.causal), s.limit) : 0;
+      float ref = -INFINITY, sum = 0.f, sum_rounded = 0.f;
+      for (int i = 0; i < n; ++i, ++tile) {
+        const TileRows rows(p, s, s.first_tile + i, lane);
+        const int32_t vis = min(max(seen - (s.first_tile + i) * kTok - kHalf * half, 0), kHalf);
+        // a wait that gave up is agreed on at the next barrier of the row's two warps
+        failed |= !__all_sync(0xffffffffu, wait(&ctl->s_full[tile & 1], (tile >> 1) & 1));
+        tc_fence_after();
+        uint32_t x[64];
+        {
+          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(x);
+          uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(x + 32);
+          tmem_ld32(tmem + lanes + kColS + 64 * (tile & 1), lo);
+          tmem_ld32(tmem + lanes + kColS + 64 * (tile & 1) + 32, hi);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_mbar_arrive(s_bar[tile & 1]);
+        const uint32_t bad = (rows.bad >> (4 * half)) & 15u;
+        if (vis < kHalf || bad) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k >= vis || (bad >> (k >> 4) & 1)) x[k] = 0xFF800000u;   // -inf
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+        ctl->part[tile & 1][half][row] = top;
+        if (named_bar_or(1 + (quad & 1), 64, failed)) return false;
+        top = fmaxf(top, ctl->part[tile & 1][half ^ 1][row]) * scale;
+        float grow_by = 1.f;
+        if (top > ref + 8.f) {   // from -inf at once
+          grow_by = exp2_approx(ref - top);
+          ref = top;
+          sum *= grow_by;
+          sum_rounded *= grow_by;
+        }
+        const float base = ref == -INFINITY ? 0.f : ref;
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float a = exp2_approx(fmaf(__uint_as_float(x[2 * k]), scale, -base));
+          const float b = exp2_approx(fmaf(__uint_as_float(x[2 * k + 1]), scale, -base));
+          w[k] = pack_bf16(make_float2(a, b));
+          sum += a + b;
+          sum_rounded += bf16_lo(w[k]) + bf16_hi(w[k]);
+        }
+        if (tile > 0) failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (tile - 1) & 1));
+        if (i > 0 && __any_sync(0xffffffffu, grow_by != 1.f)) {   // rare: 8 more bits than any tile before
+          tc_fence_after();
+          for (int c = 0; c < 256; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tmem + lanes + kColO + c, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * grow_by);
+            tmem_st16(tmem + lanes + kColO + c, o);
+          }
+          tc_fence_before();
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(prow + ((k ^ (row & 7)) << 4)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) cluster_mbar_arrive(p_bar);
+      }
+      // the row's output: whole, or this cluster's part of it
+      if (n > 0) {
+        ctl->sums[0][half][row] = sum_rounded;
+        ctl->sums[1][half][row] = sum;
+        if (named_bar_or(1 + (quad & 1), 64, failed)) return false;
+        sum_rounded += ctl->sums[0][half ^ 1][row];
+        sum += ctl->sums[1][half ^ 1][row];
+        failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (tile - 1) & 1));
+        tc_fence_after();
+      }
+      const float inv = sum_rounded > 0.f || sum_rounded != sum_rounded ? 1.f / sum_rounded : 0.f;
+      const float lse = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+      const bool whole = s.first_tile == 0 && s.end_tile == s.tiles;
+      const int slot = 2 * cluster + (s.first ? 0 : 1);
+      if (!whole) {
+        slots_used |= s.first ? 1 : 2;
+        if (rank == 0 && l == 0)
+          p.segments[slot] = make_int4(s.first_tile == 0 ? kOpens : kContinues, static_cast<int32_t>(s.row0), s.rows, 0);
+      }
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(tmem + lanes + kColO + c, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+        __syncwarp();
+        if (!valid) continue;
+        const bool none = sum == 0.f;     // no row seen: O may hold anything
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+        const int col = 256 * half + c;
+        if (whole) {
+          uint4* out = reinterpret_cast<uint4*>(p.a.o + grow * kDc + col);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              h[q] = pack_bf16(make_float2(__uint_as_float(o[8 * k + 2 * q]), __uint_as_float(o[8 * k + 2 * q + 1])));
+            out[k] = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+          uint4* out = reinterpret_cast<uint4*>(p.part_o + (static_cast<int64_t>(slot) * kRows + at) * kDc + col);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) out[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (valid && half == 0) {
+        if (whole)
+          p.a.lse[grow] = lse;
+        else
+          p.part_lse[slot * kRows + at] = lse;
+      }
+      tc_fence_before();
+      return true;
+    });
+    if (rank == 0 && l == 0) {
+      const bool idle = ctl->work[0] == ctl->work[3] && ctl->work[1] == ctl->work[4] && ctl->work[2] == ctl->work[5];
+      if (!(slots_used & 1)) p.segments[2 * cluster] = make_int4(idle ? kIdle : kNone, 0, 0, 0);
+      if (!(slots_used & 2)) p.segments[2 * cluster + 1] = make_int4(kNone, 0, 0, 0);
+    }
+  }
+  __syncwarp();
+  if (*abort) let_copies_land();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();           // neither CTA leaves while the other may still write to it
+  tc_fence_after();
+  if (warp == 2) pair_tmem_dealloc(tmem, 512);
+  __syncthreads();
+  cluster_sync_all();           // nor leave before both have given it back
+}
+
+// The merge of row tiles that were cut: lse = ln sum exp(lse_i), o = sum
+// exp(lse_i - lse) o_i over the parts in order.  Block (slot, rows): the slot
+// that opens a row tile walks the clusters that continue it.
+constexpr int kMergeRows = 4;
+
+__global__ void __launch_bounds__(128) mla_chunk_merge_kernel(const __grid_constant__ AttendKernelParams p, int clusters) {
+  after_predecessor();
+  const int slot = blockIdx.x;
+  const int4 own = p.segments[slot];
+  const int first = blockIdx.y * kMergeRows;
+  if (own.x != kOpens || first >= own.z) return;
+  const int rows = min(kMergeRows, own.z - first);
+  int end = slot / 2 + 1;       // clusters behind it that continue the row tile, or have no work
+  while (end < clusters) {
+    const int4 s = p.segments[2 * end];
+    if (s.x != kIdle && !(s.x == kContinues && s.y == own.y)) break;
+    ++end;
+  }
+  for (int r = first; r < first + rows; ++r) {
+    float top = p.part_lse[slot * kRows + r];
+    for (int c = slot / 2 + 1; c < end; ++c)
+      if (p.segments[2 * c].x == kContinues) top = fmaxf(top, p.part_lse[2 * c * kRows + r]);
+    const int64_t grow = own.y + static_cast<int64_t>(r);
+    uint2* out = reinterpret_cast<uint2*>(p.a.o + grow * kDc) + threadIdx.x;
+    if (top == -INFINITY) {
+      *out = make_uint2(0, 0);
+      if (threadIdx.x == 0) p.a.lse[grow] = -INFINITY;
+      continue;
+    }
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = slot / 2; c < end; ++c) {
+      const int from = c == slot / 2 ? slot : 2 * c;
+      if (c != slot / 2 && p.segments[from].x != kContinues) continue;
+      const float part = p.part_lse[from * kRows + r];
+      const float e = part == -INFINITY ? 0.f : expf(part - top);
+      const float4 o = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(from) * kRows + r) * kDc)[threadIdx.x];
+      sum += e;
+      acc.x = fmaf(e, o.x, acc.x);
+      acc.y = fmaf(e, o.y, acc.y);
+      acc.z = fmaf(e, o.z, acc.z);
+      acc.w = fmaf(e, o.w, acc.w);
+    }
+    const float inv = 1.f / sum;
+    *out = make_uint2(pack_bf16(make_float2(acc.x * inv, acc.y * inv)), pack_bf16(make_float2(acc.z * inv, acc.w * inv)));
+    if (threadIdx.x == 0) p.a.lse[grow] = top + logf(sum);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_attend(const AttendParams& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.c.tokens) * p.c.heads;
-  const dim3 grid(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
-  const auto launch = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * kWarps, 0, stream, p); };
-  return p.c.kv_dtype == MLA_KV_BF16            ? launch(mla_chunk_attend_kernel<MLA_KV_BF16>)
-         : p.c.kv_dtype == MLA_KV_FP8_E4M3_E8M0 ? launch(mla_chunk_attend_kernel<MLA_KV_FP8_E4M3_E8M0>)
-                                                : launch(mla_chunk_attend_kernel<MLA_KV_FP4_E2M1_E8M0>);
-}
-
-cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t stream) {
-  const dim3 grid(1024, p.c.batch);
-  const auto launch = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * kWarps, 0, stream, p); };
-  return p.c.kv_dtype == MLA_KV_BF16            ? launch(mla_cache_weights_kernel<MLA_KV_BF16>)
-         : p.c.kv_dtype == MLA_KV_FP8_E4M3_E8M0 ? launch(mla_cache_weights_kernel<MLA_KV_FP8_E4M3_E8M0>)
-                                                : launch(mla_cache_weights_kernel<MLA_KV_FP4_E2M1_E8M0>);
+cudaError_t launch_chunk_attend(const AttendParams& a, const ChunkWorkspace& w, cudaStream_t stream) {
+  AttendKernelParams p;
+  p.a = a;
+  p.part_o = w.part_o;
+  p.part_lse = w.part_lse;
+  p.segments = reinterpret_cast<int4*>(w.segments);
+  p.dense = w.starts;
+  p.capacity = w.capacity;
+  p.box_rows = w.starts ? kHalf : a.c.page_shift > 6 ? kHalf : 1 << a.c.page_shift;
+  const void* rows = w.starts ? static_cast<const void*>(w.rows) : a.c.kv;
+  const uint64_t count = w.starts ? static_cast<uint64_t>(w.capacity > 0 ? w.capacity : 1) : static_cast<uint64_t>(a.c.num_pages) << a.c.page_shift;
+  Maps maps;
+  if (!make_map_chunks_bf16(&maps.q, a.c.q, kDqk, static_cast<uint64_t>(a.c.tokens) * a.c.heads, kDqk * 2, kHalf, kKChunks) ||
+      !make_map_chunks_bf16(&maps.k, rows, kDqk, count, kDqk * 2, p.box_rows, p.box_rows == kHalf ? kKChunks : 1) ||
+      !make_map_chunks_bf16(&maps.v, rows, kDqk, count, kDqk * 2, p.box_rows < 32 ? p.box_rows : 32, 4) ||
+      !make_map_bf16(&maps.gather, rows, kDqk, count, kDqk * 2, kChunkElems, 1))
+    return cudaErrorInvalidValue;
+  cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(mla_chunk_attend_kernel), kSmemAttrChunk, kSmemBytes);
+  if (err != cudaSuccess) return err;
+  err = launch_dependent(mla_chunk_attend_kernel, dim3(2 * w.clusters), kThreads, kSmemBytes, stream, p, maps);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(mla_chunk_merge_kernel, dim3(2 * w.clusters, kRows / kMergeRows), 128, 0, stream, p, w.clusters);
 }
 
 }  // namespace mla

@@ -34,7 +34,8 @@ int check_chunk_problem(const mla_problem* pr) {
   if (pr->num_heads < 1 || !(pr->causal == 0 || pr->causal == 1) || !std::isfinite(pr->sm_scale) ||
       pr->sm_scale <= 0.f)
     return MLA_ERR_INVALID_ARGUMENT;
-  if (pr->num_heads > MLA_CHUNK_MAX_HEADS || pr->topk_width != 0) return MLA_ERR_UNSUPPORTED;
+  if (pr->num_heads > MLA_CHUNK_MAX_HEADS || pr->batch > MLA_CHUNK_MAX_REQUESTS || pr->topk_width != 0)
+    return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
 
@@ -67,6 +68,20 @@ int fill_chunk(const mla_chunk_plan* plan, const void* q, const int32_t* starts,
   p->causal = pr.causal;
   p->scale_log2 = pr.sm_scale * 1.4426950408889634f;
   return MLA_OK;
+}
+
+ChunkWorkspace workspace_of(const mla_chunk_plan& plan, void* workspace) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const bool quantised = plan.problem.kv_dtype != MLA_KV_BF16;
+  ChunkWorkspace w;
+  w.part_o = reinterpret_cast<float*>(ws + plan.ws_partial_o);
+  w.part_lse = reinterpret_cast<float*>(ws + plan.ws_partial_lse);
+  w.segments = reinterpret_cast<int32_t*>(ws + plan.ws_segments);
+  w.starts = quantised ? reinterpret_cast<int32_t*>(ws + plan.ws_starts) : nullptr;
+  w.rows = quantised ? reinterpret_cast<uint16_t*>(ws + plan.ws_rows) : nullptr;
+  w.capacity = static_cast<int32_t>(plan.context_tokens);
+  w.clusters = plan.clusters;
+  return w;
 }
 
 }  // namespace
@@ -123,7 +138,10 @@ int mla_chunk_attend(const mla_chunk_plan* plan, const void* q_hat, const int32_
   if (plan->tokens == 0 || plan->problem.batch == 0) return MLA_OK;
   p.o = static_cast<uint16_t*>(o_lat);
   p.lse = lse;
-  return launch_chunk_attend(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const ChunkWorkspace w = workspace_of(*plan, workspace);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (w.starts && launch_expand(p.c, w, st) != cudaSuccess) return MLA_ERR_CUDA;
+  return launch_chunk_attend(p, w, st) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_cache_weights(const mla_chunk_plan* plan, const void* q_hat, const float* lse,

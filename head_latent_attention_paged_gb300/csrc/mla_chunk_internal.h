@@ -24,7 +24,21 @@ struct AttendParams {
   uint16_t* o;                  // bf16 [tokens][heads][512]
   float* lse;                   // [tokens][heads]
 };
-cudaError_t launch_chunk_attend(const AttendParams& p, cudaStream_t stream);
+struct ChunkWorkspace {
+  float* part_o;                // [2 * clusters][128][512]
+  float* part_lse;              // [2 * clusters][128]
+  int32_t* segments;            // [2 * clusters][4]
+  int32_t* starts;              // [batch + 1] each request's first expanded row; null: rows in pages
+  uint16_t* rows;               // bf16 [capacity][576]
+  int32_t capacity, clusters;
+};
+cudaError_t launch_chunk_attend(const AttendParams& p, const ChunkWorkspace& w, cudaStream_t stream);
+
+// A quantised cache's rows, of the requests that have new tokens, as bf16 rows
+// one request behind the other.
+cudaError_t launch_expand(const ChunkParams& p, const ChunkWorkspace& w, cudaStream_t stream);
+
+constexpr int kSmemAttrChunk = 16, kSmemAttrWeights = 17;   // slots of set_smem_attr_once
 
 struct WeightsParams {
   ChunkParams c;

@@ -133,6 +133,16 @@ cudaError_t launch_q_absorb(const CUtensorMap* w_map, const uint16_t* q, uint16_
 // attribute belongs to the current device's context).
 cudaError_t set_smem_attr_once(const void* func, int slot, int bytes);
 
+// 2-D bf16 tensor map: `rows` rows of `cols` elements (row stride `row_bytes`),
+// box of box_cols x box_rows, 128-byte swizzle.
+bool make_map_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                   uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows);
+// 3-D map of the same rows (cols a multiple of 64) as chunks of 64 elements,
+// box of 64 x box_rows x box_chunks: one copy lays the chunks' swizzled tiles
+// of [box_rows][128 bytes] one after another.
+bool make_map_chunks_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                          uint64_t row_bytes, uint32_t box_rows, uint32_t box_chunks);
+
 // The current CUDA context (nullptr if none or unknown).
 void* current_context();
 

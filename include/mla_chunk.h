@@ -36,6 +36,7 @@ extern "C" {
 #endif
 
 #define MLA_CHUNK_MAX_HEADS 128
+#define MLA_CHUNK_MAX_REQUESTS 8192
 
 /* Filled by mla_chunk_make_plan; treat as opaque, keep it alive while in use. */
 typedef struct {
@@ -57,9 +58,9 @@ typedef struct {
 /*
  * mla_chunk_make_plan -- validate a problem and lay out the workspace (host
  * only, no CUDA call).
- *   problem        : the cache and the queries: batch, num_heads (1 ..
- *                    MLA_CHUNK_MAX_HEADS), page_size, num_pages,
- *                    max_pages_per_seq, kv_dtype, causal, sm_scale and the
+ *   problem        : the cache and the queries: batch (up to
+ *                    MLA_CHUNK_MAX_REQUESTS), num_heads (1 .. MLA_CHUNK_MAX_HEADS), page_size,
+ *                    num_pages, max_pages_per_seq, kv_dtype, causal, sm_scale and the
  *                    widths of the row; q_len is not read, topk_width must be 0
  *   tokens         : query tokens of all requests together, >= 0
  *   context_tokens : quantised caches: the most rows that the requests of one

@@ -222,3 +222,16 @@ def test_starts_and_lengths_out_of_range_are_reported(m):
     ro, to, rl, tl = C.attend(case.queries(0), case.paged.rows(0), SCALE)
     L.assert_rounded(f64(case.o[:4]), ro, to, "bf16")
     assert torch.all(case.o[4:] == 0) and torch.all(torch.isinf(case.lse[4:]))
+
+
+def test_fewer_expanded_rows_than_there_are(m):
+    """A quantised cache's rows behind context_tokens are masked out."""
+    case = Case(m, [(2, 90), (3, 200)], 4, 64, "fp8", seed=7)
+    case.plan = m.mla_chunk_make_plan(case.problem, case.tokens, context_tokens=190)
+    case.attend()
+    torch.cuda.synchronize()
+    assert int(case.status) == m.MLA_STATUS_BAD_INDEX
+    ro, to, rl, tl = C.attend(case.queries(0), case.paged.rows(0), SCALE)
+    L.assert_rounded(f64(case.o[:2]), ro, to, "bf16")
+    ro, to, rl, tl = C.attend(case.queries(1), case.paged.rows(1)[:100], SCALE, causal=False)
+    L.assert_rounded(f64(case.o[2:5]), ro, to, "bf16")
