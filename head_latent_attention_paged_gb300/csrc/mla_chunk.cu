@@ -170,6 +170,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // A warp's view of a tile's cached rows: lane l < 8 holds the pool row of the
 // tile's tokens 16 l .. 16 l + 15, or -1.
 struct TileRows {
@@ -194,6 +200,19 @@ struct TileRows {
     const int32_t at = __shfl_sync(0xffffffffu, base, t >> 4);
 #pragma unroll
     for (int q = 0; q < 4; ++q) row[q] = at >= 0 && t + q < left ? at + (t & 15) + q : -1;
+  }
+};
+
+// Which of a tile's pieces of 16 tokens lie in pages outside the pool: lane l < 8
+// looks its piece's page up a tile ahead.
+struct PageCheck {
+  int32_t page;
+  __device__ __forceinline__ void load(const AttendKernelParams& p, const Segment& s, int32_t tile, int lane) {
+    const int32_t tok = tile * kTok + 16 * (lane & 7);
+    page = tok < s.limit ? p.a.c.block_table[static_cast<int64_t>(s.b) * p.a.c.max_pages + (tok >> p.a.c.page_shift)] : 0;
+  }
+  __device__ __forceinline__ uint32_t bad(const AttendKernelParams& p) const {
+    return __ballot_sync(0xffffffffu, page < 0 || page >= p.a.c.num_pages) & 255u;
   }
 };
 
@@ -468,8 +487,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int32_t token = static_cast<int32_t>((static_cast<int64_t>(s.row_tile) * kRows + at) / p.a.c.heads);
       const int32_t seen = valid ? min(s.r.seen(token, p.a.c.causal), s.limit) : 0;
       float ref = -INFINITY, sum = 0.f, sum_rounded = 0.f;
+      PageCheck pages;
+      if (n > 0) pages.load(p, s, s.first_tile, lane);
       for (int i = 0; i < n; ++i, ++tile) {
-        const TileRows rows(p, s, s.first_tile + i, lane);
+        const uint32_t bad = (pages.bad(p) >> (4 * half)) & 15u;
+        if (i + 1 < n) pages.load(p, s, s.first_tile + i + 1, lane);
         const int32_t vis = min(max(seen - (s.first_tile + i) * kTok - kHalf * half, 0), kHalf);
         // a wait that gave up is agreed on at the next barrier of the row's two warps
         failed |= !__all_sync(0xffffffffu, wait(&ctl->s_full[tile & 1], (tile >> 1) & 1));
@@ -484,15 +506,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) cluster_mbar_arrive(s_bar[tile & 1]);
-        const uint32_t bad = (rows.bad >> (4 * half)) & 15u;
         if (vis < kHalf || bad) {
 #pragma unroll
           for (int k = 0; k < 64; ++k)
             if (k >= vis || (bad >> (k >> 4) & 1)) x[k] = 0xFF800000u;   // -inf
         }
-        float top = -INFINITY;
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // chains that run side by side
 #pragma unroll
-        for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+        for (int k = 0; k < 64; k += 2)
+          tops[(k >> 1) & 3] = max3(tops[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+        float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         ctl->part[tile & 1][half][row] = top;
         if (named_bar_or(1 + (quad & 1), 64, failed)) return false;
         top = fmaxf(top, ctl->part[tile & 1][half ^ 1][row]) * scale;
@@ -504,15 +527,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sum_rounded *= grow_by;
         }
         const float base = ref == -INFINITY ? 0.f : ref;
+        const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
         uint32_t w[32];
+        float2 sums[2] = {}, rounded[2] = {};
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          const float a = exp2_approx(fmaf(__uint_as_float(x[2 * k]), scale, -base));
-          const float b = exp2_approx(fmaf(__uint_as_float(x[2 * k + 1]), scale, -base));
-          w[k] = pack_bf16(make_float2(a, b));
-          sum += a + b;
-          sum_rounded += bf16_lo(w[k]) + bf16_hi(w[k]);
+          float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2, base2);
+          e.x = exp2_approx(e.x);
+          e.y = exp2_approx(e.y);
+          w[k] = pack_bf16(e);
+          sums[k & 1] = __fadd2_rn(sums[k & 1], e);
+          rounded[k & 1] = __fadd2_rn(rounded[k & 1], make_float2(bf16_lo(w[k]), bf16_hi(w[k])));
         }
+        sum += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+        sum_rounded += (rounded[0].x + rounded[0].y) + (rounded[1].x + rounded[1].y);
         if (tile > 0) failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (tile - 1) & 1));
         if (i > 0 && __any_sync(0xffffffffu, grow_by != 1.f)) {   // rare: 8 more bits than any tile before
           tc_fence_after();
