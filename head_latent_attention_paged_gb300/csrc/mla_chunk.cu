@@ -638,25 +638,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // The merge of row tiles that were cut: lse = ln sum exp(lse_i), o = sum
 // exp(lse_i - lse) o_i over the parts in order.  Block (slot, rows): the slot
 // that opens a row tile walks the clusters that continue it.
-constexpr int kMergeRows = 4;
+constexpr int kMergeRows = 4, kMergeThreads = 128;   // a thread for 4 of the 512 columns
+constexpr int kMaxParts = kMaxChunkClusters + 1;
 
-__global__ void __launch_bounds__(128) mla_chunk_merge_kernel(const __grid_constant__ AttendKernelParams p, int clusters) {
+__global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const __grid_constant__ AttendKernelParams p, int clusters) {
   after_predecessor();
   const int slot = blockIdx.x;
   const int4 own = p.segments[slot];
   const int first = blockIdx.y * kMergeRows;
   if (own.x != kOpens || first >= own.z) return;
   const int rows = min(kMergeRows, own.z - first);
-  int end = slot / 2 + 1;       // clusters behind it that continue the row tile, or have no work
-  while (end < clusters) {
-    const int4 s = p.segments[2 * end];
-    if (s.x != kIdle && !(s.x == kContinues && s.y == own.y)) break;
-    ++end;
+  // the parts in order: this slot and the first ones of the clusters behind it that
+  // continue the row tile (idle ones between them have none), found side by side
+  __shared__ int parts[kMaxParts], count, done;
+  if (threadIdx.x == 0) {
+    parts[0] = slot;
+    count = 1;
+    done = 0;
+  }
+  __syncthreads();
+  for (int base = slot / 2 + 1; base < clusters && !done; base += kMergeThreads) {
+    const int c = base + threadIdx.x, lane = threadIdx.x & 31;
+    const int4 s = c < clusters ? p.segments[2 * c] : make_int4(kNone, 0, 0, 0);
+    const bool part = s.x == kContinues && s.y == own.y, stop = !part && s.x != kIdle;
+    for (int w = 0; w < kMergeThreads / 32; ++w) {   // a warp's 32 clusters at a time
+      if (w == threadIdx.x >> 5 && !done) {
+        const uint32_t stops = __ballot_sync(0xffffffffu, stop);
+        const uint32_t before = stops ? (1u << (__ffs(stops) - 1)) - 1u : 0xffffffffu;
+        const uint32_t found = __ballot_sync(0xffffffffu, part) & before;
+        if (found >> lane & 1) parts[count + __popc(found & ((1u << lane) - 1u))] = 2 * c;
+        __syncwarp();
+        if (lane == 0) {
+          count += __popc(found);
+          done = stops != 0;
+        }
+      }
+      __syncthreads();
+    }
   }
   for (int r = first; r < first + rows; ++r) {
-    float top = p.part_lse[slot * kRows + r];
-    for (int c = slot / 2 + 1; c < end; ++c)
-      if (p.segments[2 * c].x == kContinues) top = fmaxf(top, p.part_lse[2 * c * kRows + r]);
+    float top = -INFINITY;
+    for (int i = 0; i < count; ++i) top = fmaxf(top, p.part_lse[parts[i] * kRows + r]);
     const int64_t grow = own.y + static_cast<int64_t>(r);
     uint2* out = reinterpret_cast<uint2*>(p.a.o + grow * kDc) + threadIdx.x;
     if (top == -INFINITY) {
@@ -666,9 +688,9 @@ __global__ void __launch_bounds__(128) mla_chunk_merge_kernel(const __grid_const
     }
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = slot / 2; c < end; ++c) {
-      const int from = c == slot / 2 ? slot : 2 * c;
-      if (c != slot / 2 && p.segments[from].x != kContinues) continue;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const int from = parts[i];
       const float part = p.part_lse[from * kRows + r];
       const float e = part == -INFINITY ? 0.f : expf(part - top);
       const float4 o = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(from) * kRows + r) * kDc)[threadIdx.x];
@@ -707,7 +729,7 @@ cudaError_t launch_chunk_attend(const AttendParams& a, const ChunkWorkspace& w, 
   if (err != cudaSuccess) return err;
   err = launch_dependent(mla_chunk_attend_kernel, dim3(2 * w.clusters), kThreads, kSmemBytes, stream, p, maps);
   if (err != cudaSuccess) return err;
-  return launch_dependent(mla_chunk_merge_kernel, dim3(2 * w.clusters, kRows / kMergeRows), 128, 0, stream, p, w.clusters);
+  return launch_dependent(mla_chunk_merge_kernel, dim3(2 * w.clusters, kRows / kMergeRows), kMergeThreads, 0, stream, p, w.clusters);
 }
 
 }  // namespace mla

@@ -105,7 +105,7 @@ int mla_chunk_make_plan(const mla_problem* problem, int32_t tokens, int64_t cont
   pl.tokens = tokens;
   pl.sm_count = sm_count;
   pl.context_tokens = quantised ? context_tokens : 0;
-  pl.clusters = sm_count > 1 ? sm_count / 2 : 1;
+  pl.clusters = sm_count < 4 ? 1 : sm_count / 2 < kMaxChunkClusters ? sm_count / 2 : kMaxChunkClusters;
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t here = at;

@@ -38,6 +38,7 @@ cudaError_t launch_chunk_attend(const AttendParams& p, const ChunkWorkspace& w, 
 // one request behind the other.
 cudaError_t launch_expand(const ChunkParams& p, const ChunkWorkspace& w, cudaStream_t stream);
 
+constexpr int kMaxChunkClusters = 512;   // of a plan: more SMs are taken as 1,024
 constexpr int kSmemAttrChunk = 16, kSmemAttrWeights = 17;   // slots of set_smem_attr_once
 
 struct WeightsParams {
