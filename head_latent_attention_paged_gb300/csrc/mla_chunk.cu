@@ -27,11 +27,12 @@ namespace {
 constexpr int kRows = 128;              // rows of a row tile, 64 in each CTA
 constexpr int kHalf = 64;
 constexpr int kTok = 128;               // cached rows of a tile
-constexpr int kThreads = 256;           // 4 warps that load and issue, 4 of the softmax
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 128 + 32 * kSoftmaxWarps;   // 4 warps that load and issue
 // Two rings, each a tile deep and filled by a warp of its own (a wait by parity
 // cannot tell a slot's use from the one two before, so every slot has one warp
 // that fills it): K in three 64-wide chunks of this CTA's 64 tokens, V in 32
-// tokens of its 256 columns.
+// tokens of its 256 columns.  A slot holds the same part of every tile.
 constexpr int kKChunks = 3, kKSlots = 3, kKSlotBytes = kKChunks * kChunkBytes;
 constexpr int kVTokens = 32, kVSlots = 4, kVSlotBytes = kVTokens * 512;
 constexpr int kQBytes = kChunks * kChunkBytes;
@@ -47,8 +48,7 @@ struct Control {
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_free[2], p_full, pv_done;
-  float part[2][2][kHalf];                // [parity][half of the tile][row]: maxima
-  float sums[2][2][kHalf];                // [rounded, not][half][row]
+  float part[2][4][kHalf];                // [parity][quarter of the tile][row]: maxima, at the end sums
   int64_t warp_sum[kThreads / 32];
   int32_t work[6];                        // first (request, row tile, tile) and end
   uint32_t tmem;
@@ -75,31 +75,34 @@ struct AttendKernelParams {
 enum SegmentKind : int32_t { kNone = 0, kOpens = 1, kContinues = 2, kIdle = 3 };
 
 // A request as the work is cut: its rows, row tiles and what each of them sees.
+// (Rows of all requests together are below 2^31 - 128: checked by the host.)
 struct Rows {
   ChunkRequest r;
   int32_t limit;                // rows from here on are masked out (expanded rows there are)
-  int64_t rows;                 // (token, head)
+  int32_t rows;                 // (token, head)
   int32_t row_tiles;
   __device__ __forceinline__ Rows(const AttendKernelParams& p, int32_t b) : r(p.a.c, b) {
-    rows = static_cast<int64_t>(r.count) * p.a.c.heads;
-    row_tiles = static_cast<int32_t>((rows + kRows - 1) / kRows);
+    rows = r.count * p.a.c.heads;
+    row_tiles = (rows + kRows - 1) / kRows;
     limit = r.len;
     if (p.dense && r.count > 0) limit = min(r.len, max(p.capacity - p.dense[b], 0));
   }
   __device__ __forceinline__ int32_t tiles(const AttendKernelParams& p, int32_t i) const {
-    const int64_t last = min(static_cast<int64_t>(i + 1) * kRows, rows) - 1;
-    const int32_t n = min(r.seen(static_cast<int32_t>(last / p.a.c.heads), p.a.c.causal), limit);
-    return (n + kTok - 1) / kTok;
+    const int32_t last = min((i + 1) * kRows, rows) - 1;
+    const int32_t n = min(r.seen(last / p.a.c.heads, p.a.c.causal), limit);
+    return static_cast<int32_t>((static_cast<uint32_t>(n) + kTok - 1) / kTok);
   }
-  // the cost of the first i row tiles: what they see, to within a tile each
+  // heads times the cost of the first i row tiles: what they see, to within a
+  // tile each (i below 2^24, heads at most 128: the sum over requests stays
+  // below 2^63)
   __device__ __forceinline__ int64_t cost(const AttendKernelParams& p, int64_t i) const {
-    const int32_t first = p.a.c.causal ? max(r.len - r.count, 0) : r.len;
-    return i * (kRowTileCost + first) + (p.a.c.causal ? i * i * (kRows / 2) / p.a.c.heads : 0);
+    const int64_t first = p.a.c.causal ? max(r.len - r.count, 0) : r.len;
+    return i * (kRowTileCost + first) * p.a.c.heads + (p.a.c.causal ? i * i * (kRows / 2) : 0);
   }
 };
 
 // Where cost x lies: request, row tile and tile.
-__device__ void find_cut(const AttendKernelParams& p, const int64_t* prefix, int64_t x, int32_t* cut) {
+__device__ __noinline__ void find_cut(const AttendKernelParams& p, const int64_t* prefix, int64_t x, int32_t* cut) {
   const int32_t batch = p.a.c.batch;
   if (x >= prefix[batch]) {
     cut[0] = batch;
@@ -127,41 +130,38 @@ __device__ void find_cut(const AttendKernelParams& p, const int64_t* prefix, int
 // A stretch of one row tile's tiles.
 struct Segment {
   int32_t b, first_tile, end_tile, tiles;   // tiles: of the whole row tile
-  int32_t row_tile;
-  int64_t row0;                 // of all rows (token, head)
-  int32_t rows;                 // valid ones of 128
-  ChunkRequest r;
+  int32_t row_tile, row0, rows; // row0: of all rows (token, head); rows: valid ones of 128
+  int32_t len, count;           // of the request
   int32_t limit;
-  bool first;                   // of this cluster
+  int32_t first;                // 1: of this cluster
 };
 
 // The segments between a cluster's cuts, in order; every role walks them itself.
+// Not inlined: the roles' loops run from the instruction cache, which one copy of
+// this in each of them would fill.
 struct Walk {
-  int32_t b, i, k;
-  const int32_t* end;
-  bool first = true;
-  __device__ __forceinline__ explicit Walk(const int32_t* work) : b(work[0]), i(work[1]), k(work[2]), end(work + 3) {}
-  template <typename F>
-  __device__ __forceinline__ void each(const AttendKernelParams& p, F f) {
-    while (b < end[0] || (b == end[0] && (i < end[1] || (i == end[1] && k < end[2])))) {
-      const Rows r(p, b);
-      if (i >= r.row_tiles) {
-        ++b;
-        i = k = 0;
-        continue;
-      }
-      const bool last = b == end[0] && i == end[1];
-      const int32_t tiles = r.tiles(p, i);
-      const int64_t local = static_cast<int64_t>(i) * kRows;
-      Segment s{b, k, last ? end[2] : tiles, tiles, i, static_cast<int64_t>(r.r.first) * p.a.c.heads + local,
-                static_cast<int32_t>(min(static_cast<int64_t>(kRows), r.rows - local)), r.r, r.limit, first};
-      first = false;
-      if (!f(s) || last) return;
-      ++i;
-      k = 0;
-    }
-  }
+  int32_t b, i, k, first;
 };
+__device__ __noinline__ bool next_segment(const AttendKernelParams& p, const int32_t* end, Walk* w, Segment* s) {
+  while (w->b < end[0] || (w->b == end[0] && (w->i < end[1] || (w->i == end[1] && w->k < end[2])))) {
+    const Rows r(p, w->b);
+    if (w->i >= r.row_tiles) {
+      ++w->b;
+      w->i = w->k = 0;
+      continue;
+    }
+    const bool last = w->b == end[0] && w->i == end[1];
+    const int32_t tiles = r.tiles(p, w->i), local = w->i * kRows;
+    *s = Segment{w->b, w->k, last ? end[2] : tiles, tiles, w->i, r.r.first * p.a.c.heads + local,
+                 min(kRows, r.rows - local), r.r.len, r.r.count, r.limit, w->first};
+    w->first = 0;
+    ++w->i;
+    w->k = 0;
+    if (last) w->b = end[0] + 1;          // that was all
+    return true;
+  }
+  return false;
+}
 
 // 2^x with the hardware approximation (2^-inf = 0).
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -176,43 +176,40 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// A warp's view of a tile's cached rows: lane l < 8 holds the pool row of the
-// tile's tokens 16 l .. 16 l + 15, or -1.
-struct TileRows {
-  int32_t base;
-  uint32_t bad;                 // pieces of 16 tokens in pages outside the pool
-  bool whole;                   // 128 rows, all there
-  __device__ __forceinline__ TileRows(const AttendKernelParams& p, const Segment& s, int32_t tile, int lane) {
-    const ChunkParams& c = p.a.c;
-    const int32_t tok = tile * kTok + 16 * (lane & 7);
-    base = -1;
-    bool out = false;
-    if (tok < s.limit) {
-      const int32_t page = c.block_table[static_cast<int64_t>(s.b) * c.max_pages + (tok >> c.page_shift)];
-      out = page < 0 || page >= c.num_pages;
-      if (!out) base = p.dense ? p.dense[s.b] + tok : (page << c.page_shift) + (tok & ((1 << c.page_shift) - 1));
-    }
-    bad = __ballot_sync(0xffffffffu, out) & 255u;
-    whole = __all_sync(0xffffffffu, base >= 0) && (tile + 1) * static_cast<int64_t>(kTok) <= s.limit;
-  }
-  // the pool rows of four tokens from t (of the tile, a multiple of 4), -1 for none
-  __device__ __forceinline__ void four(int32_t t, int32_t left, int32_t (&row)[4]) const {
-    const int32_t at = __shfl_sync(0xffffffffu, base, t >> 4);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) row[q] = at >= 0 && t + q < left ? at + (t & 15) + q : -1;
-  }
-};
-
-// Which of a tile's pieces of 16 tokens lie in pages outside the pool: lane l < 8
-// looks its piece's page up a tile ahead.
-struct PageCheck {
+// The pages of a tile, looked up a tile ahead: lane l < 8 has the one of the tile's
+// tokens 16 l .. 16 l + 15.
+struct TilePages {
   int32_t page;
   __device__ __forceinline__ void load(const AttendKernelParams& p, const Segment& s, int32_t tile, int lane) {
     const int32_t tok = tile * kTok + 16 * (lane & 7);
     page = tok < s.limit ? p.a.c.block_table[static_cast<int64_t>(s.b) * p.a.c.max_pages + (tok >> p.a.c.page_shift)] : 0;
   }
+  // pieces of 16 tokens in pages outside the pool
   __device__ __forceinline__ uint32_t bad(const AttendKernelParams& p) const {
     return __ballot_sync(0xffffffffu, page < 0 || page >= p.a.c.num_pages) & 255u;
+  }
+};
+
+// Where a tile's cached rows are: lane l < 8 holds the pool row of the tile's
+// tokens 16 l .. 16 l + 15, or -1.
+struct TileRows {
+  int32_t base, left;           // left: rows of the request from the tile's first on
+  bool whole;                   // 128 rows, all there
+  __device__ __forceinline__ TileRows(const AttendKernelParams& p, const Segment& s, int32_t tile, const TilePages& at,
+                                      int32_t dense, int lane) {
+    const ChunkParams& c = p.a.c;
+    const int32_t tok = tile * kTok + 16 * (lane & 7);
+    left = s.limit - tile * kTok;
+    base = -1;
+    if (tok < s.limit && at.page >= 0 && at.page < c.num_pages)
+      base = p.dense ? dense + tok : (at.page << c.page_shift) + (tok & ((1 << c.page_shift) - 1));
+    whole = __all_sync(0xffffffffu, base >= 0) && left >= kTok;
+  }
+  // the pool rows of four tokens from t (of the tile, a multiple of 4), -1 for none
+  __device__ __forceinline__ void four(int32_t t, int32_t (&row)[4]) const {
+    const int32_t at = __shfl_sync(0xffffffffu, base, t >> 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q] = at >= 0 && t + q < left ? at + (t & 15) + q : -1;
   }
 };
 
@@ -220,21 +217,119 @@ struct Maps {
   CUtensorMap q, k, v, gather;  // boxes of queries, K, V, and one row high
 };
 
-__device__ __forceinline__ void give_up(Control* c, uint32_t* status) {
-  c->abort = 1;
+__device__ __forceinline__ uint8_t* shared_base() {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  return smem;
+}
+__device__ __forceinline__ Control* control() { return reinterpret_cast<Control*>(shared_base() + kOffControl); }
+
+// A wait of a role; false once a role of this CTA has given up.  What rarely runs
+// is kept out of the loops around it (the instruction cache).
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  Control* ctl = control();
+  if (pair_wait(bar, parity, &ctl->abort, kWaitLimitNs)) return true;
+  ctl->abort = 1;
   if (status) atomicOr(status, MLA_STATUS_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  return mbar_test(bar, parity) || wait_on(bar, parity, status);
 }
 
 // Copies in flight when a role has given up land within microseconds.
-__device__ __forceinline__ void let_copies_land() {
+__device__ __noinline__ void let_copies_land() {
   const uint64_t t0 = globaltimer_ns();
   while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
 }
 
+// The loads of one tile into slots that need many copies each: pages below 64 (K)
+// or 32 (V) tokens in boxes of one page, tiles that are not whole row by row in
+// gathers of four, where rows that are not there read as zeros.  Warp-wide; `use`
+// counts the ring's tiles.
+__device__ __noinline__ bool load_k_pieces(const AttendKernelParams& p, const Maps& maps, const TileRows& rows,
+                                           uint32_t use) {
+  Control* ctl = control();
+  const uint32_t rank = cluster_ctarank();
+  const int lane = threadIdx.x & 31;
+  const int pieces = kHalf / p.box_rows, piece = lane & (pieces - 1), chunk = lane / pieces;
+  const int32_t row = __shfl_sync(0xffffffffu, rows.base, 4 * rank + piece * (p.box_rows >> 4));
+  int32_t four[4];
+  rows.four(kHalf * rank + 4 * (lane & 15), four);
+  for (int j = 0; j < kKSlots; ++j) {
+    bool ok = true;
+    if (lane == 0) {
+      ok = use == 0 || wait_on(&ctl->k_empty[j], (use - 1) & 1, p.a.c.status);
+      if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->k_full[j], 2 * kKSlotBytes);
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    uint8_t* dst = shared_base() + kOffK + j * kKSlotBytes;
+    const uint32_t bar = mapa_shared(smem_u32(&ctl->k_full[j]), 0);
+    if (rows.whole) {
+      if (chunk < kKChunks)
+        pair_tma_load_3d(dst + chunk * kChunkBytes + piece * p.box_rows * 128, &maps.k, bar, 0, row, kKChunks * j + chunk);
+    } else {
+      for (int c = lane >> 4; c < kKChunks; c += 2)
+        pair_tma_gather4(dst + c * kChunkBytes + (lane & 15) * 512, &maps.gather, bar, (kKChunks * j + c) * kChunkElems, four);
+    }
+  }
+  return true;
+}
+__device__ __noinline__ bool load_v_pieces(const AttendKernelParams& p, const Maps& maps, const TileRows& rows,
+                                           uint32_t use) {
+  Control* ctl = control();
+  const uint32_t rank = cluster_ctarank();
+  const int lane = threadIdx.x & 31;
+  for (int g = 0; g < kVSlots; ++g) {
+    bool ok = true;
+    if (lane == 0) {
+      ok = use == 0 || wait_on(&ctl->v_empty[g], (use - 1) & 1, p.a.c.status);
+      if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->v_full[g], 2 * kVSlotBytes);
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    uint8_t* dst = shared_base() + kOffV + g * kVSlotBytes;
+    const uint32_t bar = mapa_shared(smem_u32(&ctl->v_full[g]), 0);
+    if (rows.whole) {           // two boxes of 16 tokens, each with its four column tiles
+      const int32_t row = __shfl_sync(0xffffffffu, rows.base, 2 * g + (lane & 1));
+      if (lane < 2) pair_tma_load_3d(dst + lane * (kVSlotBytes / 2), &maps.v, bar, 0, row, 4 * rank);
+    } else {
+      const int atom = lane >> 3, group = lane & 7;
+      int32_t four[4];
+      rows.four(kVTokens * g + 4 * group, four);
+      const int offset = p.box_rows >= kVTokens ? atom * 4096 + group * 512
+                                                : (group >> 2) * (kVSlotBytes / 2) + atom * 2048 + (group & 3) * 512;
+      pair_tma_gather4(dst + offset, &maps.gather, bar, (4 * rank + atom) * kChunkElems, four);
+    }
+  }
+  return true;
+}
+
+// The loads of a whole tile with one copy a slot: lane j < slots has slot j and
+// fills it as soon as it is free.  x: the map's row of each lane, z its chunk.
+template <int kSlots, int kSlotBytes>
+__device__ __forceinline__ bool load_slots(uint64_t* full, uint64_t* empty, uint32_t full_at, uint8_t* dst,
+                                           const CUtensorMap* map, int32_t row, int32_t chunk, uint32_t use,
+                                           bool leader, uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  bool todo = lane < kSlots;
+  for (uint32_t n = 1; __any_sync(0xffffffffu, todo); ++n) {
+    if (todo && (use == 0 || mbar_poll(&empty[lane], (use - 1) & 1))) {
+      if (leader) mbar_arrive_expect_tx(&full[lane], 2 * kSlotBytes);
+      pair_tma_load_3d(dst + lane * kSlotBytes, map, full_at + 8 * lane, 0, row, chunk);
+      todo = false;
+    }
+    if ((n & 1023u) == 0) {     // the slowest of them, with a limit
+      bool ok = true;
+      if (todo) ok = wait_on(&empty[lane], (use - 1) & 1, status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+    }
+  }
+  return true;
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mla_chunk_attend_kernel(const __grid_constant__ AttendKernelParams p, const __grid_constant__ Maps maps) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  Control* ctl = reinterpret_cast<Control*>(smem + kOffControl);
+  uint8_t* const smem = shared_base();
+  Control* const ctl = control();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
@@ -251,9 +346,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->s_free[i], 8);
+      mbar_init(&ctl->s_free[i], 2 * kSoftmaxWarps);
     }
-    mbar_init(&ctl->p_full, 8);
+    mbar_init(&ctl->p_full, 2 * kSoftmaxWarps);
     mbar_init(&ctl->pv_done, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -312,213 +407,172 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
 
   const uint32_t tmem = ctl->tmem;
-  volatile int* abort = &ctl->abort;
-  const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (pair_wait(bar, parity, abort, kWaitLimitNs)) return true;
-    give_up(ctl, p.a.c.status);
-    return false;
-  };
-  Walk walk(ctl->work);
-  // Use `pos` of a ring of n slots: free to be filled, and (in the leader) what
-  // both CTAs will write to it announced.
-  const auto next_slot = [&](uint64_t* full, uint64_t* empty, uint32_t slot, uint32_t use, uint32_t bytes) {
-    bool ok = true;
-    if (lane == 0) {
-      if (use > 0) ok = wait(&empty[slot], (use - 1) & 1);
-      if (ok && rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
-    }
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-  };
+  uint32_t* const status = p.a.c.status;
+  Walk walk{ctl->work[0], ctl->work[1], ctl->work[2], 1};
+  const int32_t* const end = ctl->work + 3;
+  Segment s;
+  bool ok = true;
 
   if (warp == 0) {
     // queries and K: this CTA's 64 rows, and its 64 tokens of every tile
-    uint32_t pos = 0, nq = 0;
-    walk.each(p, [&](const Segment& s) {
-      const int n = s.end_tile - s.first_tile;
-      if (n <= 0) return true;
-      bool ok = true;
-      if (nq > 0 && lane == 0) ok = wait(&ctl->q_empty, (nq - 1) & 1);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    const uint32_t q_bar = mapa_shared(smem_u32(&ctl->q_full), 0), k_bar = mapa_shared(smem_u32(ctl->k_full), 0);
+    uint32_t use = 0, nq = 0;
+    while (ok && next_segment(p, end, &walk, &s)) {
+      if (s.end_tile <= s.first_tile) continue;
+      TilePages pages;
+      pages.load(p, s, s.first_tile, lane);
+      const int32_t dense = p.dense ? p.dense[s.b] : 0;
+      ok = nq == 0 || wait(&ctl->q_empty, (nq - 1) & 1, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
       ++nq;
-      const uint32_t q_bar = mapa_shared(smem_u32(&ctl->q_full), 0);
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(&ctl->q_full, 2 * kQBytes);
-        for (int c = 0; c < kChunks; c += kKChunks)
-          pair_tma_load_3d(smem + c * kChunkBytes, &maps.q, q_bar, 0, static_cast<int32_t>(s.row0) + kHalf * rank, c);
+      if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->q_full, 2 * kQBytes);
+      if (lane < kChunks / kKChunks)
+        pair_tma_load_3d(smem + lane * kKSlotBytes, &maps.q, q_bar, 0, s.row0 + kHalf * static_cast<int32_t>(rank), kKChunks * lane);
+#pragma unroll 1
+      for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
+        const TileRows rows(p, s, tile, pages, dense, lane);
+        if (pages.bad(p) && rank == 0 && lane == 0 && status) atomicOr(status, MLA_STATUS_BAD_PAGE);
+        if (tile + 1 < s.end_tile) pages.load(p, s, tile + 1, lane);
+        if (rows.whole && p.box_rows == kHalf)
+          ok = load_slots<kKSlots, kKSlotBytes>(ctl->k_full, ctl->k_empty, k_bar, smem + kOffK, &maps.k,
+                                                __shfl_sync(0xffffffffu, rows.base, 4 * rank), kKChunks * lane, use,
+                                                rank == 0, status);
+        else
+          ok = load_k_pieces(p, maps, rows, use);
       }
-      for (int i = 0; i < n; ++i) {
-        const int32_t tile = s.first_tile + i;
-        const TileRows rows(p, s, tile, lane);
-        if (rows.bad && rank == 0 && lane == 0 && p.a.c.status) atomicOr(p.a.c.status, MLA_STATUS_BAD_PAGE);
-        const int32_t left = s.limit - tile * kTok;
-        // boxes of box_rows tokens, all three chunks at once where a box holds all 64
-        const int pieces = kHalf / p.box_rows, boxes = pieces == 1 ? 1 : kKChunks * pieces;
-        const int piece = lane & (pieces - 1), chunk = lane / pieces;
-        const int32_t row = __shfl_sync(0xffffffffu, rows.base, 4 * rank + piece * (p.box_rows >> 4));
-        int32_t four[4];
-        rows.four(kHalf * rank + 4 * (lane & 15), left, four);
-        for (int j = 0; j < kKSlots; ++j, ++pos) {
-          const uint32_t slot = pos % kKSlots;
-          if (!next_slot(ctl->k_full, ctl->k_empty, slot, pos / kKSlots, kKSlotBytes)) return false;
-          uint8_t* dst = smem + kOffK + slot * kKSlotBytes;
-          const uint32_t bar = mapa_shared(smem_u32(&ctl->k_full[slot]), 0);
-          if (rows.whole) {
-            if (lane < boxes)
-              pair_tma_load_3d(dst + chunk * kChunkBytes + piece * p.box_rows * 128, &maps.k, bar, 0, row,
-                               kKChunks * j + chunk);
-          } else {
-            for (int c = lane >> 4; c < kKChunks; c += 2)
-              pair_tma_gather4(dst + c * kChunkBytes + (lane & 15) * 512, &maps.gather, bar,
-                               (kKChunks * j + c) * kChunkElems, four);
-          }
-        }
-      }
-      return true;
-    });
+    }
   } else if (warp == 3) {
     // V: this CTA's 256 latent columns of every token of the tile
-    uint32_t pos = 0;
-    const int v_rows = min(p.box_rows, 32);
-    walk.each(p, [&](const Segment& s) {
-      const int n = s.end_tile - s.first_tile;
-      if (n <= 0) return true;
-      for (int i = 0; i < n; ++i) {
-        const int32_t tile = s.first_tile + i;
-        const TileRows rows(p, s, tile, lane);
-        const int32_t left = s.limit - tile * kTok;
-        for (int g = 0; g < kVSlots; ++g, ++pos) {
-          const uint32_t slot = pos % kVSlots;
-          if (!next_slot(ctl->v_full, ctl->v_empty, slot, pos / kVSlots, kVSlotBytes)) return false;
-          uint8_t* dst = smem + kOffV + slot * kVSlotBytes;
-          const uint32_t bar = mapa_shared(smem_u32(&ctl->v_full[slot]), 0);
-          if (rows.whole) {
-            const int32_t row = __shfl_sync(0xffffffffu, rows.base, 2 * g + (lane & 1));
-            if (lane < 32 / v_rows)
-              pair_tma_load_3d(dst + lane * (kVSlotBytes / 2), &maps.v, bar, 0, row, 4 * rank);
-          } else {
-            const int atom = lane >> 3, group = lane & 7;
-            int32_t four[4];
-            rows.four(32 * g + 4 * group, left, four);
-            const int offset = v_rows == 32 ? atom * 4096 + group * 512
-                                            : (group >> 2) * (kVSlotBytes / 2) + atom * 2048 + (group & 3) * 512;
-            pair_tma_gather4(dst + offset, &maps.gather, bar, (4 * rank + atom) * kChunkElems, four);
-          }
-        }
+    const uint32_t v_bar = mapa_shared(smem_u32(ctl->v_full), 0);
+    uint32_t use = 0;
+    while (ok && next_segment(p, end, &walk, &s)) {
+      if (s.end_tile <= s.first_tile) continue;
+      TilePages pages;
+      pages.load(p, s, s.first_tile, lane);
+      const int32_t dense = p.dense ? p.dense[s.b] : 0;
+#pragma unroll 1
+      for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
+        const TileRows rows(p, s, tile, pages, dense, lane);
+        if (tile + 1 < s.end_tile) pages.load(p, s, tile + 1, lane);
+        if (rows.whole && p.box_rows >= kVTokens)
+          ok = load_slots<kVSlots, kVSlotBytes>(ctl->v_full, ctl->v_empty, v_bar, smem + kOffV, &maps.v,
+                                                __shfl_sync(0xffffffffu, rows.base, (2 * lane) & 7), 4 * rank, use,
+                                                rank == 0, status);
+        else
+          ok = load_v_pieces(p, maps, rows, use);
       }
-      return true;
-    });
+    }
   } else if (warp == 1) {
+    // The pair's MMAs go out from two threads, S from this one and O from warp 2's,
+    // so that one's run while the other waits.
     if (rank == 0 && elect_one()) {
-      // the pair's MMAs: S of tile i, then O += P V of tile i - 1
-      const uint32_t idesc_s = make_idesc_bf16(kRows, kTok, false, false);
-      const uint32_t idesc_o = make_idesc_bf16(kRows, 256, false, true);
+      const uint32_t idesc = make_idesc_bf16(kRows, kTok, false, false);
       const uint64_t q0 = make_smem_desc(smem_u32(smem), 16, 1024, kSmemLayoutSW128);
-      const uint64_t p0 = make_smem_desc(smem_u32(smem + kOffP), 16, 1024, kSmemLayoutSW128);
       const uint64_t k0 = make_smem_desc(smem_u32(smem + kOffK), 16, 1024, kSmemLayoutSW128);
-      const int v_rows = min(p.box_rows, 32), v_atom = v_rows * 128;
-      const uint64_t v0 = make_smem_desc(smem_u32(smem + kOffV), v_atom, 1024, kSmemLayoutSW128);
-      const int v_step = v_rows == 32 ? 2048 : kVSlotBytes / 2;   // to the slot's second 16 tokens
-      uint32_t k_pos = 0, v_pos = 0, nq = 0, tile = 0;
-      walk.each(p, [&](const Segment& s) {
-        const int n = s.end_tile - s.first_tile;
-        if (n <= 0) return true;
-        if (!wait(&ctl->q_full, nq & 1)) return false;
-        ++nq;
-        for (int i = 0; i <= n; ++i) {
-          if (i < n) {
-            const uint32_t t = tile + i, col = tmem + kColS + 64 * (t & 1);
-            if (t >= 2 && !wait(&ctl->s_free[t & 1], ((t >> 1) - 1) & 1)) return false;
-            for (int j = 0; j < kKSlots; ++j, ++k_pos) {
-              const uint32_t slot = k_pos % kKSlots;
-              if (!wait(&ctl->k_full[slot], (k_pos / kKSlots) & 1)) return false;
+      uint32_t use = 0, nq = 0;
+      while (ok && next_segment(p, end, &walk, &s)) {
+        if (s.end_tile <= s.first_tile) continue;
+        ok = wait(&ctl->q_full, nq++ & 1, status);
+#pragma unroll 1
+        for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
+          const uint32_t col = tmem + kColS + 64 * (use & 1);
+          ok = use < 2 || wait(&ctl->s_free[use & 1], ((use >> 1) - 1) & 1, status);
+#pragma unroll 1
+          for (int c = 0; ok && c < kChunks; ++c) {
+            if (c % kKChunks == 0) {
+              ok = wait(&ctl->k_full[c / kKChunks], use & 1, status);
               tc_fence_after();
-              const uint64_t kb = k0 + ((slot * kKSlotBytes) >> 4), qa = q0 + ((j * kKSlotBytes) >> 4);
-#pragma unroll
-              for (int m = 0; m < 4 * kKChunks; ++m) {
-                const uint64_t o = ((m >> 2) * kChunkBytes + (m & 3) * 32) >> 4;
-                pair_mma_bf16(col, qa + o, kb + o, idesc_s, j > 0 || m > 0);
-              }
-              pair_commit(&ctl->k_empty[slot]);
             }
-            pair_commit(&ctl->s_full[t & 1]);
-            if (i == n - 1) pair_commit(&ctl->q_empty);
-          }
-          if (i > 0) {
-            const uint32_t t = tile + i - 1;
-            if (!wait(&ctl->p_full, t & 1)) return false;
-            for (int g = 0; g < kVSlots; ++g, ++v_pos) {
-              const uint32_t slot = v_pos % kVSlots;
-              if (!wait(&ctl->v_full[slot], (v_pos / kVSlots) & 1)) return false;
-              tc_fence_after();
-              const uint64_t vb = v0 + ((slot * kVSlotBytes) >> 4);
-              const uint64_t pa = p0 + (((g >> 1) * kChunkBytes + (g & 1) * 64) >> 4);
+            const uint64_t at = (c * kChunkBytes) >> 4;
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {   // 16 tokens m & 1, columns 128 (m >> 1) .. of each CTA's 256
-                pair_mma_bf16(tmem + kColO + 128 * (m >> 1), pa + (((m & 1) * 32) >> 4),
-                              vb + (((m & 1) * v_step + (m >> 1) * 2 * v_atom) >> 4), idesc_o,
-                              i > 1 || g > 0 || (m & 1));
-              }
-              pair_commit(&ctl->v_empty[slot]);
-            }
-            pair_commit(&ctl->pv_done);
+            for (int m = 0; m < 4; ++m) pair_mma_bf16(col, q0 + at + 2 * m, k0 + at + 2 * m, idesc, c > 0 || m > 0);
+            if (c % kKChunks == kKChunks - 1) pair_commit(&ctl->k_empty[c / kKChunks]);
           }
+          pair_commit(&ctl->s_full[use & 1]);
         }
-        tile += n;
-        return true;
-      });
+        pair_commit(&ctl->q_empty);
+      }
     }
     __syncwarp();
-  } else if (warp >= 4) {
-    // softmax: lane l of tensor memory is row l % 64, tokens 64 (l / 64) ..
-    const int l = threadIdx.x & 127, row = l & 63, half = l >> 6, quad = warp & 3;
+  } else if (warp == 2) {
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = make_idesc_bf16(kRows, 256, false, true);
+      const uint64_t p0 = make_smem_desc(smem_u32(smem + kOffP), 16, 1024, kSmemLayoutSW128);
+      const int v_rows = min(p.box_rows, kVTokens), v_atom = v_rows * 128;
+      const uint64_t v0 = make_smem_desc(smem_u32(smem + kOffV), v_atom, 1024, kSmemLayoutSW128);
+      const int v_step = v_rows == kVTokens ? 2048 : kVSlotBytes / 2;   // to the slot's second 16 tokens
+      uint32_t use = 0;
+      while (ok && next_segment(p, end, &walk, &s)) {
+#pragma unroll 1
+        for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
+          ok = wait(&ctl->p_full, use & 1, status);
+#pragma unroll 1
+          for (int g = 0; ok && g < kVSlots; ++g) {
+            ok = wait(&ctl->v_full[g], use & 1, status);
+            tc_fence_after();
+            const uint64_t vb = v0 + ((g * kVSlotBytes) >> 4);
+            const uint64_t pa = p0 + (((g >> 1) * kChunkBytes + (g & 1) * 64) >> 4);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {   // 16 tokens m & 1, columns 128 (m >> 1) .. of each CTA's 256
+              pair_mma_bf16(tmem + kColO + 128 * (m >> 1), pa + (((m & 1) * 32) >> 4),
+                            vb + (((m & 1) * v_step + (m >> 1) * 2 * v_atom) >> 4), idesc,
+                            tile > s.first_tile || g > 0 || (m & 1));
+            }
+            pair_commit(&ctl->v_empty[g]);
+          }
+          pair_commit(&ctl->pv_done);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // softmax: lane l of tensor memory is row l % 64, tokens 64 (l / 64) .. of which
+    // the warps 4 .. 7 take the first 32 and 8 .. 11 the others
+    const int quad = warp & 3, l = quad * 32 + lane, row = l & 63, half = l >> 6, side = (warp >> 2) - 1;
+    const int quarter = 2 * half + side;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t p_bar = mapa_shared(smem_u32(&ctl->p_full), 0);
-    const uint32_t s_bar[2] = {mapa_shared(smem_u32(&ctl->s_free[0]), 0), mapa_shared(smem_u32(&ctl->s_free[1]), 0)};
+    const uint32_t p_bar = mapa_shared(smem_u32(&ctl->p_full), 0), s_bar = mapa_shared(smem_u32(ctl->s_free), 0);
+    const uint32_t row_bar = 1 + (quad & 1);   // the 128 threads of 32 rows
     uint8_t* const prow = smem + kOffP + half * kChunkBytes + row * 128;
     const float scale = p.a.c.scale_log2;
-    uint32_t tile = 0;
+    uint32_t use = 0;
     int slots_used = 0;
     bool failed = false;
-    walk.each(p, [&](const Segment& s) {
+    while (next_segment(p, end, &walk, &s)) {
       const int n = s.end_tile - s.first_tile;
-      const int32_t at = static_cast<int32_t>(kHalf * rank) + row;   // of the row tile
+      const int32_t at = kHalf * static_cast<int32_t>(rank) + row;   // of the row tile
       const bool valid = at < s.rows;
-      const int64_t grow = s.row0 + at;
-      const int32_t token = static_cast<int32_t>((static_cast<int64_t>(s.row_tile) * kRows + at) / p.a.c.heads);
-      const int32_t seen = valid ? min(s.r.seen(token, p.a.c.causal), s.limit) : 0;
+      const ChunkRequest request(s.len, s.count);
+      const int32_t seen = valid ? min(request.seen((s.row_tile * kRows + at) / p.a.c.heads, p.a.c.causal), s.limit) : 0;
       float ref = -INFINITY, sum = 0.f, sum_rounded = 0.f;
-      PageCheck pages;
+      TilePages pages;
       if (n > 0) pages.load(p, s, s.first_tile, lane);
-      for (int i = 0; i < n; ++i, ++tile) {
-        const uint32_t bad = (pages.bad(p) >> (4 * half)) & 15u;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++use) {
+        const uint32_t bad = (pages.bad(p) >> (2 * quarter)) & 3u;
         if (i + 1 < n) pages.load(p, s, s.first_tile + i + 1, lane);
-        const int32_t vis = min(max(seen - (s.first_tile + i) * kTok - kHalf * half, 0), kHalf);
-        // a wait that gave up is agreed on at the next barrier of the row's two warps
-        failed |= !__all_sync(0xffffffffu, wait(&ctl->s_full[tile & 1], (tile >> 1) & 1));
+        const int32_t vis = min(max(seen - (s.first_tile + i) * kTok - 32 * quarter, 0), 32);
+        // a wait that gave up is agreed on at the next barrier of the row's warps
+        failed |= !__all_sync(0xffffffffu, wait(&ctl->s_full[use & 1], (use >> 1) & 1, status));
         tc_fence_after();
-        uint32_t x[64];
-        {
-          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(x);
-          uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(x + 32);
-          tmem_ld32(tmem + lanes + kColS + 64 * (tile & 1), lo);
-          tmem_ld32(tmem + lanes + kColS + 64 * (tile & 1) + 32, hi);
-        }
+        uint32_t x[32];
+        tmem_ld32(tmem + lanes + kColS + 64 * (use & 1) + 32 * side, x);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cluster_mbar_arrive(s_bar[tile & 1]);
-        if (vis < kHalf || bad) {
+        if (lane == 0) cluster_mbar_arrive(s_bar + 8 * (use & 1));
+        if (vis < 32 || bad) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
+          for (int k = 0; k < 32; ++k)
             if (k >= vis || (bad >> (k >> 4) & 1)) x[k] = 0xFF800000u;   // -inf
         }
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // chains that run side by side
 #pragma unroll
-        for (int k = 0; k < 64; k += 2)
+        for (int k = 0; k < 32; k += 2)
           tops[(k >> 1) & 3] = max3(tops[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-        float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-        ctl->part[tile & 1][half][row] = top;
-        if (named_bar_or(1 + (quad & 1), 64, failed)) return false;
-        top = fmaxf(top, ctl->part[tile & 1][half ^ 1][row]) * scale;
+        float* const part = &ctl->part[use & 1][0][row];
+        part[kHalf * quarter] = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+        if (named_bar_or(row_bar, 128, failed)) break;
+        const float top = fmaxf(max3(part[0], part[kHalf], part[2 * kHalf]), part[3 * kHalf]) * scale;
         float grow_by = 1.f;
         if (top > ref + 8.f) {   // from -inf at once
           grow_by = exp2_approx(ref - top);
@@ -528,10 +582,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const float base = ref == -INFINITY ? 0.f : ref;
         const float2 scale2 = make_float2(scale, scale), base2 = make_float2(-base, -base);
-        uint32_t w[32];
+        uint32_t w[16];
         float2 sums[2] = {}, rounded[2] = {};
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
           float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2, base2);
           e.x = exp2_approx(e.x);
           e.y = exp2_approx(e.y);
@@ -541,10 +595,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         sum += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
         sum_rounded += (rounded[0].x + rounded[0].y) + (rounded[1].x + rounded[1].y);
-        if (tile > 0) failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (tile - 1) & 1));
+        if (use > 0) failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (use - 1) & 1, status));
         if (i > 0 && __any_sync(0xffffffffu, grow_by != 1.f)) {   // rare: 8 more bits than any tile before
           tc_fence_after();
-          for (int c = 0; c < 256; c += 16) {
+#pragma unroll 1
+          for (int c = 128 * side; c < 128 * side + 128; c += 16) {
             uint32_t o[16];
             tmem_ld16(tmem + lanes + kColO + c, o);
 #pragma unroll
@@ -554,47 +609,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_before();
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(prow + ((k ^ (row & 7)) << 4)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(prow + (((4 * side + k) ^ (row & 7)) << 4)) =
+              make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) cluster_mbar_arrive(p_bar);
       }
       // the row's output: whole, or this cluster's part of it
       if (n > 0) {
-        ctl->sums[0][half][row] = sum_rounded;
-        ctl->sums[1][half][row] = sum;
-        if (named_bar_or(1 + (quad & 1), 64, failed)) return false;
-        sum_rounded += ctl->sums[0][half ^ 1][row];
-        sum += ctl->sums[1][half ^ 1][row];
-        failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (tile - 1) & 1));
+        if (named_bar_or(row_bar, 128, failed)) break;   // the maxima have been read
+        ctl->part[0][quarter][row] = sum_rounded;
+        ctl->part[1][quarter][row] = sum;
+        failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (use - 1) & 1, status));
+        if (named_bar_or(row_bar, 128, failed)) break;
+        sum_rounded = sum = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          sum_rounded += ctl->part[0][k][row];
+          sum += ctl->part[1][k][row];
+        }
         tc_fence_after();
       }
       const float inv = sum_rounded > 0.f || sum_rounded != sum_rounded ? 1.f / sum_rounded : 0.f;
-      const float lse = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-      const bool whole = s.first_tile == 0 && s.end_tile == s.tiles;
+      const bool whole = s.first_tile == 0 && s.end_tile == s.tiles, none = sum == 0.f;   // none: O may hold anything
       const int slot = 2 * cluster + (s.first ? 0 : 1);
       if (!whole) {
         slots_used |= s.first ? 1 : 2;
-        if (rank == 0 && l == 0)
-          p.segments[slot] = make_int4(s.first_tile == 0 ? kOpens : kContinues, static_cast<int32_t>(s.row0), s.rows, 0);
+        if (rank == 0 && threadIdx.x == 128)
+          p.segments[slot] = make_int4(s.first_tile == 0 ? kOpens : kContinues, s.row0, s.rows, 0);
       }
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(tmem + lanes + kColO + c, o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-        }
+#pragma unroll 1
+      for (int c = 128 * side; c < 128 * side + 128; c += 32) {
+        uint32_t o[32] = {};
         __syncwarp();
+        if (n > 0) tmem_ld32(tmem + lanes + kColO + c, o);
         if (!valid) continue;
-        const bool none = sum == 0.f;     // no row seen: O may hold anything
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
         const int col = 256 * half + c;
         if (whole) {
-          uint4* out = reinterpret_cast<uint4*>(p.a.o + grow * kDc + col);
+          uint4* out = reinterpret_cast<uint4*>(p.a.o + static_cast<int64_t>(s.row0 + at) * kDc + col);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t h[4];
@@ -609,22 +663,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 8; ++k) out[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      if (valid && half == 0) {
-        if (whole)
-          p.a.lse[grow] = lse;
-        else
-          p.part_lse[slot * kRows + at] = lse;
-      }
+      if (valid && quarter == 0)
+        (whole ? p.a.lse[s.row0 + at] : p.part_lse[slot * kRows + at]) =
+            none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       tc_fence_before();
-      return true;
-    });
-    if (rank == 0 && l == 0) {
-      const bool idle = ctl->work[0] == ctl->work[3] && ctl->work[1] == ctl->work[4] && ctl->work[2] == ctl->work[5];
+      if (n > 0 && named_bar_or(row_bar, 128, failed)) break;   // the sums have been read
+    }
+    if (rank == 0 && threadIdx.x == 128) {
+      const bool idle = ctl->work[0] == end[0] && ctl->work[1] == end[1] && ctl->work[2] == end[2];
       if (!(slots_used & 1)) p.segments[2 * cluster] = make_int4(idle ? kIdle : kNone, 0, 0, 0);
       if (!(slots_used & 2)) p.segments[2 * cluster + 1] = make_int4(kNone, 0, 0, 0);
     }
   }
   __syncwarp();
+  volatile int* const abort = &ctl->abort;
   if (*abort) let_copies_land();
   tc_fence_before();
   __syncthreads();

@@ -82,6 +82,7 @@ struct ChunkRequest {
     len = min(max(l, 0), most);
     bad = s != first || e != first + count || l != len;
   }
+  __device__ __forceinline__ ChunkRequest(int32_t rows, int32_t tokens) : first(0), count(tokens), len(rows), bad(false) {}
   // rows that token j of the request sees
   __device__ __forceinline__ int32_t seen(int32_t j, int32_t causal) const {
     return causal ? min(max(len - count + j + 1, 0), len) : len;

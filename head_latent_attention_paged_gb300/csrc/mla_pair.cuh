@@ -46,14 +46,18 @@ __device__ __forceinline__ void cluster_mbar_arrive(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// As mbar_wait without sleeping between looks (the roles that wait here are on the
-// path of every tile).
+// As mbar_wait for roles on the path of every tile: no sleep between looks, and the
+// clock, whose reading takes longer than most of these waits, is looked at only
+// after some hundred of them.
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  if (mbar_test(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
     if (mbar_test(bar, parity)) return true;
-    if ((n & 15u) == 0 && (*abort || globaltimer_ns() - t0 > limit_ns)) return false;
+    if ((n & 255u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort || now - t0 > limit_ns) return false;
+    }
   }
 }
 
