@@ -41,7 +41,7 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s per wait
 constexpr int kColO = 0, kColS = 256;   // tensor memory columns
 // What a row tile costs besides its tiles, in tokens of one (its queries' load,
 // its output): the work is cut where the sum of tokens and this is even.
-constexpr int kRowTileCost = 256;
+constexpr int kRowTileCost = 448;
 
 struct Control {
   uint64_t k_full[kKSlots], k_empty[kKSlots];   // full: in the leader, both CTAs' bytes
@@ -81,6 +81,7 @@ struct Rows {
   int32_t limit;                // rows from here on are masked out (expanded rows there are)
   int32_t rows;                 // (token, head)
   int32_t row_tiles;
+  Rows() = default;
   __device__ __forceinline__ Rows(const AttendKernelParams& p, int32_t b) : r(p.a.c, b) {
     rows = r.count * p.a.c.heads;
     row_tiles = (rows + kRows - 1) / kRows;
@@ -141,10 +142,17 @@ struct Segment {
 // this in each of them would fill.
 struct Walk {
   int32_t b, i, k, first;
+  Rows r;                       // of request `of`
+  int32_t of;
+  __device__ __forceinline__ explicit Walk(const int32_t* work) : b(work[0]), i(work[1]), k(work[2]), first(1), of(-1) {}
 };
 __device__ __noinline__ bool next_segment(const AttendKernelParams& p, const int32_t* end, Walk* w, Segment* s) {
   while (w->b < end[0] || (w->b == end[0] && (w->i < end[1] || (w->i == end[1] && w->k < end[2])))) {
-    const Rows r(p, w->b);
+    if (w->of != w->b) {
+      w->r = Rows(p, w->b);
+      w->of = w->b;
+    }
+    const Rows& r = w->r;
     if (w->i >= r.row_tiles) {
       ++w->b;
       w->i = w->k = 0;
@@ -408,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const uint32_t tmem = ctl->tmem;
   uint32_t* const status = p.a.c.status;
-  Walk walk{ctl->work[0], ctl->work[1], ctl->work[2], 1};
+  Walk walk(ctl->work);
   const int32_t* const end = ctl->work + 3;
   Segment s;
   bool ok = true;
@@ -638,29 +646,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0 && threadIdx.x == 128)
           p.segments[slot] = make_int4(s.first_tile == 0 ? kOpens : kContinues, s.row0, s.rows, 0);
       }
+      // 32 columns of the warp's 32 rows at a time, turned in its part of P (which the
+      // products have read) so that four lanes write 64 bytes of a row together: one
+      // row a lane takes the memory pipe 32 cycles for each store
+      uint8_t* const turn = smem + kOffP + half * kChunkBytes + (quad & 1) * 4096 + side * 2048;
+      const int32_t row0 = kHalf * static_cast<int32_t>(rank) + 32 * (quad & 1);   // of the row tile
 #pragma unroll 1
       for (int c = 128 * side; c < 128 * side + 128; c += 32) {
         uint32_t o[32] = {};
-        __syncwarp();
         if (n > 0) tmem_ld32(tmem + lanes + kColO + c, o);
-        if (!valid) continue;
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
         const int col = 256 * half + c;
         if (whole) {
-          uint4* out = reinterpret_cast<uint4*>(p.a.o + static_cast<int64_t>(s.row0 + at) * kDc + col);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            o[k] = pack_bf16(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])));
+        }
+#pragma unroll 1
+        for (int part = 0; part < (whole ? 1 : 2); ++part) {   // 64 bytes of each row
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t h[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              h[q] = pack_bf16(make_float2(__uint_as_float(o[8 * k + 2 * q]), __uint_as_float(o[8 * k + 2 * q + 1])));
-            out[k] = make_uint4(h[0], h[1], h[2], h[3]);
+            const uint4 v = part == 0 ? make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3])
+                                      : make_uint4(o[16 + 4 * k], o[17 + 4 * k], o[18 + 4 * k], o[19 + 4 * k]);
+            *reinterpret_cast<uint4*>(turn + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = v;
           }
-        } else {
-          uint4* out = reinterpret_cast<uint4*>(p.part_o + (static_cast<int64_t>(slot) * kRows + at) * kDc + col);
+          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) out[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + (lane >> 2), k = lane & 3;
+            const uint4 v = *reinterpret_cast<const uint4*>(turn + r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
+            if (row0 + r < s.rows) {
+              if (whole)
+                *reinterpret_cast<uint4*>(p.a.o + static_cast<int64_t>(s.row0 + row0 + r) * kDc + col + 8 * k) = v;
+              else
+                *reinterpret_cast<uint4*>(p.part_o + (static_cast<int64_t>(slot) * kRows + row0 + r) * kDc + col + 16 * part + 4 * k) = v;
+            }
+          }
+          __syncwarp();
         }
       }
       if (valid && quarter == 0)
@@ -688,74 +711,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // The merge of row tiles that were cut: lse = ln sum exp(lse_i), o = sum
-// exp(lse_i - lse) o_i over the parts in order.  Block (slot, rows): the slot
-// that opens a row tile walks the clusters that continue it.
-constexpr int kMergeRows = 4, kMergeThreads = 128;   // a thread for 4 of the 512 columns
+// exp(lse_i - lse) o_i over the parts in order.  Block (slot, 8 rows), a warp for
+// a row; the slot that opens a row tile looks for the clusters that continue it.
+constexpr int kMergeWarps = 8;
 constexpr int kMaxParts = kMaxChunkClusters + 1;
 
-__global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const __grid_constant__ AttendKernelParams p, int clusters) {
+__global__ void __launch_bounds__(32 * kMergeWarps) mla_chunk_merge_kernel(const __grid_constant__ AttendKernelParams p, int clusters) {
+  __shared__ int parts[kMaxParts], s_count;
   after_predecessor();
-  const int slot = blockIdx.x;
+  const int slot = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 own = p.segments[slot];
-  const int first = blockIdx.y * kMergeRows;
-  if (own.x != kOpens || first >= own.z) return;
-  const int rows = min(kMergeRows, own.z - first);
-  // the parts in order: this slot and the first ones of the clusters behind it that
-  // continue the row tile (idle ones between them have none), found side by side
-  __shared__ int parts[kMaxParts], count, done;
-  if (threadIdx.x == 0) {
-    parts[0] = slot;
-    count = 1;
-    done = 0;
+  const int r = blockIdx.y * kMergeWarps + warp;
+  if (own.x != kOpens || static_cast<int>(blockIdx.y) * kMergeWarps >= own.z) return;
+  // the parts in order: this slot, and the first ones of the clusters behind it that
+  // continue the row tile (idle ones between them have none)
+  if (warp == 0) {
+    int count = 1;
+    if (lane == 0) parts[0] = slot;
+    for (int base = slot / 2 + 1; base < clusters; base += 32) {
+      const int c = base + lane;
+      const int4 s = c < clusters ? p.segments[2 * c] : make_int4(kNone, 0, 0, 0);
+      const bool part = s.x == kContinues && s.y == own.y, stop = !part && s.x != kIdle;
+      const uint32_t stops = __ballot_sync(0xffffffffu, stop);
+      const uint32_t before = stops ? (1u << (__ffs(stops) - 1)) - 1u : 0xffffffffu;
+      const uint32_t found = __ballot_sync(0xffffffffu, part) & before;
+      if (found >> lane & 1) parts[count + __popc(found & ((1u << lane) - 1u))] = 2 * c;
+      count += __popc(found);
+      if (stops) break;
+    }
+    if (lane == 0) s_count = count;
   }
   __syncthreads();
-  for (int base = slot / 2 + 1; base < clusters && !done; base += kMergeThreads) {
-    const int c = base + threadIdx.x, lane = threadIdx.x & 31;
-    const int4 s = c < clusters ? p.segments[2 * c] : make_int4(kNone, 0, 0, 0);
-    const bool part = s.x == kContinues && s.y == own.y, stop = !part && s.x != kIdle;
-    for (int w = 0; w < kMergeThreads / 32; ++w) {   // a warp's 32 clusters at a time
-      if (w == threadIdx.x >> 5 && !done) {
-        const uint32_t stops = __ballot_sync(0xffffffffu, stop);
-        const uint32_t before = stops ? (1u << (__ffs(stops) - 1)) - 1u : 0xffffffffu;
-        const uint32_t found = __ballot_sync(0xffffffffu, part) & before;
-        if (found >> lane & 1) parts[count + __popc(found & ((1u << lane) - 1u))] = 2 * c;
-        __syncwarp();
-        if (lane == 0) {
-          count += __popc(found);
-          done = stops != 0;
-        }
-      }
-      __syncthreads();
-    }
-  }
-  for (int r = first; r < first + rows; ++r) {
-    float top = -INFINITY;
-    for (int i = 0; i < count; ++i) top = fmaxf(top, p.part_lse[parts[i] * kRows + r]);
-    const int64_t grow = own.y + static_cast<int64_t>(r);
-    uint2* out = reinterpret_cast<uint2*>(p.a.o + grow * kDc) + threadIdx.x;
-    if (top == -INFINITY) {
-      *out = make_uint2(0, 0);
-      if (threadIdx.x == 0) p.a.lse[grow] = -INFINITY;
-      continue;
-    }
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+  const int count = s_count;
+  if (r >= own.z) return;
+  float top = -INFINITY;
+  for (int i = lane; i < count; i += 32) top = fmaxf(top, p.part_lse[parts[i] * kRows + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f;
+  float4 acc[4] = {};
+  if (top != -INFINITY) {
+#pragma unroll 2
     for (int i = 0; i < count; ++i) {
       const int from = parts[i];
+      const float4* o = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(from) * kRows + r) * kDc) + lane;
       const float part = p.part_lse[from * kRows + r];
       const float e = part == -INFINITY ? 0.f : expf(part - top);
-      const float4 o = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(from) * kRows + r) * kDc)[threadIdx.x];
       sum += e;
-      acc.x = fmaf(e, o.x, acc.x);
-      acc.y = fmaf(e, o.y, acc.y);
-      acc.z = fmaf(e, o.z, acc.z);
-      acc.w = fmaf(e, o.w, acc.w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = o[32 * k];
+        acc[k].x = fmaf(e, v.x, acc[k].x);
+        acc[k].y = fmaf(e, v.y, acc[k].y);
+        acc[k].z = fmaf(e, v.z, acc[k].z);
+        acc[k].w = fmaf(e, v.w, acc[k].w);
+      }
     }
-    const float inv = 1.f / sum;
-    *out = make_uint2(pack_bf16(make_float2(acc.x * inv, acc.y * inv)), pack_bf16(make_float2(acc.z * inv, acc.w * inv)));
-    if (threadIdx.x == 0) p.a.lse[grow] = top + logf(sum);
   }
+  const float inv = top == -INFINITY ? 0.f : 1.f / sum;
+  const int64_t grow = own.y + static_cast<int64_t>(r);
+  uint2* out = reinterpret_cast<uint2*>(p.a.o + grow * kDc) + lane;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    out[32 * k] = make_uint2(pack_bf16(make_float2(acc[k].x * inv, acc[k].y * inv)),
+                             pack_bf16(make_float2(acc[k].z * inv, acc[k].w * inv)));
+  if (lane == 0) p.a.lse[grow] = top == -INFINITY ? -INFINITY : top + logf(sum);
 }
 
 }  // namespace
@@ -781,7 +801,7 @@ cudaError_t launch_chunk_attend(const AttendParams& a, const ChunkWorkspace& w, 
   if (err != cudaSuccess) return err;
   err = launch_dependent(mla_chunk_attend_kernel, dim3(2 * w.clusters), kThreads, kSmemBytes, stream, p, maps);
   if (err != cudaSuccess) return err;
-  return launch_dependent(mla_chunk_merge_kernel, dim3(2 * w.clusters, kRows / kMergeRows), kMergeThreads, 0, stream, p, w.clusters);
+  return launch_dependent(mla_chunk_merge_kernel, dim3(2 * w.clusters, kRows / kMergeWarps), 32 * kMergeWarps, 0, stream, p, w.clusters);
 }
 
 }  // namespace mla

@@ -74,6 +74,7 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream);
 struct ChunkRequest {
   int32_t first, count, len;
   bool bad;
+  ChunkRequest() = default;
   __device__ __forceinline__ ChunkRequest(const ChunkParams& p, int32_t b) {
     const int32_t s = p.starts[b], e = p.starts[b + 1], l = p.lens[b];
     const int32_t most = p.max_pages << p.page_shift;
