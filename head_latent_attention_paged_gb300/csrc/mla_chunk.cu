@@ -17,7 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "mla_chunk_internal.h"
-#include "mla_pair.cuh"
+#include "mla_chunk_tiles.cuh"
 #include "mla_rows.cuh"
 
 namespace mla {
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kRows = 128;              // rows of a row tile, 64 in each CTA
 constexpr int kHalf = 64;
-constexpr int kTok = 128;               // cached rows of a tile
+constexpr int kTok = kTileRows;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 128 + 32 * kSoftmaxWarps;   // 4 warps that load and issue
 // Two rings, each a tile deep and filled by a warp of its own (a wait by parity
@@ -37,7 +37,6 @@ constexpr int kKChunks = 3, kKSlots = 3, kKSlotBytes = kKChunks * kChunkBytes;
 constexpr int kVTokens = 32, kVSlots = 4, kVSlotBytes = kVTokens * 512;
 constexpr int kQBytes = kChunks * kChunkBytes;
 constexpr int kPBytes = 2 * kChunkBytes;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;   // 1 s per wait
 constexpr int kColO = 0, kColS = 256;   // tensor memory columns
 // What a row tile costs besides its tiles, in tokens of one (its queries' load,
 // its output): the work is cut where the sum of tokens and this is even.
@@ -66,8 +65,8 @@ struct AttendKernelParams {
   float* part_o;                // [2 * clusters][128][512]
   float* part_lse;              // [2 * clusters][128]
   int4* segments;               // [2 * clusters]: kind, first row, rows, 0
-  const int32_t* dense;         // [batch + 1] first expanded row, or null: rows in pages
-  int32_t capacity;             // expanded rows there are
+  const int32_t* dense;         // as in RowSource
+  int32_t capacity;
   int32_t box_rows;             // rows of a K box, min(page, 64)
 };
 
@@ -85,8 +84,7 @@ struct Rows {
   __device__ __forceinline__ Rows(const AttendKernelParams& p, int32_t b) : r(p.a.c, b) {
     rows = r.count * p.a.c.heads;
     row_tiles = (rows + kRows - 1) / kRows;
-    limit = r.len;
-    if (p.dense && r.count > 0) limit = min(r.len, max(p.capacity - p.dense[b], 0));
+    limit = RowSource{p.a.c, p.dense, p.capacity}.limit(r, b);
   }
   __device__ __forceinline__ int32_t tiles(const AttendKernelParams& p, int32_t i) const {
     const int32_t last = min((i + 1) * kRows, rows) - 1;
@@ -171,56 +169,6 @@ __device__ __noinline__ bool next_segment(const AttendKernelParams& p, const int
   return false;
 }
 
-// 2^x with the hardware approximation (2^-inf = 0).
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// The pages of a tile, looked up a tile ahead: lane l < 8 has the one of the tile's
-// tokens 16 l .. 16 l + 15.
-struct TilePages {
-  int32_t page;
-  __device__ __forceinline__ void load(const AttendKernelParams& p, const Segment& s, int32_t tile, int lane) {
-    const int32_t tok = tile * kTok + 16 * (lane & 7);
-    page = tok < s.limit ? p.a.c.block_table[static_cast<int64_t>(s.b) * p.a.c.max_pages + (tok >> p.a.c.page_shift)] : 0;
-  }
-  // pieces of 16 tokens in pages outside the pool
-  __device__ __forceinline__ uint32_t bad(const AttendKernelParams& p) const {
-    return __ballot_sync(0xffffffffu, page < 0 || page >= p.a.c.num_pages) & 255u;
-  }
-};
-
-// Where a tile's cached rows are: lane l < 8 holds the pool row of the tile's
-// tokens 16 l .. 16 l + 15, or -1.
-struct TileRows {
-  int32_t base, left;           // left: rows of the request from the tile's first on
-  bool whole;                   // 128 rows, all there
-  __device__ __forceinline__ TileRows(const AttendKernelParams& p, const Segment& s, int32_t tile, const TilePages& at,
-                                      int32_t dense, int lane) {
-    const ChunkParams& c = p.a.c;
-    const int32_t tok = tile * kTok + 16 * (lane & 7);
-    left = s.limit - tile * kTok;
-    base = -1;
-    if (tok < s.limit && at.page >= 0 && at.page < c.num_pages)
-      base = p.dense ? dense + tok : (at.page << c.page_shift) + (tok & ((1 << c.page_shift) - 1));
-    whole = __all_sync(0xffffffffu, base >= 0) && left >= kTok;
-  }
-  // the pool rows of four tokens from t (of the tile, a multiple of 4), -1 for none
-  __device__ __forceinline__ void four(int32_t t, int32_t (&row)[4]) const {
-    const int32_t at = __shfl_sync(0xffffffffu, base, t >> 4);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) row[q] = at >= 0 && t + q < left ? at + (t & 15) + q : -1;
-  }
-};
-
 struct Maps {
   CUtensorMap q, k, v, gather;  // boxes of queries, K, V, and one row high
 };
@@ -231,23 +179,8 @@ __device__ __forceinline__ uint8_t* shared_base() {
 }
 __device__ __forceinline__ Control* control() { return reinterpret_cast<Control*>(shared_base() + kOffControl); }
 
-// A wait of a role; false once a role of this CTA has given up.  What rarely runs
-// is kept out of the loops around it (the instruction cache).
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  Control* ctl = control();
-  if (pair_wait(bar, parity, &ctl->abort, kWaitLimitNs)) return true;
-  ctl->abort = 1;
-  if (status) atomicOr(status, MLA_STATUS_TIMEOUT);
-  return false;
-}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  return mbar_test(bar, parity) || wait_on(bar, parity, status);
-}
-
-// Copies in flight when a role has given up land within microseconds.
-__device__ __noinline__ void let_copies_land() {
-  const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  return mbar_test(bar, parity) || wait_on(bar, parity, &control()->abort, status);
 }
 
 // The loads of one tile into slots that need many copies each: pages below 64 (K)
@@ -266,7 +199,7 @@ __device__ __noinline__ bool load_k_pieces(const AttendKernelParams& p, const Ma
   for (int j = 0; j < kKSlots; ++j) {
     bool ok = true;
     if (lane == 0) {
-      ok = use == 0 || wait_on(&ctl->k_empty[j], (use - 1) & 1, p.a.c.status);
+      ok = use == 0 || wait_on(&ctl->k_empty[j], (use - 1) & 1, &ctl->abort, p.a.c.status);
       if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->k_full[j], 2 * kKSlotBytes);
     }
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
@@ -290,7 +223,7 @@ __device__ __noinline__ bool load_v_pieces(const AttendKernelParams& p, const Ma
   for (int g = 0; g < kVSlots; ++g) {
     bool ok = true;
     if (lane == 0) {
-      ok = use == 0 || wait_on(&ctl->v_empty[g], (use - 1) & 1, p.a.c.status);
+      ok = use == 0 || wait_on(&ctl->v_empty[g], (use - 1) & 1, &ctl->abort, p.a.c.status);
       if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->v_full[g], 2 * kVSlotBytes);
     }
     if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
@@ -327,7 +260,7 @@ __device__ __forceinline__ bool load_slots(uint64_t* full, uint64_t* empty, uint
     }
     if ((n & 1023u) == 0) {     // the slowest of them, with a limit
       bool ok = true;
-      if (todo) ok = wait_on(&empty[lane], (use - 1) & 1, status);
+      if (todo) ok = wait_on(&empty[lane], (use - 1) & 1, &control()->abort, status);
       if (!__all_sync(0xffffffffu, ok)) return false;
     }
   }
@@ -428,8 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (ok && next_segment(p, end, &walk, &s)) {
       if (s.end_tile <= s.first_tile) continue;
       TilePages pages;
-      pages.load(p, s, s.first_tile, lane);
-      const int32_t dense = p.dense ? p.dense[s.b] : 0;
+      pages.load(p.a.c, s.b, s.limit, s.first_tile, lane);
+      const int32_t dense = p.dense ? p.dense[s.b] : -1;
       ok = nq == 0 || wait(&ctl->q_empty, (nq - 1) & 1, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       ++nq;
@@ -438,9 +371,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         pair_tma_load_3d(smem + lane * kKSlotBytes, &maps.q, q_bar, 0, s.row0 + kHalf * static_cast<int32_t>(rank), kKChunks * lane);
 #pragma unroll 1
       for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
-        const TileRows rows(p, s, tile, pages, dense, lane);
-        if (pages.bad(p) && rank == 0 && lane == 0 && status) atomicOr(status, MLA_STATUS_BAD_PAGE);
-        if (tile + 1 < s.end_tile) pages.load(p, s, tile + 1, lane);
+        const TileRows rows(p.a.c, s.limit, tile, pages, dense, lane);
+        if (pages.bad(p.a.c) && rank == 0 && lane == 0 && status) atomicOr(status, MLA_STATUS_BAD_PAGE);
+        if (tile + 1 < s.end_tile) pages.load(p.a.c, s.b, s.limit, tile + 1, lane);
         if (rows.whole && p.box_rows == kHalf)
           ok = load_slots<kKSlots, kKSlotBytes>(ctl->k_full, ctl->k_empty, k_bar, smem + kOffK, &maps.k,
                                                 __shfl_sync(0xffffffffu, rows.base, 4 * rank), kKChunks * lane, use,
@@ -456,12 +389,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     while (ok && next_segment(p, end, &walk, &s)) {
       if (s.end_tile <= s.first_tile) continue;
       TilePages pages;
-      pages.load(p, s, s.first_tile, lane);
-      const int32_t dense = p.dense ? p.dense[s.b] : 0;
+      pages.load(p.a.c, s.b, s.limit, s.first_tile, lane);
+      const int32_t dense = p.dense ? p.dense[s.b] : -1;
 #pragma unroll 1
       for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
-        const TileRows rows(p, s, tile, pages, dense, lane);
-        if (tile + 1 < s.end_tile) pages.load(p, s, tile + 1, lane);
+        const TileRows rows(p.a.c, s.limit, tile, pages, dense, lane);
+        if (tile + 1 < s.end_tile) pages.load(p.a.c, s.b, s.limit, tile + 1, lane);
         if (rows.whole && p.box_rows >= kVTokens)
           ok = load_slots<kVSlots, kVSlotBytes>(ctl->v_full, ctl->v_empty, v_bar, smem + kOffV, &maps.v,
                                                 __shfl_sync(0xffffffffu, rows.base, (2 * lane) & 7), 4 * rank, use,
@@ -554,11 +487,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int32_t seen = valid ? min(request.seen((s.row_tile * kRows + at) / p.a.c.heads, p.a.c.causal), s.limit) : 0;
       float ref = -INFINITY, sum = 0.f, sum_rounded = 0.f;
       TilePages pages;
-      if (n > 0) pages.load(p, s, s.first_tile, lane);
+      if (n > 0) pages.load(p.a.c, s.b, s.limit, s.first_tile, lane);
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++use) {
-        const uint32_t bad = (pages.bad(p) >> (2 * quarter)) & 3u;
-        if (i + 1 < n) pages.load(p, s, s.first_tile + i + 1, lane);
+        const uint32_t bad = (pages.bad(p.a.c) >> (2 * quarter)) & 3u;
+        if (i + 1 < n) pages.load(p.a.c, s.b, s.limit, s.first_tile + i + 1, lane);
         const int32_t vis = min(max(seen - (s.first_tile + i) * kTok - 32 * quarter, 0), 32);
         // a wait that gave up is agreed on at the next barrier of the row's warps
         failed |= !__all_sync(0xffffffffu, wait(&ctl->s_full[use & 1], (use >> 1) & 1, status));

@@ -162,7 +162,10 @@ int mla_cache_weights(const mla_chunk_plan* plan, const void* q_hat, const float
   p.in = weights_in;
   p.out = weights_out;
   p.stride = stride;
-  return launch_cache_weights(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const ChunkWorkspace w = workspace_of(*plan, workspace);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (w.starts && launch_expand(p.c, w, st) != cudaSuccess) return MLA_ERR_CUDA;
+  return launch_cache_weights(p, w, st) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_evict_make_plan(const mla_problem* problem, int32_t budget, int32_t sinks, int32_t recent,

@@ -24,6 +24,14 @@ struct AttendParams {
   uint16_t* o;                  // bf16 [tokens][heads][512]
   float* lse;                   // [tokens][heads]
 };
+struct WeightsParams {
+  ChunkParams c;
+  const float* lse;
+  const float* in;              // [batch][stride], or null
+  float* out;                   // [batch][stride]
+  int64_t stride;
+};
+
 struct ChunkWorkspace {
   float* part_o;                // [2 * clusters][128][512]
   float* part_lse;              // [2 * clusters][128]
@@ -34,21 +42,14 @@ struct ChunkWorkspace {
 };
 cudaError_t launch_chunk_attend(const AttendParams& p, const ChunkWorkspace& w, cudaStream_t stream);
 
+cudaError_t launch_cache_weights(const WeightsParams& p, const ChunkWorkspace& w, cudaStream_t stream);
+
 // A quantised cache's rows, of the requests that have new tokens, as bf16 rows
 // one request behind the other.
 cudaError_t launch_expand(const ChunkParams& p, const ChunkWorkspace& w, cudaStream_t stream);
 
 constexpr int kMaxChunkClusters = 512;   // of a plan: more SMs are taken as 1,024
 constexpr int kSmemAttrChunk = 16, kSmemAttrWeights = 17;   // slots of set_smem_attr_once
-
-struct WeightsParams {
-  ChunkParams c;
-  const float* lse;
-  const float* in;              // [batch][stride], or null
-  float* out;                   // [batch][stride]
-  int64_t stride;
-};
-cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t stream);
 
 struct EvictParams {
   uint8_t* kv;

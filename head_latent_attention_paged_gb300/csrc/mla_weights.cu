@@ -1,94 +1,388 @@
-// The weights that queries give to cached rows: one warp per cached row.
+// The weight that queries give to each cached row: a matrix product whose epilogue
+// sums exponentials, on pairs of CTAs (tcgen05, cta_group::2).
+//
+//     S^T [256 tokens x N rows] = K [256 x 576] Q^T, N up to 256
+//     w_t += sum over rows r of exp2(scale s_rt - lse_r log2 e)
+//
+// Tokens are the rows of the accumulator, 128 in each CTA, so that a token's sum
+// over queries runs along its own lane: no exchange between lanes, and one thread
+// adds a token's weight in a fixed order.  Both operands stream through one ring in
+// chunks of 64 of the 576 values.  Work is cut between clusters at tiles of 256
+// tokens, each cluster walking all queries of its tiles.
 #include <cuda_runtime.h>
 
 #include "mla_chunk_internal.h"
-#include "mla_rows.cuh"
+#include "mla_chunk_tiles.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kTokens = 2 * kTileRows;  // of a pair's tile
+constexpr int kMaxN = 256;              // rows (token, head) of a block
+constexpr int kSlots = 6;
+constexpr int kABytes = kTileRows * 128, kBBytes = kMaxN / 2 * 128, kSlotBytes = kABytes + kBBytes;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = 128 + 32 * kSumWarps;   // 4 warps that load and issue
+constexpr int kBoxRows = 32;            // of the queries' boxes
 
-struct RowValues {   // a lane's 18 of a row's 576 values
-  float v[18];
+struct Control {
+  uint64_t full[kSlots], empty[kSlots]; // full: in the leader, both CTAs' bytes of both operands
+  uint64_t d_full[2], d_free[2];
+  float neg_lse[2][kMaxN];              // [block's parity][row]: -lse log2 e, -inf for no row
+  int32_t seen[2][kMaxN];
+  float sums[2][kTileRows];
+  int64_t warp_sum[kThreads / 32];
+  int32_t work[4];                      // first (request, tile) and end
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kOffControl = kSlots * kSlotBytes, kSmemBytes = kOffControl + sizeof(Control);
+static_assert(kSmemBytes <= kMaxSmemBytes, "shared memory");
+static_assert((MLA_CHUNK_MAX_REQUESTS + 1) * 8 <= kOffControl, "the cost prefix borrows the ring");
+
+struct WeightsKernelParams {
+  WeightsParams w;
+  const int32_t* dense;         // as in RowSource
+  int32_t capacity;
+  int32_t box_rows;             // cached rows of a box: min(page, 128)
+};
+struct Maps {
+  CUtensorMap q, k, gather;
 };
 
-__device__ __forceinline__ RowValues values_of(const RowWords& r) {
-  RowValues x;
-  const uint32_t w[9] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w, r.key};
-#pragma unroll
-  for (int i = 0; i < 9; ++i) {
-    x.v[2 * i] = bf16_lo(w[i]);
-    x.v[2 * i + 1] = bf16_hi(w[i]);
+__device__ __forceinline__ uint8_t* shared_base() {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  return smem;
+}
+__device__ __forceinline__ Control* control() { return reinterpret_cast<Control*>(shared_base() + kOffControl); }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  return mbar_test(bar, parity) || wait_on(bar, parity, &control()->abort, status);
+}
+
+// A request's tiles and what each costs: a read of its rows and its products, in
+// the latter's time for 64 rows of queries.
+struct Tiles {
+  ChunkRequest r;
+  int32_t end, tiles;           // end: weights that there are
+  int64_t cost;
+  Tiles() = default;
+  __device__ __forceinline__ Tiles(const WeightsKernelParams& p, int32_t b) : r(p.w.c, b) {
+    end = static_cast<int32_t>(min(static_cast<int64_t>(r.len), p.w.stride));
+    tiles = static_cast<int32_t>((static_cast<int64_t>(end) + kTokens - 1) / kTokens);
+    cost = 1 + (r.count > 0 ? 5 + (r.count * p.w.c.heads + 63) / 64 : 0);
   }
-  return x;
-}
+};
 
-__device__ __forceinline__ float dot(const RowValues& a, const RowValues& b) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 18; ++i) s = fmaf(a.v[i], b.v[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// The pool slot of row t of request b, or -1.
-__device__ __forceinline__ int32_t slot_of(const ChunkParams& p, int32_t b, int32_t t) {
-  const int32_t page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (t >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) {
-    if (p.status) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
-    return -1;
+// A tile of a request and the blocks of queries that see any of it.
+struct Unit {
+  int32_t b, tile, end, limit;
+  int32_t row0, rows;           // the request's first row (token, head) of all, and how many
+  int32_t block, blocks;        // blocks of 256 rows: from the first that sees the tile
+  int32_t len, count;
+};
+struct Walk {
+  int32_t b, tile, of;
+  Tiles t;
+};
+__device__ __noinline__ bool next_unit(const WeightsKernelParams& p, const int32_t* end, Walk* w, Unit* u) {
+  const ChunkParams& c = p.w.c;
+  while (w->b < end[0] || (w->b == end[0] && w->tile < end[1])) {
+    if (w->of != w->b) {
+      w->t = Tiles(p, w->b);
+      w->of = w->b;
+    }
+    if (w->tile >= w->t.tiles) {
+      ++w->b;
+      w->tile = 0;
+      continue;
+    }
+    const ChunkRequest& r = w->t.r;
+    const int32_t rows = r.count * c.heads;
+    // the first token of the request that sees the tile's first row
+    const int64_t first = c.causal ? static_cast<int64_t>(w->tile) * kTokens - (r.len - r.count) : 0;
+    const int32_t from = static_cast<int32_t>(min(max(first, int64_t{0}), static_cast<int64_t>(r.count)));
+    *u = Unit{w->b, w->tile, w->t.end, RowSource{c, p.dense, p.capacity}.limit(r, w->b), r.first * c.heads, rows,
+              from * c.heads / kMaxN, (rows + kMaxN - 1) / kMaxN, r.len, r.count};
+    if (from == r.count) u->block = u->blocks;
+    ++w->tile;
+    return true;
   }
-  return (page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+  return false;
 }
 
-template <int kKv>
-__device__ __forceinline__ RowValues cached_row(const ChunkParams& p, int32_t slot, int lane) {
-  CachedRow<kKv> c;
-  load_cached(&c, p.kv, slot, lane);
-  return values_of(cached_to_bf16(c, slot));
+__device__ __forceinline__ int block_columns(const Unit& u, int32_t block) {   // N of its MMAs
+  return min(kMaxN, (u.rows - block * kMaxN + 63) / 64 * 64);
 }
 
-template <int kKv>
-__global__ void __launch_bounds__(32 * kWarps) mla_cache_weights_kernel(const __grid_constant__ WeightsParams p) {
-  const int lane = threadIdx.x & 31;
+__device__ __noinline__ void find_cut(const WeightsKernelParams& p, const int64_t* prefix, int64_t x, int32_t* cut) {
+  const int32_t batch = p.w.c.batch;
+  cut[0] = batch;
+  cut[1] = 0;
+  if (x >= prefix[batch]) return;
+  int32_t lo = 0, hi = batch - 1;         // the last request whose prefix is at most x
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) / 2;
+    if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  cut[0] = lo;
+  cut[1] = static_cast<int32_t>((x - prefix[lo]) / Tiles(p, lo).cost);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mla_cache_weights_kernel(const __grid_constant__ WeightsKernelParams p, const __grid_constant__ Maps maps) {
+  uint8_t* const smem = shared_base();
+  Control* const ctl = control();
+  const ChunkParams& c = p.w.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&ctl->full[i], 2);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->d_full[i], 1);
+      mbar_init(&ctl->d_free[i], 2 * kSumWarps);
+    }
+    ctl->abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.q);
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.gather);
+  }
+  // the pair allocates together: not before both CTAs run
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 2) pair_tmem_alloc(&ctl->tmem, 512);
   after_predecessor();
-  const int32_t b = blockIdx.y;
-  const ChunkRequest r(p.c, b);
-  if (r.bad && p.c.status && threadIdx.x == 0) atomicOr(p.c.status, MLA_STATUS_BAD_INDEX);
-  const int64_t end = r.len < p.stride ? r.len : p.stride;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < end;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    float sum = 0.f;
-    const int32_t slot = r.count > 0 ? slot_of(p.c, b, static_cast<int32_t>(t)) : -1;
-    if (slot >= 0) {
-      const RowValues k = cached_row<kKv>(p.c, slot, lane);
-      for (int32_t j = 0; j < r.count; ++j) {
-        if (t >= r.seen(j, p.c.causal)) continue;
-        for (int32_t h = 0; h < p.c.heads; ++h) {
-          const int64_t row = static_cast<int64_t>(r.first + j) * p.c.heads + h;
-          RowWords qw;
-          load_row(&qw, p.c.q + row * kDqk, lane);
-          const float lse = p.lse[row];
-          const float s = dot(values_of(qw), k) * p.c.scale_log2;
-          sum += lse == -INFINITY ? 0.f : exp2f(s - lse * 1.4426950408889634f);
+
+  // the cost prefix over requests, and this cluster's cuts
+  {
+    int64_t* prefix = reinterpret_cast<int64_t*>(smem);
+    const int32_t batch = c.batch, each = (batch + kThreads - 1) / kThreads;
+    const int32_t lo = min(static_cast<int32_t>(threadIdx.x) * each, batch), hi = min(lo + each, batch);
+    int64_t sum = 0;
+    bool bad = false;
+    for (int32_t b = lo; b < hi; ++b) {
+      const Tiles t(p, b);
+      bad |= t.r.bad || RowSource{c, p.dense, p.capacity}.limit(t.r, b) < t.r.len;
+      sum += t.tiles * t.cost;
+    }
+    if (bad && blockIdx.x == 0 && c.status) atomicOr(c.status, MLA_STATUS_BAD_INDEX);
+    int64_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) ctl->warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t at = upto - sum;
+    for (int w = 0; w < warp; ++w) at += ctl->warp_sum[w];
+    for (int32_t b = lo; b < hi; ++b) {
+      prefix[b] = at;
+      const Tiles t(p, b);
+      at += t.tiles * t.cost;
+    }
+    if (threadIdx.x == kThreads - 1) prefix[batch] = at;
+    __syncthreads();
+    if (threadIdx.x == 0 || threadIdx.x == 32) {
+      const int64_t total = prefix[batch];
+      const int k = cluster + (threadIdx.x == 32);
+      find_cut(p, prefix, total / clusters * k + min(static_cast<int64_t>(k), total % clusters),
+               ctl->work + (threadIdx.x == 32 ? 2 : 0));
+    }
+    fence_proxy_async_smem();   // before copies land on the prefix
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();           // both CTAs have their half of tensor memory
+  tc_fence_after();
+
+  const uint32_t tmem = ctl->tmem;
+  uint32_t* const status = c.status;
+  Walk walk;
+  walk.b = ctl->work[0];
+  walk.tile = ctl->work[1];
+  walk.of = -1;
+  const int32_t* const end = ctl->work + 2;
+  Unit u;
+  bool ok = true;
+
+  if (warp == 0 || warp == 3) {
+    // warp 0: this CTA's 128 cached rows, warp 3: its half of the block's queries
+    const bool cached = warp == 0;
+    const uint32_t full_at = mapa_shared(smem_u32(ctl->full), 0);
+    uint32_t slot = 0, phase = 1;         // phase: of `empty`, at first complete
+    while (ok && next_unit(p, end, &walk, &u)) {
+      if (u.block >= u.blocks) continue;
+      const int32_t tile = 2 * u.tile + static_cast<int32_t>(rank);
+      TilePages pages;
+      pages.load(c, u.b, u.limit, tile, lane);
+      const TileRows rows(c, u.limit, tile, pages, p.dense ? p.dense[u.b] : -1, lane);
+      if (cached && pages.bad(c) && lane == 0 && status) atomicOr(status, MLA_STATUS_BAD_PAGE);
+      const int32_t boxed = __shfl_sync(0xffffffffu, rows.base, (lane * (p.box_rows >> 4)) & 7);
+      int32_t four[4];
+      rows.four(4 * lane, four);
+      for (int32_t block = u.block; ok && block < u.blocks; ++block) {
+        const int32_t half = block_columns(u, block) / 2, row = u.row0 + block * kMaxN + half * static_cast<int32_t>(rank);
+#pragma unroll 1
+        for (int k = 0; k < kChunks; ++k) {
+          if (lane == 0) {
+            ok = wait(&ctl->empty[slot], phase, status);
+            if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->full[slot], 2 * (cached ? kABytes : half * 128));
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          uint8_t* dst = smem + slot * kSlotBytes;
+          const uint32_t bar = full_at + 8 * slot;
+          if (!cached) {
+            if (lane < half / kBoxRows)
+              pair_tma_load_3d(dst + kABytes + lane * (kBoxRows * 128), &maps.q, bar, 0, row + kBoxRows * lane, k);
+          } else if (rows.whole) {
+            if (lane < kTileRows / p.box_rows)
+              pair_tma_load_3d(dst + lane * p.box_rows * 128, &maps.k, bar, 0, boxed, k);
+          } else {
+            pair_tma_gather4(dst + lane * 512, &maps.gather, bar, k * kChunkElems, four);
+          }
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
     }
-    if (lane == 0) p.out[b * p.stride + t] = (p.in ? p.in[b * p.stride + t] : 0.f) + sum;
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      const uint64_t a0 = make_smem_desc(smem_u32(smem), 16, 1024, kSmemLayoutSW128);
+      uint32_t slot = 0, phase = 0, done = 0;
+      while (ok && next_unit(p, end, &walk, &u)) {
+#pragma unroll 1
+        for (int32_t block = u.block; ok && block < u.blocks; ++block, ++done) {
+          const uint32_t idesc = make_idesc_bf16(kTokens, block_columns(u, block), false, false);
+          const uint32_t col = tmem + kMaxN * (done & 1);
+          ok = done < 2 || wait(&ctl->d_free[done & 1], ((done >> 1) - 1) & 1, status);
+#pragma unroll 1
+          for (int k = 0; ok && k < kChunks; ++k) {
+            ok = wait(&ctl->full[slot], phase, status);
+            tc_fence_after();
+            const uint64_t a = a0 + ((slot * kSlotBytes) >> 4), b = a + (kABytes >> 4);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) pair_mma_bf16(col, a + 2 * m, b + 2 * m, idesc, k > 0 || m > 0);
+            pair_commit(&ctl->empty[slot]);
+            if (++slot == kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+          pair_commit(&ctl->d_full[done & 1]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // sums: a lane of tensor memory is a token; the warps 8 .. 11 take the second half
+    // of a block's rows
+    const int quad = warp & 3, l = quad * 32 + lane, side = (warp >> 2) - 1, e = threadIdx.x - 128;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t free_bar = mapa_shared(smem_u32(ctl->d_free), 0);
+    const float2 scale2 = make_float2(c.scale_log2, c.scale_log2);
+    uint32_t done = 0, units = 0;
+    bool failed = false;
+    for (; next_unit(p, end, &walk, &u); ++units) {
+      const int64_t first = static_cast<int64_t>(u.tile) * kTokens + kTileRows * rank, t = first + l;
+      const ChunkRequest r(u.len, u.count);
+      bool there = t < min(u.end, u.limit);
+      if (there) {
+        const int32_t page = c.block_table[static_cast<int64_t>(u.b) * c.max_pages + (t >> c.page_shift)];
+        there = page >= 0 && page < c.num_pages;
+      }
+      float2 acc[2] = {};
+#pragma unroll 1
+      for (int32_t block = u.block; block < u.blocks; ++block, ++done) {
+        const int columns = block_columns(u, block);
+        float* const neg = ctl->neg_lse[done & 1];
+        int32_t* const seen = ctl->seen[done & 1];
+        if (e < columns) {
+          const int32_t row = block * kMaxN + e;
+          const float lse = row < u.rows ? p.w.lse[u.row0 + row] : INFINITY;
+          neg[e] = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;   // no weight from a row that saw nothing
+          seen[e] = row < u.rows ? r.seen(row / c.heads, c.causal) : 0;
+        }
+        failed |= !wait(&ctl->d_full[done & 1], (done >> 1) & 1, status);
+        if (named_bar_or(1, 32 * kSumWarps, failed)) break;
+        tc_fence_after();
+        const bool all = seen[0] >= first + kTileRows && (block + 1) * kMaxN <= u.rows;
+#pragma unroll 1
+        for (int k = side * columns / 2; k < (side + 1) * columns / 2; k += 32) {
+          uint32_t x[32];
+          tmem_ld32(tmem + lanes + kMaxN * (done & 1) + k, x);
+          const float4* n4 = reinterpret_cast<const float4*>(neg + k);
+          float v[32];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 n = n4[q];
+            const float2 a = __ffma2_rn(make_float2(__uint_as_float(x[4 * q]), __uint_as_float(x[4 * q + 1])), scale2, make_float2(n.x, n.y));
+            const float2 b = __ffma2_rn(make_float2(__uint_as_float(x[4 * q + 2]), __uint_as_float(x[4 * q + 3])), scale2, make_float2(n.z, n.w));
+            v[4 * q] = exp2_approx(a.x);
+            v[4 * q + 1] = exp2_approx(a.y);
+            v[4 * q + 2] = exp2_approx(b.x);
+            v[4 * q + 3] = exp2_approx(b.y);
+          }
+          if (!all) {                     // rows that do not see the token, and none
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = t < seen[k + q] ? v[q] : 0.f;
+          }
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[q & 1] = __fadd2_rn(acc[q & 1], make_float2(v[2 * q], v[2 * q + 1]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_mbar_arrive(free_bar + 8 * (done & 1));
+      }
+      const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      if (side == 1) ctl->sums[units & 1][l] = sum;
+      if (named_bar_or(1, 32 * kSumWarps, failed)) break;
+      if (side == 0 && t < u.end) {
+        const int64_t at = u.b * p.w.stride + t;
+        p.w.out[at] = (p.w.in ? p.w.in[at] : 0.f) + (there ? sum + ctl->sums[units & 1][l] : 0.f);
+      }
+    }
   }
+  __syncwarp();
+  volatile int* const abort = &ctl->abort;
+  if (*abort) let_copies_land();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();           // neither CTA leaves while the other may still write to it
+  tc_fence_after();
+  if (warp == 2) pair_tmem_dealloc(tmem, 512);
+  __syncthreads();
+  cluster_sync_all();           // nor leave before both have given it back
 }
 
 }  // namespace
 
-cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t stream) {
-  const dim3 grid(1024, p.c.batch);
-  const auto launch = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * kWarps, 0, stream, p); };
-  return p.c.kv_dtype == MLA_KV_BF16            ? launch(mla_cache_weights_kernel<MLA_KV_BF16>)
-         : p.c.kv_dtype == MLA_KV_FP8_E4M3_E8M0 ? launch(mla_cache_weights_kernel<MLA_KV_FP8_E4M3_E8M0>)
-                                                : launch(mla_cache_weights_kernel<MLA_KV_FP4_E2M1_E8M0>);
+cudaError_t launch_cache_weights(const WeightsParams& w, const ChunkWorkspace& ws, cudaStream_t stream) {
+  WeightsKernelParams p;
+  p.w = w;
+  p.dense = ws.starts;
+  p.capacity = ws.capacity;
+  p.box_rows = ws.starts ? kTileRows : 1 << w.c.page_shift;
+  const void* rows = ws.starts ? static_cast<const void*>(ws.rows) : w.c.kv;
+  const uint64_t count = ws.starts ? static_cast<uint64_t>(ws.capacity > 0 ? ws.capacity : 1)
+                                   : static_cast<uint64_t>(w.c.num_pages) << w.c.page_shift;
+  const uint64_t queries = static_cast<uint64_t>(w.c.tokens > 0 ? w.c.tokens : 1) * w.c.heads;
+  Maps maps;
+  if (!make_map_chunks_bf16(&maps.q, w.c.q, kDqk, queries, kDqk * 2, kBoxRows, 1) ||
+      !make_map_chunks_bf16(&maps.k, rows, kDqk, count, kDqk * 2, p.box_rows, 1) ||
+      !make_map_bf16(&maps.gather, rows, kDqk, count, kDqk * 2, kChunkElems, 1))
+    return cudaErrorInvalidValue;
+  cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(mla_cache_weights_kernel), kSmemAttrWeights, kSmemBytes);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(mla_cache_weights_kernel, dim3(2 * ws.clusters), kThreads, kSmemBytes, stream, p, maps);
 }
 
 }  // namespace mla
