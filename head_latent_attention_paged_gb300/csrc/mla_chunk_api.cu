@@ -173,6 +173,7 @@ int mla_evict_make_plan(const mla_problem* problem, int32_t budget, int32_t sink
   const int rc = check_cache_shape(problem);
   if (rc != MLA_OK) return rc;
   if (budget < 1 || sinks < 0 || recent < 0 || plan_out == nullptr) return MLA_ERR_INVALID_ARGUMENT;
+  if (problem->batch > MLA_CHUNK_MAX_REQUESTS) return MLA_ERR_UNSUPPORTED;
   mla_evict_plan pl;
   std::memset(&pl, 0, sizeof(pl));
   pl.problem = *problem;

@@ -49,7 +49,7 @@ cudaError_t launch_cache_weights(const WeightsParams& p, const ChunkWorkspace& w
 cudaError_t launch_expand(const ChunkParams& p, const ChunkWorkspace& w, cudaStream_t stream);
 
 constexpr int kMaxChunkClusters = 512;   // of a plan: more SMs are taken as 1,024
-constexpr int kSmemAttrChunk = 16, kSmemAttrWeights = 17;   // slots of set_smem_attr_once
+constexpr int kSmemAttrChunk = 16, kSmemAttrWeights = 17, kSmemAttrEvict = 18;   // slots of set_smem_attr_once
 
 struct EvictParams {
   uint8_t* kv;

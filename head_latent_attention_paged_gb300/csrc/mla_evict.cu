@@ -1,18 +1,29 @@
-// Eviction: each request's slots selected by weight, and the kept rows behind
-// the budget moved into the slots below it that became free.
+// Eviction: each request's slots selected by weight, and the kept rows behind the
+// budget moved into the slots below it that became free.
+//
+// The budget-th greatest weight is found digit by digit (11, 11 and 10 bits of an
+// order-preserving integer) from counts; its equals are taken in the order of slots.
+// A cluster of CTAs holds a request: every slot's key is made once and stays in
+// shared memory, counts and prefixes go through the cluster's shared memory.  Only
+// rows that leave a slot behind the budget move, so a cache that has grown by a few
+// rows over its budget moves a few rows.
 #include <cuda_runtime.h>
 
 #include "mla_chunk_internal.h"
+#include "sm103_ptx.cuh"
 
 namespace mla {
 
 namespace {
 
-constexpr int kSelectThreads = 1024;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxKeys = 49152;         // of a CTA, in shared memory; those behind are made again
 constexpr int kMoveWarps = 4;
 
-// A slot's rank as an unsigned number: protected slots above every weight,
-// NaN below, -0 as 0.
+// A slot's rank as an unsigned number: protected slots above every weight, NaN
+// below, -0 as 0.
 __device__ __forceinline__ uint32_t rank_key(float w, bool safe) {
   if (safe) return 0xFFFFFFFFu;
   if (w != w) return 0u;
@@ -20,32 +31,57 @@ __device__ __forceinline__ uint32_t rank_key(float w, bool safe) {
   return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
 }
 
-// Exclusive prefix of v over the block's threads, and the block's total.
-__device__ __forceinline__ int block_prefix(int v, int* total) {
-  __shared__ int sums[kSelectThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < kSelectThreads / 32; ++i) {
-    if (i < warp) before += sums[i];
-    all += sums[i];
-  }
-  __syncthreads();
-  *total = all;
-  return before + x - v;
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) mla_evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int hist[256], s_newest, s_digit, s_left;
+struct Shared {
+  int hist[kBins];
+  int total[kBins];             // over the cluster
+  int sums[kWarps];
+  int newest, digit, left, ties;
+  int tie[kWarps], hole[kWarps], mover[kWarps];   // of each warp
+  int all[3];                   // of this CTA
+};
+
+// Inclusive prefix of v over the block's threads.
+__device__ __forceinline__ int block_prefix(Shared* s, int v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) s->sums[warp] = v;
+  __syncthreads();
+  int before = lane < warp ? s->sums[lane] : 0;   // 32 warps, a lane for each
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  return v + before;
+}
+
+// What stands before this warp: counts[w] of the warps before it in the CTA, and the
+// CTAs' `all` before it in the cluster.  Warp-wide; after a cluster barrier.
+__device__ __forceinline__ int before_warp(const int* counts, const int* all, uint32_t rank) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v = lane < warp ? counts[lane] : 0;
+  if (lane < static_cast<int>(rank)) v += ld_cluster(mapa_shared(smem_u32(all), lane));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// One cluster per request (kMaxKeys slots a CTA without making keys again; 32,768
+// slots cut to 4,096 by eight CTAs and moved 24 us, by one CTA that read them again
+// for every digit 410 us).
+__global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __grid_constant__ EvictParams p, const int clusters, const int cap) {
+  extern __shared__ uint32_t keys[];
+  __shared__ Shared s;
   after_predecessor();
-  const int b = blockIdx.x, tid = threadIdx.x;
+  const int b = blockIdx.x / clusters, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % clusters;
   const float* w = p.weights + b * p.stride;
   const int32_t* pos = p.positions + b * p.stride;
   float* w_out = p.weights_out + b * p.stride;
@@ -53,119 +89,243 @@ __global__ void __launch_bounds__(kSelectThreads) mla_evict_select_kernel(const 
   const int64_t most = min(static_cast<int64_t>(p.max_pages) << p.page_shift, p.stride);
   const int32_t given = p.lens[b];
   const int32_t n = static_cast<int32_t>(min(max(static_cast<int64_t>(given), int64_t{0}), most));
-  if (n != given && p.status && tid == 0) atomicOr(p.status, MLA_STATUS_BAD_INDEX);
   const int32_t budget = min(n, p.budget);
+  // each warp has consecutive slots, 32 at a time
+  const int32_t each = static_cast<int32_t>((static_cast<int64_t>(n) + clusters * kThreads - 1) / (clusters * kThreads)) * 32;
+  const int64_t at = (static_cast<int64_t>(rank) * kWarps + warp) * each;
+  const int32_t first = static_cast<int32_t>(min(at, static_cast<int64_t>(n)));
+  const int32_t steps = (min(each, n - first) + 31) / 32;
   int32_t* moves = p.moves + b * p.most_moves * 2;
-  int count = 0;
-  if (n > budget) {
-    if (tid == 0) s_newest = -1;
+  if (rank == 0 && tid == 0 && n != given && p.status) atomicOr(p.status, MLA_STATUS_BAD_INDEX);
+
+  int32_t moved = 0;
+  if (n > budget) {             // the same for the whole cluster
+    if (tid == 0) s.newest = -1;
+    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
     __syncthreads();
     int newest = -1;
-    for (int t = tid; t < n; t += kSelectThreads) newest = max(newest, pos[t]);
-    atomicMax(&s_newest, newest);
-    __syncthreads();
-    const int64_t border = static_cast<int64_t>(s_newest) - p.recent;
-    const auto key_of = [&](int t) { return rank_key(w[t], pos[t] < p.sinks || pos[t] > border); };
-    // the budget-th greatest key, eight bits at a time
-    uint32_t prefix = 0, mask = 0;
-    int left = budget;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int t = tid; t < n; t += kSelectThreads) {
-        const uint32_t k = key_of(t);
-        if ((k & mask) == prefix) atomicAdd(&hist[k >> shift & 255], 1);
+    for (int k = 0; k < steps; ++k) {
+      const int t = first + 32 * k + lane;
+      if (t < n) newest = max(newest, pos[t]);
+    }
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (lane == 0) atomicMax(&s.newest, newest);
+    cluster_sync_all();
+    newest = lane < clusters ? ld_cluster(mapa_shared(smem_u32(&s.newest), lane)) : -1;
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    const int64_t border = static_cast<int64_t>(newest) - p.recent;
+    const auto make_key = [&](int t) { return rank_key(w[t], pos[t] < p.sinks || pos[t] > border); };
+    const int own = warp * each;          // of this CTA's keys
+    const auto key_at = [&](int k) {
+      const int i = own + 32 * k + lane;
+      return i < cap ? keys[i] : make_key(first + 32 * k + lane);
+    };
+    // the budget-th greatest key
+    uint32_t found = 0, mask = 0;
+    int left = budget, ties = 0;
+    for (int digit = 0; digit < 3; ++digit) {
+      const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
+      for (int k = 0; k < steps; ++k) {
+        const int t = first + 32 * k + lane;
+        if (t >= n) continue;
+        uint32_t key;
+        if (digit == 0) {
+          key = make_key(t);
+          const int i = own + 32 * k + lane;
+          if (i < cap) keys[i] = key;
+        } else {
+          key = key_at(k);
+        }
+        if ((key & mask) == found) atomicAdd(&s.hist[key >> shift & ((1 << bits) - 1)], 1);
+      }
+      cluster_sync_all();
+      for (int i = tid; i < kBins; i += kThreads) {
+        int sum = 0;
+        for (int r = 0; r < clusters; ++r) sum += ld_cluster(mapa_shared(smem_u32(&s.hist[i]), r));
+        s.total[i] = sum;
       }
       __syncthreads();
-      if (tid == 0) {
-        int d = 255;
-        while (hist[d] < left) left -= hist[d--];
-        s_digit = d;
-        s_left = left;
+      // from the greatest bin down: thread t has the two bins behind 2 t others
+      const int hi = s.total[kBins - 1 - 2 * tid], lo = s.total[kBins - 2 - 2 * tid];
+      const int upto = block_prefix(&s, hi + lo), before = upto - hi - lo;
+      if (before < left && left <= upto) {
+        const bool second = left > before + hi;
+        s.digit = kBins - 1 - 2 * tid - second;
+        s.left = left - before - (second ? hi : 0);
+        s.ties = second ? lo : hi;
       }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(s_digit) << shift;
-      mask |= 255u << shift;
-      left = s_left;
+      cluster_sync_all();       // everyone has read every CTA's counts
+      for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+      found |= static_cast<uint32_t>(s.digit) << shift;
+      mask |= ((1u << bits) - 1u) << shift;
+      left = s.left;
+      ties = s.ties;
       __syncthreads();
     }
-    // in the order of slots: the first `left` of those that equal it are kept;
+    // equal ones: the first `left` of `ties` in the order of slots
+    int ties_before = 0;
+    if (ties != left) {
+      int count = 0;
+      for (int k = 0; k < steps; ++k) {
+        const int t = first + 32 * k + lane;
+        count += __popc(__ballot_sync(0xffffffffu, t < n && key_at(min(k, steps - 1)) == found));
+      }
+      if (lane == 0) s.tie[warp] = count;
+      __syncthreads();
+      if (warp == 0) {
+        const int all = __reduce_add_sync(0xffffffffu, s.tie[lane]);
+        if (lane == 0) s.all[0] = all;
+      }
+      cluster_sync_all();
+      ties_before = before_warp(s.tie, &s.all[0], rank);
+    }
+    const auto kept_at = [&](int k, int* tied) {   // tied: of this warp so far
+      const int t = first + 32 * k + lane;
+      const uint32_t key = t < n ? key_at(k) : 0u;
+      const bool tie = t < n && key == found;
+      const uint32_t same = __ballot_sync(0xffffffffu, tie);
+      const int at_tie = ties_before + *tied + __popc(same & ((1u << lane) - 1u));
+      *tied += __popc(same);
+      return t < n && (key > found || (tie && (ties == left || at_tie < left)));
+    };
     // the i-th free slot below the budget takes the i-th kept row behind it
-    int equal = 0, holes = 0, movers = 0;
-    for (int base = 0; base < n; base += kSelectThreads) {
-      const int t = base + tid;
-      const uint32_t k = t < n ? key_of(t) : 0;
-      int total;
-      const bool tie = t < n && k == prefix;
-      const int rank = equal + block_prefix(tie, &total);
-      equal += total;
-      const bool kept = t < n && (k > prefix || (tie && rank < left));
-      const bool hole = t < budget && !kept, mover = kept && t >= budget;
-      const int h = holes + block_prefix(hole, &total);
-      holes += total;
-      if (hole) moves[2 * h] = t;
-      const int m = movers + block_prefix(mover, &total);
-      movers += total;
-      if (mover) moves[2 * m + 1] = t;
+    int holes = 0, movers = 0, tied = 0;
+    for (int k = 0; k < steps; ++k) {
+      const int t = first + 32 * k + lane;
+      const bool kept = kept_at(k, &tied);
+      holes += __popc(__ballot_sync(0xffffffffu, t < budget && !kept));
+      movers += __popc(__ballot_sync(0xffffffffu, t >= budget && kept));
     }
-    count = holes;
-    __syncthreads();
-    for (int i = tid; i < count; i += kSelectThreads) {
-      const int to = moves[2 * i], from = moves[2 * i + 1];
-      w_out[to] = w[from];
-      pos_out[to] = pos[from];
+    if (lane == 0) {
+      s.hole[warp] = holes;
+      s.mover[warp] = movers;
     }
     __syncthreads();
-  }
-  // what stays, where the outputs are other arrays, and the slots given up
-  if (w_out != w || pos_out != pos) {
-    int next = 0;   // holes below t
-    for (int t = tid; t < budget; t += kSelectThreads) {
-      while (next < count && moves[2 * next] < t) ++next;
-      if (next < count && moves[2 * next] == t) continue;
-      w_out[t] = w[t];
-      pos_out[t] = pos[t];
+    if (warp == 0) {
+      const int h = __reduce_add_sync(0xffffffffu, s.hole[lane]), m = __reduce_add_sync(0xffffffffu, s.mover[lane]);
+      if (lane == 0) {
+        s.all[1] = h;
+        s.all[2] = m;
+      }
+    }
+    cluster_sync_all();
+    const int first_hole = before_warp(s.hole, &s.all[1], rank), first_mover = before_warp(s.mover, &s.all[2], rank);
+    moved = lane < clusters ? ld_cluster(mapa_shared(smem_u32(&s.all[1]), lane)) : 0;
+    moved = __reduce_add_sync(0xffffffffu, moved);
+    holes = first_hole;
+    movers = first_mover;
+    tied = 0;
+    for (int k = 0; k < steps; ++k) {
+      const int t = first + 32 * k + lane;
+      const bool kept = kept_at(k, &tied), hole = t < budget && !kept, mover = t >= budget && kept;
+      const uint32_t h = __ballot_sync(0xffffffffu, hole), m = __ballot_sync(0xffffffffu, mover), below = (1u << lane) - 1u;
+      if (hole) moves[2 * (holes + __popc(h & below))] = t;
+      if (mover) moves[2 * (movers + __popc(m & below)) + 1] = t;
+      holes += __popc(h);
+      movers += __popc(m);
+      if (kept && !mover) {     // stays where it is
+        w_out[t] = w[t];
+        pos_out[t] = pos[t];
+      }
+    }
+    __threadfence();
+    cluster_sync_all();         // the list is whole
+    for (int i = rank * kThreads + tid; i < moved; i += clusters * kThreads) {
+      const int2 move = __ldcg(reinterpret_cast<const int2*>(moves) + i);
+      w_out[move.x] = w[move.y];
+      pos_out[move.x] = pos[move.y];
+    }
+    cluster_sync_all();         // before the slots given up are cleared, in place
+    for (int k = 0; k < steps; ++k) {
+      const int t = first + 32 * k + lane;
+      if (t >= budget && t < n) {
+        w_out[t] = 0.f;
+        pos_out[t] = -1;
+      }
+    }
+  } else if (w_out != w || pos_out != pos) {
+    for (int k = 0; k < steps; ++k) {
+      const int t = first + 32 * k + lane;
+      if (t < n) {
+        w_out[t] = w[t];
+        pos_out[t] = pos[t];
+      }
     }
   }
-  for (int t = budget + tid; t < n; t += kSelectThreads) {
-    w_out[t] = 0.f;
-    pos_out[t] = -1;
-  }
-  if (tid == 0) {
-    p.counts[b] = count;
+  if (rank == 0 && tid == 0) {
+    p.counts[b] = moved;
     p.lens_out[b] = budget;
   }
 }
 
-// One warp per row: its bytes in units of 2, which divide every format's rows.
+// One warp per row, in units that divide the format's rows.
+template <typename Unit, int kRowBytes>
 __global__ void __launch_bounds__(32 * kMoveWarps) mla_evict_move_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kUnits = kRowBytes / sizeof(Unit), kEach = (kUnits + 31) / 32;
   const int lane = threadIdx.x & 31;
   after_predecessor();
   const int b = blockIdx.y, count = p.counts[b];
   const int32_t* moves = p.moves + b * p.most_moves * 2;
   const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
+  const int in_page = (1 << p.page_shift) - 1;
   for (int i = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); i < count; i += gridDim.x * kMoveWarps) {
-    const int to = moves[2 * i], from = moves[2 * i + 1];
-    const int32_t pt = table[to >> p.page_shift], pf = table[from >> p.page_shift];
+    const int2 move = reinterpret_cast<const int2*>(moves)[i];
+    const int32_t pt = table[move.x >> p.page_shift], pf = table[move.y >> p.page_shift];
     if (pt < 0 || pt >= p.num_pages || pf < 0 || pf >= p.num_pages) {
       if (p.status && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
       continue;
     }
-    const int in_page = (1 << p.page_shift) - 1;
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(
-        p.kv + ((static_cast<int64_t>(pf) << p.page_shift) + (from & in_page)) * p.row_bytes);
-    uint16_t* dst = reinterpret_cast<uint16_t*>(
-        p.kv + ((static_cast<int64_t>(pt) << p.page_shift) + (to & in_page)) * p.row_bytes);
-    for (int k = lane; k < p.row_bytes / 2; k += 32) dst[k] = src[k];
+    const Unit* src = reinterpret_cast<const Unit*>(
+        p.kv + ((static_cast<int64_t>(pf) << p.page_shift) + (move.y & in_page)) * kRowBytes);
+    Unit* dst = reinterpret_cast<Unit*>(
+        p.kv + ((static_cast<int64_t>(pt) << p.page_shift) + (move.x & in_page)) * kRowBytes);
+    Unit v[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (32 * k + lane < kUnits) v[k] = src[32 * k + lane];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (32 * k + lane < kUnits) dst[32 * k + lane] = v[k];
   }
 }
 
 }  // namespace
 
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream) {
-  cudaError_t err = launch_dependent(mla_evict_select_kernel, dim3(p.batch), kSelectThreads, 0, stream, p);
+  const int64_t slots = p.stride < (static_cast<int64_t>(p.max_pages) << p.page_shift)
+                            ? p.stride : static_cast<int64_t>(p.max_pages) << p.page_shift;
+  // CTAs for a request: more while there are multiprocessors for them and slots for
+  // their threads
+  int cluster = 1;
+  while (cluster < kMaxCluster && 2 * cluster * static_cast<int64_t>(p.batch) <= 152 && slots > cluster * kThreads) cluster *= 2;
+  const int64_t own = (slots + cluster * kThreads - 1) / (cluster * kThreads) * kThreads;
+  const int cap = static_cast<int>(own < kMaxKeys ? own : kMaxKeys);
+  cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(mla_evict_select_kernel), kSmemAttrEvict, kMaxKeys * 4);
   if (err != cudaSuccess) return err;
-  return launch_dependent(mla_evict_move_kernel, dim3(128, p.batch), 32 * kMoveWarps, 0, stream, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.batch * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = cap * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, mla_evict_select_kernel, p, cluster, cap);
+  if (err != cudaSuccess || p.most_moves == 0) return err;
+  // rows of all requests over a few blocks a multiprocessor, at most one warp a move
+  int64_t blocks = (p.most_moves + kMoveWarps - 1) / kMoveWarps;
+  const int64_t fill = (152 * 8 + p.batch - 1) / p.batch;
+  if (blocks > fill) blocks = fill;
+  const dim3 grid(static_cast<unsigned>(blocks), p.batch);
+  const auto launch = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * kMoveWarps, 0, stream, p); };
+  return p.row_bytes == kDqk * 2       ? launch(mla_evict_move_kernel<uint4, kDqk * 2>)
+         : p.row_bytes == kFp8RowBytes ? launch(mla_evict_move_kernel<uint16_t, kFp8RowBytes>)
+                                       : launch(mla_evict_move_kernel<uint32_t, kFp4RowBytes>);
 }
 
 }  // namespace mla

@@ -154,8 +154,9 @@ typedef struct {
 /*
  * mla_evict_make_plan -- validate an eviction and lay out its workspace (host
  * only, no CUDA call).
- *   problem : the cache: batch, page_size, num_pages, max_pages_per_seq, kv_dtype
- *             and the widths of the row; the other fields are not read
+ *   problem : the cache: batch (up to MLA_CHUNK_MAX_REQUESTS), page_size, num_pages,
+ *             max_pages_per_seq, kv_dtype and the widths of the row; the other
+ *             fields are not read
  *   budget  : rows that each request keeps at most, >= 1
  *   sinks   : tokens of positions below this are kept before all others, >= 0
  *   recent  : so are the tokens of the last `recent` positions, >= 0
