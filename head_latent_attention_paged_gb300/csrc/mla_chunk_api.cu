@@ -47,6 +47,7 @@ int fill_chunk(const mla_chunk_plan* plan, const void* q, const int32_t* starts,
   const mla_problem& pr = plan->problem;
   const int rc = check_chunk_problem(&pr);
   if (rc != MLA_OK) return rc;
+  if (q == nullptr && plan->tokens == 0) q = workspace;   // no query is read
   if (!q || !starts || !kv || !block_table || !lens || !workspace) return MLA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < static_cast<size_t>(plan->workspace_bytes)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(workspace, 16) || !aligned(starts, 4) ||
@@ -133,9 +134,9 @@ int mla_chunk_attend(const mla_chunk_plan* plan, const void* q_hat, const int32_
   const int rc = fill_chunk(plan, q_hat, query_starts, kv_cache, block_table, seq_lens, workspace,
                             workspace_bytes, status, &p.c);
   if (rc != MLA_OK) return rc;
+  if (plan->tokens == 0 || plan->problem.batch == 0) return MLA_OK;
   if (!o_lat || !lse) return MLA_ERR_INVALID_ARGUMENT;
   if (!aligned(o_lat, 16) || !aligned(lse, 4)) return MLA_ERR_MISALIGNED;
-  if (plan->tokens == 0 || plan->problem.batch == 0) return MLA_OK;
   p.o = static_cast<uint16_t*>(o_lat);
   p.lse = lse;
   const ChunkWorkspace w = workspace_of(*plan, workspace);
@@ -153,7 +154,7 @@ int mla_cache_weights(const mla_chunk_plan* plan, const void* q_hat, const float
   const int rc = fill_chunk(plan, q_hat, query_starts, kv_cache, block_table, seq_lens, workspace,
                             workspace_bytes, status, &p.c);
   if (rc != MLA_OK) return rc;
-  if (!lse || !weights_out || stride < 1 || stride > INT64_MAX / 8 / (p.c.batch + 1)) return MLA_ERR_INVALID_ARGUMENT;
+  if ((!lse && plan->tokens > 0) || !weights_out || stride < 1 || stride > INT64_MAX / 8 / (p.c.batch + 1)) return MLA_ERR_INVALID_ARGUMENT;
   if (!aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4)) return MLA_ERR_MISALIGNED;
   const int64_t bytes = p.c.batch * stride * 4;
   if (weights_in != weights_out && overlap(weights_in, bytes, weights_out, bytes)) return MLA_ERR_INVALID_ARGUMENT;

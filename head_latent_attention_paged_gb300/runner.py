@@ -9,8 +9,10 @@ import torch
 
 from . import (MLA_KV_BF16, MLA_KV_FP4_E2M1_E8M0, MLA_KV_FP8_E4M3_E8M0, MlaRopePlan,
                make_norm_problem, make_problem, make_rope_problem, mla_cache_append_tokens,
-               mla_cache_gather, mla_clear_status, mla_combine, mla_decode_plan, mla_decode_run,
-               mla_decode_step, mla_get_status, mla_q_absorb, mla_rms_norm, mla_rope, mla_uv_proj)
+               mla_cache_evict, mla_cache_gather, mla_cache_weights, mla_chunk_attend,
+               mla_chunk_make_plan, mla_clear_status, mla_combine, mla_decode_plan, mla_decode_run,
+               mla_decode_step, mla_evict_make_plan, mla_get_status, mla_q_absorb, mla_rms_norm,
+               mla_rope, mla_uv_proj)
 
 
 def to_device_bf16(bits: np.ndarray, device) -> torch.Tensor:
@@ -153,12 +155,19 @@ class AttentionLayer:
         out = o W_o                                      (library product)
 
     decode() runs a whole step of `q_len` tokens for each of `batch` requests;
+    prefill() does the same for any number of new tokens of each (mla_chunk_attend
+    in the place of mla_decode_step, the up-projection a library product);
     prompt() only caches the rows of a prompt's tokens (any mixture of
-    requests), context() reads cached rows back.  Weights are bf16 tensors on
+    requests), context() reads cached rows back.  With `track` the layer keeps
+    what evict() needs: the attention weight that each cached row got from
+    every decode() and prefill() (mla_cache_weights) and the position of the
+    token in each slot.  After an eviction a request's cache is shorter than
+    the positions it has seen, and new tokens go to `slots` of their own.
+    Weights are bf16 tensors on
     the device: hidden_norm [hidden], w_qkv_a [hidden, q_rank + 576], q_norm
     [q_rank], kv_norm [512], w_q_b [q_rank, H * 256], w_uk [H, 512, 192], w_uv
     [H, 512, 256], w_o [H * 256, hidden].  decode()'s buffers are made once,
-    prompt() and context() take theirs from torch's allocator; these three can
+    the others take theirs from torch's allocator; all but status() can
     be captured in a CUDA graph, and calls of one AttentionLayer are
     ordered on one stream, the current one of the layer's device (which need
     not be the current device).
@@ -169,7 +178,7 @@ class AttentionLayer:
     def __init__(self, *, hidden_norm, w_qkv_a, q_norm, kv_norm, w_q_b, w_uk, w_uv, w_o, batch: int,
                  q_len: int = 1, page_size: int = 64, num_pages: int, max_pages: int,
                  rope: MlaRopePlan, kv_dtype: int = MLA_KV_BF16, eps: float = 1e-6,
-                 sm_scale: float = 1.0 / 16.0, sm_count: Optional[int] = None):
+                 sm_scale: float = 1.0 / 16.0, sm_count: Optional[int] = None, track: bool = False):
         dev = w_qkv_a.device
         self.device, self.eps, self.rope = dev, float(eps), rope
         self.B, self.Q, self.H = batch, q_len, int(w_uk.shape[0])
@@ -214,6 +223,20 @@ class AttentionLayer:
         self.q_problem = make_norm_problem(rows, self.q_rank, eps=self.eps,
                                            x_stride=self.q_rank + self.ROW)
         self.rope_problem = make_rope_problem(rows, self.H, self.HEAD, rope_offset=self.NOPE)
+        self.sm_count = sm_count
+        self.weights = self.slot_positions = None
+        if track:   # one entry more than there are slots: padding's
+            self.weights = torch.zeros((batch, max_pages * page_size + 1), dtype=torch.float32, device=dev)
+            self.slot_positions = torch.full_like(self.weights, -1, dtype=torch.int32)
+            self.step_plan = mla_chunk_make_plan(self.problem, rows, self._context(None), sm_count)
+            self.step_workspace = torch.empty(int(self.step_plan.workspace_bytes), dtype=torch.uint8, device=dev)
+            self.step_starts = torch.arange(0, rows + 1, q_len, dtype=torch.int32, device=dev)
+            self.step_requests = torch.arange(rows, dtype=torch.int32, device=dev) // q_len
+
+    def _context(self, rows):
+        """Rows that one call can find cached: those of every request, or of the pool."""
+        pr = self.problem
+        return min(pr.batch * pr.max_pages_per_seq, pr.num_pages) * pr.page_size if rows is None else int(rows)
 
     def _check_int32(self, **int32):
         """Kernels take addresses: what their arguments' shapes say has to be so."""
@@ -229,17 +252,34 @@ class AttentionLayer:
     def _check_table(self, block_table):
         self._check_int32(block_table=(block_table, self.B * self.problem.max_pages_per_seq))
 
-    def _append(self, qkv_a, positions, block_table, requests, stream):
-        width = self.q_rank + self.ROW
-        mla_cache_append_tokens(self.problem, int(qkv_a.shape[0]), qkv_a[:, self.q_rank:], positions,
+    def _append(self, qkv_a, positions, block_table, requests, stream, slots=None):
+        """Cache the rows at their positions, or turned to them at `slots`."""
+        width, n = self.q_rank + self.ROW, int(qkv_a.shape[0])
+        rope, at = self.rope, positions
+        if slots is not None:   # the append's position is the slot: the key is turned ahead of it
+            mla_rope(make_rope_problem(n, 1, self.ROPE, x_token_stride=width), self.rope,
+                     qkv_a[:, self.q_rank + 512:], positions, stream=stream)
+            rope, at = None, slots
+        mla_cache_append_tokens(self.problem, n, qkv_a[:, self.q_rank:], at,
                                 block_table, self.cache, requests=requests, row_stride=width,
-                                norm_weight=self.kv_norm, norm_eps=self.eps, rope=self.rope,
+                                norm_weight=self.kv_norm, norm_eps=self.eps, rope=rope,
                                 status=self.status_word, stream=stream)
+        if self.slot_positions is not None:
+            width = self.slot_positions.shape[1]
+            requests = self.step_requests if requests is None else requests
+            where = torch.where((at >= 0) & (positions >= 0), at, width - 1).clamp_(max=width - 1)
+            self.slot_positions.view(-1)[requests.long() * width + where] = positions
 
-    def decode(self, hidden, residual, positions, block_table, seq_lens):
+    def _weigh(self, plan, q_hat, lse, starts, block_table, seq_lens, workspace, stream):
+        if self.weights is not None:
+            mla_cache_weights(plan, q_hat, lse, starts, self.cache, block_table, seq_lens, workspace, self.weights,
+                              weights_in=self.weights, status=self.status_word, stream=stream)
+
+    def decode(self, hidden, residual, positions, block_table, seq_lens, slots=None):
         """hidden, residual (or None): bf16 [B * Q, hidden]; positions int32
         [B * Q] of the new tokens (-1: a padded row, whose request has length
-        0); seq_lens int32 [B] with the new tokens.  Returns (out, residual):
+        0); slots int32 [B * Q]: where the tokens are cached (None: at their
+        positions); seq_lens int32 [B] with the new tokens.  Returns (out, residual):
         the attention's output and the residual stream to add it to (hidden
         itself without a residual).  Both may be the layer's own buffers, which
         the next decode() overwrites; either may be an input to that call."""
@@ -247,6 +287,8 @@ class AttentionLayer:
             self._check_hidden(h, self.rows)
         self._check_int32(positions=(positions, self.rows), seq_lens=(seq_lens, self.B))
         self._check_table(block_table)
+        if slots is not None:
+            self._check_int32(slots=(slots, self.rows))
         with torch.cuda.device(self.device):
             stream = torch.cuda.current_stream(self.device)
             if residual is None and hidden.data_ptr() == self.out.data_ptr():
@@ -254,14 +296,84 @@ class AttentionLayer:
             mla_rms_norm(self.hidden_problem, hidden, self.hidden_norm, self.x, residual=residual,
                          residual_out=None if residual is None else self.residual, stream=stream)
             torch.matmul(self.x, self.w_qkv_a, out=self.qkv_a)
-            self._append(self.qkv_a, positions, block_table, None, stream)
+            self._append(self.qkv_a, positions, block_table, None, stream, slots)
             mla_rms_norm(self.q_problem, self.qkv_a, self.q_norm, self.q_a, stream=stream)
             torch.matmul(self.q_a, self.w_q_b, out=self.q.view(self.rows, -1))
             mla_rope(self.rope_problem, self.rope, self.q, positions, stream=stream)
             mla_decode_step(self.plan, self.q, self.w_uk, self.cache, block_table, seq_lens, None,
                             self.workspace, self.w_uv, self.o_lat, self.lse, self.o, stream)
+            if self.weights is not None:
+                self._weigh(self.step_plan, self.workspace[int(self.plan.ws_q_hat):], self.lse, self.step_starts,
+                            block_table, seq_lens, self.step_workspace, stream)
             torch.matmul(self.o.view(self.rows, -1), self.w_o, out=self.out)
         return self.out, hidden if residual is None else self.residual
+
+    def prefill(self, hidden, residual, positions, requests, query_starts, block_table, seq_lens, slots=None,
+                context_tokens=None):
+        """decode() for a chunk: T new tokens, request b's those from
+        query_starts[b] (int32 [B + 1]) on, token t at positions[t] of
+        requests[t] (int32 [T]; a padded one behind query_starts[B] at -1);
+        seq_lens int32 [B] with the new tokens; context_tokens: over a quantised
+        cache, the most rows cached by the requests together (None: as many as
+        the pool holds, whose bf16 form is then set aside).  Returns (out,
+        residual) in tensors of their own; padded tokens' are zeros' and theirs."""
+        n = int(positions.numel())
+        for h in (hidden, residual) if residual is not None else (hidden,):
+            self._check_hidden(h, n)
+        self._check_int32(positions=(positions, n), requests=(requests, n), query_starts=(query_starts, self.B + 1),
+                          seq_lens=(seq_lens, self.B))
+        self._check_table(block_table)
+        if slots is not None:
+            self._check_int32(slots=(slots, n))
+        with torch.cuda.device(self.device):
+            stream = torch.cuda.current_stream(self.device)
+            x = torch.empty_like(hidden)
+            summed = None if residual is None else torch.empty_like(hidden)
+            mla_rms_norm(make_norm_problem(n, self.hidden, eps=self.eps), hidden, self.hidden_norm, x,
+                         residual=residual, residual_out=summed, stream=stream)
+            qkv_a = torch.matmul(x, self.w_qkv_a)
+            self._append(qkv_a, positions, block_table, requests, stream, slots)
+            q_a = torch.empty((n, self.q_rank), dtype=torch.bfloat16, device=self.device)
+            mla_rms_norm(make_norm_problem(n, self.q_rank, eps=self.eps, x_stride=self.q_rank + self.ROW), qkv_a,
+                         self.q_norm, q_a, stream=stream)
+            q = torch.matmul(q_a, self.w_q_b).view(n, self.H, self.HEAD)
+            mla_rope(make_rope_problem(n, self.H, self.HEAD, rope_offset=self.NOPE), self.rope, q, positions,
+                     stream=stream)
+            q_hat = torch.empty((n, self.H, self.ROW), dtype=torch.bfloat16, device=self.device)
+            pr = self.problem
+            mla_q_absorb(mla_decode_plan(make_problem(n, 1, self.H, pr.page_size, 1, 1), None, self.sm_count), q,
+                         self.w_uk, q_hat, stream)
+            plan = mla_chunk_make_plan(pr, n, self._context(context_tokens), self.sm_count)
+            workspace = torch.empty(int(plan.workspace_bytes), dtype=torch.uint8, device=self.device)
+            o_lat = torch.zeros((n, self.H, 512), dtype=torch.bfloat16, device=self.device)
+            lse = torch.empty((n, self.H), dtype=torch.float32, device=self.device)
+            mla_chunk_attend(plan, q_hat, query_starts, self.cache, block_table, seq_lens, workspace, o_lat, lse,
+                             status=self.status_word, stream=stream)
+            self._weigh(plan, q_hat, lse, query_starts, block_table, seq_lens, workspace, stream)
+            o = torch.bmm(o_lat.transpose(0, 1), self.w_uv).transpose(0, 1).reshape(n, -1)
+            out = torch.matmul(o, self.w_o)
+        return out, hidden if residual is None else summed
+
+    def evict(self, budget: int, block_table, seq_lens, sinks: int = 0, recent: int = 0):
+        """Cut every request's cache to `budget` rows, the first `sinks` and last
+        `recent` positions before those with the greatest weights: seq_lens
+        (int32 [B]) is updated, and pages from ceil(budget / page) on are free.
+        Needs a layer made with track."""
+        if self.weights is None:
+            raise ValueError("evict() needs a layer that tracks weights (track=True)")
+        self._check_int32(seq_lens=(seq_lens, self.B))
+        self._check_table(block_table)
+        with torch.cuda.device(self.device):
+            plan = mla_evict_make_plan(self.problem, budget, sinks, recent)
+            workspace = torch.empty(int(plan.workspace_bytes), dtype=torch.uint8, device=self.device)
+            mla_cache_evict(plan, self.cache, block_table, seq_lens, self.weights, self.slot_positions, workspace,
+                            status=self.status_word, stream=torch.cuda.current_stream(self.device))
+
+    def forget(self, request: int):
+        """Clear what is tracked of a request whose place another one takes."""
+        if self.weights is not None:
+            self.weights[request].zero_()
+            self.slot_positions[request].fill_(-1)
 
     def prompt(self, hidden, positions, requests, block_table):
         """Cache the rows of prompt tokens: hidden bf16 [T, hidden] (the layer's
