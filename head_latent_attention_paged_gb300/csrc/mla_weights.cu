@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kTokens = 2 * kTileRows;  // of a pair's tile
 constexpr int kMaxN = 256;              // rows (token, head) of a block
-constexpr int kSlots = 6;
+constexpr int kSlots = 6;                // a multiple of 3: chunks are loaded three at a time
 constexpr int kABytes = kTileRows * 128, kBBytes = kMaxN / 2 * 128, kSlotBytes = kABytes + kBBytes;
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 128 + 32 * kSumWarps;   // 4 warps that load and issue
@@ -48,7 +48,7 @@ struct WeightsKernelParams {
   int32_t box_rows;             // cached rows of a box: min(page, 128)
 };
 struct Maps {
-  CUtensorMap q, k, gather;
+  CUtensorMap q, k;
 };
 
 __device__ __forceinline__ uint8_t* shared_base() {
@@ -144,13 +144,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->d_full[i], 1);
-      mbar_init(&ctl->d_free[i], 2 * kSumWarps);
+      mbar_init(&ctl->d_free[i], kSumWarps);   // a group's four of each CTA
     }
     ctl->abort = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.q);
     prefetch_tmap(&maps.k);
-    prefetch_tmap(&maps.gather);
   }
   // the pair allocates together: not before both CTAs run
   __syncthreads();
@@ -212,42 +211,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if (warp == 0 || warp == 3) {
-    // warp 0: this CTA's 128 cached rows, warp 3: its half of the block's queries
+    // warp 0: this CTA's 128 cached rows, warp 3: its half of the block's queries;
+    // three chunks at a time, a lane for each of their boxes (8 of cached rows or 4
+    // of queries a chunk at most).  A unit is looked up one ahead.
     const bool cached = warp == 0;
     const uint32_t full_at = mapa_shared(smem_u32(ctl->full), 0);
+    const int chunk = lane >> 3, box = lane & 7;
     uint32_t slot = 0, phase = 1;         // phase: of `empty`, at first complete
-    while (ok && next_unit(p, end, &walk, &u)) {
-      if (u.block >= u.blocks) continue;
+    Unit next;
+    TilePages pages;
+    const auto advance = [&]() {          // the next unit with blocks, and its pages
+      while (next_unit(p, end, &walk, &next)) {
+        if (next.block >= next.blocks) continue;
+        pages.load(c, next.b, next.limit, 2 * next.tile + static_cast<int32_t>(rank), lane);
+        return true;
+      }
+      return false;
+    };
+    bool more = advance();
+    while (ok && more) {
+      u = next;
       const int32_t tile = 2 * u.tile + static_cast<int32_t>(rank);
-      TilePages pages;
-      pages.load(c, u.b, u.limit, tile, lane);
-      const TileRows rows(c, u.limit, tile, pages, p.dense ? p.dense[u.b] : -1, lane);
+      const TileRows rows(c, u.limit, tile, pages, -1, lane);
       if (cached && pages.bad(c) && lane == 0 && status) atomicOr(status, MLA_STATUS_BAD_PAGE);
-      const int32_t boxed = __shfl_sync(0xffffffffu, rows.base, (lane * (p.box_rows >> 4)) & 7);
-      int32_t four[4];
-      rows.four(4 * lane, four);
-      for (int32_t block = u.block; ok && block < u.blocks; ++block) {
-        const int32_t half = block_columns(u, block) / 2, row = u.row0 + block * kMaxN + half * static_cast<int32_t>(rank);
+      more = advance();
+      // Slots that hold no row of the request are read all the same, pages that are not
+      // there from the pool's start: a token's sums see no other token's row.
+      int32_t boxed = max(__shfl_sync(0xffffffffu, rows.base, (box * (p.box_rows >> 4)) & 7), 0);
+      if (p.dense) boxed = rows.left > 0 ? p.dense[u.b] + tile * kTileRows : 0;
 #pragma unroll 1
-        for (int k = 0; k < kChunks; ++k) {
-          if (lane == 0) {
-            ok = wait(&ctl->empty[slot], phase, status);
-            if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->full[slot], 2 * (cached ? kABytes : half * 128));
+      for (int32_t block = u.block; ok && block < u.blocks; ++block) {
+        const int32_t half = block_columns(u, block) / 2;
+        const int32_t row = u.row0 + block * kMaxN + half * static_cast<int32_t>(rank) + kBoxRows * box;
+        const int boxes = cached ? kTileRows / p.box_rows : half / kBoxRows;
+        const uint32_t bytes = cached ? kABytes : half * 128;
+#pragma unroll 1
+        for (int k = 0; ok && k < kChunks; k += 3) {
+          const uint32_t mine = slot + chunk;   // this lane's
+          bool todo = chunk < 3 && box < boxes;
+          for (uint32_t n = 1; __any_sync(0xffffffffu, todo); ++n) {
+            if (todo && mbar_poll(&ctl->empty[mine], phase)) {
+              if (box == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->full[mine], 2 * bytes);
+              uint8_t* const dst = smem + mine * kSlotBytes;
+              if (cached)
+                pair_tma_load_3d(dst + box * p.box_rows * 128, &maps.k, full_at + 8 * mine, 0, boxed, k + chunk);
+              else
+                pair_tma_load_3d(dst + kABytes + box * (kBoxRows * 128), &maps.q, full_at + 8 * mine, 0, row, k + chunk);
+              todo = false;
+            }
+            if ((n & 1023u) == 0) {     // the slowest of them, with a limit
+              bool there = true;
+              if (todo) there = wait_on(&ctl->empty[mine], phase, &ctl->abort, status);
+              ok = __all_sync(0xffffffffu, there);
+              if (!ok) break;
+            }
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          uint8_t* dst = smem + slot * kSlotBytes;
-          const uint32_t bar = full_at + 8 * slot;
-          if (!cached) {
-            if (lane < half / kBoxRows)
-              pair_tma_load_3d(dst + kABytes + lane * (kBoxRows * 128), &maps.q, bar, 0, row + kBoxRows * lane, k);
-          } else if (rows.whole) {
-            if (lane < kTileRows / p.box_rows)
-              pair_tma_load_3d(dst + lane * p.box_rows * 128, &maps.k, bar, 0, boxed, k);
-          } else {
-            pair_tma_gather4(dst + lane * 512, &maps.gather, bar, k * kChunkElems, four);
-          }
-          if (++slot == kSlots) {
+          slot += 3;
+          if (slot == kSlots) {
             slot = 0;
             phase ^= 1;
           }
@@ -283,42 +303,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 4) {
-    // sums: a lane of tensor memory is a token; the warps 8 .. 11 take the second half
-    // of a block's rows
-    const int quad = warp & 3, l = quad * 32 + lane, side = (warp >> 2) - 1, e = threadIdx.x - 128;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t free_bar = mapa_shared(smem_u32(ctl->d_free), 0);
+    // Sums: a lane of tensor memory is a token.  Blocks go to the warps 4 .. 7 and 8 ..
+    // 11 in turn, each with an accumulator of its own: what stands between a group's
+    // blocks (a unit's end, the next one's look-up) runs beside the other's sums.
+    const int quad = warp & 3, l = quad * 32 + lane, group = (warp >> 2) - 1;
+    const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kMaxN * group;
+    const uint32_t free_bar = mapa_shared(smem_u32(&ctl->d_free[group]), 0);
     const float2 scale2 = make_float2(c.scale_log2, c.scale_log2);
-    uint32_t done = 0, units = 0;
+    float* const neg = ctl->neg_lse[group];
+    int32_t* const seen = ctl->seen[group];
+    uint32_t done = 0, joined = 0;
     bool failed = false;
-    for (; next_unit(p, end, &walk, &u); ++units) {
+    while (next_unit(p, end, &walk, &u)) {
+      const int32_t blocks = u.blocks - u.block;
+      // a unit of one block is its group's alone
+      if (blocks < 2 && (blocks == 0 ? 0 : static_cast<int>(done & 1)) != group) {
+        done += blocks;
+        continue;
+      }
       const int64_t first = static_cast<int64_t>(u.tile) * kTokens + kTileRows * rank, t = first + l;
       const ChunkRequest r(u.len, u.count);
-      bool there = t < min(u.end, u.limit);
-      if (there) {
-        const int32_t page = c.block_table[static_cast<int64_t>(u.b) * c.max_pages + (t >> c.page_shift)];
-        there = page >= 0 && page < c.num_pages;
-      }
+      const bool writes = blocks < 2 || group == 0;
+      // used at the end: what it is added to, and whether the row is there
+      const int64_t out = u.b * p.w.stride + t;
+      const float before = writes && t < u.end && p.w.in ? p.w.in[out] : 0.f;
+      const int32_t page = writes && t < min(u.end, u.limit)
+                               ? c.block_table[static_cast<int64_t>(u.b) * c.max_pages + (t >> c.page_shift)] : -1;
       float2 acc[2] = {};
 #pragma unroll 1
       for (int32_t block = u.block; block < u.blocks; ++block, ++done) {
+        if (static_cast<int>(done & 1) != group) continue;
         const int columns = block_columns(u, block);
-        float* const neg = ctl->neg_lse[done & 1];
-        int32_t* const seen = ctl->seen[done & 1];
-        if (e < columns) {
+#pragma unroll 1
+        for (int e = l; e < columns; e += kTileRows) {
           const int32_t row = block * kMaxN + e;
           const float lse = row < u.rows ? p.w.lse[u.row0 + row] : INFINITY;
           neg[e] = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;   // no weight from a row that saw nothing
           seen[e] = row < u.rows ? r.seen(row / c.heads, c.causal) : 0;
         }
-        failed |= !wait(&ctl->d_full[done & 1], (done >> 1) & 1, status);
-        if (named_bar_or(1, 32 * kSumWarps, failed)) break;
+        failed |= !wait(&ctl->d_full[group], (done >> 1) & 1, status);
+        if (named_bar_or(1 + group, 128, failed)) break;
         tc_fence_after();
         const bool all = seen[0] >= first + kTileRows && (block + 1) * kMaxN <= u.rows;
 #pragma unroll 1
-        for (int k = side * columns / 2; k < (side + 1) * columns / 2; k += 32) {
+        for (int k = 0; k < columns; k += 32) {
           uint32_t x[32];
-          tmem_ld32(tmem + lanes + kMaxN * (done & 1) + k, x);
+          tmem_ld32(from + k, x);
           const float4* n4 = reinterpret_cast<const float4*>(neg + k);
           float v[32];
 #pragma unroll
@@ -339,16 +369,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 16; ++q) acc[q & 1] = __fadd2_rn(acc[q & 1], make_float2(v[2 * q], v[2 * q + 1]));
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) cluster_mbar_arrive(free_bar + 8 * (done & 1));
+        if (named_bar_or(1 + group, 128, failed)) break;   // neg and seen have been read
+        if (lane == 0) cluster_mbar_arrive(free_bar);
       }
-      const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-      if (side == 1) ctl->sums[units & 1][l] = sum;
-      if (named_bar_or(1, 32 * kSumWarps, failed)) break;
-      if (side == 0 && t < u.end) {
-        const int64_t at = u.b * p.w.stride + t;
-        p.w.out[at] = (p.w.in ? p.w.in[at] : 0.f) + (there ? sum + ctl->sums[units & 1][l] : 0.f);
+      float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      if (blocks >= 2) {                  // both groups have a part
+        float* const other = ctl->sums[joined++ & 1];
+        if (group == 1) other[l] = sum;
+        if (named_bar_or(3, 32 * kSumWarps, failed)) break;
+        sum += group == 0 ? other[l] : 0.f;
+      } else if (failed) {
+        break;
       }
+      if (writes && t < u.end) p.w.out[out] = before + (page >= 0 && page < c.num_pages ? sum : 0.f);
     }
   }
   __syncwarp();
@@ -377,8 +410,7 @@ cudaError_t launch_cache_weights(const WeightsParams& w, const ChunkWorkspace& w
   const uint64_t queries = static_cast<uint64_t>(w.c.tokens > 0 ? w.c.tokens : 1) * w.c.heads;
   Maps maps;
   if (!make_map_chunks_bf16(&maps.q, w.c.q, kDqk, queries, kDqk * 2, kBoxRows, 1) ||
-      !make_map_chunks_bf16(&maps.k, rows, kDqk, count, kDqk * 2, p.box_rows, 1) ||
-      !make_map_bf16(&maps.gather, rows, kDqk, count, kDqk * 2, kChunkElems, 1))
+      !make_map_chunks_bf16(&maps.k, rows, kDqk, count, kDqk * 2, p.box_rows, 1))
     return cudaErrorInvalidValue;
   cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(mla_cache_weights_kernel), kSmemAttrWeights, kSmemBytes);
   if (err != cudaSuccess) return err;
