@@ -40,7 +40,7 @@ constexpr int kPBytes = 2 * kChunkBytes;
 constexpr int kColO = 0, kColS = 256;   // tensor memory columns
 // What a row tile costs besides its tiles, in tokens of one (its queries' load,
 // its output): the work is cut where the sum of tokens and this is even.
-constexpr int kRowTileCost = 448;
+constexpr int kRowTileCost = 512;
 
 struct Control {
   uint64_t k_full[kKSlots], k_empty[kKSlots];   // full: in the leader, both CTAs' bytes
@@ -68,6 +68,7 @@ struct AttendKernelParams {
   const int32_t* dense;         // as in RowSource
   int32_t capacity;
   int32_t box_rows;             // rows of a K box, min(page, 64)
+  int32_t map_rows;             // rows that there are to read
 };
 
 // What a cluster's segment slots say to the merge.
@@ -183,84 +184,27 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* s
   return mbar_test(bar, parity) || wait_on(bar, parity, &control()->abort, status);
 }
 
-// The loads of one tile into slots that need many copies each: pages below 64 (K)
-// or 32 (V) tokens in boxes of one page, tiles that are not whole row by row in
-// gathers of four, where rows that are not there read as zeros.  Warp-wide; `use`
-// counts the ring's tiles.
-__device__ __noinline__ bool load_k_pieces(const AttendKernelParams& p, const Maps& maps, const TileRows& rows,
-                                           uint32_t use) {
-  Control* ctl = control();
-  const uint32_t rank = cluster_ctarank();
-  const int lane = threadIdx.x & 31;
-  const int pieces = kHalf / p.box_rows, piece = lane & (pieces - 1), chunk = lane / pieces;
-  const int32_t row = __shfl_sync(0xffffffffu, rows.base, 4 * rank + piece * (p.box_rows >> 4));
-  int32_t four[4];
-  rows.four(kHalf * rank + 4 * (lane & 15), four);
-  for (int j = 0; j < kKSlots; ++j) {
-    bool ok = true;
-    if (lane == 0) {
-      ok = use == 0 || wait_on(&ctl->k_empty[j], (use - 1) & 1, &ctl->abort, p.a.c.status);
-      if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->k_full[j], 2 * kKSlotBytes);
-    }
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-    uint8_t* dst = shared_base() + kOffK + j * kKSlotBytes;
-    const uint32_t bar = mapa_shared(smem_u32(&ctl->k_full[j]), 0);
-    if (rows.whole) {
-      if (chunk < kKChunks)
-        pair_tma_load_3d(dst + chunk * kChunkBytes + piece * p.box_rows * 128, &maps.k, bar, 0, row, kKChunks * j + chunk);
-    } else {
-      for (int c = lane >> 4; c < kKChunks; c += 2)
-        pair_tma_gather4(dst + c * kChunkBytes + (lane & 15) * 512, &maps.gather, bar, (kKChunks * j + c) * kChunkElems, four);
-    }
-  }
-  return true;
-}
-__device__ __noinline__ bool load_v_pieces(const AttendKernelParams& p, const Maps& maps, const TileRows& rows,
-                                           uint32_t use) {
-  Control* ctl = control();
-  const uint32_t rank = cluster_ctarank();
-  const int lane = threadIdx.x & 31;
-  for (int g = 0; g < kVSlots; ++g) {
-    bool ok = true;
-    if (lane == 0) {
-      ok = use == 0 || wait_on(&ctl->v_empty[g], (use - 1) & 1, &ctl->abort, p.a.c.status);
-      if (ok && rank == 0) mbar_arrive_expect_tx(&ctl->v_full[g], 2 * kVSlotBytes);
-    }
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-    uint8_t* dst = shared_base() + kOffV + g * kVSlotBytes;
-    const uint32_t bar = mapa_shared(smem_u32(&ctl->v_full[g]), 0);
-    if (rows.whole) {           // two boxes of 16 tokens, each with its four column tiles
-      const int32_t row = __shfl_sync(0xffffffffu, rows.base, 2 * g + (lane & 1));
-      if (lane < 2) pair_tma_load_3d(dst + lane * (kVSlotBytes / 2), &maps.v, bar, 0, row, 4 * rank);
-    } else {
-      const int atom = lane >> 3, group = lane & 7;
-      int32_t four[4];
-      rows.four(kVTokens * g + 4 * group, four);
-      const int offset = p.box_rows >= kVTokens ? atom * 4096 + group * 512
-                                                : (group >> 2) * (kVSlotBytes / 2) + atom * 2048 + (group & 3) * 512;
-      pair_tma_gather4(dst + offset, &maps.gather, bar, (4 * rank + atom) * kChunkElems, four);
-    }
-  }
-  return true;
-}
-
-// The loads of a whole tile with one copy a slot: lane j < slots has slot j and
-// fills it as soon as it is free.  x: the map's row of each lane, z its chunk.
-template <int kSlots, int kSlotBytes>
-__device__ __forceinline__ bool load_slots(uint64_t* full, uint64_t* empty, uint32_t full_at, uint8_t* dst,
-                                           const CUtensorMap* map, int32_t row, int32_t chunk, uint32_t use,
-                                           bool leader, uint32_t* status) {
-  const int lane = threadIdx.x & 31;
-  bool todo = lane < kSlots;
-  for (uint32_t n = 1; __any_sync(0xffffffffu, todo); ++n) {
-    if (todo && (use == 0 || mbar_poll(&empty[lane], (use - 1) & 1))) {
-      if (leader) mbar_arrive_expect_tx(&full[lane], 2 * kSlotBytes);
-      pair_tma_load_3d(dst + lane * kSlotBytes, map, full_at + 8 * lane, 0, row, chunk);
-      todo = false;
+// One box of a slot, a lane for each: filled as soon as its slot is free.  first: of
+// the slot's lanes the one that announces (in the leader) what both CTAs will write;
+// copy: whether this lane has a box of its own.  Warp-wide.
+struct Box {
+  bool todo, first, copy;
+  uint64_t *full, *empty;
+  uint32_t full_addr;           // of the leader's
+  uint8_t* dst;
+  int32_t row, chunk;
+};
+__device__ __forceinline__ bool load_boxes(Box b, const CUtensorMap* map, uint32_t bytes, uint32_t use, bool leader,
+                                           uint32_t* status) {
+  for (uint32_t n = 1; __any_sync(0xffffffffu, b.todo); ++n) {
+    if (b.todo && (use == 0 || mbar_poll(b.empty, (use - 1) & 1))) {
+      if (b.first && leader) mbar_arrive_expect_tx(b.full, 2 * bytes);
+      if (b.copy) pair_tma_load_3d(b.dst, map, b.full_addr, 0, b.row, b.chunk);
+      b.todo = false;
     }
     if ((n & 1023u) == 0) {     // the slowest of them, with a limit
       bool ok = true;
-      if (todo) ok = wait_on(&empty[lane], (use - 1) & 1, &control()->abort, status);
+      if (b.todo) ok = wait_on(b.empty, (use - 1) & 1, &control()->abort, status);
       if (!__all_sync(0xffffffffu, ok)) return false;
     }
   }
@@ -357,6 +301,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // queries and K: this CTA's 64 rows, and its 64 tokens of every tile
     const uint32_t q_bar = mapa_shared(smem_u32(&ctl->q_full), 0), k_bar = mapa_shared(smem_u32(ctl->k_full), 0);
+    const int pieces = kHalf / p.box_rows, boxes = pieces == 1 ? 1 : kKChunks * pieces;   // of a slot
+    const int slots_at_once = min(kKSlots, 32 / boxes);
     uint32_t use = 0, nq = 0;
     while (ok && next_segment(p, end, &walk, &s)) {
       if (s.end_tile <= s.first_tile) continue;
@@ -374,17 +320,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const TileRows rows(p.a.c, s.limit, tile, pages, dense, lane);
         if (pages.bad(p.a.c) && rank == 0 && lane == 0 && status) atomicOr(status, MLA_STATUS_BAD_PAGE);
         if (tile + 1 < s.end_tile) pages.load(p.a.c, s.b, s.limit, tile + 1, lane);
-        if (rows.whole && p.box_rows == kHalf)
-          ok = load_slots<kKSlots, kKSlotBytes>(ctl->k_full, ctl->k_empty, k_bar, smem + kOffK, &maps.k,
-                                                __shfl_sync(0xffffffffu, rows.base, 4 * rank), kKChunks * lane, use,
-                                                rank == 0, status);
-        else
-          ok = load_k_pieces(p, maps, rows, use);
+        // boxes of 64 tokens and the slot's chunks, or of a smaller page and one chunk.
+        // Slots that hold no row are read all the same, pages that are not there from
+        // the pool's start: their scores are masked out.
+        for (int j0 = 0; ok && j0 < kKSlots; j0 += slots_at_once) {
+          const int j = j0 + lane / boxes, i = lane % boxes, piece = i & (pieces - 1), chunk = i / pieces;
+          const int piece_at = 4 * static_cast<int>(rank) + piece * (p.box_rows >> 4);
+          int32_t row = max(__shfl_sync(0xffffffffu, rows.base, piece_at), 0);
+          if (p.dense) row = dense + tile * kTok + 16 * piece_at;   // whole tiles side by side, whatever the pages
+          const bool todo = lane < slots_at_once * boxes && j < kKSlots;
+          ok = load_boxes(Box{todo, i == 0, true, &ctl->k_full[j], &ctl->k_empty[j], k_bar + 8 * j,
+                              smem + kOffK + j * kKSlotBytes + chunk * kChunkBytes + piece * p.box_rows * 128, row,
+                              kKChunks * j + chunk},
+                          &maps.k, kKSlotBytes, use, rank == 0, status);
+        }
       }
     }
   } else if (warp == 3) {
     // V: this CTA's 256 latent columns of every token of the tile
     const uint32_t v_bar = mapa_shared(smem_u32(ctl->v_full), 0);
+    const int v_rows = min(p.box_rows, kVTokens), pieces = kVTokens / v_rows;
     uint32_t use = 0;
     while (ok && next_segment(p, end, &walk, &s)) {
       if (s.end_tile <= s.first_tile) continue;
@@ -395,12 +350,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
         const TileRows rows(p.a.c, s.limit, tile, pages, dense, lane);
         if (tile + 1 < s.end_tile) pages.load(p.a.c, s.b, s.limit, tile + 1, lane);
-        if (rows.whole && p.box_rows >= kVTokens)
-          ok = load_slots<kVSlots, kVSlotBytes>(ctl->v_full, ctl->v_empty, v_bar, smem + kOffV, &maps.v,
-                                                __shfl_sync(0xffffffffu, rows.base, (2 * lane) & 7), 4 * rank, use,
-                                                rank == 0, status);
-        else
-          ok = load_v_pieces(p, maps, rows, use);
+        // pieces of 32 tokens, or of a smaller page.  What no row stands in is zeros (its
+        // weight is zero, and nothing else must come of the product): pieces without
+        // any row are read behind the tensor's end, which fills with zeros
+        const int g = lane / pieces, piece = lane % pieces, t = kVTokens * g + v_rows * piece;
+        const int32_t base = __shfl_sync(0xffffffffu, rows.base, (t >> 4) & 7);
+        const int32_t last = __shfl_sync(0xffffffffu, rows.base, ((t + v_rows - 16) >> 4) & 7);
+        const bool todo = lane < kVSlots * pieces, none = base < 0 && last < 0;
+        const bool whole = base >= 0 && last >= 0 && rows.left - t >= v_rows;
+        uint32_t part = __ballot_sync(0xffffffffu, todo && !none && !whole);
+        ok = load_boxes(Box{todo, piece == 0, none || whole, &ctl->v_full[g], &ctl->v_empty[g], v_bar + 8 * g,
+                            smem + kOffV + g * kVSlotBytes + piece * (kVSlotBytes / 2), whole ? base : p.map_rows,
+                            4 * static_cast<int>(rank)},
+                        &maps.v, kVSlotBytes, use, rank == 0, status);
+        // pieces of which some rows are there (the last token's, or half a page where
+        // rows are expanded) row by row, in gathers of four
+        for (; ok && part; part &= part - 1) {
+          const int from = __ffs(part) - 1, groups = v_rows / 4, atom = lane / groups, group = lane % groups;
+          int32_t four[4];
+          rows.four((kVTokens * (from / pieces) + v_rows * (from % pieces) + 4 * group) & (kTok - 1), four);
+          if (lane < v_rows)
+            pair_tma_gather4(smem + kOffV + (from / pieces) * kVSlotBytes + (from % pieces) * (kVSlotBytes / 2) +
+                                 atom * v_rows * 128 + group * 512,
+                             &maps.gather, v_bar + 8 * (from / pieces), (4 * rank + atom) * kChunkElems, four);
+        }
       }
     }
   } else if (warp == 1) {
@@ -479,7 +452,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t use = 0;
     int slots_used = 0;
     bool failed = false;
-    while (next_segment(p, end, &walk, &s)) {
+    Segment next;
+    for (bool more = next_segment(p, end, &walk, &next); more;) {
+      s = next;
       const int n = s.end_tile - s.first_tile;
       const int32_t at = kHalf * static_cast<int32_t>(rank) + row;   // of the row tile
       const bool valid = at < s.rows;
@@ -557,6 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) cluster_mbar_arrive(p_bar);
       }
+      more = next_segment(p, end, &walk, &next);   // while the last product runs
       // the row's output: whole, or this cluster's part of it
       if (n > 0) {
         if (named_bar_or(row_bar, 128, failed)) break;   // the maxima have been read
@@ -724,6 +700,7 @@ cudaError_t launch_chunk_attend(const AttendParams& a, const ChunkWorkspace& w, 
   p.box_rows = w.starts ? kHalf : a.c.page_shift > 6 ? kHalf : 1 << a.c.page_shift;
   const void* rows = w.starts ? static_cast<const void*>(w.rows) : a.c.kv;
   const uint64_t count = w.starts ? static_cast<uint64_t>(w.capacity > 0 ? w.capacity : 1) : static_cast<uint64_t>(a.c.num_pages) << a.c.page_shift;
+  p.map_rows = static_cast<int32_t>(count);
   Maps maps;
   if (!make_map_chunks_bf16(&maps.q, a.c.q, kDqk, static_cast<uint64_t>(a.c.tokens) * a.c.heads, kDqk * 2, kHalf, kKChunks) ||
       !make_map_chunks_bf16(&maps.k, rows, kDqk, count, kDqk * 2, p.box_rows, p.box_rows == kHalf ? kKChunks : 1) ||
