@@ -170,6 +170,13 @@ __device__ __noinline__ bool next_segment(const AttendKernelParams& p, const int
   return false;
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 struct Maps {
   CUtensorMap q, k, v, gather;  // boxes of queries, K, V, and one row high
 };
@@ -555,11 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0 && threadIdx.x == 128)
           p.segments[slot] = make_int4(s.first_tile == 0 ? kOpens : kContinues, s.row0, s.rows, 0);
       }
-      // 32 columns of the warp's 32 rows at a time, turned in its part of P (which the
-      // products have read) so that four lanes write 64 bytes of a row together: one
-      // row a lane takes the memory pipe 32 cycles for each store
-      uint8_t* const turn = smem + kOffP + half * kChunkBytes + (quad & 1) * 4096 + side * 2048;
-      const int32_t row0 = kHalf * static_cast<int32_t>(rank) + 32 * (quad & 1);   // of the row tile
+      // 32 columns of a row at a time, in stores of 32 bytes: a whole sector each
 #pragma unroll 1
       for (int c = 128 * side; c < 128 * side + 128; c += 32) {
         uint32_t o[32] = {};
@@ -567,33 +570,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
         const int col = 256 * half + c;
-        if (whole) {
+        if (!whole) {
+          float* out = p.part_o + (static_cast<int64_t>(slot) * kRows + at) * kDc + col;
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_global_32(out + 8 * k, o + 8 * k);
+          }
+        } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             o[k] = pack_bf16(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])));
-        }
-#pragma unroll 1
-        for (int part = 0; part < (whole ? 1 : 2); ++part) {   // 64 bytes of each row
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 v = part == 0 ? make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3])
-                                      : make_uint4(o[16 + 4 * k], o[17 + 4 * k], o[18 + 4 * k], o[19 + 4 * k]);
-            *reinterpret_cast<uint4*>(turn + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = v;
+          uint16_t* out = p.a.o + static_cast<int64_t>(s.row0 + at) * kDc + col;
+          if (valid) {
+            st_global_32(out, o);
+            st_global_32(out + 16, o + 8);
           }
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = 8 * j + (lane >> 2), k = lane & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(turn + r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
-            if (row0 + r < s.rows) {
-              if (whole)
-                *reinterpret_cast<uint4*>(p.a.o + static_cast<int64_t>(s.row0 + row0 + r) * kDc + col + 8 * k) = v;
-              else
-                *reinterpret_cast<uint4*>(p.part_o + (static_cast<int64_t>(slot) * kRows + row0 + r) * kDc + col + 16 * part + 4 * k) = v;
-            }
-          }
-          __syncwarp();
         }
+        __syncwarp();
       }
       if (valid && quarter == 0)
         (whole ? p.a.lse[s.row0 + at] : p.part_lse[slot * kRows + at]) =

@@ -136,7 +136,7 @@ int mla_chunk_attend(const mla_chunk_plan* plan, const void* q_hat, const int32_
   if (rc != MLA_OK) return rc;
   if (plan->tokens == 0 || plan->problem.batch == 0) return MLA_OK;
   if (!o_lat || !lse) return MLA_ERR_INVALID_ARGUMENT;
-  if (!aligned(o_lat, 16) || !aligned(lse, 4)) return MLA_ERR_MISALIGNED;
+  if (!aligned(o_lat, 32) || !aligned(lse, 4)) return MLA_ERR_MISALIGNED;
   p.o = static_cast<uint16_t*>(o_lat);
   p.lse = lse;
   const ChunkWorkspace w = workspace_of(*plan, workspace);

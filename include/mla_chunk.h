@@ -106,7 +106,7 @@ MLA_API int mla_chunk_make_plan(const mla_problem* problem, int32_t tokens, int6
  *                  more rows than context_tokens, the surplus masked out;
  *                  MLA_STATUS_TIMEOUT: an internal wait hit its limit
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT, MLA_ERR_MISALIGNED (a pointer not on
- * 16 bytes; int32, lse and status: 4), MLA_ERR_WORKSPACE_TOO_SMALL or
+ * 16 bytes; o_lat: 32; int32, lse and status: 4), MLA_ERR_WORKSPACE_TOO_SMALL or
  * MLA_ERR_CUDA.
  */
 MLA_API int mla_chunk_attend(const mla_chunk_plan* plan, const void* q_hat,

@@ -110,6 +110,8 @@ def test_missing_and_misaligned_pointers(m, call, names):
         assert _code(m, call, m, **{name: A[9] + 2}) == m.MLA_ERR_MISALIGNED, name
     for name in {_attend: ("q", "cache", "ws", "o"), _weigh: ("q", "cache", "ws"), _evict: ("cache", "ws")}[call]:
         assert _code(m, call, m, **{name: A[9] + 4}) == m.MLA_ERR_MISALIGNED, name
+    if call is _attend:
+        assert _code(m, call, m, o=A[9] + 16) == m.MLA_ERR_MISALIGNED
     assert _code(m, call, m, status=A[9] + 2) == m.MLA_ERR_MISALIGNED
     assert _code(m, call, m, size=100) == m.MLA_ERR_WORKSPACE_TOO_SMALL
 
