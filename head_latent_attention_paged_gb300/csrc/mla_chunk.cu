@@ -384,59 +384,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // The pair's MMAs go out from two threads, S from this one and O from warp 2's,
-    // so that one's run while the other waits.
-    if (rank == 0 && elect_one()) {
+    // The pair's MMAs go out from two warps, S from this one and O from warp 2, so that
+    // one's run while the other waits.
+    if (rank == 0) {
       const uint32_t idesc = make_idesc_bf16(kRows, kTok, false, false);
-      const uint64_t q0 = make_smem_desc(smem_u32(smem), 16, 1024, kSmemLayoutSW128);
-      const uint64_t k0 = make_smem_desc(smem_u32(smem + kOffK), 16, 1024, kSmemLayoutSW128);
+      const MatrixWords q0(smem, 16, 1024), k0(smem + kOffK, 16, 1024);
       uint32_t use = 0, nq = 0;
       while (ok && next_segment(p, end, &walk, &s)) {
         if (s.end_tile <= s.first_tile) continue;
-        ok = wait(&ctl->q_full, nq++ & 1, status);
+        ok = __all_sync(0xffffffffu, wait(&ctl->q_full, nq++ & 1, status));
 #pragma unroll 1
         for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
           const uint32_t col = tmem + kColS + 64 * (use & 1);
-          ok = use < 2 || wait(&ctl->s_free[use & 1], ((use >> 1) - 1) & 1, status);
+          ok = use < 2 || __all_sync(0xffffffffu, wait(&ctl->s_free[use & 1], ((use >> 1) - 1) & 1, status));
 #pragma unroll 1
-          for (int c = 0; ok && c < kChunks; ++c) {
-            if (c % kKChunks == 0) {
-              ok = wait(&ctl->k_full[c / kKChunks], use & 1, status);
-              tc_fence_after();
-            }
-            const uint64_t at = (c * kChunkBytes) >> 4;
+          for (int j = 0; ok && j < kKSlots; ++j) {
+            ok = __all_sync(0xffffffffu, wait(&ctl->k_full[j], use & 1, status));
+            tc_fence_after();
+            const uint32_t at = (j * kKSlotBytes) >> 4;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) pair_mma_bf16(col, q0 + at + 2 * m, k0 + at + 2 * m, idesc, c > 0 || m > 0);
-            if (c % kKChunks == kKChunks - 1) pair_commit(&ctl->k_empty[c / kKChunks]);
+            for (int m = 0; m < 4 * kKChunks; ++m) {
+              const uint32_t o = at + (((m >> 2) * kChunkBytes + (m & 3) * 32) >> 4);
+              pair_mma_bf16(col, q0.lo + o, q0.hi, k0.lo + o, k0.hi, idesc, j > 0 || m > 0);
+            }
+            pair_commit(&ctl->k_empty[j]);
           }
           pair_commit(&ctl->s_full[use & 1]);
         }
         pair_commit(&ctl->q_empty);
       }
     }
-    __syncwarp();
   } else if (warp == 2) {
-    if (rank == 0 && elect_one()) {
+    if (rank == 0) {
       const uint32_t idesc = make_idesc_bf16(kRows, 256, false, true);
-      const uint64_t p0 = make_smem_desc(smem_u32(smem + kOffP), 16, 1024, kSmemLayoutSW128);
       const int v_rows = min(p.box_rows, kVTokens), v_atom = v_rows * 128;
-      const uint64_t v0 = make_smem_desc(smem_u32(smem + kOffV), v_atom, 1024, kSmemLayoutSW128);
-      const int v_step = v_rows == kVTokens ? 2048 : kVSlotBytes / 2;   // to the slot's second 16 tokens
+      const MatrixWords p0(smem + kOffP, 16, 1024), v0(smem + kOffV, v_atom, 1024);
+      const uint32_t v_step = (v_rows == kVTokens ? 2048 : kVSlotBytes / 2) >> 4;   // to the slot's second 16 tokens
+      const uint32_t v_half = (2 * v_atom) >> 4;                                    // to the second 128 columns
       uint32_t use = 0;
       while (ok && next_segment(p, end, &walk, &s)) {
 #pragma unroll 1
         for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
-          ok = wait(&ctl->p_full, use & 1, status);
+          ok = __all_sync(0xffffffffu, wait(&ctl->p_full, use & 1, status));
 #pragma unroll 1
           for (int g = 0; ok && g < kVSlots; ++g) {
-            ok = wait(&ctl->v_full[g], use & 1, status);
+            ok = __all_sync(0xffffffffu, wait(&ctl->v_full[g], use & 1, status));
             tc_fence_after();
-            const uint64_t vb = v0 + ((g * kVSlotBytes) >> 4);
-            const uint64_t pa = p0 + (((g >> 1) * kChunkBytes + (g & 1) * 64) >> 4);
+            const uint32_t vb = v0.lo + ((g * kVSlotBytes) >> 4);
+            const uint32_t pa = p0.lo + (((g >> 1) * kChunkBytes + (g & 1) * 64) >> 4);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {   // 16 tokens m & 1, columns 128 (m >> 1) .. of each CTA's 256
-              pair_mma_bf16(tmem + kColO + 128 * (m >> 1), pa + (((m & 1) * 32) >> 4),
-                            vb + (((m & 1) * v_step + (m >> 1) * 2 * v_atom) >> 4), idesc,
+              pair_mma_bf16(tmem + kColO + 128 * (m >> 1), pa + 2 * (m & 1), p0.hi,
+                            vb + (m & 1) * v_step + (m >> 1) * v_half, v0.hi, idesc,
                             tile > s.first_tile || g > 0 || (m & 1));
             }
             pair_commit(&ctl->v_empty[g]);
@@ -445,7 +444,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-    __syncwarp();
   } else {
     // softmax: lane l of tensor memory is row l % 64, tokens 64 (l / 64) .. of which
     // the warps 4 .. 7 take the first 32 and 8 .. 11 the others

@@ -19,19 +19,35 @@ __device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// D (+)= A B over both CTAs' halves; one thread of the leader.
-__device__ __forceinline__ void pair_mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// The words of a shared-memory matrix descriptor: the low one moves with the address
+// (in units of 16 bytes), the high one does not.
+struct MatrixWords {
+  uint32_t lo, hi;
+  __device__ __forceinline__ MatrixWords(const void* smem, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+    const uint64_t d = make_smem_desc(smem_u32(smem), lbo_bytes, sbo_bytes, kSmemLayoutSW128);
+    lo = static_cast<uint32_t>(d);
+    hi = static_cast<uint32_t>(d >> 32);
+  }
+};
+
+// D (+)= A B over both CTAs' halves.  Called by a whole warp of the leader, converged,
+// of which one thread issues: with every operand the same across the warp the
+// addresses stay in uniform registers (from inside a branch that one thread takes,
+// an MMA took 80-90 cycles to issue, two and a half times what it runs).
+__device__ __forceinline__ void pair_mma_bf16(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                              uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrive on `bar` of both CTAs once this thread's MMAs so far have completed.
+// Arrive on `bar` of both CTAs once the warp's MMAs so far have completed.
 __device__ __forceinline__ void pair_commit(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");

@@ -275,22 +275,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (rank == 0 && elect_one()) {
-      const uint64_t a0 = make_smem_desc(smem_u32(smem), 16, 1024, kSmemLayoutSW128);
+    if (rank == 0) {
+      const MatrixWords a0(smem, 16, 1024);
       uint32_t slot = 0, phase = 0, done = 0;
       while (ok && next_unit(p, end, &walk, &u)) {
 #pragma unroll 1
         for (int32_t block = u.block; ok && block < u.blocks; ++block, ++done) {
           const uint32_t idesc = make_idesc_bf16(kTokens, block_columns(u, block), false, false);
           const uint32_t col = tmem + kMaxN * (done & 1);
-          ok = done < 2 || wait(&ctl->d_free[done & 1], ((done >> 1) - 1) & 1, status);
+          ok = done < 2 || __all_sync(0xffffffffu, wait(&ctl->d_free[done & 1], ((done >> 1) - 1) & 1, status));
 #pragma unroll 1
           for (int k = 0; ok && k < kChunks; ++k) {
-            ok = wait(&ctl->full[slot], phase, status);
+            ok = __all_sync(0xffffffffu, wait(&ctl->full[slot], phase, status));
             tc_fence_after();
-            const uint64_t a = a0 + ((slot * kSlotBytes) >> 4), b = a + (kABytes >> 4);
+            const uint32_t a = a0.lo + ((slot * kSlotBytes) >> 4), b = a + (kABytes >> 4);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) pair_mma_bf16(col, a + 2 * m, b + 2 * m, idesc, k > 0 || m > 0);
+            for (int m = 0; m < 4; ++m) pair_mma_bf16(col, a + 2 * m, a0.hi, b + 2 * m, a0.hi, idesc, k > 0 || m > 0);
             pair_commit(&ctl->empty[slot]);
             if (++slot == kSlots) {
               slot = 0;
@@ -301,7 +301,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-    __syncwarp();
   } else if (warp >= 4) {
     // Sums: a lane of tensor memory is a token.  Blocks go to the warps 4 .. 7 and 8 ..
     // 11 in turn, each with an accumulator of its own: what stands between a group's
