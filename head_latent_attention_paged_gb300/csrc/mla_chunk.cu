@@ -46,7 +46,8 @@ struct Control {
   uint64_t k_full[kKSlots], k_empty[kKSlots];   // full: in the leader, both CTAs' bytes
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], s_free[2], p_full, pv_done;
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full[2], pv_done[2];         // of the tile's first 64 tokens and the others
   float part[2][4][kHalf];                // [parity][quarter of the tile][row]: maxima, at the end sums
   int64_t warp_sum[kThreads / 32];
   int32_t work[6];                        // first (request, row tile, tile) and end
@@ -240,8 +241,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->s_free[i], 2 * kSoftmaxWarps);
     }
-    mbar_init(&ctl->p_full, 2 * kSoftmaxWarps);
-    mbar_init(&ctl->pv_done, 1);
+    mbar_init(&ctl->p_full[0], 2 * kSoftmaxWarps);
+    mbar_init(&ctl->p_full[1], kSoftmaxWarps);
+    mbar_init(&ctl->pv_done[0], 1);
+    mbar_init(&ctl->pv_done[1], 1);
     ctl->abort = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.q);
@@ -425,9 +428,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       while (ok && next_segment(p, end, &walk, &s)) {
 #pragma unroll 1
         for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
-          ok = __all_sync(0xffffffffu, wait(&ctl->p_full, use & 1, status));
 #pragma unroll 1
           for (int g = 0; ok && g < kVSlots; ++g) {
+            if ((g & 1) == 0) ok = __all_sync(0xffffffffu, wait(&ctl->p_full[g >> 1], use & 1, status));
+            if (!ok) break;
             ok = __all_sync(0xffffffffu, wait(&ctl->v_full[g], use & 1, status));
             tc_fence_after();
             const uint32_t vb = v0.lo + ((g * kVSlotBytes) >> 4);
@@ -439,8 +443,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tile > s.first_tile || g > 0 || (m & 1));
             }
             pair_commit(&ctl->v_empty[g]);
+            if (g & 1) pair_commit(&ctl->pv_done[g >> 1]);
           }
-          pair_commit(&ctl->pv_done);
         }
       }
     }
@@ -450,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, l = quad * 32 + lane, row = l & 63, half = l >> 6, side = (warp >> 2) - 1;
     const int quarter = 2 * half + side;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t p_bar = mapa_shared(smem_u32(&ctl->p_full), 0), s_bar = mapa_shared(smem_u32(ctl->s_free), 0);
+    const uint32_t p_bar = mapa_shared(smem_u32(ctl->p_full), 0), s_bar = mapa_shared(smem_u32(ctl->s_free), 0);
     const uint32_t row_bar = 1 + (quad & 1);   // the 128 threads of 32 rows
     uint8_t* const prow = smem + kOffP + half * kChunkBytes + row * 128;
     const float scale = p.a.c.scale_log2;
@@ -516,8 +520,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         sum += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
         sum_rounded += (rounded[0].x + rounded[0].y) + (rounded[1].x + rounded[1].y);
-        if (use > 0) failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (use - 1) & 1, status));
+        // P's half is written when the last tile's product has read it.  The first half's
+        // product starts on its own: it also waits for the other half's warps to say that
+        // their lanes of O are ready, once the last tile's first product is through
+        if (use > 0) failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done[0], (use - 1) & 1, status));
         if (i > 0 && __any_sync(0xffffffffu, grow_by != 1.f)) {   // rare: 8 more bits than any tile before
+          failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done[1], (use - 1) & 1, status));
           tc_fence_after();
 #pragma unroll 1
           for (int c = 128 * side; c < 128 * side + 128; c += 16) {
@@ -528,6 +536,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_st16(tmem + lanes + kColO + c, o);
           }
           tc_fence_before();
+          __syncwarp();
+        }
+        if (half == 1) {
+          if (lane == 0) cluster_mbar_arrive(p_bar);
+          if (use > 0) failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done[1], (use - 1) & 1, status));
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -535,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) cluster_mbar_arrive(p_bar);
+        if (lane == 0) cluster_mbar_arrive(p_bar + 8 * half);
       }
       more = next_segment(p, end, &walk, &next);   // while the last product runs
       // the row's output: whole, or this cluster's part of it
@@ -543,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (named_bar_or(row_bar, 128, failed)) break;   // the maxima have been read
         ctl->part[0][quarter][row] = sum_rounded;
         ctl->part[1][quarter][row] = sum;
-        failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done, (use - 1) & 1, status));
+        failed |= !__all_sync(0xffffffffu, wait(&ctl->pv_done[1], (use - 1) & 1, status));
         if (named_bar_or(row_bar, 128, failed)) break;
         sum_rounded = sum = 0.f;
         for (int k = 0; k < 4; ++k) {
