@@ -117,15 +117,18 @@ __device__ __noinline__ void find_cut(const AttendKernelParams& p, const int64_t
   }
   const Rows r(p, lo);
   const int64_t y = x - prefix[lo];
-  int32_t i = 0, last = r.row_tiles - 1;
-  while (i < last) {
-    const int32_t mid = i + (last - i + 1) / 2;
-    if (r.cost(p, mid) <= y) i = mid; else last = mid - 1;
-  }
+  // the last row tile whose cost is at most y: near the root of cost(i) = y, then to
+  // the right of it (a float's error is far below a row tile but for millions of them)
+  const float slope = static_cast<float>(r.cost(p, 1)) - (p.a.c.causal ? kRows / 2 : 0), fy = static_cast<float>(y);
+  const float near = p.a.c.causal ? 2.f * fy / (slope + sqrtf(fmaf(slope, slope, 2.f * kRows * fy))) : fy / slope;
+  int32_t i = min(max(static_cast<int32_t>(near), 0), r.row_tiles - 1);
+  while (i > 0 && r.cost(p, i) > y) --i;
+  while (i + 1 < r.row_tiles && r.cost(p, i + 1) <= y) ++i;
   const int64_t from = r.cost(p, i), to = r.cost(p, i + 1);
+  const int32_t tiles = r.tiles(p, i);
   cut[0] = lo;
   cut[1] = i;
-  cut[2] = static_cast<int32_t>(r.tiles(p, i) * (y - from) / (to - from));
+  cut[2] = min(static_cast<int32_t>(tiles * (static_cast<float>(y - from) / static_cast<float>(to - from))), max(tiles - 1, 0));
 }
 
 // A stretch of one row tile's tiles.
@@ -289,9 +292,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == kThreads - 1) prefix[batch] = at;
     __syncthreads();
     if (threadIdx.x == 0 || threadIdx.x == 32) {
+      // the same for both sides of a cut, and not descending: that is all it has to be
       const int64_t total = prefix[batch];
       const int c = cluster + (threadIdx.x == 32);
-      find_cut(p, prefix, total / clusters * c + min(static_cast<int64_t>(c), total % clusters),
+      const float share = static_cast<float>(total) * (static_cast<float>(c) / static_cast<float>(clusters));
+      find_cut(p, prefix, c == clusters ? total : min(static_cast<int64_t>(share), total),
                ctl->work + (threadIdx.x == 32 ? 3 : 0));
     }
     fence_proxy_async_smem();   // before copies land on the prefix

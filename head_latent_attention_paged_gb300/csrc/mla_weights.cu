@@ -188,9 +188,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == kThreads - 1) prefix[batch] = at;
     __syncthreads();
     if (threadIdx.x == 0 || threadIdx.x == 32) {
+      // the same for both sides of a cut, and not descending: that is all it has to be
       const int64_t total = prefix[batch];
       const int k = cluster + (threadIdx.x == 32);
-      find_cut(p, prefix, total / clusters * k + min(static_cast<int64_t>(k), total % clusters),
+      const float share = static_cast<float>(total) * (static_cast<float>(k) / static_cast<float>(clusters));
+      find_cut(p, prefix, k == clusters ? total : min(static_cast<int64_t>(share), total),
                ctl->work + (threadIdx.x == 32 ? 2 : 0));
     }
     fence_proxy_async_smem();   // before copies land on the prefix
