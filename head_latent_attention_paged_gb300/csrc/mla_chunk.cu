@@ -66,8 +66,7 @@ struct AttendKernelParams {
   float* part_o;                // [2 * clusters][128][512]
   float* part_lse;              // [2 * clusters][128]
   int4* segments;               // [2 * clusters]: kind, first row, rows, 0
-  const int32_t* dense;         // as in RowSource
-  int32_t capacity;
+  const int2* dense;            // ChunkWorkspace::starts
   int32_t box_rows;             // rows of a K box, min(page, 64)
   int32_t map_rows;             // rows that there are to read
 };
@@ -86,7 +85,7 @@ struct Rows {
   __device__ __forceinline__ Rows(const AttendKernelParams& p, int32_t b) : r(p.a.c, b) {
     rows = r.count * p.a.c.heads;
     row_tiles = (rows + kRows - 1) / kRows;
-    limit = RowSource{p.a.c, p.dense, p.capacity}.limit(r, b);
+    limit = rows_there(p.dense, r, b);
   }
   __device__ __forceinline__ int32_t tiles(const AttendKernelParams& p, int32_t i) const {
     const int32_t last = min((i + 1) * kRows, rows) - 1;
@@ -323,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (s.end_tile <= s.first_tile) continue;
       TilePages pages;
       pages.load(p.a.c, s.b, s.limit, s.first_tile, lane);
-      const int32_t dense = p.dense ? p.dense[s.b] : -1;
+      const int32_t dense = p.dense ? p.dense[s.b].x : -1;
       ok = nq == 0 || wait(&ctl->q_empty, (nq - 1) & 1, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       ++nq;
@@ -360,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (s.end_tile <= s.first_tile) continue;
       TilePages pages;
       pages.load(p.a.c, s.b, s.limit, s.first_tile, lane);
-      const int32_t dense = p.dense ? p.dense[s.b] : -1;
+      const int32_t dense = p.dense ? p.dense[s.b].x : -1;
 #pragma unroll 1
       for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
         const TileRows rows(p.a.c, s.limit, tile, pages, dense, lane);
@@ -370,17 +369,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // any row are read behind the tensor's end, which fills with zeros
         const int g = lane / pieces, piece = lane % pieces, t = kVTokens * g + v_rows * piece;
         const int32_t base = __shfl_sync(0xffffffffu, rows.base, (t >> 4) & 7);
-        const int32_t last = __shfl_sync(0xffffffffu, rows.base, ((t + v_rows - 16) >> 4) & 7);
-        const bool todo = lane < kVSlots * pieces, none = base < 0 && last < 0;
-        const bool whole = base >= 0 && last >= 0 && rows.left - t >= v_rows;
-        uint32_t part = __ballot_sync(0xffffffffu, todo && !none && !whole);
+        const bool todo = lane < kVSlots * pieces, none = base < 0, whole = !none && rows.left - t >= v_rows;
+        const uint32_t part = __ballot_sync(0xffffffffu, todo && !none && !whole);
         ok = load_boxes(Box{todo, piece == 0, none || whole, &ctl->v_full[g], &ctl->v_empty[g], v_bar + 8 * g,
                             smem + kOffV + g * kVSlotBytes + piece * (kVSlotBytes / 2), whole ? base : p.map_rows,
                             4 * static_cast<int>(rank)},
                         &maps.v, kVSlotBytes, use, rank == 0, status);
-        // pieces of which some rows are there (the last token's, or half a page where
-        // rows are expanded) row by row, in gathers of four
-        for (; ok && part; part &= part - 1) {
+        // the piece of the last token row by row, in gathers of four
+        if (ok && part) {
           const int from = __ffs(part) - 1, groups = v_rows / 4, atom = lane / groups, group = lane % groups;
           int32_t four[4];
           rows.four((kVTokens * (from / pieces) + v_rows * (from % pieces) + 4 * group) & (kTok - 1), four);
@@ -705,7 +701,6 @@ cudaError_t launch_chunk_attend(const AttendParams& a, const ChunkWorkspace& w, 
   p.part_lse = w.part_lse;
   p.segments = reinterpret_cast<int4*>(w.segments);
   p.dense = w.starts;
-  p.capacity = w.capacity;
   p.box_rows = w.starts ? kHalf : a.c.page_shift > 6 ? kHalf : 1 << a.c.page_shift;
   const void* rows = w.starts ? static_cast<const void*>(w.rows) : a.c.kv;
   const uint64_t count = w.starts ? static_cast<uint64_t>(w.capacity > 0 ? w.capacity : 1) : static_cast<uint64_t>(a.c.num_pages) << a.c.page_shift;

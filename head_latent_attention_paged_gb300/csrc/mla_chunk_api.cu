@@ -71,6 +71,11 @@ int fill_chunk(const mla_chunk_plan* plan, const void* q, const int32_t* starts,
   return MLA_OK;
 }
 
+// Expanded rows with each request's padding.
+int64_t dense_rows(int64_t context_tokens, int32_t batch) {
+  return context_tokens + static_cast<int64_t>(batch) * (kDensePad - 1);
+}
+
 ChunkWorkspace workspace_of(const mla_chunk_plan& plan, void* workspace) {
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool quantised = plan.problem.kv_dtype != MLA_KV_BF16;
@@ -78,9 +83,10 @@ ChunkWorkspace workspace_of(const mla_chunk_plan& plan, void* workspace) {
   w.part_o = reinterpret_cast<float*>(ws + plan.ws_partial_o);
   w.part_lse = reinterpret_cast<float*>(ws + plan.ws_partial_lse);
   w.segments = reinterpret_cast<int32_t*>(ws + plan.ws_segments);
-  w.starts = quantised ? reinterpret_cast<int32_t*>(ws + plan.ws_starts) : nullptr;
+  w.starts = quantised ? reinterpret_cast<int2*>(ws + plan.ws_starts) : nullptr;
   w.rows = quantised ? reinterpret_cast<uint16_t*>(ws + plan.ws_rows) : nullptr;
-  w.capacity = static_cast<int32_t>(plan.context_tokens);
+  w.context = static_cast<int32_t>(plan.context_tokens);
+  w.capacity = quantised ? static_cast<int32_t>(dense_rows(plan.context_tokens, plan.problem.batch)) : 0;
   w.clusters = plan.clusters;
   return w;
 }
@@ -98,7 +104,7 @@ int mla_chunk_make_plan(const mla_problem* problem, int32_t tokens, int64_t cont
     return MLA_ERR_INVALID_ARGUMENT;
   // rows of queries, and expanded rows, are 32-bit coordinates
   if (static_cast<int64_t>(tokens) * problem->num_heads > INT32_MAX - kRowsOfTile ||
-      (quantised && context_tokens > INT32_MAX - kRowsOfTile))
+      (quantised && (context_tokens > INT32_MAX || dense_rows(context_tokens, problem->batch) > INT32_MAX - kRowsOfTile)))
     return MLA_ERR_UNSUPPORTED;
   mla_chunk_plan pl;
   std::memset(&pl, 0, sizeof(pl));
@@ -117,8 +123,8 @@ int mla_chunk_make_plan(const mla_problem* problem, int32_t tokens, int64_t cont
   pl.ws_partial_o = take(parts * kRowsOfTile * kDc * 4);
   pl.ws_partial_lse = take(parts * kRowsOfTile * 4);
   pl.ws_segments = take(parts * 16);
-  pl.ws_starts = take((static_cast<int64_t>(problem->batch) + 1) * 4);
-  pl.ws_rows = take(pl.context_tokens * kDqk * 2);
+  pl.ws_starts = take((static_cast<int64_t>(problem->batch) + 1) * 8);
+  pl.ws_rows = take(quantised ? dense_rows(context_tokens, problem->batch) * kDqk * 2 : 0);
   pl.workspace_bytes = at;
   pl.mark = kChunkPlanMark;
   *plan_out = pl;

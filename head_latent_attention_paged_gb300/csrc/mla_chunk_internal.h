@@ -36,16 +36,19 @@ struct ChunkWorkspace {
   float* part_o;                // [2 * clusters][128][512]
   float* part_lse;              // [2 * clusters][128]
   int32_t* segments;            // [2 * clusters][4]
-  int32_t* starts;              // [batch + 1] each request's first expanded row; null: rows in pages
+  int2* starts;                 // [batch + 1] each request's first expanded row, and how many of its
+                                // rows there is room for; null: rows are read in pages
   uint16_t* rows;               // bf16 [capacity][576]
-  int32_t capacity, clusters;
+  int32_t context, capacity;    // rows of requests there is room for, and with each one's padding
+  int32_t clusters;
 };
+constexpr int kDensePad = 32;   // an expanded request's rows end with zeros to a multiple of this
 cudaError_t launch_chunk_attend(const AttendParams& p, const ChunkWorkspace& w, cudaStream_t stream);
 
 cudaError_t launch_cache_weights(const WeightsParams& p, const ChunkWorkspace& w, cudaStream_t stream);
 
 // A quantised cache's rows, of the requests that have new tokens, as bf16 rows
-// one request behind the other.
+// one request behind the other, each with its padding.
 cudaError_t launch_expand(const ChunkParams& p, const ChunkWorkspace& w, cudaStream_t stream);
 
 constexpr int kMaxChunkClusters = 512;   // of a plan: more SMs are taken as 1,024

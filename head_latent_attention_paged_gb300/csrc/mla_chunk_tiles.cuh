@@ -23,17 +23,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// The cached rows that a kernel reads: in pages, or expanded one request behind the
-// other.
-struct RowSource {
-  const ChunkParams& c;
-  const int32_t* dense;         // [batch + 1] each request's first expanded row, or null
-  int32_t capacity;             // expanded rows there are
-  // rows of a request that there are: from there on they are masked out
-  __device__ __forceinline__ int32_t limit(const ChunkRequest& r, int32_t b) const {
-    return dense && r.count > 0 ? min(r.len, max(capacity - dense[b], 0)) : r.len;
-  }
-};
+// Rows of a request that there are, from where on they are masked out.  dense: as in
+// ChunkWorkspace::starts, null where rows are read in pages.
+__device__ __forceinline__ int32_t rows_there(const int2* dense, const ChunkRequest& r, int32_t b) {
+  return dense && r.count > 0 ? dense[b].y : r.len;
+}
 
 // The pages of a tile, looked up a tile ahead: lane l < 8 has the one of the tile's
 // tokens 16 l .. 16 l + 15.
@@ -53,19 +47,21 @@ struct TilePages {
 // tokens 16 l .. 16 l + 15, or -1.
 struct TileRows {
   int32_t base, left;           // left: rows of the request from the tile's first on
-  bool whole;                   // 128 rows, all there
-  // dense: the request's first expanded row, or -1 where rows are in pages
+  // dense: the request's first expanded row, or -1 where rows are in pages.  An
+  // expanded request ends with zeros to a multiple of kDensePad rows, and those of
+  // pages that are not there are zeros.
   __device__ __forceinline__ TileRows(const ChunkParams& c, int32_t limit, int32_t tile, const TilePages& at,
                                       int32_t dense, int lane) {
     const int64_t first = static_cast<int64_t>(tile) * kTileRows;
     const int32_t in = 16 * (lane & 7);
     left = static_cast<int32_t>(max(static_cast<int64_t>(limit) - first, int64_t{0}));
     base = -1;
-    if (in < left && at.page >= 0 && at.page < c.num_pages) {
-      const int32_t tok = static_cast<int32_t>(first) + in;
-      base = dense >= 0 ? dense + tok : (at.page << c.page_shift) + (tok & ((1 << c.page_shift) - 1));
+    if (dense >= 0) {
+      left = (left + kDensePad - 1) / kDensePad * kDensePad;
+      if (in < left) base = dense + static_cast<int32_t>(first) + in;
+    } else if (in < left && at.page >= 0 && at.page < c.num_pages) {
+      base = (at.page << c.page_shift) + ((static_cast<int32_t>(first) + in) & ((1 << c.page_shift) - 1));
     }
-    whole = __all_sync(0xffffffffu, base >= 0) && left >= kTileRows;
   }
   // the pool rows of four tokens from t (of the tile, a multiple of 4), -1 for none
   __device__ __forceinline__ void four(int32_t t, int32_t (&row)[4]) const {

@@ -43,8 +43,7 @@ static_assert((MLA_CHUNK_MAX_REQUESTS + 1) * 8 <= kOffControl, "the cost prefix 
 
 struct WeightsKernelParams {
   WeightsParams w;
-  const int32_t* dense;         // as in RowSource
-  int32_t capacity;
+  const int2* dense;            // ChunkWorkspace::starts
   int32_t box_rows;             // cached rows of a box: min(page, 128)
 };
 struct Maps {
@@ -102,7 +101,7 @@ __device__ __noinline__ bool next_unit(const WeightsKernelParams& p, const int32
     // the first token of the request that sees the tile's first row
     const int64_t first = c.causal ? static_cast<int64_t>(w->tile) * kTokens - (r.len - r.count) : 0;
     const int32_t from = static_cast<int32_t>(min(max(first, int64_t{0}), static_cast<int64_t>(r.count)));
-    *u = Unit{w->b, w->tile, w->t.end, RowSource{c, p.dense, p.capacity}.limit(r, w->b), r.first * c.heads, rows,
+    *u = Unit{w->b, w->tile, w->t.end, rows_there(p.dense, r, w->b), r.first * c.heads, rows,
               from * c.heads / kMaxN, (rows + kMaxN - 1) / kMaxN, r.len, r.count};
     if (from == r.count) u->block = u->blocks;
     ++w->tile;
@@ -166,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool bad = false;
     for (int32_t b = lo; b < hi; ++b) {
       const Tiles t(p, b);
-      bad |= t.r.bad || RowSource{c, p.dense, p.capacity}.limit(t.r, b) < t.r.len;
+      bad |= t.r.bad || rows_there(p.dense, t.r, b) < t.r.len;
       sum += t.tiles * t.cost;
     }
     if (bad && blockIdx.x == 0 && c.status) atomicOr(c.status, MLA_STATUS_BAD_INDEX);
@@ -240,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // Slots that hold no row of the request are read all the same, pages that are not
       // there from the pool's start: a token's sums see no other token's row.
       int32_t boxed = max(__shfl_sync(0xffffffffu, rows.base, (box * (p.box_rows >> 4)) & 7), 0);
-      if (p.dense) boxed = rows.left > 0 ? p.dense[u.b] + tile * kTileRows : 0;
+      if (p.dense) boxed = rows.left > 0 ? p.dense[u.b].x + tile * kTileRows : 0;
 #pragma unroll 1
       for (int32_t block = u.block; ok && block < u.blocks; ++block) {
         const int32_t half = block_columns(u, block) / 2;
@@ -403,7 +402,6 @@ cudaError_t launch_cache_weights(const WeightsParams& w, const ChunkWorkspace& w
   WeightsKernelParams p;
   p.w = w;
   p.dense = ws.starts;
-  p.capacity = ws.capacity;
   p.box_rows = ws.starts ? kTileRows : 1 << w.c.page_shift;
   const void* rows = ws.starts ? static_cast<const void*>(ws.rows) : w.c.kv;
   const uint64_t count = ws.starts ? static_cast<uint64_t>(ws.capacity > 0 ? ws.capacity : 1)

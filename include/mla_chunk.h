@@ -49,9 +49,9 @@ typedef struct {
   int64_t ws_partial_o;     /* byte offset of f32 [2 * clusters][128][512] */
   int64_t ws_partial_lse;   /* byte offset of f32 [2 * clusters][128] */
   int64_t ws_segments;      /* byte offset of int32 [2 * clusters][4] */
-  int64_t ws_starts;        /* byte offset of int32 [batch + 1]: a quantised cache's
+  int64_t ws_starts;        /* byte offset of int32 [batch + 1][2]: a quantised cache's
                                requests in ws_rows */
-  int64_t ws_rows;          /* byte offset of bf16 [context_tokens][576] */
+  int64_t ws_rows;          /* byte offset of bf16 [context_tokens + 31 batch][576] */
   int64_t workspace_bytes;
 } mla_chunk_plan;
 
@@ -65,8 +65,8 @@ typedef struct {
  *   tokens         : query tokens of all requests together, >= 0
  *   context_tokens : quantised caches: the most rows that the requests of one
  *                    call have cached together (their rows are expanded to
- *                    bf16 in the workspace, 1,152 bytes each); MLA_KV_BF16: not
- *                    read
+ *                    bf16 in the workspace, 1,152 bytes each and up to 31 rows
+ *                    more a request); MLA_KV_BF16: not read
  *   sm_count       : streaming multiprocessors to fill (152 on GB300), > 0
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT or MLA_ERR_UNSUPPORTED.
  */
