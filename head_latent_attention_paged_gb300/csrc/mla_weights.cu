@@ -20,24 +20,29 @@ namespace {
 
 constexpr int kTokens = 2 * kTileRows;  // of a pair's tile
 constexpr int kMaxN = 256;              // rows (token, head) of a block
-constexpr int kSlots = 6;                // a multiple of 3: chunks are loaded three at a time
-constexpr int kABytes = kTileRows * 128, kBBytes = kMaxN / 2 * 128, kSlotBytes = kABytes + kBBytes;
+// The ring: a slot has a chunk of the CTA's tokens and one of its half of a block's
+// rows, as many slots as there is room for (a multiple of 3, chunks being loaded three
+// at a time): 6 for blocks of 256 rows, 9 where no request has more than 64, as in a
+// decode step, which memory bounds (with 6: decode step of 64 75 us).
+constexpr int kABytes = kTileRows * 128;
+constexpr int kMaxSlots = 9, kRingBytes = 216 * 1024;
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 128 + 32 * kSumWarps;   // 4 warps that load and issue
 constexpr int kBoxRows = 32;            // of the queries' boxes
 
 struct Control {
-  uint64_t full[kSlots], empty[kSlots]; // full: in the leader, both CTAs' bytes of both operands
+  uint64_t full[kMaxSlots], empty[kMaxSlots]; // full: in the leader, both CTAs' bytes of both operands
   uint64_t d_full[2], d_free[2];
   float neg_lse[2][kMaxN];              // [block's parity][row]: -lse log2 e, -inf for no row
   int32_t seen[2][kMaxN];
   float sums[2][kTileRows];
   int64_t warp_sum[kThreads / 32];
   int32_t work[4];                      // first (request, tile) and end
+  int32_t most_rows;                    // (token, head) of a request
   uint32_t tmem;
   int abort;
 };
-constexpr int kOffControl = kSlots * kSlotBytes, kSmemBytes = kOffControl + sizeof(Control);
+constexpr int kOffControl = kRingBytes, kSmemBytes = kOffControl + sizeof(Control);
 static_assert(kSmemBytes <= kMaxSmemBytes, "shared memory");
 static_assert((MLA_CHUNK_MAX_REQUESTS + 1) * 8 <= kOffControl, "the cost prefix borrows the ring");
 
@@ -137,7 +142,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&ctl->full[i], 2);
       mbar_init(&ctl->empty[i], 1);
     }
@@ -146,6 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->d_free[i], kSumWarps);   // a group's four of each CTA
     }
     ctl->abort = 0;
+    ctl->most_rows = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.q);
     prefetch_tmap(&maps.k);
@@ -162,12 +168,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int32_t batch = c.batch, each = (batch + kThreads - 1) / kThreads;
     const int32_t lo = min(static_cast<int32_t>(threadIdx.x) * each, batch), hi = min(lo + each, batch);
     int64_t sum = 0;
+    int32_t most = 0;
     bool bad = false;
     for (int32_t b = lo; b < hi; ++b) {
       const Tiles t(p, b);
       bad |= t.r.bad || rows_there(p.dense, t.r, b) < t.r.len;
       sum += t.tiles * t.cost;
+      most = max(most, t.r.count * c.heads);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0 && most > 0) atomicMax(&ctl->most_rows, most);
     if (bad && blockIdx.x == 0 && c.status) atomicOr(c.status, MLA_STATUS_BAD_INDEX);
     int64_t upto = sum;
 #pragma unroll
@@ -203,6 +213,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const uint32_t tmem = ctl->tmem;
   uint32_t* const status = c.status;
+  const uint32_t slot_bytes = kABytes + min(kMaxN, (ctl->most_rows + 63) / 64 * 64) * 64;
+  const uint32_t slots = min(kMaxSlots, static_cast<int>(kRingBytes / slot_bytes / 3 * 3));
   Walk walk;
   walk.b = ctl->work[0];
   walk.tile = ctl->work[1];
@@ -253,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (uint32_t n = 1; __any_sync(0xffffffffu, todo); ++n) {
             if (todo && mbar_poll(&ctl->empty[mine], phase)) {
               if (box == 0 && rank == 0) mbar_arrive_expect_tx(&ctl->full[mine], 2 * bytes);
-              uint8_t* const dst = smem + mine * kSlotBytes;
+              uint8_t* const dst = smem + mine * slot_bytes;
               if (cached)
                 pair_tma_load_3d(dst + box * p.box_rows * 128, &maps.k, full_at + 8 * mine, 0, boxed, k + chunk);
               else
@@ -268,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           slot += 3;
-          if (slot == kSlots) {
+          if (slot == slots) {
             slot = 0;
             phase ^= 1;
           }
@@ -289,11 +301,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; ok && k < kChunks; ++k) {
             ok = __all_sync(0xffffffffu, wait(&ctl->full[slot], phase, status));
             tc_fence_after();
-            const uint32_t a = a0.lo + ((slot * kSlotBytes) >> 4), b = a + (kABytes >> 4);
+            const uint32_t a = a0.lo + ((slot * slot_bytes) >> 4), b = a + (kABytes >> 4);
 #pragma unroll
             for (int m = 0; m < 4; ++m) pair_mma_bf16(col, a + 2 * m, a0.hi, b + 2 * m, a0.hi, idesc, k > 0 || m > 0);
             pair_commit(&ctl->empty[slot]);
-            if (++slot == kSlots) {
+            if (++slot == slots) {
               slot = 0;
               phase ^= 1;
             }
