@@ -95,7 +95,9 @@ MLA_API int mla_chunk_make_plan(const mla_problem* problem, int32_t tokens, int6
  *                  and reported); tokens from query_starts[batch] on are padding
  *   kv_cache, block_table, seq_lens : as for mla_decode_run, cached rows of
  *                  every kv_dtype.  Slots that hold no row of the request
- *                  (behind its last) may hold anything, NaN too
+ *                  (behind its last) may hold anything, NaN too; a row of the
+ *                  request that holds a NaN or an infinity may also reach tokens
+ *                  of its call that do not see it (their weight for it is 0)
  *   workspace    : device buffer of workspace_bytes >= plan->workspace_bytes
  *   o_lat        : bf16 [tokens][num_heads][512] (the decode's is f32; a chunk's
  *                  goes into a matrix product of its own); padding is left as it was
