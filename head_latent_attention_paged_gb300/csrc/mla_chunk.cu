@@ -42,25 +42,6 @@ constexpr int kColO = 0, kColS = 256;   // tensor memory columns
 // its output): the work is cut where the sum of tokens and this is even.
 constexpr int kRowTileCost = 512;
 
-struct Control {
-  uint64_t k_full[kKSlots], k_empty[kKSlots];   // full: in the leader, both CTAs' bytes
-  uint64_t v_full[kVSlots], v_empty[kVSlots];
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], s_free[2];
-  uint64_t p_full[2], pv_done[2];         // of the tile's first 64 tokens and the others
-  float part[2][4][kHalf];                // [parity][quarter of the tile][row]: maxima, at the end sums
-  int64_t warp_sum[kThreads / 32];
-  int32_t work[6];                        // first (request, row tile, tile) and end
-  uint32_t tmem;
-  int abort;
-};
-
-constexpr int kOffP = kQBytes, kOffK = kOffP + kPBytes, kOffV = kOffK + kKSlots * kKSlotBytes;
-constexpr int kOffControl = kOffV + kVSlots * kVSlotBytes;
-constexpr int kSmemBytes = kOffControl + sizeof(Control);
-static_assert(kSmemBytes <= kMaxSmemBytes, "shared memory");
-static_assert((MLA_CHUNK_MAX_REQUESTS + 1) * 8 <= kKSlots * kKSlotBytes, "the cost prefix borrows the ring");
-
 struct AttendKernelParams {
   AttendParams a;
   float* part_o;                // [2 * clusters][128][512]
@@ -101,21 +82,27 @@ struct Rows {
   }
 };
 
-// Where cost x lies: request, row tile and tile.
-__device__ __noinline__ void find_cut(const AttendKernelParams& p, const int64_t* prefix, int64_t x, int32_t* cut) {
-  const int32_t batch = p.a.c.batch;
-  if (x >= prefix[batch]) {
-    cut[0] = batch;
-    cut[1] = cut[2] = 0;
-    return;
-  }
-  int32_t lo = 0, hi = batch - 1;         // the last request whose prefix is at most x
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) / 2;
-    if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  const Rows r(p, lo);
-  const int64_t y = x - prefix[lo];
+struct Control {
+  uint64_t k_full[kKSlots], k_empty[kKSlots];   // full: in the leader, both CTAs' bytes
+  uint64_t v_full[kVSlots], v_empty[kVSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full[2], pv_done[2];         // of the tile's first 64 tokens and the others
+  float part[2][4][kHalf];                // [parity][quarter of the tile][row]: maxima, at the end sums
+  int64_t warp_sum[kThreads / 32];
+  int32_t cut[2][3];                      // begin and end: request, row tile, tile
+  Rows rows;                              // of the first request
+  uint32_t tmem;
+  int abort;
+};
+
+constexpr int kOffP = kQBytes, kOffK = kOffP + kPBytes, kOffV = kOffK + kKSlots * kKSlotBytes;
+constexpr int kOffControl = kOffV + kVSlots * kVSlotBytes;
+constexpr int kSmemBytes = kOffControl + sizeof(Control);
+static_assert(kSmemBytes <= kMaxSmemBytes, "shared memory");
+
+// Where cost y of a request lies: row tile and tile.
+__device__ __noinline__ void find_cut(const AttendKernelParams& p, const Rows& r, int64_t y, int32_t* cut) {
   // the last row tile whose cost is at most y: near the root of cost(i) = y, then to
   // the right of it (a float's error is far below a row tile but for millions of them)
   const float slope = static_cast<float>(r.cost(p, 1)) - (p.a.c.causal ? kRows / 2 : 0), fy = static_cast<float>(y);
@@ -125,9 +112,8 @@ __device__ __noinline__ void find_cut(const AttendKernelParams& p, const int64_t
   while (i + 1 < r.row_tiles && r.cost(p, i + 1) <= y) ++i;
   const int64_t from = r.cost(p, i), to = r.cost(p, i + 1);
   const int32_t tiles = r.tiles(p, i);
-  cut[0] = lo;
-  cut[1] = i;
-  cut[2] = min(static_cast<int32_t>(tiles * (static_cast<float>(y - from) / static_cast<float>(to - from))), max(tiles - 1, 0));
+  cut[0] = i;
+  cut[1] = min(static_cast<int32_t>(tiles * (static_cast<float>(y - from) / static_cast<float>(to - from))), max(tiles - 1, 0));
 }
 
 // A stretch of one row tile's tiles.
@@ -146,7 +132,8 @@ struct Walk {
   int32_t b, i, k, first;
   Rows r;                       // of request `of`
   int32_t of;
-  __device__ __forceinline__ explicit Walk(const int32_t* work) : b(work[0]), i(work[1]), k(work[2]), first(1), of(-1) {}
+  __device__ __forceinline__ Walk(const int32_t* begin, const Rows& rows)
+      : b(begin[0]), i(begin[1]), k(begin[2]), first(1), r(rows), of(begin[0]) {}
 };
 __device__ __noinline__ bool next_segment(const AttendKernelParams& p, const int32_t* end, Walk* w, Segment* s) {
   while (w->b < end[0] || (w->b == end[0] && (w->i < end[1] || (w->i == end[1] && w->k < end[2])))) {
@@ -260,15 +247,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 2) pair_tmem_alloc(&ctl->tmem, 512);
   after_predecessor();
 
-  // the cost prefix over requests, and this cluster's cuts
+  // the cost prefix over requests, and this cluster's cuts: half of the threads for
+  // its begin, half for its end, found by the thread in whose requests it lies
   {
-    int64_t* prefix = reinterpret_cast<int64_t*>(smem + kOffK);
-    const int32_t batch = p.a.c.batch, each = (batch + kThreads - 1) / kThreads;
-    const int32_t lo = min(static_cast<int32_t>(threadIdx.x) * each, batch), hi = min(lo + each, batch);
+    constexpr int kSide = kThreads / 2;
+    const int side = threadIdx.x / kSide, t = threadIdx.x % kSide;
+    const int32_t batch = p.a.c.batch, each = (batch + kSide - 1) / kSide;
+    const int32_t lo = min(t * each, batch), hi = min(lo + each, batch);
     int64_t sum = 0;
     bool bad = false;
-    for (int32_t b = lo; b < hi; ++b) {
-      const Rows r(p, b);
+    Rows r;
+    for (int32_t b = hi; b-- > lo;) {     // down, so that r ends as the first one's
+      r = Rows(p, b);
       bad |= r.r.bad || r.limit < r.r.len;
       sum += r.cost(p, r.row_tiles);
     }
@@ -280,25 +270,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane >= o) upto += y;
     }
     if (lane == 31) ctl->warp_sum[warp] = upto;
-    __syncthreads();
-    int64_t at = upto - sum;
-    for (int w = 0; w < warp; ++w) at += ctl->warp_sum[w];
-    for (int32_t b = lo; b < hi; ++b) {
-      prefix[b] = at;
-      const Rows r(p, b);
-      at += r.cost(p, r.row_tiles);
+    if (t == 0) {                         // a cut at the end of the work lies in no request
+      ctl->cut[side][0] = batch;
+      ctl->cut[side][1] = ctl->cut[side][2] = 0;
     }
-    if (threadIdx.x == kThreads - 1) prefix[batch] = at;
     __syncthreads();
-    if (threadIdx.x == 0 || threadIdx.x == 32) {
-      // the same for both sides of a cut, and not descending: that is all it has to be
-      const int64_t total = prefix[batch];
-      const int c = cluster + (threadIdx.x == 32);
-      const float share = static_cast<float>(total) * (static_cast<float>(c) / static_cast<float>(clusters));
-      find_cut(p, prefix, c == clusters ? total : min(static_cast<int64_t>(share), total),
-               ctl->work + (threadIdx.x == 32 ? 3 : 0));
+    int64_t at = upto - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kSide / 32; ++w) {
+      const int64_t of = ctl->warp_sum[side * (kSide / 32) + w];
+      if (w < t / 32) at += of;
+      total += of;
     }
-    fence_proxy_async_smem();   // before copies land on the prefix
+    // the same for both sides of a cut, and not descending: that is all it has to be
+    const int c = cluster + side;
+    const float share = static_cast<float>(total) * (static_cast<float>(c) / static_cast<float>(clusters));
+    const int64_t x = c == clusters ? total : min(static_cast<int64_t>(share), total);
+    if (at <= x && x < at + sum) {
+      int32_t b = lo;
+      int64_t cost = r.cost(p, r.row_tiles);
+      while (x >= at + cost) {
+        at += cost;
+        r = Rows(p, ++b);
+        cost = r.cost(p, r.row_tiles);
+      }
+      ctl->cut[side][0] = b;
+      if (side == 0) ctl->rows = r;
+      find_cut(p, r, x - at, ctl->cut[side] + 1);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -307,8 +306,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const uint32_t tmem = ctl->tmem;
   uint32_t* const status = p.a.c.status;
-  Walk walk(ctl->work);
-  const int32_t* const end = ctl->work + 3;
+  Walk walk(ctl->cut[0], ctl->rows);
+  const int32_t* const end = ctl->cut[1];
   Segment s;
   bool ok = true;
 
@@ -607,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (n > 0 && named_bar_or(row_bar, 128, failed)) break;   // the sums have been read
     }
     if (rank == 0 && threadIdx.x == 128) {
-      const bool idle = ctl->work[0] == end[0] && ctl->work[1] == end[1] && ctl->work[2] == end[2];
+      const bool idle = ctl->cut[0][0] == end[0] && ctl->cut[0][1] == end[1] && ctl->cut[0][2] == end[2];
       if (!(slots_used & 1)) p.segments[2 * cluster] = make_int4(idle ? kIdle : kNone, 0, 0, 0);
       if (!(slots_used & 2)) p.segments[2 * cluster + 1] = make_int4(kNone, 0, 0, 0);
     }

@@ -30,22 +30,6 @@ constexpr int kSumWarps = 8;
 constexpr int kThreads = 128 + 32 * kSumWarps;   // 4 warps that load and issue
 constexpr int kBoxRows = 32;            // of the queries' boxes
 
-struct Control {
-  uint64_t full[kMaxSlots], empty[kMaxSlots]; // full: in the leader, both CTAs' bytes of both operands
-  uint64_t d_full[2], d_free[2];
-  float neg_lse[2][kMaxN];              // [block's parity][row]: -lse log2 e, -inf for no row
-  int32_t seen[2][kMaxN];
-  float sums[2][kTileRows];
-  int64_t warp_sum[kThreads / 32];
-  int32_t work[4];                      // first (request, tile) and end
-  int32_t most_rows;                    // (token, head) of a request
-  uint32_t tmem;
-  int abort;
-};
-constexpr int kOffControl = kRingBytes, kSmemBytes = kOffControl + sizeof(Control);
-static_assert(kSmemBytes <= kMaxSmemBytes, "shared memory");
-static_assert((MLA_CHUNK_MAX_REQUESTS + 1) * 8 <= kOffControl, "the cost prefix borrows the ring");
-
 struct WeightsKernelParams {
   WeightsParams w;
   const int2* dense;            // ChunkWorkspace::starts
@@ -54,15 +38,6 @@ struct WeightsKernelParams {
 struct Maps {
   CUtensorMap q, k;
 };
-
-__device__ __forceinline__ uint8_t* shared_base() {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  return smem;
-}
-__device__ __forceinline__ Control* control() { return reinterpret_cast<Control*>(shared_base() + kOffControl); }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  return mbar_test(bar, parity) || wait_on(bar, parity, &control()->abort, status);
-}
 
 // A request's tiles and what each costs: a read of its rows and its products, in
 // the latter's time for 64 rows of queries.
@@ -77,6 +52,31 @@ struct Tiles {
     cost = 1 + (r.count > 0 ? 5 + (r.count * p.w.c.heads + 63) / 64 : 0);
   }
 };
+
+struct Control {
+  uint64_t full[kMaxSlots], empty[kMaxSlots]; // full: in the leader, both CTAs' bytes of both operands
+  uint64_t d_full[2], d_free[2];
+  float neg_lse[2][kMaxN];              // [block's parity][row]: -lse log2 e, -inf for no row
+  int32_t seen[2][kMaxN];
+  float sums[2][kTileRows];
+  int64_t warp_sum[kThreads / 32];
+  int32_t cut[2][2];                    // begin and end: request, tile
+  Tiles tiles;                          // of the first request
+  int32_t most_rows;                    // (token, head) of a request
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kOffControl = kRingBytes, kSmemBytes = kOffControl + sizeof(Control);
+static_assert(kSmemBytes <= kMaxSmemBytes, "shared memory");
+
+__device__ __forceinline__ uint8_t* shared_base() {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  return smem;
+}
+__device__ __forceinline__ Control* control() { return reinterpret_cast<Control*>(shared_base() + kOffControl); }
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  return mbar_test(bar, parity) || wait_on(bar, parity, &control()->abort, status);
+}
 
 // A tile of a request and the blocks of queries that see any of it.
 struct Unit {
@@ -119,20 +119,6 @@ __device__ __forceinline__ int block_columns(const Unit& u, int32_t block) {   /
   return min(kMaxN, (u.rows - block * kMaxN + 63) / 64 * 64);
 }
 
-__device__ __noinline__ void find_cut(const WeightsKernelParams& p, const int64_t* prefix, int64_t x, int32_t* cut) {
-  const int32_t batch = p.w.c.batch;
-  cut[0] = batch;
-  cut[1] = 0;
-  if (x >= prefix[batch]) return;
-  int32_t lo = 0, hi = batch - 1;         // the last request whose prefix is at most x
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) / 2;
-    if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  cut[0] = lo;
-  cut[1] = static_cast<int32_t>((x - prefix[lo]) / Tiles(p, lo).cost);
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mla_cache_weights_kernel(const __grid_constant__ WeightsKernelParams p, const __grid_constant__ Maps maps) {
   uint8_t* const smem = shared_base();
@@ -162,22 +148,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 2) pair_tmem_alloc(&ctl->tmem, 512);
   after_predecessor();
 
-  // the cost prefix over requests, and this cluster's cuts
+  // the cost prefix over requests, and this cluster's cuts: half of the threads for
+  // its begin, half for its end, found by the thread in whose requests it lies
   {
-    int64_t* prefix = reinterpret_cast<int64_t*>(smem);
-    const int32_t batch = c.batch, each = (batch + kThreads - 1) / kThreads;
-    const int32_t lo = min(static_cast<int32_t>(threadIdx.x) * each, batch), hi = min(lo + each, batch);
+    constexpr int kSide = kThreads / 2;
+    const int side = threadIdx.x / kSide, i = threadIdx.x % kSide;
+    const int32_t batch = c.batch, each = (batch + kSide - 1) / kSide;
+    const int32_t lo = min(i * each, batch), hi = min(lo + each, batch);
     int64_t sum = 0;
     int32_t most = 0;
     bool bad = false;
-    for (int32_t b = lo; b < hi; ++b) {
-      const Tiles t(p, b);
+    Tiles t;
+    for (int32_t b = hi; b-- > lo;) {     // down, so that t ends as the first one's
+      t = Tiles(p, b);
       bad |= t.r.bad || rows_there(p.dense, t.r, b) < t.r.len;
       sum += t.tiles * t.cost;
       most = max(most, t.r.count * c.heads);
     }
     most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0 && most > 0) atomicMax(&ctl->most_rows, most);
+    if (side == 0 && lane == 0 && most > 0) atomicMax(&ctl->most_rows, most);
     if (bad && blockIdx.x == 0 && c.status) atomicOr(c.status, MLA_STATUS_BAD_INDEX);
     int64_t upto = sum;
 #pragma unroll
@@ -186,25 +175,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane >= o) upto += y;
     }
     if (lane == 31) ctl->warp_sum[warp] = upto;
-    __syncthreads();
-    int64_t at = upto - sum;
-    for (int w = 0; w < warp; ++w) at += ctl->warp_sum[w];
-    for (int32_t b = lo; b < hi; ++b) {
-      prefix[b] = at;
-      const Tiles t(p, b);
-      at += t.tiles * t.cost;
+    if (i == 0) {                         // a cut at the end of the work lies in no request
+      ctl->cut[side][0] = batch;
+      ctl->cut[side][1] = 0;
     }
-    if (threadIdx.x == kThreads - 1) prefix[batch] = at;
     __syncthreads();
-    if (threadIdx.x == 0 || threadIdx.x == 32) {
-      // the same for both sides of a cut, and not descending: that is all it has to be
-      const int64_t total = prefix[batch];
-      const int k = cluster + (threadIdx.x == 32);
-      const float share = static_cast<float>(total) * (static_cast<float>(k) / static_cast<float>(clusters));
-      find_cut(p, prefix, k == clusters ? total : min(static_cast<int64_t>(share), total),
-               ctl->work + (threadIdx.x == 32 ? 2 : 0));
+    int64_t at = upto - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kSide / 32; ++w) {
+      const int64_t of = ctl->warp_sum[side * (kSide / 32) + w];
+      if (w < i / 32) at += of;
+      total += of;
     }
-    fence_proxy_async_smem();   // before copies land on the prefix
+    // the same for both sides of a cut, and not descending: that is all it has to be
+    const int k = cluster + side;
+    const float share = static_cast<float>(total) * (static_cast<float>(k) / static_cast<float>(clusters));
+    const int64_t x = k == clusters ? total : min(static_cast<int64_t>(share), total);
+    if (at <= x && x < at + sum) {
+      int32_t b = lo;
+      while (x >= at + t.tiles * t.cost) {
+        at += t.tiles * t.cost;
+        t = Tiles(p, ++b);
+      }
+      ctl->cut[side][0] = b;
+      ctl->cut[side][1] = min(static_cast<int32_t>(static_cast<float>(x - at) / static_cast<float>(t.cost)), t.tiles);
+      if (side == 0) ctl->tiles = t;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -216,10 +212,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t slot_bytes = kABytes + min(kMaxN, (ctl->most_rows + 63) / 64 * 64) * 64;
   const uint32_t slots = min(kMaxSlots, static_cast<int>(kRingBytes / slot_bytes / 3 * 3));
   Walk walk;
-  walk.b = ctl->work[0];
-  walk.tile = ctl->work[1];
-  walk.of = -1;
-  const int32_t* const end = ctl->work + 2;
+  walk.b = walk.of = ctl->cut[0][0];
+  walk.tile = ctl->cut[0][1];
+  walk.t = ctl->tiles;
+  const int32_t* const end = ctl->cut[1];
   Unit u;
   bool ok = true;
 
