@@ -37,29 +37,31 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ int64_t ld_cluster_two(uint32_t addr) {
+  int64_t v;
+  asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 struct Shared {
-  int hist[kBins];
-  int total[kBins];             // over the cluster
+  alignas(8) int hist[3][kBins];          // of each digit
   int sums[kWarps];
   int newest, digit, left, ties;
   int tie[kWarps], hole[kWarps], mover[kWarps];   // of each warp
   int all[3];                   // of this CTA
 };
 
-// Inclusive prefix of v over the block's threads.
-__device__ __forceinline__ int block_prefix(Shared* s, int v) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The sum of v over the threads behind this one.
+__device__ __forceinline__ int block_behind(Shared* s, int v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
+    const int y = __shfl_down_sync(0xffffffffu, v, o);
+    if (lane + o < 32) v += y;
   }
-  if (lane == 31) s->sums[warp] = v;
+  if (lane == 0) s->sums[warp] = v;
   __syncthreads();
-  int before = lane < warp ? s->sums[lane] : 0;   // 32 warps, a lane for each
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  return v + before;
+  return v - own + __reduce_add_sync(0xffffffffu, lane > warp ? s->sums[lane] : 0);   // 32 warps, a lane for each
 }
 
 // What stands before this warp: counts[w] of the warps before it in the CTA, and the
@@ -68,9 +70,7 @@ __device__ __forceinline__ int before_warp(const int* counts, const int* all, ui
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int v = lane < warp ? counts[lane] : 0;
   if (lane < static_cast<int>(rank)) v += ld_cluster(mapa_shared(smem_u32(all), lane));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  return __reduce_add_sync(0xffffffffu, v);
 }
 
 // One cluster per request (kMaxKeys slots a CTA without making keys again; 32,768
@@ -101,12 +101,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
   int32_t moved = 0;
   if (n > budget) {             // the same for the whole cluster
     if (tid == 0) s.newest = -1;
-    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+    for (int i = tid; i < 3 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
     __syncthreads();
+    const int own = warp * each;          // of this CTA's keys
     int newest = -1;
-    for (int k = 0; k < steps; ++k) {
-      const int t = first + 32 * k + lane;
+#pragma unroll 4
+    for (int k = 0; k < steps; ++k) {     // weights too, while they are waited for anyway
+      const int t = first + 32 * k + lane, i = own + 32 * k + lane;
       if (t < n) newest = max(newest, pos[t]);
+      if (t < n && i < cap) keys[i] = __float_as_uint(w[t]);
     }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) atomicMax(&s.newest, newest);
@@ -114,11 +117,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
     newest = lane < clusters ? ld_cluster(mapa_shared(smem_u32(&s.newest), lane)) : -1;
     newest = __reduce_max_sync(0xffffffffu, newest);
     const int64_t border = static_cast<int64_t>(newest) - p.recent;
-    const auto make_key = [&](int t) { return rank_key(w[t], pos[t] < p.sinks || pos[t] > border); };
-    const int own = warp * each;          // of this CTA's keys
+    const auto make_key = [&](int t, float weight) { return rank_key(weight, pos[t] < p.sinks || pos[t] > border); };
     const auto key_at = [&](int k) {
       const int i = own + 32 * k + lane;
-      return i < cap ? keys[i] : make_key(first + 32 * k + lane);
+      return i < cap ? keys[i] : make_key(first + 32 * k + lane, w[first + 32 * k + lane]);
     };
     // the budget-th greatest key
     uint32_t found = 0, mask = 0;
@@ -130,37 +132,36 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
         if (t >= n) continue;
         uint32_t key;
         if (digit == 0) {
-          key = make_key(t);
           const int i = own + 32 * k + lane;
+          key = make_key(t, i < cap ? __uint_as_float(keys[i]) : w[t]);
           if (i < cap) keys[i] = key;
         } else {
           key = key_at(k);
         }
-        if ((key & mask) == found) atomicAdd(&s.hist[key >> shift & ((1 << bits) - 1)], 1);
+        if ((key & mask) == found) atomicAdd(&s.hist[digit][key >> shift & ((1 << bits) - 1)], 1);
       }
       cluster_sync_all();
-      for (int i = tid; i < kBins; i += kThreads) {
-        int sum = 0;
-        for (int r = 0; r < clusters; ++r) sum += ld_cluster(mapa_shared(smem_u32(&s.hist[i]), r));
-        s.total[i] = sum;
-      }
-      __syncthreads();
-      // from the greatest bin down: thread t has the two bins behind 2 t others
-      const int hi = s.total[kBins - 1 - 2 * tid], lo = s.total[kBins - 2 - 2 * tid];
-      const int upto = block_prefix(&s, hi + lo), before = upto - hi - lo;
+      // two bins of every CTA, all of them on their way at once
+      int64_t sums[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        sums[r] = r < clusters ? ld_cluster_two(mapa_shared(smem_u32(&s.hist[digit][2 * tid]), r)) : 0;
+      int64_t sum = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) sum += sums[r];   // neither half carries: below 2^31
+      const int lo = static_cast<int>(sum), hi = static_cast<int>(sum >> 32);
+      const int before = block_behind(&s, hi + lo), upto = before + hi + lo;
       if (before < left && left <= upto) {
         const bool second = left > before + hi;
-        s.digit = kBins - 1 - 2 * tid - second;
+        s.digit = 2 * tid + !second;
         s.left = left - before - (second ? hi : 0);
         s.ties = second ? lo : hi;
       }
-      cluster_sync_all();       // everyone has read every CTA's counts
-      for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+      __syncthreads();
       found |= static_cast<uint32_t>(s.digit) << shift;
       mask |= ((1u << bits) - 1u) << shift;
       left = s.left;
       ties = s.ties;
-      __syncthreads();
     }
     // equal ones: the first `left` of `ties` in the order of slots
     int ties_before = 0;
@@ -226,22 +227,21 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
       if (kept && !mover) {     // stays where it is
         w_out[t] = w[t];
         pos_out[t] = pos[t];
+      } else if (t >= budget && t < n && !kept) {
+        w_out[t] = 0.f;
+        pos_out[t] = -1;
       }
     }
     __threadfence();
     cluster_sync_all();         // the list is whole
     for (int i = rank * kThreads + tid; i < moved; i += clusters * kThreads) {
       const int2 move = __ldcg(reinterpret_cast<const int2*>(moves) + i);
-      w_out[move.x] = w[move.y];
-      pos_out[move.x] = pos[move.y];
-    }
-    cluster_sync_all();         // before the slots given up are cleared, in place
-    for (int k = 0; k < steps; ++k) {
-      const int t = first + 32 * k + lane;
-      if (t >= budget && t < n) {
-        w_out[t] = 0.f;
-        pos_out[t] = -1;
-      }
+      const float weight = w[move.y];
+      const int32_t position = pos[move.y];
+      w_out[move.x] = weight;
+      pos_out[move.x] = position;
+      w_out[move.y] = 0.f;      // read by this thread alone
+      pos_out[move.y] = -1;
     }
   } else if (w_out != w || pos_out != pos) {
     for (int k = 0; k < steps; ++k) {
