@@ -16,8 +16,8 @@ namespace mla {
 
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kThreadsShift = 10, kThreads = 1 << kThreadsShift, kWarps = kThreads / 32;
+constexpr int kBins = 2048, kCoarse = kBins / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 49152;         // of a CTA, in shared memory; those behind are made again
 constexpr int kMoveWarps = 4;
@@ -44,24 +44,54 @@ __device__ __forceinline__ int64_t ld_cluster_two(uint32_t addr) {
 }
 
 struct Shared {
-  alignas(8) int hist[3][kBins];          // of each digit
-  int sums[kWarps];
+  int hist[3][kBins];           // of each digit
+  alignas(8) int coarse[3][kCoarse];      // of 32 bins each
   int newest, digit, left, ties;
   int tie[kWarps], hole[kWarps], mover[kWarps];   // of each warp
   int all[3];                   // of this CTA
 };
 
-// The sum of v over the threads behind this one.
-__device__ __forceinline__ int block_behind(Shared* s, int v) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = v;
+// The sum of v over the lanes behind this one.
+__device__ __forceinline__ int behind(int v) {
+  const int lane = threadIdx.x & 31, own = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_down_sync(0xffffffffu, v, o);
     if (lane + o < 32) v += y;
   }
-  if (lane == 0) s->sums[warp] = v;
-  __syncthreads();
-  return v - own + __reduce_add_sync(0xffffffffu, lane > warp ? s->sums[lane] : 0);   // 32 warps, a lane for each
+  return v - own;
+}
+
+// The bin that holds the left-th greatest key, from the cluster's counts: the 32 bins
+// around it first, then it, 64 and 32 counts of each CTA (all 2,048 of eight CTAs took
+// 2 us a digit).  One warp; the loads of all CTAs are on their way at once.
+__device__ __noinline__ void find_digit(Shared* s, int digit, int clusters, int left) {
+  const int lane = threadIdx.x & 31;
+  int64_t two[kMaxCluster], both = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    two[r] = r < clusters ? ld_cluster_two(mapa_shared(smem_u32(&s->coarse[digit][2 * lane]), r)) : 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) both += two[r];   // neither half carries: below 2^31
+  const int lo = static_cast<int>(both), hi = static_cast<int>(both >> 32);
+  int before = behind(lo + hi);
+  const bool second = left > before + hi;
+  const uint32_t here = __ballot_sync(0xffffffffu, before < left && left <= before + lo + hi);
+  const int at = __ffs(here) - 1;
+  const int coarse = __shfl_sync(0xffffffffu, 2 * lane + !second, at);
+  left -= __shfl_sync(0xffffffffu, before + (second ? hi : 0), at);
+  int count[kMaxCluster], sum = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    count[r] = r < clusters ? ld_cluster(mapa_shared(smem_u32(&s->hist[digit][32 * coarse + lane]), r)) : 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) sum += count[r];
+  before = behind(sum);
+  if (before < left && left <= before + sum) {
+    s->digit = 32 * coarse + lane;
+    s->left = left - before;
+    s->ties = sum;
+  }
 }
 
 // What stands before this warp: counts[w] of the warps before it in the CTA, and the
@@ -76,12 +106,13 @@ __device__ __forceinline__ int before_warp(const int* counts, const int* all, ui
 // One cluster per request (kMaxKeys slots a CTA without making keys again; 32,768
 // slots cut to 4,096 by eight CTAs and moved 24 us, by one CTA that read them again
 // for every digit 410 us).
-__global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __grid_constant__ EvictParams p, const int clusters, const int cap) {
+__global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __grid_constant__ EvictParams p, const int cluster_shift, const int cap) {
   extern __shared__ uint32_t keys[];
   __shared__ Shared s;
   after_predecessor();
-  const int b = blockIdx.x / clusters, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = blockIdx.x % clusters;
+  const int clusters = 1 << cluster_shift, b = blockIdx.x >> cluster_shift;   // CTAs of a request
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x & (clusters - 1);
   const float* w = p.weights + b * p.stride;
   const int32_t* pos = p.positions + b * p.stride;
   float* w_out = p.weights_out + b * p.stride;
@@ -91,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
   const int32_t n = static_cast<int32_t>(min(max(static_cast<int64_t>(given), int64_t{0}), most));
   const int32_t budget = min(n, p.budget);
   // each warp has consecutive slots, 32 at a time
-  const int32_t each = static_cast<int32_t>((static_cast<int64_t>(n) + clusters * kThreads - 1) / (clusters * kThreads)) * 32;
+  const int32_t each = static_cast<int32_t>((static_cast<int64_t>(n) + clusters * kThreads - 1) >> (cluster_shift + kThreadsShift)) * 32;
   const int64_t at = (static_cast<int64_t>(rank) * kWarps + warp) * each;
   const int32_t first = static_cast<int32_t>(min(at, static_cast<int64_t>(n)));
   const int32_t steps = (min(each, n - first) + 31) / 32;
@@ -102,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
   if (n > budget) {             // the same for the whole cluster
     if (tid == 0) s.newest = -1;
     for (int i = tid; i < 3 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+    if (tid < 3 * kCoarse) (&s.coarse[0][0])[tid] = 0;
     __syncthreads();
     const int own = warp * each;          // of this CTA's keys
     int newest = -1;
@@ -138,25 +170,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
         } else {
           key = key_at(k);
         }
-        if ((key & mask) == found) atomicAdd(&s.hist[digit][key >> shift & ((1 << bits) - 1)], 1);
+        if ((key & mask) == found) {
+          const int bin = key >> shift & ((1 << bits) - 1);
+          atomicAdd(&s.hist[digit][bin], 1);
+          atomicAdd(&s.coarse[digit][bin >> 5], 1);
+        }
       }
       cluster_sync_all();
-      // two bins of every CTA, all of them on their way at once
-      int64_t sums[kMaxCluster];
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r)
-        sums[r] = r < clusters ? ld_cluster_two(mapa_shared(smem_u32(&s.hist[digit][2 * tid]), r)) : 0;
-      int64_t sum = 0;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) sum += sums[r];   // neither half carries: below 2^31
-      const int lo = static_cast<int>(sum), hi = static_cast<int>(sum >> 32);
-      const int before = block_behind(&s, hi + lo), upto = before + hi + lo;
-      if (before < left && left <= upto) {
-        const bool second = left > before + hi;
-        s.digit = 2 * tid + !second;
-        s.left = left - before - (second ? hi : 0);
-        s.ties = second ? lo : hi;
-      }
+      if (warp == 0) find_digit(&s, digit, clusters, left);
       __syncthreads();
       found |= static_cast<uint32_t>(s.digit) << shift;
       mask |= ((1u << bits) - 1u) << shift;
@@ -191,9 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
     };
     // the i-th free slot below the budget takes the i-th kept row behind it
     int holes = 0, movers = 0, tied = 0;
+#pragma unroll 4
     for (int k = 0; k < steps; ++k) {
       const int t = first + 32 * k + lane;
       const bool kept = kept_at(k, &tied);
+      if (t < budget && kept) { // stays where it is
+        w_out[t] = w[t];
+        pos_out[t] = pos[t];
+      }
       holes += __popc(__ballot_sync(0xffffffffu, t < budget && !kept));
       movers += __popc(__ballot_sync(0xffffffffu, t >= budget && kept));
     }
@@ -213,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
     const int first_hole = before_warp(s.hole, &s.all[1], rank), first_mover = before_warp(s.mover, &s.all[2], rank);
     moved = lane < clusters ? ld_cluster(mapa_shared(smem_u32(&s.all[1]), lane)) : 0;
     moved = __reduce_add_sync(0xffffffffu, moved);
+    cluster_arrive();           // what this CTA reads of the others it has read
     holes = first_hole;
     movers = first_mover;
     tied = 0;
@@ -224,25 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
       if (mover) moves[2 * (movers + __popc(m & below)) + 1] = t;
       holes += __popc(h);
       movers += __popc(m);
-      if (kept && !mover) {     // stays where it is
-        w_out[t] = w[t];
-        pos_out[t] = pos[t];
-      } else if (t >= budget && t < n && !kept) {
+      if (t >= budget && t < n && !kept) {   // given up; a mover's slot is cleared as it moves
         w_out[t] = 0.f;
         pos_out[t] = -1;
       }
     }
-    __threadfence();
-    cluster_sync_all();         // the list is whole
-    for (int i = rank * kThreads + tid; i < moved; i += clusters * kThreads) {
-      const int2 move = __ldcg(reinterpret_cast<const int2*>(moves) + i);
-      const float weight = w[move.y];
-      const int32_t position = pos[move.y];
-      w_out[move.x] = weight;
-      pos_out[move.x] = position;
-      w_out[move.y] = 0.f;      // read by this thread alone
-      pos_out[move.y] = -1;
-    }
+    cluster_wait();
   } else if (w_out != w || pos_out != pos) {
     for (int k = 0; k < steps; ++k) {
       const int t = first + 32 * k + lane;
@@ -258,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
   }
 }
 
-// One warp per row, in units that divide the format's rows.
+// One warp per row, in units that divide the format's rows; its weight and position
+// move with it.  No slot is in two moves.
 template <typename Unit, int kRowBytes>
 __global__ void __launch_bounds__(32 * kMoveWarps) mla_evict_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kUnits = kRowBytes / sizeof(Unit), kEach = (kUnits + 31) / 32;
@@ -266,10 +281,22 @@ __global__ void __launch_bounds__(32 * kMoveWarps) mla_evict_move_kernel(const _
   after_predecessor();
   const int b = blockIdx.y, count = p.counts[b];
   const int32_t* moves = p.moves + b * p.most_moves * 2;
+  const float* w = p.weights + b * p.stride;
+  const int32_t* pos = p.positions + b * p.stride;
+  float* w_out = p.weights_out + b * p.stride;
+  int32_t* pos_out = p.positions_out + b * p.stride;
   const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_pages;
   const int in_page = (1 << p.page_shift) - 1;
   for (int i = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); i < count; i += gridDim.x * kMoveWarps) {
     const int2 move = reinterpret_cast<const int2*>(moves)[i];
+    if (lane == 0) {
+      const float weight = w[move.y];
+      const int32_t position = pos[move.y];
+      w_out[move.x] = weight;
+      pos_out[move.x] = position;
+      w_out[move.y] = 0.f;
+      pos_out[move.y] = -1;
+    }
     const int32_t pt = table[move.x >> p.page_shift], pf = table[move.y >> p.page_shift];
     if (pt < 0 || pt >= p.num_pages || pf < 0 || pf >= p.num_pages) {
       if (p.status && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
@@ -296,8 +323,9 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream) {
                             ? p.stride : static_cast<int64_t>(p.max_pages) << p.page_shift;
   // CTAs for a request: more while there are multiprocessors for them and slots for
   // their threads
-  int cluster = 1;
-  while (cluster < kMaxCluster && 2 * cluster * static_cast<int64_t>(p.batch) <= 152 && slots > cluster * kThreads) cluster *= 2;
+  int shift = 0;
+  while (1 << shift < kMaxCluster && (int64_t{2} << shift) * p.batch <= 152 && slots > kThreads << shift) ++shift;
+  const int cluster = 1 << shift;
   const int64_t own = (slots + cluster * kThreads - 1) / (cluster * kThreads) * kThreads;
   const int cap = static_cast<int>(own < kMaxKeys ? own : kMaxKeys);
   cudaError_t err = set_smem_attr_once(reinterpret_cast<const void*>(mla_evict_select_kernel), kSmemAttrEvict, kMaxKeys * 4);
@@ -315,7 +343,7 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = cudaLaunchKernelEx(&cfg, mla_evict_select_kernel, p, cluster, cap);
+  err = cudaLaunchKernelEx(&cfg, mla_evict_select_kernel, p, shift, cap);
   if (err != cudaSuccess || p.most_moves == 0) return err;
   // rows of all requests over a few blocks a multiprocessor, at most one warp a move
   int64_t blocks = (p.most_moves + kMoveWarps - 1) / kMoveWarps;
