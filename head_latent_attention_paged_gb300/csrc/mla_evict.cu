@@ -138,10 +138,17 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
     const int own = warp * each;          // of this CTA's keys
     int newest = -1;
 #pragma unroll 4
-    for (int k = 0; k < steps; ++k) {     // weights too, while they are waited for anyway
+    for (int k = 0; k < steps; ++k) {
       const int t = first + 32 * k + lane, i = own + 32 * k + lane;
-      if (t < n) newest = max(newest, pos[t]);
-      if (t < n && i < cap) keys[i] = __float_as_uint(w[t]);
+      if (t >= n) continue;
+      const int position = pos[t];
+      const float weight = w[t];
+      newest = max(newest, position);
+      if (i < cap) keys[i] = __float_as_uint(weight);
+      if (t < budget) {         // for rows that stay; the others' slots are written again
+        w_out[t] = weight;
+        pos_out[t] = position;
+      }
     }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) atomicMax(&s.newest, newest);
@@ -212,14 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __g
     };
     // the i-th free slot below the budget takes the i-th kept row behind it
     int holes = 0, movers = 0, tied = 0;
-#pragma unroll 4
     for (int k = 0; k < steps; ++k) {
       const int t = first + 32 * k + lane;
       const bool kept = kept_at(k, &tied);
-      if (t < budget && kept) { // stays where it is
-        w_out[t] = w[t];
-        pos_out[t] = pos[t];
-      }
       holes += __popc(__ballot_sync(0xffffffffu, t < budget && !kept));
       movers += __popc(__ballot_sync(0xffffffffu, t >= budget && kept));
     }
