@@ -41,10 +41,11 @@ constexpr int kColO = 0, kColS = 256;   // tensor memory columns
 // What a row tile costs besides its tiles, in tokens of one (its queries' load,
 // its output): the work is cut where the sum of tokens and this is even.
 constexpr int kRowTileCost = 512;
+constexpr int kSegments = 4;
 
 struct AttendKernelParams {
   AttendParams a;
-  float* part_o;                // [2 * clusters][128][512]
+  float* part_o;                // [2 * clusters][64][128][8]: eight columns of all rows side by side
   float* part_lse;              // [2 * clusters][128]
   int4* segments;               // [2 * clusters]: kind, first row, rows, 0
   const int2* dense;            // ChunkWorkspace::starts
@@ -82,6 +83,16 @@ struct Rows {
   }
 };
 
+// A stretch of one row tile's tiles.
+struct alignas(16) Segment {
+  int32_t b, first_tile, end_tile, tiles;   // tiles: of the whole row tile
+  int32_t row_tile, row0, rows; // row0: of all rows (token, head); rows: valid ones of 128
+  int32_t len, count;           // of the request
+  int32_t limit;
+  int32_t first;                // 1: of this cluster
+  int32_t more;                 // 0: no segment, the ones before it were all
+};
+
 struct Control {
   uint64_t k_full[kKSlots], k_empty[kKSlots];   // full: in the leader, both CTAs' bytes
   uint64_t v_full[kVSlots], v_empty[kVSlots];
@@ -92,6 +103,8 @@ struct Control {
   int64_t warp_sum[kThreads / 32];
   int32_t cut[2][3];                      // begin and end: request, row tile, tile
   Rows rows;                              // of the first request
+  Segment segments[kSegments];            // what warp 0 has walked to and not every role has taken
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint32_t tmem;
   int abort;
 };
@@ -116,18 +129,9 @@ __device__ __noinline__ void find_cut(const AttendKernelParams& p, const Rows& r
   cut[1] = min(static_cast<int32_t>(tiles * (static_cast<float>(y - from) / static_cast<float>(to - from))), max(tiles - 1, 0));
 }
 
-// A stretch of one row tile's tiles.
-struct Segment {
-  int32_t b, first_tile, end_tile, tiles;   // tiles: of the whole row tile
-  int32_t row_tile, row0, rows; // row0: of all rows (token, head); rows: valid ones of 128
-  int32_t len, count;           // of the request
-  int32_t limit;
-  int32_t first;                // 1: of this cluster
-};
-
-// The segments between a cluster's cuts, in order; every role walks them itself.
-// Not inlined: the roles' loops run from the instruction cache, which one copy of
-// this in each of them would fill.
+// The segments between a cluster's cuts, in order, walked by warp 0 of each CTA.  The
+// other roles take them from shared memory: walked by each of them, the code alone
+// (cold each time, behind a row tile's loop) held up a row tile by 1.3 us and more.
 struct Walk {
   int32_t b, i, k, first;
   Rows r;                       // of request `of`
@@ -150,7 +154,7 @@ __device__ __noinline__ bool next_segment(const AttendKernelParams& p, const int
     const bool last = w->b == end[0] && w->i == end[1];
     const int32_t tiles = r.tiles(p, w->i), local = w->i * kRows;
     *s = Segment{w->b, w->k, last ? end[2] : tiles, tiles, w->i, r.r.first * p.a.c.heads + local,
-                 min(kRows, r.rows - local), r.r.len, r.r.count, r.limit, w->first};
+                 min(kRows, r.rows - local), r.r.len, r.r.count, r.limit, w->first, 1};
     w->first = 0;
     ++w->i;
     w->k = 0;
@@ -208,6 +212,20 @@ __device__ __forceinline__ bool load_boxes(Box b, const CUtensorMap* map, uint32
   return true;
 }
 
+// The next segment for this warp, which says so; false behind the last one and, with
+// `ok` false, once a wait gave up.
+__device__ __forceinline__ bool take(uint32_t* turn, Segment* s, bool* ok, uint32_t* status) {
+  Control* const ctl = control();
+  const uint32_t at = *turn % kSegments, parity = (*turn / kSegments) & 1;
+  *ok = __all_sync(0xffffffffu, wait(&ctl->seg_full[at], parity, status));
+  if (!*ok) return false;
+  *s = ctl->segments[at];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl->seg_empty[at]);
+  ++*turn;
+  return s->more != 0;
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mla_chunk_attend_kernel(const __grid_constant__ AttendKernelParams p, const __grid_constant__ Maps maps) {
   uint8_t* const smem = shared_base();
@@ -226,6 +244,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->q_empty, 1);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(&ctl->seg_full[i], 1);
+      mbar_init(&ctl->seg_empty[i], kSoftmaxWarps + (rank == 0 ? 3 : 1));   // the leader's MMAs too
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->s_free[i], 2 * kSoftmaxWarps);
@@ -306,9 +328,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const uint32_t tmem = ctl->tmem;
   uint32_t* const status = p.a.c.status;
-  Walk walk(ctl->cut[0], ctl->rows);
   const int32_t* const end = ctl->cut[1];
   Segment s;
+  uint32_t turn = 0;            // segments walked to, or taken
   bool ok = true;
 
   if (warp == 0) {
@@ -316,8 +338,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t q_bar = mapa_shared(smem_u32(&ctl->q_full), 0), k_bar = mapa_shared(smem_u32(ctl->k_full), 0);
     const int pieces = kHalf / p.box_rows, boxes = pieces == 1 ? 1 : kKChunks * pieces;   // of a slot
     const int slots_at_once = min(kKSlots, 32 / boxes);
+    Walk walk(ctl->cut[0], ctl->rows);
     uint32_t use = 0, nq = 0;
-    while (ok && next_segment(p, end, &walk, &s)) {
+    for (;; ++turn) {
+      if (!next_segment(p, end, &walk, &s)) s.more = 0;
+      const uint32_t at = turn % kSegments;
+      ok = __all_sync(0xffffffffu, ok && (turn < kSegments || wait(&ctl->seg_empty[at], (turn / kSegments - 1) & 1, status)));
+      if (!ok) break;
+      if (lane == 0) {
+        ctl->segments[at] = s;
+        mbar_arrive(&ctl->seg_full[at]);
+      }
+      if (!s.more) break;
       if (s.end_tile <= s.first_tile) continue;
       TilePages pages;
       pages.load(p.a.c, s.b, s.limit, s.first_tile, lane);
@@ -354,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t v_bar = mapa_shared(smem_u32(ctl->v_full), 0);
     const int v_rows = min(p.box_rows, kVTokens), pieces = kVTokens / v_rows;
     uint32_t use = 0;
-    while (ok && next_segment(p, end, &walk, &s)) {
+    while (ok && take(&turn, &s, &ok, status)) {
       if (s.end_tile <= s.first_tile) continue;
       TilePages pages;
       pages.load(p.a.c, s.b, s.limit, s.first_tile, lane);
@@ -393,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t idesc = make_idesc_bf16(kRows, kTok, false, false);
       const MatrixWords q0(smem, 16, 1024), k0(smem + kOffK, 16, 1024);
       uint32_t use = 0, nq = 0;
-      while (ok && next_segment(p, end, &walk, &s)) {
+      while (ok && take(&turn, &s, &ok, status)) {
         if (s.end_tile <= s.first_tile) continue;
         ok = __all_sync(0xffffffffu, wait(&ctl->q_full, nq++ & 1, status));
 #pragma unroll 1
@@ -425,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t v_step = (v_rows == kVTokens ? 2048 : kVSlotBytes / 2) >> 4;   // to the slot's second 16 tokens
       const uint32_t v_half = (2 * v_atom) >> 4;                                    // to the second 128 columns
       uint32_t use = 0;
-      while (ok && next_segment(p, end, &walk, &s)) {
+      while (ok && take(&turn, &s, &ok, status)) {
 #pragma unroll 1
         for (int32_t tile = s.first_tile; ok && tile < s.end_tile; ++tile, ++use) {
 #pragma unroll 1
@@ -462,7 +494,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int slots_used = 0;
     bool failed = false;
     Segment next;
-    for (bool more = next_segment(p, end, &walk, &next); more;) {
+    bool more = take(&turn, &next, &ok, status);
+    // a wait that gave up is agreed on at the next barrier of the row's warps
+    if (named_bar_or(row_bar, 128, !ok)) more = false;
+    while (more) {
       s = next;
       const int n = s.end_tile - s.first_tile;
       const int32_t at = kHalf * static_cast<int32_t>(rank) + row;   // of the row tile
@@ -477,7 +512,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t bad = (pages.bad(p.a.c) >> (2 * quarter)) & 3u;
         if (i + 1 < n) pages.load(p.a.c, s.b, s.limit, s.first_tile + i + 1, lane);
         const int32_t vis = min(max(seen - (s.first_tile + i) * kTok - 32 * quarter, 0), 32);
-        // a wait that gave up is agreed on at the next barrier of the row's warps
         failed |= !__all_sync(0xffffffffu, wait(&ctl->s_full[use & 1], (use >> 1) & 1, status));
         tc_fence_after();
         uint32_t x[32];
@@ -550,7 +584,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) cluster_mbar_arrive(p_bar + 8 * half);
       }
-      more = next_segment(p, end, &walk, &next);   // while the last product runs
+      more = take(&turn, &next, &ok, status);   // while the last product runs
+      failed |= !ok;
       // the row's output: whole, or this cluster's part of it
       if (n > 0) {
         if (named_bar_or(row_bar, 128, failed)) break;   // the maxima have been read
@@ -582,10 +617,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
         const int col = 256 * half + c;
         if (!whole) {
-          float* out = p.part_o + (static_cast<int64_t>(slot) * kRows + at) * kDc + col;
+          float* out = p.part_o + static_cast<int64_t>(slot) * kRows * kDc + (col * kRows + 8 * at);
           if (valid) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) st_global_32(out + 8 * k, o + 8 * k);
+            for (int k = 0; k < 4; ++k) st_global_32(out + 8 * k * kRows, o + 8 * k);
           }
         } else {
 #pragma unroll
@@ -603,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         (whole ? p.a.lse[s.row0 + at] : p.part_lse[slot * kRows + at]) =
             none ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       tc_fence_before();
-      if (n > 0 && named_bar_or(row_bar, 128, failed)) break;   // the sums have been read
+      if (named_bar_or(row_bar, 128, failed)) break;   // the sums have been read
     }
     if (rank == 0 && threadIdx.x == 128) {
       const bool idle = ctl->cut[0][0] == end[0] && ctl->cut[0][1] == end[1] && ctl->cut[0][2] == end[2];
@@ -624,13 +659,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // The merge of row tiles that were cut: lse = ln sum exp(lse_i), o = sum
-// exp(lse_i - lse) o_i over the parts in order.  Block (slot, 8 rows), a warp for
-// a row; the slot that opens a row tile looks for the clusters that continue it.
+// exp(lse_i - lse) o_i over the parts in order.  Block (slot, 8 rows); the slot that opens a row tile looks for the clusters that continue it.
 constexpr int kMergeWarps = 8;
 constexpr int kMaxParts = kMaxChunkClusters + 1;
 
 __global__ void __launch_bounds__(32 * kMergeWarps) mla_chunk_merge_kernel(const __grid_constant__ AttendKernelParams p, int clusters) {
   __shared__ int parts[kMaxParts], s_count;
+  __shared__ float weight[kMaxParts * kMergeWarps], s_inv[kMergeWarps];
   after_predecessor();
   const int slot = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 own = p.segments[slot];
@@ -656,39 +691,51 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_chunk_merge_kernel(const
   }
   __syncthreads();
   const int count = s_count;
-  if (r >= own.z) return;
-  float top = -INFINITY;
-  for (int i = lane; i < count; i += 32) top = fmaxf(top, p.part_lse[parts[i] * kRows + r]);
+  // a warp for a row's weights
+  const bool valid = r < own.z;
+  float top = -INFINITY, sum = 0.f;
+  for (int i = lane; i < count; i += 32)
+    if (valid) top = fmaxf(top, p.part_lse[parts[i] * kRows + r]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f;
-  float4 acc[4] = {};
-  if (top != -INFINITY) {
-#pragma unroll 2
-    for (int i = 0; i < count; ++i) {
-      const int from = parts[i];
-      const float4* o = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(from) * kRows + r) * kDc) + lane;
-      const float part = p.part_lse[from * kRows + r];
-      const float e = part == -INFINITY ? 0.f : expf(part - top);
-      sum += e;
+  for (int i = lane; i < count; i += 32) {
+    const float part = valid ? p.part_lse[parts[i] * kRows + r] : -INFINITY;
+    const float e = part == -INFINITY ? 0.f : expf(part - top);
+    weight[i * kMergeWarps + warp] = e;
+    sum += e;
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = o[32 * k];
-        acc[k].x = fmaf(e, v.x, acc[k].x);
-        acc[k].y = fmaf(e, v.y, acc[k].y);
-        acc[k].z = fmaf(e, v.z, acc[k].z);
-        acc[k].w = fmaf(e, v.w, acc[k].w);
-      }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int64_t row0 = own.y + static_cast<int64_t>(blockIdx.y) * kMergeWarps;
+  if (lane == 0) {
+    s_inv[warp] = top == -INFINITY ? 0.f : 1.f / sum;
+    if (valid) p.a.lse[row0 + warp] = top == -INFINITY ? -INFINITY : top + logf(sum);
+  }
+  __syncthreads();
+  // and for 64 columns of all rows: 4 of a row's a lane, two groups of eight at once
+  const int row = (lane >> 1) & 7, group = 8 * warp + (lane >> 4);
+  if (static_cast<int>(blockIdx.y) * kMergeWarps + row >= own.z) return;
+  const float* const from = p.part_o + (group * kRows + static_cast<int>(blockIdx.y) * kMergeWarps + row) * 8 + 4 * (lane & 1);
+  float4 acc[4] = {};
+#pragma unroll 2
+  for (int i = 0; i < count; ++i) {
+    const float* o = from + static_cast<int64_t>(parts[i]) * kRows * kDc;
+    const float e = weight[i * kMergeWarps + row];
+    if (e == 0.f) continue;     // its columns may hold anything
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(o + 2 * k * 8 * kRows);
+      acc[k].x = fmaf(e, v.x, acc[k].x);
+      acc[k].y = fmaf(e, v.y, acc[k].y);
+      acc[k].z = fmaf(e, v.z, acc[k].z);
+      acc[k].w = fmaf(e, v.w, acc[k].w);
     }
   }
-  const float inv = top == -INFINITY ? 0.f : 1.f / sum;
-  const int64_t grow = own.y + static_cast<int64_t>(r);
-  uint2* out = reinterpret_cast<uint2*>(p.a.o + grow * kDc) + lane;
+  const float inv = s_inv[row];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    out[32 * k] = make_uint2(pack_bf16(make_float2(acc[k].x * inv, acc[k].y * inv)),
-                             pack_bf16(make_float2(acc[k].z * inv, acc[k].w * inv)));
-  if (lane == 0) p.a.lse[grow] = top == -INFINITY ? -INFINITY : top + logf(sum);
+    *reinterpret_cast<uint2*>(p.a.o + (row0 + row) * kDc + 8 * (group + 2 * k) + 4 * (lane & 1)) =
+        make_uint2(pack_bf16(make_float2(acc[k].x * inv, acc[k].y * inv)), pack_bf16(make_float2(acc[k].z * inv, acc[k].w * inv)));
 }
 
 }  // namespace

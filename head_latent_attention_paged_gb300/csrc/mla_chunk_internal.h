@@ -33,7 +33,7 @@ struct WeightsParams {
 };
 
 struct ChunkWorkspace {
-  float* part_o;                // [2 * clusters][128][512]
+  float* part_o;                // [2 * clusters][64][128][8]
   float* part_lse;              // [2 * clusters][128]
   int32_t* segments;            // [2 * clusters][4]
   int2* starts;                 // [batch + 1] each request's first expanded row, and how many of its
