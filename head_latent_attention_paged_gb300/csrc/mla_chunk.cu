@@ -668,7 +668,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_chunk_merge_kernel(const
   __shared__ float weight[kMaxParts * kMergeWarps], s_inv[kMergeWarps];
   after_predecessor();
   const int slot = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 own = p.segments[slot];
+  const int4 none = make_int4(kNone, 0, 0, 0), own = p.segments[slot];
+  // with it, ahead of its use, what the next 32 clusters open with
+  int4 next = slot / 2 + 1 + lane < clusters && warp == 0 ? p.segments[2 * (slot / 2 + 1 + lane)] : none;
   const int r = blockIdx.y * kMergeWarps + warp;
   if (own.x != kOpens || static_cast<int>(blockIdx.y) * kMergeWarps >= own.z) return;
   // the parts in order: this slot, and the first ones of the clusters behind it that
@@ -678,7 +680,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_chunk_merge_kernel(const
     if (lane == 0) parts[0] = slot;
     for (int base = slot / 2 + 1; base < clusters; base += 32) {
       const int c = base + lane;
-      const int4 s = c < clusters ? p.segments[2 * c] : make_int4(kNone, 0, 0, 0);
+      const int4 s = next;
+      next = c + 32 < clusters ? p.segments[2 * (c + 32)] : none;
       const bool part = s.x == kContinues && s.y == own.y, stop = !part && s.x != kIdle;
       const uint32_t stops = __ballot_sync(0xffffffffu, stop);
       const uint32_t before = stops ? (1u << (__ffs(stops) - 1)) - 1u : 0xffffffffu;
@@ -717,11 +720,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_chunk_merge_kernel(const
   if (static_cast<int>(blockIdx.y) * kMergeWarps + row >= own.z) return;
   const float* const from = p.part_o + (group * kRows + static_cast<int>(blockIdx.y) * kMergeWarps + row) * 8 + 4 * (lane & 1);
   float4 acc[4] = {};
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < count; ++i) {
     const float* o = from + static_cast<int64_t>(parts[i]) * kRows * kDc;
     const float e = weight[i * kMergeWarps + row];
-    if (e == 0.f) continue;     // its columns may hold anything
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float4 v = *reinterpret_cast<const float4*>(o + 2 * k * 8 * kRows);
