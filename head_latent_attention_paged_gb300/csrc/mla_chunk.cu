@@ -212,6 +212,16 @@ __device__ __forceinline__ bool load_boxes(Box b, const CUtensorMap* map, uint32
   return true;
 }
 
+// The lanes whose bit `x` is not set give `hi` for their partner's `lo`.
+__device__ __forceinline__ void exchange(uint32_t lo[8], uint32_t hi[8], int x) {
+  const bool upper = threadIdx.x & x;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? lo[k] : hi[k], x);
+    (upper ? lo[k] : hi[k]) = got;
+  }
+}
+
 // The next segment for this warp, which says so; false behind the last one and, with
 // `ok` false, once a wait gave up.
 __device__ __forceinline__ bool take(uint32_t* turn, Segment* s, bool* ok, uint32_t* status) {
@@ -608,29 +618,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0 && threadIdx.x == 128)
           p.segments[slot] = make_int4(s.first_tile == 0 ? kOpens : kContinues, s.row0, s.rows, 0);
       }
-      // 32 columns of a row at a time, in stores of 32 bytes: a whole sector each
+      // 64 columns of a row at a time.  Parts go out as they are (ChunkWorkspace's layout
+      // puts the lanes' 32 bytes side by side); of whole rows' bf16 four lanes exchange
+      // their 32-byte pieces first, so that a store writes 128 bytes of each of 8 rows
 #pragma unroll 1
-      for (int c = 128 * side; c < 128 * side + 128; c += 32) {
-        uint32_t o[32] = {};
-        if (n > 0) tmem_ld32(tmem + lanes + kColO + c, o);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+      for (int c = 128 * side; c < 128 * side + 128; c += 64) {
+        uint32_t w[4][8];
         const int col = 256 * half + c;
-        if (!whole) {
-          float* out = p.part_o + static_cast<int64_t>(slot) * kRows * kDc + (col * kRows + 8 * at);
-          if (valid) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) st_global_32(out + 8 * k * kRows, o + 8 * k);
-          }
-        } else {
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[32] = {};
+          if (n > 0) tmem_ld32(tmem + lanes + kColO + c + 32 * h, o);
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            o[k] = pack_bf16(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])));
-          uint16_t* out = p.a.o + static_cast<int64_t>(s.row0 + at) * kDc + col;
-          if (valid) {
-            st_global_32(out, o);
-            st_global_32(out + 16, o + 8);
+          for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+          if (!whole) {
+            float* out = p.part_o + static_cast<int64_t>(slot) * kRows * kDc + ((col + 32 * h) * kRows + 8 * at);
+            if (valid) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) st_global_32(out + 8 * k * kRows, o + 8 * k);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              w[2 * h + (k >> 3)][k & 7] = pack_bf16(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])));
           }
+        }
+        if (whole) {
+          exchange(w[0], w[1], 1);
+          exchange(w[2], w[3], 1);
+          exchange(w[0], w[2], 2);
+          exchange(w[1], w[3], 2);
+          const int32_t row0 = at & ~3;
+          uint16_t* out = p.a.o + static_cast<int64_t>(s.row0 + row0) * kDc + col + 16 * (lane & 3);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (row0 + k < s.rows) st_global_32(out + k * kDc, w[k]);
         }
         __syncwarp();
       }
