@@ -104,8 +104,9 @@ __device__ __forceinline__ int before_warp(const int* counts, const int* all, ui
 }
 
 // One cluster per request (kMaxKeys slots a CTA without making keys again; 32,768
-// slots cut to 4,096 by eight CTAs and moved 24 us, by one CTA that read them again
-// for every digit 410 us).
+// slots cut to 4,096 by eight CTAs and moved 19 us, by one CTA that read them again
+// for every digit 410 us).  Bound by latency: 13 us are six barriers of the cluster and
+// what lies between them (a digit 1.5 us), not the 0.3 MB read.
 __global__ void __launch_bounds__(kThreads, 1) mla_evict_select_kernel(const __grid_constant__ EvictParams p, const int cluster_shift, const int cap) {
   extern __shared__ uint32_t keys[];
   __shared__ Shared s;
