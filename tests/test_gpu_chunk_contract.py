@@ -55,6 +55,16 @@ def test_a_query_that_saw_nothing_gives_nothing(m):
     assert abs(float(out[0].sum()) - 4 * 7) < 1e-3 and float(out[1].abs().sum()) == 0
 
 
+@pytest.mark.parametrize("sm_count", [2, 9, 152])
+@pytest.mark.parametrize("kv", ["bf16", "fp4"])
+def test_long_runs_of_rows_that_see_nothing(m, kv, sm_count):
+    """More row tiles without any tile, one after another, than are handed on at once."""
+    case = Case(m, [(40, 0), (300, 5), (12, 200), (200, 0), (90, 31)], 16, 32, kv, lead=1, pad=2)
+    case.make_plan(sm_count=sm_count)
+    case.attend()
+    case.check_attention()
+
+
 def test_requests_that_share_pages(m):
     """A prefix that several requests have in common is read in place."""
     case = Case(m, [(4, 200), (6, 200)], 8, 64, "bf16", seed=3)
