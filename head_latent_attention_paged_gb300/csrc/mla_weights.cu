@@ -355,7 +355,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           seen[e] = row < u.rows ? r.seen(row / c.heads, c.causal) : 0;
         }
         failed |= !wait(&ctl->d_full[group], (done >> 1) & 1, status);
-        if (named_bar_or(1 + group, 128, failed)) break;
+        failed = named_bar_or(1 + group, 128, failed);   // agreed on by the group
+        if (failed) break;
         tc_fence_after();
         const bool all = seen[0] >= first + kTileRows && (block + 1) * kMaxN <= u.rows;
 #pragma unroll 1
@@ -382,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 16; ++q) acc[q & 1] = __fadd2_rn(acc[q & 1], make_float2(v[2 * q], v[2 * q + 1]));
         }
         tc_fence_before();
-        if (named_bar_or(1 + group, 128, failed)) break;   // neg and seen have been read
+        named_bar_or(1 + group, 128, false);   // neg and seen have been read
         if (lane == 0) cluster_mbar_arrive(free_bar);
       }
       float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
@@ -392,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (named_bar_or(3, 32 * kSumWarps, failed)) break;
         sum += group == 0 ? other[l] : 0.f;
       } else if (failed) {
-        break;
+        continue;               // to where the other group waits, or the end
       }
       if (writes && t < u.end) p.w.out[out] = before + (page >= 0 && page < c.num_pages ? sum : 0.f);
     }
