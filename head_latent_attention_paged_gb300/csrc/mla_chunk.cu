@@ -18,7 +18,7 @@
 // Work is a row tile's tiles one after another, and all of it in a line that is cut
 // evenly between the pairs; row tiles that were cut are merged by a second kernel.
 // Long chunks are bound by the tensor cores (2,048 tokens of 20 heads behind 14,336:
-// 710-740 us, 1,850-1,930 TFLOP/s of a library product's 1,905).  Between two row
+// 710-765 us by machine, 1,790-1,930 TFLOP/s of a library product's 1,905).  Between two row
 // tiles the softmax warps stand for about 3.5 us: the last product, the output's 64 KB,
 // the next row tile's first scores.  Chunks with few tiles a row tile pay that often
 // (two whole prompts of 1,283 tokens, 5 tiles each: 110 us, 1,040 TFLOP/s).  A single
