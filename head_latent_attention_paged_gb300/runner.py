@@ -265,10 +265,20 @@ class AttentionLayer:
                                 norm_weight=self.kv_norm, norm_eps=self.eps, rope=rope,
                                 status=self.status_word, stream=stream)
         if self.slot_positions is not None:
-            width = self.slot_positions.shape[1]
-            requests = self.step_requests if requests is None else requests
-            where = torch.where((at >= 0) & (positions >= 0), at, width - 1).clamp_(max=width - 1)
-            self.slot_positions.view(-1)[requests.long() * width + where] = positions
+            self._track(at, positions, requests)
+
+    def _track(self, at, positions, requests):
+        """Note which token stands in each slot.  Tokens that the append leaves alone or
+        reports (a request outside the batch, say) go to padding's entries."""
+        width = self.slot_positions.shape[1]
+        live = (at >= 0) & (positions >= 0)
+        if requests is None:
+            requests = self.step_requests
+        else:
+            live &= (requests >= 0) & (requests < self.B)
+            requests = requests.clamp(0, self.B - 1)
+        where = torch.where(live, at, width - 1).clamp_(max=width - 1)
+        self.slot_positions.view(-1)[requests.long() * width + where] = positions
 
     def _weigh(self, plan, q_hat, lse, starts, block_table, seq_lens, workspace, stream):
         if self.weights is not None:

@@ -1,0 +1,49 @@
+"""What a tracking runner.AttentionLayer notes of the tokens it caches, and what
+eviction makes of it, where tokens are padding, out of range, or written again."""
+import numpy as np
+import pytest
+
+from chunk_testlib import f64, put
+from mla_testlib import ensure_built
+from test_gpu_attention_layer import HIDDEN
+from test_gpu_chunk_layer import _tracked
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def m():
+    ensure_built()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import head_latent_attention_paged_gb300 as mod
+    return mod
+
+
+def _states(n, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(n, HIDDEN, generator=g, device="cuda", dtype=torch.bfloat16)
+
+
+def _table(batch=2, max_pages=6):
+    return put(np.arange(batch * max_pages).reshape(batch, max_pages), np.int32)
+
+
+def test_requests_outside_the_batch_are_reported(m):
+    """As by a layer that does not track: a status bit, and nothing written."""
+    _, layer = _tracked(m, 4, 2, 1, m.MLA_KV_BF16, "bf16")
+    bt, lens = _table(), put([4, 3], np.int32)
+    layer.prefill(_states(7, 1), None, put([0, 1, 2, 3, 0, 1, 2], np.int32), put([0] * 4 + [1] * 3, np.int32),
+                  put([0, 4, 7], np.int32), bt, lens)
+    torch.cuda.synchronize()
+    assert layer.status() == 0
+    cache, weights, positions = layer.cache.clone(), layer.weights.clone(), layer.slot_positions.clone()
+    bad = put([-1, 2, 1 << 30, -5], np.int32)
+    layer.prompt(_states(4, 2), put([0, 1, 2, 3], np.int32), bad, bt)
+    torch.cuda.synchronize()
+    assert layer.status() == m.MLA_STATUS_BAD_INDEX
+    assert torch.equal(layer.cache, cache)
+    slots = 6 * 64
+    assert torch.equal(layer.weights[:, :slots], weights[:, :slots])
+    assert torch.equal(layer.slot_positions[:, :slots], positions[:, :slots])

@@ -1,0 +1,69 @@
+"""What a tracking runner.AttentionLayer notes of the tokens it caches (the slots'
+positions and weights), with the layer's tensors on the host and recorded calls in
+place of the library's."""
+import pytest
+
+from test_attention_layer_cpu import BATCH, HIDDEN, MAX_PAGES, _int, _make
+
+torch = pytest.importorskip("torch")
+
+SLOTS = MAX_PAGES * 64
+
+
+class _Nowhere:
+    def __init__(self, device):
+        pass
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        pass
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """[(name, arguments, keywords)] of the library's calls, none of which is made."""
+    from head_latent_attention_paged_gb300 import runner
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device", _Nowhere)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    for name in ("mla_rms_norm", "mla_rope", "mla_cache_append_tokens", "mla_q_absorb", "mla_decode_step",
+                 "mla_chunk_attend", "mla_cache_weights"):
+        monkeypatch.setattr(runner, name, lambda *a, name=name, **k: seen.append((name, a, k)))
+    return seen
+
+
+def _i32(*values):
+    return torch.tensor(values, dtype=torch.int32)
+
+
+def _live(layer):
+    """The slots' entries, without the one of padding."""
+    return layer.slot_positions[:, :SLOTS], layer.weights[:, :SLOTS]
+
+
+def _hidden(n):
+    return torch.zeros(n, HIDDEN, dtype=torch.bfloat16)
+
+
+def test_requests_outside_the_batch_note_nothing(calls):
+    """The append reports them and writes no row; neither is anything noted."""
+    layer = _make(track=True)
+    table = _int(BATCH, MAX_PAGES)
+    bad = [-1, BATCH, BATCH + 1, 2**31 - 1, -2**31]
+    positions, requests = _i32(5, *[7] * len(bad), 6), _i32(1, *bad, 0)
+    n = len(bad) + 2
+    want = torch.full((BATCH, SLOTS), -1, dtype=torch.int32)
+    want[1, 5], want[0, 6] = 5, 6
+    layer.prompt(_hidden(n), positions, requests, table)
+    assert torch.equal(_live(layer)[0], want)
+    layer.slot_positions.fill_(-1)
+    layer.prefill(_hidden(n), None, positions, requests, _i32(0, 1, n), table, _i32(7, 6), context_tokens=0)
+    assert torch.equal(_live(layer)[0], want)
+    # slots of their own, and positions and slots out of range
+    layer.slot_positions.fill_(-1)
+    layer.prefill(_hidden(n), None, positions, requests, _i32(0, 1, n), table, _i32(7, 6), context_tokens=0,
+                  slots=_i32(5, *[2] * len(bad), SLOTS))
+    want[0, 6] = -1
+    assert torch.equal(_live(layer)[0], want)
