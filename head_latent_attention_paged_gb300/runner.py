@@ -264,7 +264,7 @@ class AttentionLayer:
                                 block_table, self.cache, requests=requests, row_stride=width,
                                 norm_weight=self.kv_norm, norm_eps=self.eps, rope=rope,
                                 status=self.status_word, stream=stream)
-        if self.slot_positions is not None:
+        if self.slot_positions is not None and self.B > 0:
             self._track(at, positions, requests)
 
     def _track(self, at, positions, requests):

@@ -67,3 +67,10 @@ def test_requests_outside_the_batch_note_nothing(calls):
                   slots=_i32(5, *[2] * len(bad), SLOTS))
     want[0, 6] = -1
     assert torch.equal(_live(layer)[0], want)
+
+
+def test_a_layer_of_no_requests_notes_nothing(calls):
+    """Every request is outside its batch."""
+    layer = _make(track=True, batch=0)
+    layer.prompt(_hidden(2), _i32(0, 1), _i32(0, -1), _int(0, MAX_PAGES))
+    assert calls[-1][0] == "mla_cache_append_tokens" and layer.slot_positions.numel() == 0
