@@ -259,7 +259,7 @@ class AttentionLayer:
         if slots is not None:   # the append's position is the slot: the key is turned ahead of it
             mla_rope(make_rope_problem(n, 1, self.ROPE, x_token_stride=width), self.rope,
                      qkv_a[:, self.q_rank + 512:], positions, stream=stream)
-            rope, at = None, slots
+            rope, at = None, slots.masked_fill(positions < 0, -1)
         mla_cache_append_tokens(self.problem, n, qkv_a[:, self.q_rank:], at,
                                 block_table, self.cache, requests=requests, row_stride=width,
                                 norm_weight=self.kv_norm, norm_eps=self.eps, rope=rope,
@@ -289,7 +289,7 @@ class AttentionLayer:
         """hidden, residual (or None): bf16 [B * Q, hidden]; positions int32
         [B * Q] of the new tokens (-1: a padded row, whose request has length
         0); slots int32 [B * Q]: where the tokens are cached (None: at their
-        positions); seq_lens int32 [B] with the new tokens.  Returns (out, residual):
+        positions; padding's are not read); seq_lens int32 [B] with the new tokens.  Returns (out, residual):
         the attention's output and the residual stream to add it to (hidden
         itself without a residual).  Both may be the layer's own buffers, which
         the next decode() overwrites; either may be an input to that call."""

@@ -47,3 +47,23 @@ def test_requests_outside_the_batch_are_reported(m):
     slots = 6 * 64
     assert torch.equal(layer.weights[:, :slots], weights[:, :slots])
     assert torch.equal(layer.slot_positions[:, :slots], positions[:, :slots])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_padding_with_slots_leaves_the_cache(m, kv):
+    """Slots of a padded batch filled up with zeros: no row of slot 0 is lost."""
+    kind = {"bf16": m.MLA_KV_BF16, "fp8": m.MLA_KV_FP8_E4M3_E8M0, "fp4": m.MLA_KV_FP4_E2M1_E8M0}[kv]
+    _, layer = _tracked(m, 4, 2, 1, kind, kv)
+    bt = _table()
+    layer.prefill(_states(7, 1), None, put([0, 1, 2, 3, 0, 1, 2], np.int32), put([0] * 4 + [1] * 3, np.int32),
+                  put([0, 4, 7], np.int32), bt, put([4, 3], np.int32))
+    cache, weights, positions = layer.cache.clone(), layer.weights.clone(), layer.slot_positions.clone()
+    # both requests padded in a step, and a chunk of padding alone
+    layer.decode(_states(2, 2), None, put([-1, -1], np.int32), bt, put([0, 0], np.int32), slots=put([0, 0], np.int32))
+    layer.prefill(_states(3, 3), None, put([-1] * 3, np.int32), put([0, 1, 1], np.int32), put([0, 0, 0], np.int32), bt,
+                  put([4, 3], np.int32), slots=put([0, 0, 2], np.int32))
+    torch.cuda.synchronize()
+    assert layer.status() == 0
+    slots = 6 * 64
+    assert torch.equal(layer.cache, cache) and torch.equal(layer.weights[:, :slots], weights[:, :slots])
+    assert torch.equal(layer.slot_positions[:, :slots], positions[:, :slots])

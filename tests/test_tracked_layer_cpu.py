@@ -74,3 +74,18 @@ def test_a_layer_of_no_requests_notes_nothing(calls):
     layer = _make(track=True, batch=0)
     layer.prompt(_hidden(2), _i32(0, 1), _i32(0, -1), _int(0, MAX_PAGES))
     assert calls[-1][0] == "mla_cache_append_tokens" and layer.slot_positions.numel() == 0
+
+
+def test_padding_with_slots_caches_nothing(calls):
+    """A token of position -1 is padding whatever its slot says: the append, whose
+    positions are the slots, gets a negative one for it."""
+    layer = _make(track=True)
+    table, requests = _int(BATCH, MAX_PAGES), _i32(0, 1, 0, 1)
+    positions, slots = _i32(9, 12, -1, -1), _i32(3, 4, 0, 7)
+    layer.prefill(_hidden(4), None, positions, requests, _i32(0, 1, 2), table, _i32(4, 5), context_tokens=0, slots=slots)
+    layer.decode(_hidden(BATCH), None, _i32(-1, 13), table, _i32(0, 6), slots=_i32(0, 5))
+    appends = [a for name, a, _ in calls if name == "mla_cache_append_tokens"]
+    assert [a[3].tolist() for a in appends] == [[3, 4, -1, -1], [-1, 5]]
+    where = torch.full((BATCH, SLOTS), -1, dtype=torch.int32)
+    where[0, 3], where[1, 4], where[1, 5] = 9, 12, 13
+    assert torch.equal(_live(layer)[0], where) and slots.tolist() == [3, 4, 0, 7]
