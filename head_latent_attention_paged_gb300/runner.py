@@ -161,7 +161,9 @@ class AttentionLayer:
     requests), context() reads cached rows back.  With `track` the layer keeps
     what evict() needs: the attention weight that each cached row got from
     every decode() and prefill() (mla_cache_weights) and the position of the
-    token in each slot.  After an eviction a request's cache is shorter than
+    token in each slot.  A slot that is written again (its draft was rejected, its
+    request replaced) starts from no weight; what a rejected token's query gave
+    to other rows stays theirs.  After an eviction a request's cache is shorter than
     the positions it has seen, and new tokens go to `slots` of their own.
     Weights are bf16 tensors on
     the device: hidden_norm [hidden], w_qkv_a [hidden, q_rank + 576], q_norm
@@ -268,8 +270,9 @@ class AttentionLayer:
             self._track(at, positions, requests)
 
     def _track(self, at, positions, requests):
-        """Note which token stands in each slot.  Tokens that the append leaves alone or
-        reports (a request outside the batch, say) go to padding's entries."""
+        """Note which token stands in each slot, without any weight yet (what an earlier
+        one got there, a rejected draft say, is not its).  Tokens that the append leaves
+        alone or reports (a request outside the batch, say) go to padding's entries."""
         width = self.slot_positions.shape[1]
         live = (at >= 0) & (positions >= 0)
         if requests is None:
@@ -278,7 +281,9 @@ class AttentionLayer:
             live &= (requests >= 0) & (requests < self.B)
             requests = requests.clamp(0, self.B - 1)
         where = torch.where(live, at, width - 1).clamp_(max=width - 1)
-        self.slot_positions.view(-1)[requests.long() * width + where] = positions
+        entry = requests.long() * width + where
+        self.slot_positions.view(-1)[entry] = positions
+        self.weights.view(-1).index_fill_(0, entry, 0.0)
 
     def _weigh(self, plan, q_hat, lse, starts, block_table, seq_lens, workspace, stream):
         if self.weights is not None:

@@ -67,3 +67,64 @@ def test_padding_with_slots_leaves_the_cache(m, kv):
     slots = 6 * 64
     assert torch.equal(layer.cache, cache) and torch.equal(layer.weights[:, :slots], weights[:, :slots])
     assert torch.equal(layer.slot_positions[:, :slots], positions[:, :slots])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_a_rejected_drafts_weight_is_not_its_slots_next_tokens(m, kv):
+    """Two drafts a step, the second rejected: its slot is decoded again and holds what the
+    new tokens' queries give alone, as where its weight has been cleared by hand."""
+    kind = {"bf16": m.MLA_KV_BF16, "fp8": m.MLA_KV_FP8_E4M3_E8M0}[kv]
+    layers = [_tracked(m, 4, 2, 2, kind, kv)[1] for _ in range(2)]
+    bt = _table()
+
+    def step(layer, seed, first):
+        layer.decode(_states(4, seed), None, put([first, first + 1] * 2, np.int32), bt, put([first + 2] * 2, np.int32))
+        torch.cuda.synchronize()
+        return f64(layer.weights)
+
+    for layer in layers:
+        step(layer, 5, 0)
+        rejected = step(layer, 6, 2)                   # tokens 2 and 3; 3 is rejected
+        assert np.all(rejected[:, 3] > 0)
+    layers[1].weights[:, 3] = 0
+    after = [step(layer, 7, 3) for layer in layers]    # 3 again, and 4
+    assert np.array_equal(after[0], after[1])
+    # a query gives each head's weight away, one in all.  Scores are sums of 576 products
+    # in 32 bits, off by 576 * 2^-23 of their magnitudes' sum at most, which is below 15 here
+    # (|q . row| / 16 with values of order one), and lse by as much again: 2e-3 of a weight
+    given = (after[0][:, :3] - rejected[:, :3]).sum(1) + after[0][:, 3] + after[0][:, 4]
+    assert np.allclose(given, 2 * 4, rtol=2e-3, atol=0)
+    assert layers[0].slot_positions[:, :5].tolist() == [[0, 1, 2, 3, 4]] * 2 and layers[0].status() == 0
+
+
+def test_a_draft_rejected_in_a_graph(m):
+    """The same from a captured step, replayed on positions that go back."""
+    _, eager = _tracked(m, 4, 2, 2, m.MLA_KV_BF16, "bf16")
+    _, graphed = _tracked(m, 4, 2, 2, m.MLA_KV_BF16, "bf16")
+    bt = _table()
+    static = [_states(4, 0), put([0, 1] * 2, np.int32), put([2, 2], np.int32)]
+
+    def go(layer, hidden, positions, lens):
+        return layer.decode(hidden, None, positions, bt, lens)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        go(graphed, *static)                           # loads what is loaded once
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = go(graphed, *static)
+    for layer in (eager, graphed):
+        for request in range(2):
+            layer.forget(request)
+    for seed, first in enumerate((0, 2, 3, 3, 5)):
+        args = [_states(4, seed), put([first, first + 1] * 2, np.int32), put([first + 2] * 2, np.int32)]
+        for t, v in zip(static, args):
+            t.copy_(v)
+        graph.replay()
+        want = go(eager, *args)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(graphed.weights, eager.weights)
+        assert torch.equal(graphed.slot_positions, eager.slot_positions)
+    assert eager.status() == graphed.status() == 0

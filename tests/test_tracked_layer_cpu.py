@@ -89,3 +89,35 @@ def test_padding_with_slots_caches_nothing(calls):
     where = torch.full((BATCH, SLOTS), -1, dtype=torch.int32)
     where[0, 3], where[1, 4], where[1, 5] = 9, 12, 13
     assert torch.equal(_live(layer)[0], where) and slots.tolist() == [3, 4, 0, 7]
+
+
+def test_a_slot_written_again_starts_without_weight(calls):
+    """A rejected draft's slot, or one of an earlier request's: what its token got is
+    not the new one's."""
+    layer = _make(track=True)
+    table = _int(BATCH, MAX_PAGES)
+    layer.weights.copy_(torch.arange(layer.weights.numel()).view_as(layer.weights) + 1.0)
+    want = _live(layer)[1].clone()
+    layer.prompt(_hidden(3), _i32(5, 6, -1), _i32(0, 1, 1), table)
+    want[0, 5] = want[1, 6] = 0
+    assert torch.equal(_live(layer)[1], want)
+    layer.decode(_hidden(BATCH), None, _i32(9, -1), table, _i32(10, 0))
+    want[0, 9] = 0
+    assert torch.equal(_live(layer)[1], want)
+    layer.prefill(_hidden(4), None, _i32(30, 31, 32, -1), _i32(1, 1, BATCH, 0), _i32(0, 0, 2), table, _i32(9, 4),
+                  context_tokens=0, slots=_i32(2, 3, 4, 1))
+    want[1, 2] = want[1, 3] = 0
+    assert torch.equal(_live(layer)[1], want)
+    # before the weights of the call's queries are added
+    names = [name for name, _, _ in calls]
+    assert names.index("mla_cache_append_tokens") < names.index("mla_cache_weights")
+
+
+def test_forget_clears_one_request(calls):
+    layer = _make(track=True)
+    layer.weights.fill_(3.0)
+    layer.slot_positions.fill_(8)
+    layer.forget(1)
+    assert float(layer.weights[0].min()) == 3.0 and int(layer.slot_positions[0].min()) == 8
+    assert float(layer.weights[1].abs().max()) == 0 and int(layer.slot_positions[1].max()) == -1
+    _make().forget(0)                                  # a layer that does not track has nothing to forget
