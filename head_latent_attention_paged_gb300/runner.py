@@ -325,7 +325,7 @@ class AttentionLayer:
 
     def prefill(self, hidden, residual, positions, requests, query_starts, block_table, seq_lens, slots=None,
                 context_tokens=None):
-        """decode() for a chunk: T new tokens, request b's those from
+        """decode() for a chunk: T new tokens (or none), request b's those from
         query_starts[b] (int32 [B + 1]) on, token t at positions[t] of
         requests[t] (int32 [T]; a padded one behind query_starts[B] at -1);
         seq_lens int32 [B] with the new tokens; context_tokens: over a quantised
@@ -340,6 +340,8 @@ class AttentionLayer:
         self._check_table(block_table)
         if slots is not None:
             self._check_int32(slots=(slots, n))
+        if n == 0:
+            return torch.empty_like(hidden), hidden if residual is None else torch.empty_like(hidden)
         with torch.cuda.device(self.device):
             stream = torch.cuda.current_stream(self.device)
             x = torch.empty_like(hidden)

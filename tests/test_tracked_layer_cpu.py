@@ -121,3 +121,15 @@ def test_forget_clears_one_request(calls):
     assert float(layer.weights[0].min()) == 3.0 and int(layer.slot_positions[0].min()) == 8
     assert float(layer.weights[1].abs().max()) == 0 and int(layer.slot_positions[1].max()) == -1
     _make().forget(0)                                  # a layer that does not track has nothing to forget
+
+
+@pytest.mark.parametrize("track", [False, True])
+def test_prefill_of_no_tokens(monkeypatch, track):
+    """A step of the program in which no request has new tokens: nothing is launched."""
+    monkeypatch.setattr(torch.cuda, "device", _Nowhere)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    layer = _make(track=track)
+    none, table = _i32(), _int(BATCH, MAX_PAGES)
+    for residual in (None, _hidden(0)):
+        out, summed = layer.prefill(_hidden(0), residual, none, none, _int(BATCH + 1), table, _i32(3, 4))
+        assert out.shape == summed.shape == (0, HIDDEN) and out.dtype == torch.bfloat16
