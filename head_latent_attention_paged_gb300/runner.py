@@ -165,6 +165,13 @@ class AttentionLayer:
     request replaced) starts from no weight; what a rejected token's query gave
     to other rows stays theirs.  After an eviction a request's cache is shorter than
     the positions it has seen, and new tokens go to `slots` of their own.
+    Over a quantised cache prefill(), and decode() with `track`, set the rows of
+    the call's requests aside in bf16, 1,152 bytes each: `context_tokens` is the
+    most rows that the requests of a call have cached together, a page that
+    several share counted for each (rows beyond are masked out and reported).
+    Where pages are not shared it need not be above the pool's slots; None is
+    safe for all, max_pages for each request, and with `track` that room is held
+    for the layer's life.
     Weights are bf16 tensors on
     the device: hidden_norm [hidden], w_qkv_a [hidden, q_rank + 576], q_norm
     [q_rank], kv_norm [512], w_q_b [q_rank, H * 256], w_uk [H, 512, 192], w_uv
@@ -180,7 +187,8 @@ class AttentionLayer:
     def __init__(self, *, hidden_norm, w_qkv_a, q_norm, kv_norm, w_q_b, w_uk, w_uv, w_o, batch: int,
                  q_len: int = 1, page_size: int = 64, num_pages: int, max_pages: int,
                  rope: MlaRopePlan, kv_dtype: int = MLA_KV_BF16, eps: float = 1e-6,
-                 sm_scale: float = 1.0 / 16.0, sm_count: Optional[int] = None, track: bool = False):
+                 sm_scale: float = 1.0 / 16.0, sm_count: Optional[int] = None, track: bool = False,
+                 context_tokens: Optional[int] = None):
         dev = w_qkv_a.device
         self.device, self.eps, self.rope = dev, float(eps), rope
         self.B, self.Q, self.H = batch, q_len, int(w_uk.shape[0])
@@ -225,20 +233,22 @@ class AttentionLayer:
         self.q_problem = make_norm_problem(rows, self.q_rank, eps=self.eps,
                                            x_stride=self.q_rank + self.ROW)
         self.rope_problem = make_rope_problem(rows, self.H, self.HEAD, rope_offset=self.NOPE)
-        self.sm_count = sm_count
+        self.sm_count, self.context_tokens = sm_count, context_tokens
         self.weights = self.slot_positions = None
         if track:   # one entry more than there are slots: padding's
             self.weights = torch.zeros((batch, max_pages * page_size + 1), dtype=torch.float32, device=dev)
             self.slot_positions = torch.full_like(self.weights, -1, dtype=torch.int32)
-            self.step_plan = mla_chunk_make_plan(self.problem, rows, self._context(None), sm_count)
+            self.step_plan = mla_chunk_make_plan(self.problem, rows, self._context(rows), sm_count)
             self.step_workspace = torch.empty(int(self.step_plan.workspace_bytes), dtype=torch.uint8, device=dev)
             self.step_starts = torch.arange(0, rows + 1, q_len, dtype=torch.int32, device=dev)
             self.step_requests = torch.arange(rows, dtype=torch.int32, device=dev) // q_len
 
-    def _context(self, rows):
-        """Rows that one call can find cached: those of every request, or of the pool."""
-        pr = self.problem
-        return min(pr.batch * pr.max_pages_per_seq, pr.num_pages) * pr.page_size if rows is None else int(rows)
+    def _context(self, tokens, rows=None):
+        """Rows that a call of `tokens` new tokens can find cached, each request's counted
+        by themselves (pages that requests share are read for each of them): what the
+        program says, or all that the requests with new tokens have room for."""
+        pr, rows = self.problem, self.context_tokens if rows is None else rows
+        return min(pr.batch, tokens) * pr.max_pages_per_seq * pr.page_size if rows is None else int(rows)
 
     def _check_int32(self, **int32):
         """Kernels take addresses: what their arguments' shapes say has to be so."""
@@ -328,9 +338,8 @@ class AttentionLayer:
         """decode() for a chunk: T new tokens (or none), request b's those from
         query_starts[b] (int32 [B + 1]) on, token t at positions[t] of
         requests[t] (int32 [T]; a padded one behind query_starts[B] at -1);
-        seq_lens int32 [B] with the new tokens; context_tokens: over a quantised
-        cache, the most rows cached by the requests together (None: as many as
-        the pool holds, whose bf16 form is then set aside).  Returns (out,
+        seq_lens int32 [B] with the new tokens; context_tokens: the most rows
+        cached by the call's requests together (None: the layer's).  Returns (out,
         residual) in tensors of their own; padded tokens' are zeros' and theirs."""
         n = int(positions.numel())
         for h in (hidden, residual) if residual is not None else (hidden,):
@@ -360,7 +369,7 @@ class AttentionLayer:
             pr = self.problem
             mla_q_absorb(mla_decode_plan(make_problem(n, 1, self.H, pr.page_size, 1, 1), None, self.sm_count), q,
                          self.w_uk, q_hat, stream)
-            plan = mla_chunk_make_plan(pr, n, self._context(context_tokens), self.sm_count)
+            plan = mla_chunk_make_plan(pr, n, self._context(n, context_tokens), self.sm_count)
             workspace = torch.empty(int(plan.workspace_bytes), dtype=torch.uint8, device=self.device)
             o_lat = torch.zeros((n, self.H, 512), dtype=torch.bfloat16, device=self.device)
             lse = torch.empty((n, self.H), dtype=torch.float32, device=self.device)
@@ -375,7 +384,8 @@ class AttentionLayer:
         """Cut every request's cache to `budget` rows, the first `sinks` and last
         `recent` positions before those with the greatest weights: seq_lens
         (int32 [B]) is updated, and pages from ceil(budget / page) on are free.
-        Needs a layer made with track."""
+        Requests longer than that share no pages with others.  Needs a layer made
+        with track."""
         if self.weights is None:
             raise ValueError("evict() needs a layer that tracks weights (track=True)")
         self._check_int32(seq_lens=(seq_lens, self.B))

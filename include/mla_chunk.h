@@ -64,7 +64,8 @@ typedef struct {
  *                    widths of the row; q_len is not read, topk_width must be 0
  *   tokens         : query tokens of all requests together, >= 0
  *   context_tokens : quantised caches: the most rows that the requests of one
- *                    call have cached together (their rows are expanded to
+ *                    call have cached together, a page that several share counted
+ *                    for each of them (their rows are expanded to
  *                    bf16 in the workspace, 1,152 bytes each and up to 31 rows
  *                    more a request); MLA_KV_BF16: not read
  *   sm_count       : streaming multiprocessors to fill (152 on GB300), > 0

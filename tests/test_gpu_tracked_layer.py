@@ -128,3 +128,44 @@ def test_a_draft_rejected_in_a_graph(m):
         assert torch.equal(out, want) and torch.equal(graphed.weights, eager.weights)
         assert torch.equal(graphed.slot_positions, eager.slot_positions)
     assert eager.status() == graphed.status() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_requests_that_share_a_prefix(m, kv):
+    """Four requests over one prompt's pages, more rows between them than the pool holds:
+    outputs and weights are those of requests with pages of their own."""
+    from head_latent_attention_paged_gb300.runner import AttentionLayer
+    kind = {"bf16": m.MLA_KV_BF16, "fp8": m.MLA_KV_FP8_E4M3_E8M0, "fp4": m.MLA_KV_FP4_E2M1_E8M0}[kv]
+    B, page, prefix = 4, 16, 6
+    one, apart = _tracked(m, 4, B, 1, kind, kv, page, 8)
+    names = ("hidden_norm", "w_qkv_a", "q_norm", "kv_norm", "w_q_b", "w_uk", "w_uv", "w_o")
+    shared = AttentionLayer(**{n: getattr(one, n) for n in names}, batch=B, page_size=page, num_pages=prefix + B,
+                            max_pages=8, rope=one.rope, kv_dtype=kind, eps=one.eps, track=True)
+    own = np.arange(B * 8).reshape(B, 8)
+    common = np.concatenate([np.broadcast_to(np.arange(prefix), (B, prefix)), prefix + np.arange(B)[:, None],
+                             np.zeros((B, 1), dtype=np.int64)], axis=1)
+    own, common = put(own, np.int32), put(common, np.int32)
+    # the prompt, cached once; the same bytes in every request's pages
+    n = prefix * page
+    shared.prefill(_states(n, 1), None, put(np.arange(n), np.int32), put(np.zeros(n), np.int32),
+                   put([0, n, n, n, n], np.int32), common, put([n, 0, 0, 0], np.int32))
+    for b in range(B):
+        apart.cache[own[b, :prefix].long()] = shared.cache[:prefix]
+    for layer in (shared, apart):
+        layer.weights.zero_()
+    # a turn of five tokens each, and a step
+    five = 5 * B
+    args = (_states(five, 2), None, put(np.tile(n + np.arange(5), B), np.int32), put(np.repeat(np.arange(B), 5), np.int32),
+            put(np.arange(0, five + 1, 5), np.int32))
+    lens = put([n + 5] * B, np.int32)
+    outs = [layer.prefill(*args, bt, lens)[0] for layer, bt in ((shared, common), (apart, own))]
+    torch.cuda.synchronize()
+    assert shared.status() == apart.status() == 0 and B * (n + 5) > shared.problem.num_pages * page
+    assert torch.equal(outs[0], outs[1]) and torch.equal(shared.weights, apart.weights)
+    # a query gives each head's weight away, one in all (and see the bound above)
+    assert np.allclose(f64(shared.weights).sum(1), 5 * 4, rtol=2e-3, atol=0)
+    step = (_states(B, 3), None, put([n + 5] * B, np.int32))
+    outs = [layer.decode(*step, bt, lens + 1)[0].clone() for layer, bt in ((shared, common), (apart, own))]
+    torch.cuda.synchronize()
+    assert shared.status() == apart.status() == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(shared.weights, apart.weights)

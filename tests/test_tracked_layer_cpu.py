@@ -133,3 +133,34 @@ def test_prefill_of_no_tokens(monkeypatch, track):
     for residual in (None, _hidden(0)):
         out, summed = layer.prefill(_hidden(0), residual, none, none, _int(BATCH + 1), table, _i32(3, 4))
         assert out.shape == summed.shape == (0, HIDDEN) and out.dtype == torch.bfloat16
+
+
+def _room(layer, calls):
+    """Expanded rows that the plans of a layer's calls have room for."""
+    return [a[0].context_tokens for name, a, _ in calls if name == "mla_chunk_attend"]
+
+
+def test_room_for_requests_that_share_pages(calls):
+    """Over a quantised cache each request's rows are set aside by themselves: more than
+    the pool holds where requests share pages."""
+    import head_latent_attention_paged_gb300 as m
+    kw = dict(kv_dtype=m.MLA_KV_FP8_E4M3_E8M0, num_pages=MAX_PAGES)
+    layer = _make(track=True, **kw)
+    assert layer.step_plan.context_tokens == BATCH * SLOTS
+    table = _int(BATCH, MAX_PAGES)
+
+    def prefill(layer, n, **more):
+        layer.prefill(_hidden(n), None, _int(n), _int(n), _int(BATCH + 1), table, _int(BATCH), **more)
+        return _room(layer, calls)[-1]
+
+    # a call of one token has new tokens of one request at most
+    assert prefill(layer, 1) == SLOTS and prefill(layer, 5) == BATCH * SLOTS
+    assert prefill(layer, 5, context_tokens=77) == 77
+    # what the program knows of its requests' lengths, for the layer's life
+    layer = _make(track=True, context_tokens=100, **kw)
+    assert layer.step_plan.context_tokens == 100 and prefill(layer, 5) == 100
+    assert prefill(layer, 5, context_tokens=77) == 77
+    assert prefill(_make(context_tokens=0, **kw), 5) == 0
+    for bad in (-1, 2**31):
+        with pytest.raises(m.MlaError):
+            _make(track=True, context_tokens=bad, **kw)
