@@ -245,6 +245,18 @@ def _nbytes(buf, given, plan) -> int:
     return int(plan.workspace_bytes)
 
 
+def _rows_stride(given, *rows) -> int:
+    """Elements between two requests' entries of [batch][stride] arrays: as given, else
+    the tensors' last dimension, which it is only where all are packed and equally wide."""
+    if given is not None:
+        return given
+    stride = int(rows[0].shape[-1])
+    for t in rows:
+        if hasattr(t, "is_contiguous") and (int(t.shape[-1]) != stride or not t.is_contiguous()):
+            raise ValueError(f"arrays that are not packed rows of {stride} elements need their stride given")
+    return stride
+
+
 def mla_decode_plan(problem: MlaProblem, seq_lens_host=None, sm_count: int = 152,
                     split_tokens: int = 0) -> MlaPlan:
     plan = MlaPlan()
@@ -486,10 +498,10 @@ def mla_cache_weights(plan: MlaChunkPlan, q_hat, lse, query_starts, kv_cache, bl
                       workspace, weights_out, weights_in=None, stride=None, status=None, stream=None,
                       workspace_bytes=None) -> None:
     """weights_out[b][t] = weights_in[b][t] (None: 0) + the weight that request
-    b's queries give to its cached row t, f32 [batch][stride] (stride None: of a
-    tensor, its last dimension)."""
+    b's queries give to its cached row t, f32 [batch][stride] (stride None: packed
+    tensors', their last dimension)."""
     size = _nbytes(workspace, workspace_bytes, plan)
-    stride = int(weights_out.shape[-1]) if stride is None else stride
+    stride = _rows_stride(stride, weights_out, weights_in)
     try:
         rc = _lib.mla_cache_weights(
             plan, q_hat.data_ptr(), lse.data_ptr(), query_starts.data_ptr(), kv_cache.data_ptr(),
@@ -520,9 +532,10 @@ def mla_cache_evict(plan: MlaEvictPlan, kv_cache, block_table, seq_lens, weights
                     status=None, stream=None, workspace_bytes=None) -> None:
     """Cut each request's cache to the plan's budget: kept rows behind it move
     into the slots below that became free.  Outputs that are not given are their
-    inputs."""
+    inputs; weights and positions are [batch][stride] (stride None: as in
+    mla_cache_weights)."""
     size = _nbytes(workspace, workspace_bytes, plan)
-    stride = int(weights.shape[-1]) if stride is None else stride
+    stride = _rows_stride(stride, weights, positions, weights_out, positions_out)
     seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
     weights_out = weights if weights_out is None else weights_out
     positions_out = positions if positions_out is None else positions_out
