@@ -28,6 +28,31 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return a && b && x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
 }
 
+struct Array {
+  const void* base;
+  int64_t bytes;
+  const void* own;   // of one that is written: the input that it may be
+};
+// Whether every array that is written stands alone, but for an output that is its input.
+bool stand_alone(const Array* written, int n_written, const Array* read, int n_read) {
+  for (int i = 0; i < n_written; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i].base, written[i].bytes, written[j].base, written[j].bytes)) return false;
+    for (int j = 0; j < n_read; ++j)
+      if (!(written[i].own == read[j].base && written[i].base == read[j].base) &&
+          overlap(written[i].base, written[i].bytes, read[j].base, read[j].bytes))
+        return false;
+  }
+  return true;
+}
+template <int kWritten, int kRead>
+bool stand_alone(const Array (&written)[kWritten], const Array (&read)[kRead]) {
+  return stand_alone(written, kWritten, read, kRead);
+}
+
+int64_t cache_bytes(const mla_problem& pr) { return static_cast<int64_t>(pr.num_pages) * pr.page_size * row_bytes(pr.kv_dtype); }
+int64_t table_bytes(const mla_problem& pr) { return static_cast<int64_t>(pr.batch) * pr.max_pages_per_seq * 4; }
+
 int check_chunk_problem(const mla_problem* pr) {
   const int rc = check_cache_shape(pr);
   if (rc != MLA_OK) return rc;
@@ -143,6 +168,14 @@ int mla_chunk_attend(const mla_chunk_plan* plan, const void* q_hat, const int32_
   if (plan->tokens == 0 || plan->problem.batch == 0) return MLA_OK;
   if (!o_lat || !lse) return MLA_ERR_INVALID_ARGUMENT;
   if (!aligned(o_lat, 32) || !aligned(lse, 4)) return MLA_ERR_MISALIGNED;
+  const mla_problem& pr = plan->problem;
+  const int64_t rows = static_cast<int64_t>(plan->tokens) * pr.num_heads;
+  const Array written[] = {{workspace, plan->workspace_bytes, nullptr}, {o_lat, rows * kDc * 2, nullptr},
+                           {lse, rows * 4, nullptr}, {status, 4, nullptr}};
+  const Array read[] = {{q_hat, rows * kDqk * 2, nullptr}, {query_starts, pr.batch * 4ll + 4, nullptr},
+                        {kv_cache, cache_bytes(pr), nullptr}, {block_table, table_bytes(pr), nullptr},
+                        {seq_lens, pr.batch * 4ll, nullptr}};
+  if (!stand_alone(written, read)) return MLA_ERR_INVALID_ARGUMENT;
   p.o = static_cast<uint16_t*>(o_lat);
   p.lse = lse;
   const ChunkWorkspace w = workspace_of(*plan, workspace);
@@ -162,9 +195,15 @@ int mla_cache_weights(const mla_chunk_plan* plan, const void* q_hat, const float
   if (rc != MLA_OK) return rc;
   if ((!lse && plan->tokens > 0) || !weights_out || stride < 1 || stride > INT64_MAX / 8 / (p.c.batch + 1)) return MLA_ERR_INVALID_ARGUMENT;
   if (!aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4)) return MLA_ERR_MISALIGNED;
-  const int64_t bytes = p.c.batch * stride * 4;
-  if (weights_in != weights_out && overlap(weights_in, bytes, weights_out, bytes)) return MLA_ERR_INVALID_ARGUMENT;
-  if (plan->problem.batch == 0) return MLA_OK;
+  const mla_problem& pr = plan->problem;
+  if (pr.batch == 0) return MLA_OK;
+  const int64_t bytes = pr.batch * stride * 4, rows = static_cast<int64_t>(plan->tokens) * pr.num_heads;
+  const Array written[] = {{workspace, plan->workspace_bytes, nullptr}, {weights_out, bytes, weights_in}, {status, 4, nullptr}};
+  const Array read[] = {{q_hat, rows * kDqk * 2, nullptr}, {lse, rows * 4, nullptr},
+                        {query_starts, pr.batch * 4ll + 4, nullptr}, {kv_cache, cache_bytes(pr), nullptr},
+                        {block_table, table_bytes(pr), nullptr}, {seq_lens, pr.batch * 4ll, nullptr},
+                        {weights_in, bytes, nullptr}};
+  if (!stand_alone(written, read)) return MLA_ERR_INVALID_ARGUMENT;
   p.lse = lse;
   p.in = weights_in;
   p.out = weights_out;
@@ -218,28 +257,13 @@ int mla_cache_evict(const mla_evict_plan* plan, void* kv_cache, const int32_t* b
       !aligned(positions_out, 4) || !aligned(status, 4))
     return MLA_ERR_MISALIGNED;
   if (pr.batch == 0) return MLA_OK;
-  // every array that is written stands alone, but for an output that is its input
-  const int64_t table = static_cast<int64_t>(pr.batch) * pr.max_pages_per_seq * 4, slots = pr.batch * stride * 4;
-  struct Array {
-    const void* base;
-    int64_t bytes;
-    const void* own;   // the input that it may be
-  };
-  const Array written[] = {
-      {kv_cache, static_cast<int64_t>(pr.num_pages) * pr.page_size * row_bytes(pr.kv_dtype), nullptr},
-      {workspace, plan->workspace_bytes, nullptr}, {seq_lens_out, pr.batch * 4ll, seq_lens},
-      {weights_out, slots, weights}, {positions_out, slots, positions}, {status, 4, nullptr}};
-  const Array read[] = {{block_table, table, nullptr}, {seq_lens, pr.batch * 4ll, nullptr},
+  const int64_t slots = pr.batch * stride * 4;
+  const Array written[] = {{kv_cache, cache_bytes(pr), nullptr}, {workspace, plan->workspace_bytes, nullptr},
+                           {seq_lens_out, pr.batch * 4ll, seq_lens}, {weights_out, slots, weights},
+                           {positions_out, slots, positions}, {status, 4, nullptr}};
+  const Array read[] = {{block_table, table_bytes(pr), nullptr}, {seq_lens, pr.batch * 4ll, nullptr},
                         {weights, slots, nullptr}, {positions, slots, nullptr}};
-  const int n_written = static_cast<int>(sizeof(written) / sizeof(written[0]));
-  for (int i = 0; i < n_written; ++i) {
-    for (int j = 0; j < i; ++j)
-      if (overlap(written[i].base, written[i].bytes, written[j].base, written[j].bytes)) return MLA_ERR_INVALID_ARGUMENT;
-    for (const Array& r : read)
-      if (!(written[i].own == r.base && written[i].base == r.base) &&
-          overlap(written[i].base, written[i].bytes, r.base, r.bytes))
-        return MLA_ERR_INVALID_ARGUMENT;
-  }
+  if (!stand_alone(written, read)) return MLA_ERR_INVALID_ARGUMENT;
   EvictParams p;
   p.kv = static_cast<uint8_t*>(kv_cache);
   p.block_table = block_table;

@@ -108,6 +108,8 @@ MLA_API int mla_chunk_make_plan(const mla_problem* problem, int32_t tokens, int6
  *                  MLA_STATUS_BAD_INDEX: a query start or length out of range, or
  *                  more rows than context_tokens, the surplus masked out;
  *                  MLA_STATUS_TIMEOUT: an internal wait hit its limit
+ * The workspace and each output share no memory with an input or one another
+ * (MLA_ERR_INVALID_ARGUMENT).
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT, MLA_ERR_MISALIGNED (a pointer not on
  * 16 bytes; o_lat: 32; int32, lse and status: 4), MLA_ERR_WORKSPACE_TOO_SMALL or
  * MLA_ERR_CUDA.
@@ -134,8 +136,7 @@ MLA_API int mla_chunk_attend(const mla_chunk_plan* plan, const void* q_hat,
  *   stride      : elements between two requests' weights, >= 1; slots from stride
  *                 on are neither read nor written
  * The other arguments and the result are mla_chunk_attend's (weights: 4-byte
- * alignment; weights_out overlapping weights_in otherwise than the same address
- * is MLA_ERR_INVALID_ARGUMENT).
+ * alignment; weights_out may only be weights_in itself, not overlap it).
  */
 MLA_API int mla_cache_weights(const mla_chunk_plan* plan, const void* q_hat, const float* lse,
                               const int32_t* query_starts, const void* kv_cache,
