@@ -51,6 +51,11 @@ bool stand_alone(const Array (&written)[kWritten], const Array (&read)[kRead]) {
 }
 
 int64_t cache_bytes(const mla_problem& pr) { return static_cast<int64_t>(pr.num_pages) * pr.page_size * row_bytes(pr.kv_dtype); }
+// Of [batch][stride] entries of 4 bytes: to the last request's last slot.
+int64_t entry_bytes(const mla_problem& pr, int64_t stride) {
+  const int64_t slots = static_cast<int64_t>(pr.max_pages_per_seq) * pr.page_size;
+  return ((pr.batch - 1) * stride + (stride < slots ? stride : slots)) * 4;
+}
 int64_t table_bytes(const mla_problem& pr) { return static_cast<int64_t>(pr.batch) * pr.max_pages_per_seq * 4; }
 
 int check_chunk_problem(const mla_problem* pr) {
@@ -197,7 +202,7 @@ int mla_cache_weights(const mla_chunk_plan* plan, const void* q_hat, const float
   if (!aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4)) return MLA_ERR_MISALIGNED;
   const mla_problem& pr = plan->problem;
   if (pr.batch == 0) return MLA_OK;
-  const int64_t bytes = pr.batch * stride * 4, rows = static_cast<int64_t>(plan->tokens) * pr.num_heads;
+  const int64_t bytes = entry_bytes(pr, stride), rows = static_cast<int64_t>(plan->tokens) * pr.num_heads;
   const Array written[] = {{workspace, plan->workspace_bytes, nullptr}, {weights_out, bytes, weights_in}, {status, 4, nullptr}};
   const Array read[] = {{q_hat, rows * kDqk * 2, nullptr}, {lse, rows * 4, nullptr},
                         {query_starts, pr.batch * 4ll + 4, nullptr}, {kv_cache, cache_bytes(pr), nullptr},
@@ -257,7 +262,7 @@ int mla_cache_evict(const mla_evict_plan* plan, void* kv_cache, const int32_t* b
       !aligned(positions_out, 4) || !aligned(status, 4))
     return MLA_ERR_MISALIGNED;
   if (pr.batch == 0) return MLA_OK;
-  const int64_t slots = pr.batch * stride * 4;
+  const int64_t slots = entry_bytes(pr, stride);
   const Array written[] = {{kv_cache, cache_bytes(pr), nullptr}, {workspace, plan->workspace_bytes, nullptr},
                            {seq_lens_out, pr.batch * 4ll, seq_lens}, {weights_out, slots, weights},
                            {positions_out, slots, positions}, {status, 4, nullptr}};
