@@ -327,7 +327,7 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream) {
   // CTAs for a request: more while there are multiprocessors for them and slots for
   // their threads
   int shift = 0;
-  while (1 << shift < kMaxCluster && (int64_t{2} << shift) * p.batch <= 152 && slots > kThreads << shift) ++shift;
+  while (1 << shift < kMaxCluster && (int64_t{2} << shift) * p.batch <= kSms && slots > kThreads << shift) ++shift;
   const int cluster = 1 << shift;
   const int64_t own = (slots + cluster * kThreads - 1) / (cluster * kThreads) * kThreads;
   const int cap = static_cast<int>(own < kMaxKeys ? own : kMaxKeys);
@@ -350,7 +350,7 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t stream) {
   if (err != cudaSuccess || p.most_moves == 0) return err;
   // rows of all requests over a few blocks a multiprocessor, at most one warp a move
   int64_t blocks = (p.most_moves + kMoveWarps - 1) / kMoveWarps;
-  const int64_t fill = (152 * 8 + p.batch - 1) / p.batch;
+  const int64_t fill = (kSms * 8 + p.batch - 1) / p.batch;
   if (blocks > fill) blocks = fill;
   const dim3 grid(static_cast<unsigned>(blocks), p.batch);
   const auto launch = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * kMoveWarps, 0, stream, p); };

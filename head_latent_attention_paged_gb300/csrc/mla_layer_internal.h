@@ -6,6 +6,10 @@
 
 namespace mla {
 
+// Multiprocessors that launches without a plan's sm_count are sized for (GB300's); on
+// another number the results are the same.
+constexpr int kSms = 152;
+
 // The layer operators are launched as programmatic dependents of whatever
 // precedes them on their stream: the launch itself, and the set-up before
 // after_predecessor(), overlap the predecessor's tail.  A kernel touches no

@@ -30,7 +30,7 @@ constexpr int kRopeMostHeads = 12;  // and takes altogether
 // of 256) with 512, 768 and 1,024 for each multiprocessor 3.1, 3.6 and 4.1 us, 333
 // of 29 (192, f32, halves) 3.5, 3.1 and 4.6.  A thread with eight cosines (bf16
 // halves) counts as four: 2,688 of 11 (64 of 256) 2.6 us, as one 4.0.
-constexpr int64_t kRopeFill = 152 * 768;
+constexpr int64_t kRopeFill = kSms * 768;
 
 // n / d for n < 2^31, as a multiplication (round-up method).
 struct Divider {

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(32 * kTokenWarps)
 // Tokens of a warp: one while there are multiprocessors to fill (latency),
 // then up to `most` as the warps get to more than fit at once.
 int chunk_of(int32_t tokens, int most) {
-  const int c = tokens / (152 * 32);
+  const int c = tokens / (kSms * 32);
   return c < 1 ? 1 : c > most ? most : c;
 }
 int blocks_of(int32_t tokens, int chunk) {

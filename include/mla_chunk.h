@@ -164,6 +164,7 @@ typedef struct {
  *   budget  : rows that each request keeps at most, >= 1
  *   sinks   : tokens of positions below this are kept before all others, >= 0
  *   recent  : so are the tokens of the last `recent` positions, >= 0
+ * An eviction's launches are sized for 152 multiprocessors (GB300).
  * Returns MLA_OK, MLA_ERR_INVALID_ARGUMENT or MLA_ERR_UNSUPPORTED.
  */
 MLA_API int mla_evict_make_plan(const mla_problem* problem, int32_t budget, int32_t sinks,
