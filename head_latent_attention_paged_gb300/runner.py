@@ -241,7 +241,8 @@ class AttentionLayer:
             self.step_plan = mla_chunk_make_plan(self.problem, rows, self._context(rows), sm_count)
             self.step_workspace = torch.empty(int(self.step_plan.workspace_bytes), dtype=torch.uint8, device=dev)
             self.step_starts = torch.arange(0, rows + 1, q_len, dtype=torch.int32, device=dev)
-            self.step_requests = torch.arange(rows, dtype=torch.int32, device=dev) // q_len
+            # the first entry of each of a step's rows' requests
+            self.step_entries = torch.arange(rows, device=dev) // q_len * self.weights.shape[1]
 
     def _context(self, tokens, rows=None):
         """Rows that a call of `tokens` new tokens can find cached, each request's counted
@@ -284,14 +285,13 @@ class AttentionLayer:
         one got there, a rejected draft say, is not its).  Tokens that the append leaves
         alone or reports (a request outside the batch, say) go to padding's entries."""
         width = self.slot_positions.shape[1]
-        live = (at >= 0) & (positions >= 0)
+        live = at >= 0                    # padding's are negative, at slots too
         if requests is None:
-            requests = self.step_requests
+            first = self.step_entries
         else:
             live &= (requests >= 0) & (requests < self.B)
-            requests = requests.clamp(0, self.B - 1)
-        where = torch.where(live, at, width - 1).clamp_(max=width - 1)
-        entry = requests.long() * width + where
+            first = requests.clamp(0, self.B - 1).long() * width
+        entry = torch.where(live, at, width - 1).clamp_(max=width - 1) + first
         self.slot_positions.view(-1)[entry] = positions
         self.weights.view(-1).index_fill_(0, entry, 0.0)
 
