@@ -4,21 +4,25 @@
 //     s = scale q . row        S [128 x 128] = Q [128 x 576] K^T
 //     p = exp2(s - ref)        O [128 x 512] += P [128 x 128] V
 //
-// over tiles of 128 cached rows, K the whole rows and V their first 512 values,
-// so the cached tile is the operand of both products.  The running reference
-// of the exponent moves only when a row's maximum outgrows it by 2^8.
+// over tiles of 128 cached rows, K the whole rows and V their first 512 values.
+// The running reference of the exponent moves only when a row's maximum outgrows
+// it by 2^8.  P is rounded to bf16: a product's operands have one type, and V, the
+// cached rows, is bf16.  O is divided by the sum of the rounded weights, so that
+// what is common to a row's roundings cancels; the rest is 0.5e-3 of o (16,384 rows
+// seen) to 1.4e-3 (some hundred), where o's own rounding is 1.7e-3.
 //
 // Why pairs: O takes 128 x 512 accumulators, all of one SM's tensor memory.
 // Two CTAs with 64 of the 128 rows each keep O (256 columns: with M = 128 over
 // a pair, lanes 64..127 hold the second half of a row's columns) beside two S
 // (64 columns each), and the operand that both need is read from both shared
 // memories: each CTA loads half of a tile's tokens for S and half of its latent
-// columns for O.
+// columns for O: 278 KB of copies, from L2, for a tile of 147 KB.
 //
 // Work is a row tile's tiles one after another, and all of it in a line that is cut
 // evenly between the pairs; row tiles that were cut are merged by a second kernel.
 // Long chunks are bound by the tensor cores (2,048 tokens of 20 heads behind 14,336:
-// 710-765 us by machine, 1,790-1,930 TFLOP/s of a library product's 1,905).  Between two row
+// 710-765 us by machine, 1,790-1,930 TFLOP/s of a library product's 1,905; called again
+// and again 823-841 us, at the power limit).  Between two row
 // tiles the softmax warps stand for about 3.5 us: the last product, the output's 64 KB,
 // the next row tile's first scores.  Chunks with few tiles a row tile pay that often
 // (two whole prompts of 1,283 tokens, 5 tiles each: 110 us, 1,040 TFLOP/s).  A single
@@ -569,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2, base2);
           e.x = exp2_approx(e.x);
           e.y = exp2_approx(e.y);
-          w[k] = pack_bf16(e);
+          w[k] = pack_bf16(e);            // V's type; what it costs stands at the top
           sums[k & 1] = __fadd2_rn(sums[k & 1], e);
           rounded[k & 1] = __fadd2_rn(rounded[k & 1], make_float2(bf16_lo(w[k]), bf16_hi(w[k])));
         }

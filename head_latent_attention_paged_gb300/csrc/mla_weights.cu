@@ -13,7 +13,10 @@
 // One read of the cache bounds a decode step (64 requests of 4,608 rows, 20 heads: 67 us,
 // 5.1 TB/s, 51 us at the copy rate), the products a prompt's end (64 tokens of 20 heads
 // behind 32,768: 38 us, 1,260 TFLOP/s, where each pair has 1 or 2 tiles and starts and
-// ends idle), the three launches a few drafts over a quantised cache (26 us).
+// ends idle), the three launches a few drafts over a quantised cache (26 us).  A decode
+// step over a quantised cache pays for rows expanded in HBM that it uses once (64 requests
+// of 4,608 rows: FP8 152 us, FP4 139), short whole prompts for cuts at tiles alone (2 of
+// 1,283 tokens, 32 heads: 12 tiles for 76 pairs, 413 us).
 #include <cuda_runtime.h>
 
 #include "mla_chunk_internal.h"
@@ -27,8 +30,12 @@ constexpr int kTokens = 2 * kTileRows;  // of a pair's tile
 constexpr int kMaxN = 256;              // rows (token, head) of a block
 // The ring: a slot has a chunk of the CTA's tokens and one of its half of a block's
 // rows, as many slots as there is room for (a multiple of 3, chunks being loaded three
-// at a time): 6 for blocks of 256 rows, 9 where no request has more than 64, as in a
+// at a time): 6 for blocks of 256 rows, 9 where no request has more than 128, as in a
 // decode step, which memory bounds (with 6: decode step of 64 75 us).
+// Two warps of each CTA fill a slot, and a wait by parity cannot tell a use from the one
+// two before it.  Neither warp can be that far ahead: `full` counts the arrivals of both
+// (the leader's) and the bytes of all four, so that the MMAs that free a slot wait for
+// every one of them, and none passes `empty` for the next use before all have filled this one.
 constexpr int kABytes = kTileRows * 128;
 constexpr int kMaxSlots = 9, kRingBytes = 216 * 1024;
 constexpr int kSumWarps = 8;

@@ -156,7 +156,8 @@ class AttentionLayer:
 
     decode() runs a whole step of `q_len` tokens for each of `batch` requests;
     prefill() does the same for any number of new tokens of each (mla_chunk_attend
-    in the place of mla_decode_step, the up-projection a library product);
+    in the place of mla_decode_step, the up-projection a library product; for many
+    requests faster than decode() from some four tokens of each on);
     prompt() only caches the rows of a prompt's tokens (any mixture of
     requests), context() reads cached rows back.  With `track` the layer keeps
     what evict() needs: the attention weight that each cached row got from
@@ -164,7 +165,9 @@ class AttentionLayer:
     token in each slot.  A slot that is written again (its draft was rejected, its
     request replaced) starts from no weight; what a rejected token's query gave
     to other rows stays theirs.  After an eviction a request's cache is shorter than
-    the positions it has seen, and new tokens go to `slots` of their own.
+    the positions it has seen, and new tokens go to `slots` of their own (their
+    keys are then turned and rounded to bf16 ahead of the append, whose quantiser
+    to FP8 or FP4 otherwise takes the turned key in 32 bits).
     Over a quantised cache prefill(), and decode() with `track`, set the rows of
     the call's requests aside in bf16, 1,152 bytes each: `context_tokens` is the
     most rows that the requests of a call have cached together, a page that
@@ -339,8 +342,10 @@ class AttentionLayer:
         query_starts[b] (int32 [B + 1]) on, token t at positions[t] of
         requests[t] (int32 [T]; a padded one behind query_starts[B] at -1);
         seq_lens int32 [B] with the new tokens; context_tokens: the most rows
-        cached by the call's requests together (None: the layer's).  Returns (out,
-        residual) in tensors of their own; padded tokens' are zeros' and theirs."""
+        cached by the call's requests together (None: the layer's).  A layer that
+        tracks adds the weights of all the call's queries.  Returns (out, residual)
+        in tensors of their own (hidden itself without a residual); padded tokens'
+        are zeros' and theirs."""
         n = int(positions.numel())
         for h in (hidden, residual) if residual is not None else (hidden,):
             self._check_hidden(h, n)

@@ -46,7 +46,7 @@ typedef struct {
   int64_t context_tokens;   /* quantised caches: rows expanded at most */
   int32_t clusters;         /* pairs of CTAs that share the attention's work */
   int32_t mark;             /* set by mla_chunk_make_plan */
-  int64_t ws_partial_o;     /* byte offset of f32 [2 * clusters][128][512] */
+  int64_t ws_partial_o;     /* byte offset of f32 [2 * clusters][64][128][8]: columns in eights */
   int64_t ws_partial_lse;   /* byte offset of f32 [2 * clusters][128] */
   int64_t ws_segments;      /* byte offset of int32 [2 * clusters][4] */
   int64_t ws_starts;        /* byte offset of int32 [batch + 1][2]: a quantised cache's
